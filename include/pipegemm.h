@@ -324,6 +324,131 @@ typedef struct {
 int gemm_occupancy(gemm_handle_t h, int64_t M, int64_t N, int64_t K, int dtype, int layout,
                    int stages, int variant, gemm_occupancy_t *out);
 
+/* ---- 8-bit floating point, with a scale for each block of 128 -------------
+ *
+ * One linear layer through 8 bits: gemm_rms_fp8 or gemm_quantize_fp8 make an
+ * 8-bit matrix and its scales, gemm_run_fp8 multiplies two of them, and
+ * gemm_rms_backward is the norm's backward pass.  (The product's own
+ * backward pass is two more products: dX = dY * W with W quantised by tiles
+ * and transposed, dW = dY^T * X with both quantised along the rows of X.)
+ *
+ * Types.  GEMM_E4M3 (largest value 448, no infinity) and GEMM_E5M2 (57344)
+ * are the OCP 8-bit floats, torch's float8_e4m3fn and float8_e5m2.  A stored
+ * value q of a block with scale s stands for q * s; s is fp32.
+ *
+ * Blocks are 128 consecutive values of a row (block_rows 1, "row") or 128
+ * rows by 128 columns (block_rows 128, "tile"); the last ones may be shorter.
+ * The scale of row (or row block) i and block b is at
+ * S[i * s_row + b * s_blk], both strides in elements, zero allowed; s_row = 1
+ * is the fastest for the product.
+ *
+ * Quantisation of a block (rounding to nearest even, everything in fp32):
+ *   s = max(amax |x| / largest, 2^-126); with pow2 = 1 rounded up to a power of two;
+ *   q = fp8(x * (1 / s)).
+ * A NaN stays a NaN in its place and does not enter amax; an infinity gives
+ * its block an infinite scale (every value of it then stands for NaN).
+ *
+ * All of these are asynchronous, allocate nothing, and enqueue one kernel
+ * (gemm_rms_backward: two) on `stream`, on the handle's device; any
+ * number of calls may overlap, on any streams (gemm_rms_backward: each with its own
+ * workspace).  A captured graph can hold them.  Outputs must not overlap
+ * inputs or one another, but where stated.  Sizes of zero are accepted. */
+enum { GEMM_E4M3 = 16, GEMM_E5M2 = 17 };
+
+/* Part of C that one workgroup of gemm_run_fp8 computes.  The first two stage
+ * operands through LDS and need rows that start on 16 bytes; the others take
+ * any address.  GEMM_FP8_TILE_AUTO: the largest one that the call's rows fill at
+ * least half and that gives every compute unit a workgroup. */
+enum { GEMM_FP8_TILE_AUTO = -1, GEMM_FP8_TILE_256x256 = 0, GEMM_FP8_TILE_128x128 = 1, GEMM_FP8_TILE_64x64 = 2,
+       GEMM_FP8_TILE_64x32 = 3, GEMM_FP8_TILE_32x32 = 4, GEMM_FP8_TILE_16x16 = 5 };
+
+typedef struct {
+    int32_t tile;        /* GEMM_FP8_TILE_* chosen */
+    int32_t block_m, block_n;
+    int32_t waves_k;     /* waves that share a piece's K */
+    int32_t threads;     /* per workgroup */
+    int32_t staged;      /* 1: operands pass through LDS */
+    int32_t widened;     /* 1: multiplied as bf16 (fp32 outputs) */
+    int32_t reserved;
+    int64_t grid;        /* workgroups */
+    int64_t k_blocks;    /* ceil(K / 128) */
+} gemm_fp8_info_t;
+
+/* C = A * B of 8-bit matrices, each block of products times its scales:
+ *   C[i][j] = sum over blocks b of SA[i][b] * SB[jb][b] *
+ *             sum over k in block b of A[i][k] * B[j][k],
+ * A row-major M x K with "row" scales; B column-major K x N (its N x K
+ * transpose, K contiguous: layout RC) with "tile" scales (b_scale_rows 128,
+ * jb = j / 128) or "row" scales (b_scale_rows 1, jb = j).
+ * a_type, b_type: GEMM_E4M3 or GEMM_E5M2, in any combination.  c_dtype:
+ * GEMM_F16, GEMM_BF16 or GEMM_F32; sums over blocks are fp32, rounded once.
+ * The sum inside a block is the matrix core's: for 16-bit outputs that of
+ * the 8-bit instructions (about 2e-5 off on normal data); for
+ * fp32 outputs both operands are widened to bf16, exactly, and it is fp32's
+ * (half the rate).  The order of the sums is fixed for a tile class.
+ * accumulate = 1 (fp32 only): C += instead.
+ * Leading dimensions are in elements, C may have any; an operand whose base
+ * and leading dimension are not multiples of 16 bytes is read into
+ * registers by smaller tiles, slower.  No byte at or past column K of
+ * a row counts, whatever it holds.
+ * Errors: GEMM_ERR_INVALID_ARG (NULL, a negative size or stride, an unknown
+ * type, a leading dimension below K or N), GEMM_ERR_ALIGNMENT (C, SA or SB
+ * not element-aligned, or a staged tile asked for with other rows than it
+ * takes), GEMM_ERR_UNSUPPORTED (accumulate without GEMM_F32, the 256x256
+ * tile with it, a tile's rows or a row's scales spanning 2^31 bytes),
+ * GEMM_ERR_HIP. */
+int gemm_run_fp8(gemm_handle_t h, int64_t M, int64_t N, int64_t K,
+                 int a_type, int b_type, int c_dtype, int b_scale_rows, int accumulate, int tile,
+                 const void *A, int64_t lda, const float *SA, int64_t sa_row, int64_t sa_blk,
+                 const void *B, int64_t ldb, const float *SB, int64_t sb_row, int64_t sb_blk,
+                 void *C, int64_t ldc, void *stream);
+
+/* What gemm_run_fp8 would launch on a 256-CU device, after the same checks;
+ * no HIP call.  NULL pointers are "not given" and skipped. */
+int gemm_query_fp8(int64_t M, int64_t N, int64_t K,
+                   int a_type, int b_type, int c_dtype, int b_scale_rows, int accumulate, int tile,
+                   const void *A, int64_t lda, const float *SA, int64_t sa_row, int64_t sa_blk,
+                   const void *B, int64_t ldb, const float *SB, int64_t sb_row, int64_t sb_blk,
+                   const void *C, int64_t ldc, gemm_fp8_info_t *info);
+
+/* X (M x K; GEMM_F16, GEMM_BF16 or GEMM_F32) to 8 bits.  Q, S: X by blocks
+ * of block_rows x 128.  QT, ST: its transpose (K x M), by blocks of 1 x 128
+ * along M, or 128 x 128 (the same values and scales as Q's, transposed).
+ * Either pair may be NULL, not both.  Only columns before K (M) of Q (QT) are
+ * written.  Errors as above; GEMM_ERR_UNSUPPORTED for 2^24 and more workgroups (about
+ * 2^37 values). */
+int gemm_quantize_fp8(gemm_handle_t h, int64_t M, int64_t K, int x_dtype, int fp8_type, int block_rows, int pow2,
+                      const void *X, int64_t ldx, void *Q, int64_t ldq, float *S, int64_t s_row, int64_t s_blk,
+                      void *QT, int64_t ldqt, float *ST, int64_t st_row, int64_t st_blk, void *stream);
+
+#define GEMM_RMS_MAX_D 32768
+#define GEMM_RMS_MAX_ROWS (1 << 22)
+
+/* Root-mean-square norm of each row of x + residual, to 8 bits:
+ *   h = x + residual, rounded to x's type; rstd = 1 / sqrt(mean(h^2) + eps);
+ *   y = h * rstd * w in fp32; Q, S: y by blocks of 1 x 128.
+ * X, R, H, Y: M x D of x_dtype (GEMM_F16, GEMM_BF16, GEMM_F32).  W: D
+ * values of w_dtype (x_dtype or GEMM_F32).  R may be NULL (h = x); H (h), Y
+ * (y, rounded), Q with S, and rstd (M fp32 values) are written where they are
+ * not NULL, and one of Q and Y must be given.  H may be X or R (in
+ * place).  GEMM_ERR_UNSUPPORTED above GEMM_RMS_MAX_D or GEMM_RMS_MAX_ROWS. */
+int gemm_rms_fp8(gemm_handle_t h, int64_t M, int64_t D, int x_dtype, int w_dtype, int fp8_type, int pow2, float eps,
+                 const void *X, int64_t ldx, const void *R, int64_t ldr, const void *W, void *H, int64_t ldh,
+                 void *Y, int64_t ldy, void *Q, int64_t ldq, float *S, int64_t s_row, int64_t s_blk, float *rstd,
+                 void *stream);
+
+/* The norm's backward pass, from dy = dL/dy and h, rstd of the forward pass:
+ *   dx = dh + rstd (w dy - h rstd^2 mean(w dy h)), dw = sum over rows of dy h rstd.
+ * DH (may be NULL): the gradient that reaches h from elsewhere.  dx is the
+ * gradient of x and of the residual alike; DX may be DY, DH or H (in place).  DW: D
+ * fp32 values, overwritten; rows are added in a fixed order.  workspace:
+ * gemm_rms_backward_workspace bytes of device memory, 16-byte aligned, any contents. */
+int gemm_rms_backward(gemm_handle_t h, int64_t M, int64_t D, int x_dtype, int w_dtype,
+                      const void *DY, int64_t lddy, const void *H, int64_t ldh, const void *W, const float *rstd,
+                      const void *DH, int64_t lddh, void *DX, int64_t lddx, float *DW,
+                      void *workspace, int64_t workspace_bytes, void *stream);
+int64_t gemm_rms_backward_workspace(int64_t M, int64_t D);
+
 /* Static text for a status code (never NULL). */
 const char *gemm_status_string(int status);
 

@@ -7,6 +7,7 @@ if the library is missing, loading raises.
 """
 import ctypes
 import os
+import threading
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libpipegemm.so")
@@ -17,6 +18,8 @@ GEMM_VARIANT_REG, GEMM_VARIANT_DIRECT = 0, 1
 GEMM_OK, GEMM_ERR_INVALID_ARG, GEMM_ERR_ALIGNMENT, GEMM_ERR_UNSUPPORTED, GEMM_ERR_HIP = 0, 1, 2, 3, 4
 GEMM_ERR_SCRATCH = 5
 GEMM_NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024
+GEMM_E4M3, GEMM_E5M2 = 16, 17
+GEMM_RMS_MAX_D, GEMM_RMS_MAX_ROWS = 32768, 1 << 22
 GEMM_TILE_AUTO, GEMM_TILE_256x256, GEMM_TILE_128x128, GEMM_TILE_32x64, GEMM_TILE_256x256_W8 = -1, 0, 1, 2, 3
 
 DTYPES = {"i8": GEMM_I8, "f16": GEMM_F16, "bf16": GEMM_BF16, "f32": GEMM_F32}
@@ -25,10 +28,17 @@ VARIANTS = {"reg": GEMM_VARIANT_REG, "direct": GEMM_VARIANT_DIRECT}
 TILES = {"auto": GEMM_TILE_AUTO, "256x256": GEMM_TILE_256x256, "128x128": GEMM_TILE_128x128,
          "32x64": GEMM_TILE_32x64, "256x256w8": GEMM_TILE_256x256_W8}
 
+FP8_TYPES = {"e4m3": GEMM_E4M3, "e5m2": GEMM_E5M2}
+FP8_TILES = {"auto": -1, "256x256": 0, "128x128": 1, "64x64": 2, "64x32": 3, "32x32": 4, "16x16": 5}
+FP8_BLOCK = 128   # values of a row that share a scale
+BLOCK_ROWS = {"row": 1, "tile": FP8_BLOCK}
+
 # C functions exported by the library (the names include/pipegemm.h declares)
 EXPORTS = ("gemm_create", "gemm_run", "gemm_destroy", "gemm_set_tile", "gemm_query",
            "gemm_run_splitk", "gemm_query_splitk", "gemm_status_string", "gemm_last_hip_error",
-           "gemm_run_splitk_noalloc", "gemm_occupancy", "gemm_run_streamk", "gemm_query_streamk")
+           "gemm_run_splitk_noalloc", "gemm_occupancy", "gemm_run_streamk", "gemm_query_streamk",
+           "gemm_run_fp8", "gemm_query_fp8", "gemm_quantize_fp8", "gemm_rms_fp8", "gemm_rms_backward",
+           "gemm_rms_backward_workspace")
 
 
 class GemmError(RuntimeError):
@@ -55,6 +65,15 @@ class ConfigInfo(ctypes.Structure):
 class Occupancy(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in (
         "blocks_per_cu", "waves_per_cu", "num_regs", "lds_bytes", "scratch_bytes", "threads")]
+
+    def as_dict(self):
+        return {n: getattr(self, n) for n, _ in self._fields_}
+
+
+class Fp8Info(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "tile", "block_m", "block_n", "waves_k", "threads", "staged", "widened", "reserved")] + [
+        ("grid", ctypes.c_int64), ("k_blocks", ctypes.c_int64)]
 
     def as_dict(self):
         return {n: getattr(self, n) for n, _ in self._fields_}
@@ -98,6 +117,21 @@ def _lib():
         lib.gemm_query_splitk.argtypes = [i64, i64, i64, ci, ci, ci, ci, ci, ci, vp, i64, vp, i64, vp, i64,
                                           ctypes.POINTER(ConfigInfo)]
         lib.gemm_query_splitk.restype = ci
+        operand = [vp, i64, vp, i64, i64]            # matrix, leading dimension, scales, their strides
+        lib.gemm_run_fp8.argtypes = [vp, i64, i64, i64] + [ci] * 6 + operand * 2 + [vp, i64, vp]
+        lib.gemm_run_fp8.restype = ci
+        lib.gemm_query_fp8.argtypes = [i64, i64, i64] + [ci] * 6 + operand * 2 + [vp, i64, ctypes.POINTER(Fp8Info)]
+        lib.gemm_query_fp8.restype = ci
+        lib.gemm_quantize_fp8.argtypes = [vp, i64, i64] + [ci] * 4 + [vp, i64] + operand * 2 + [vp]
+        lib.gemm_quantize_fp8.restype = ci
+        lib.gemm_rms_fp8.argtypes = ([vp, i64, i64] + [ci] * 4 + [ctypes.c_float] + [vp, i64] * 2 + [vp] +
+                                     [vp, i64] * 2 + operand + [vp, vp])
+        lib.gemm_rms_fp8.restype = ci
+        lib.gemm_rms_backward.argtypes = [vp, i64, i64, ci, ci, vp, i64, vp, i64, vp, vp, vp, i64, vp, i64, vp, vp,
+                                          i64, vp]
+        lib.gemm_rms_backward.restype = ci
+        lib.gemm_rms_backward_workspace.argtypes = [i64, i64]
+        lib.gemm_rms_backward_workspace.restype = i64
         lib.gemm_status_string.argtypes = [ci]
         lib.gemm_status_string.restype = ctypes.c_char_p
         lib.gemm_last_hip_error.argtypes = []
@@ -242,7 +276,7 @@ def gemm_query_streamk(M, N, K, dtype, layout, stages, variant, grid=0, tile="au
     return rc, info.as_dict()
 
 
-_HANDLES = {}   # device index -> Gemm, for run()
+_HANDLES = {}   # device index -> Gemm, for run() and the 8-bit functions
 
 
 def run(a, b, *, layout="RC", stages=2, variant="direct", out=None, stream=None):
@@ -285,6 +319,368 @@ def run(a, b, *, layout="RC", stages=2, variant="direct", out=None, stream=None)
     g.run(a, b, out, dtype, layout, stages, variant,
           stream if stream is not None else torch.cuda.current_stream(a.device))
     return out
+
+
+# ---- 8-bit floating point with a scale for each block of 128 -----------------
+
+def gemm_run_fp8(h, M, N, K, a_type, b_type, c_dtype, b_scale_rows, accumulate, tile, A, lda, SA, sa_row, sa_blk,
+                 B, ldb, SB, sb_row, sb_blk, C, ldc, stream=None, check=True):
+    """Enqueue C = A * B of 8-bit matrices with block scales; returns the
+    status (raises on error when check)."""
+    rc = _lib().gemm_run_fp8(h, M, N, K, _enum(a_type, FP8_TYPES), _enum(b_type, FP8_TYPES), _enum(c_dtype, DTYPES),
+                             int(b_scale_rows), int(accumulate), _enum(tile, FP8_TILES), _ptr(A), lda, _ptr(SA),
+                             sa_row, sa_blk, _ptr(B), ldb, _ptr(SB), sb_row, sb_blk, _ptr(C), ldc, _stream(stream))
+    if check and rc != GEMM_OK:
+        raise GemmError(rc, "gemm_run_fp8")
+    return rc
+
+
+def gemm_query_fp8(M, N, K, a_type="e4m3", b_type="e4m3", c_dtype="bf16", b_scale_rows=FP8_BLOCK, accumulate=0,
+                   tile="auto", A=0, lda=None, SA=0, sa_row=1, sa_blk=None, B=0, ldb=None, SB=0, sb_row=1, sb_blk=None,
+                   C=0, ldc=None, check=True):
+    """The kernel gemm_run_fp8 would use (no HIP call).  Returns (status, dict)."""
+    info = Fp8Info()
+    n_scales = N if b_scale_rows == 1 else -(-N // FP8_BLOCK)
+    rc = _lib().gemm_query_fp8(M, N, K, _enum(a_type, FP8_TYPES), _enum(b_type, FP8_TYPES), _enum(c_dtype, DTYPES),
+                               int(b_scale_rows), int(accumulate), _enum(tile, FP8_TILES), A,
+                               _rows16(K) if lda is None else lda, SA, sa_row, M if sa_blk is None else sa_blk, B,
+                               _rows16(K) if ldb is None else ldb, SB, sb_row, n_scales if sb_blk is None else sb_blk,
+                               C, N if ldc is None else ldc, ctypes.byref(info))
+    if check and rc != GEMM_OK:
+        raise GemmError(rc, "gemm_query_fp8")
+    return rc, info.as_dict()
+
+
+def gemm_quantize_fp8(h, M, K, x_dtype, fp8_type, block_rows, pow2, X, ldx, Q, ldq, S, s_row, s_blk, QT=None, ldqt=0,
+                      ST=None, st_row=0, st_blk=0, stream=None, check=True):
+    """Enqueue X (and its transpose) to 8 bits with block scales."""
+    rc = _lib().gemm_quantize_fp8(h, M, K, _enum(x_dtype, DTYPES), _enum(fp8_type, FP8_TYPES), int(block_rows),
+                                  int(pow2), _ptr(X), ldx, _ptr(Q), ldq, _ptr(S), s_row, s_blk, _ptr(QT), ldqt,
+                                  _ptr(ST), st_row, st_blk, _stream(stream))
+    if check and rc != GEMM_OK:
+        raise GemmError(rc, "gemm_quantize_fp8")
+    return rc
+
+
+def gemm_rms_fp8(h, M, D, x_dtype, w_dtype, fp8_type, pow2, eps, X, ldx, R, ldr, W, H, ldh, Y, ldy, Q, ldq, S, s_row,
+                 s_blk, rstd, stream=None, check=True):
+    """Enqueue the norm of X + R, to 8 bits with block scales."""
+    rc = _lib().gemm_rms_fp8(h, M, D, _enum(x_dtype, DTYPES), _enum(w_dtype, DTYPES), _enum(fp8_type, FP8_TYPES),
+                             int(pow2), eps, _ptr(X), ldx, _ptr(R), ldr, _ptr(W), _ptr(H), ldh, _ptr(Y), ldy, _ptr(Q),
+                             ldq, _ptr(S), s_row, s_blk, _ptr(rstd), _stream(stream))
+    if check and rc != GEMM_OK:
+        raise GemmError(rc, "gemm_rms_fp8")
+    return rc
+
+
+def gemm_rms_backward_workspace(M, D):
+    """Bytes of workspace gemm_rms_backward needs."""
+    return _lib().gemm_rms_backward_workspace(M, D)
+
+
+def gemm_rms_backward(h, M, D, x_dtype, w_dtype, DY, lddy, H, ldh, W, rstd, DH, lddh, DX, lddx, DW, workspace,
+                      workspace_bytes, stream=None, check=True):
+    """Enqueue the norm's backward pass."""
+    rc = _lib().gemm_rms_backward(h, M, D, _enum(x_dtype, DTYPES), _enum(w_dtype, DTYPES), _ptr(DY), lddy, _ptr(H),
+                                  ldh, _ptr(W), _ptr(rstd), _ptr(DH), lddh, _ptr(DX), lddx, _ptr(DW),
+                                  _ptr(workspace), int(workspace_bytes), _stream(stream))
+    if check and rc != GEMM_OK:
+        raise GemmError(rc, "gemm_rms_backward")
+    return rc
+
+
+_HANDLES_LOCK = threading.Lock()
+
+
+def _handle(index):
+    """The handle of a device, made on first use (which waits for the device,
+    so it cannot be part of a graph capture)."""
+    g = _HANDLES.get(index)
+    if g is None:
+        import torch
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("the first call on a device sets it up: make one before the graph capture")
+        with _HANDLES_LOCK:
+            g = _HANDLES.get(index)
+            if g is None:
+                g = _HANDLES[index] = Gemm(index)
+    return g.h
+
+
+def _rows16(n):
+    return (n + 15) // 16 * 16
+
+
+def _ld(t):
+    """Elements from one row to the next; a single row's is free, and taken
+    as the next multiple of 16."""
+    return t.stride(0) if t.shape[0] > 1 else _rows16(t.shape[1])
+
+
+def _matrix(t, what, dtypes, device=None, shape=None):
+    """Argument check: t is a 2-D CUDA tensor of one of dtypes with unit
+    stride along its last axis and rows that do not overlap."""
+    if not isinstance(t, _types()["tensor"]) or t.dim() != 2:
+        raise ValueError("%s must be a 2-D torch tensor" % what)
+    if t.dtype not in dtypes:
+        raise ValueError("%s must be %s (got %s)" % (what, " or ".join(str(d) for d in dtypes), t.dtype))
+    if not t.is_cuda or (device is not None and t.device != device):
+        raise ValueError("all tensors must be CUDA tensors on one device (%s is on %s)" % (what, t.device))
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError("%s must be %s (got %s)" % (what, " x ".join(map(str, shape)), tuple(t.shape)))
+    if (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+        raise ValueError("%s must have unit stride along its last axis, and rows that do not overlap" % what)
+
+
+_T = {}   # torch's types by role, filled on first use (torch is not imported with this module)
+
+
+def _types():
+    if not _T:
+        import torch
+        _T["fp8"] = {torch.float8_e4m3fn: GEMM_E4M3, torch.float8_e5m2: GEMM_E5M2}
+        _T["float"] = {torch.bfloat16: GEMM_BF16, torch.float16: GEMM_F16, torch.float32: GEMM_F32}
+        _T["tensor"], _T["f32"] = torch.Tensor, (torch.float32,)
+        _T["named"] = {"e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2,
+                       torch.float8_e4m3fn: torch.float8_e4m3fn, torch.float8_e5m2: torch.float8_e5m2}
+    return _T
+
+
+def _fp8_dtype(fp8):
+    named = _types()["named"]
+    if fp8 not in named:
+        raise ValueError("fp8 must be e4m3 or e5m2 (got %r)" % (fp8,))
+    return named[fp8]
+
+
+class _Target:
+    """Where a call is enqueued: the raw stream, and the stream that what the
+    call allocates belongs to."""
+
+    def __init__(self, stream, device):
+        import torch
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=device)
+        if stream.device != device:
+            raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, device))
+        self.raw, self.context = stream.cuda_stream, torch.cuda.stream(stream)
+
+
+def _call(stream, device, fn):
+    """fn(raw stream), with what it allocates belonging to that stream."""
+    import torch
+    if stream is None:
+        return fn(torch.cuda.current_stream(device).cuda_stream)
+    target = _Target(stream, device)
+    with target.context:
+        return fn(target.raw)
+
+
+def _check(rc, where):
+    if rc != GEMM_OK:
+        raise GemmError(rc, where)
+
+
+def _empty_rows16(rows, cols, dtype, device):
+    """rows x cols whose rows start on 16 bytes (8-bit types)."""
+    import torch
+    t = torch.empty((rows, _rows16(cols)), dtype=dtype, device=device)
+    return t if t.shape[1] == cols else t[:, :cols]
+
+
+def _empty_scales(rows, blocks, device):
+    """rows x blocks scales, one block's after another (the order the
+    product reads them in)."""
+    import torch
+    return torch.empty((blocks, rows), dtype=torch.float32, device=device).t()
+
+
+def run_fp8(a, sa, b, sb, *, out=None, out_dtype=None, accumulate=False, tile="auto", stream=None):
+    """C = A * B of 8-bit matrices with block scales, through gemm_run_fp8.
+
+    a: M x K, float8_e4m3fn or float8_e5m2; sa: its scales, M x ceil(K / 128)
+    float32.  b: B's N x K transpose; sb: ceil(N / 128) x ceil(K / 128)
+    ("tile" scales) or N x ceil(K / 128) ("row" scales).  Scales may have any
+    strides (expanded ones too).  C is M x N of out_dtype: bfloat16 (the
+    default), float16 or float32; `out` is written in place, else a new tensor
+    is allocated; accumulate=True adds to a float32 `out`.  The call is
+    enqueued on `stream` (a torch stream or its raw handle; the current stream
+    of A's device by default).  Argument errors raise ValueError, or GemmError
+    with the C status, before anything is enqueued.
+
+    Rows that start on 16 bytes (as quantize_fp8 and rms_fp8 lay them out) are
+    the fast case."""
+    import torch
+    types = _types()
+    _matrix(a, "a", types["fp8"])
+    device = a.device
+    M, K = a.shape
+    _matrix(b, "b", types["fp8"], device)
+    N = b.shape[0]
+    if b.shape[1] != K:
+        raise ValueError("inner dimensions differ: a has K = %d, b has %d" % (K, b.shape[1]))
+    blocks = (K + 127) // 128
+    for t, what in ((sa, "sa"), (sb, "sb")):
+        if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32 or t.dim() != 2 or t.device != device:
+            raise ValueError("%s must be a 2-D float32 tensor on a's device" % what)
+    if sa.shape[0] != M or sa.shape[1] != blocks:
+        raise ValueError("sa must be M x ceil(K / 128) = %d x %d (got %s)" % (M, blocks, tuple(sa.shape)))
+    b_scale_rows = 128 if sb.shape[0] == (N + 127) // 128 else 1
+    if (b_scale_rows == 1 and sb.shape[0] != N) or sb.shape[1] != blocks:
+        raise ValueError("sb must be ceil(N / 128) or N rows of ceil(K / 128) = %d scales (got %s)"
+                         % (blocks, tuple(sb.shape)))
+    if out is not None:
+        _matrix(out, "out", types["float"], device, (M, N))
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise ValueError("out is %s, out_dtype %s" % (out.dtype, out_dtype))
+        out_dtype = out.dtype
+    else:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
+        if out_dtype not in types["float"]:
+            raise ValueError("out_dtype must be bfloat16, float16 or float32 (got %s)" % out_dtype)
+    if accumulate and out_dtype is not torch.float32:
+        raise ValueError("accumulate needs a float32 out")
+    h = _handle(device.index)
+
+    def enqueue(raw):
+        c = torch.empty((M, N), dtype=out_dtype, device=device) if out is None else out
+        rc = _L.gemm_run_fp8(h, M, N, K, types["fp8"][a.dtype], types["fp8"][b.dtype], types["float"][out_dtype],
+                             b_scale_rows, 1 if accumulate else 0, _enum(tile, FP8_TILES),
+                             a.data_ptr(), _ld(a), sa.data_ptr(), *sa.stride(),
+                             b.data_ptr(), _ld(b), sb.data_ptr(), *sb.stride(),
+                             c.data_ptr(), _ld(c), raw)
+        if rc != GEMM_OK:
+            raise GemmError(rc, "gemm_run_fp8")
+        return c
+
+    return _call(stream, device, enqueue)
+
+
+def quantize_fp8(x, *, block="row", fp8="e4m3", pow2=False, rows=True, transpose=False, stream=None):
+    """x (M x K; bfloat16, float16 or float32) to 8 bits with a scale for each
+    block, through gemm_quantize_fp8: (q, s), or (q, s, qt, st) with
+    transpose=True, or (qt, st) with rows=False as well.
+
+    block "row": a scale for each 128 values of a row; s is M x ceil(K / 128).
+    "tile": one for each 128 x 128; s is ceil(M / 128) x ceil(K / 128).
+    qt (K x M) is x transposed, quantised along its own rows (by tiles: the
+    same values and scales as q, transposed); st are its scales.  fp8: "e4m3"
+    or "e5m2".  pow2: scales are powers of two.  Rows of q and qt start on 16
+    bytes.  Streams and errors as run_fp8."""
+    types = _types()
+    _matrix(x, "x", types["float"])
+    f8 = _fp8_dtype(fp8)
+    if block not in BLOCK_ROWS:
+        raise ValueError("block must be 'row' or 'tile' (got %r)" % (block,))
+    if not rows and not transpose:
+        raise ValueError("rows or transpose must be asked for")
+    device, (M, K) = x.device, x.shape
+    block_rows = BLOCK_ROWS[block]
+    h = _handle(device.index)
+
+    def enqueue(raw):
+        q = s = qt = st = None
+        if rows:
+            q = _empty_rows16(M, K, f8, device)
+            s = _empty_scales(-(-M // block_rows), -(-K // FP8_BLOCK), device)
+        if transpose:
+            qt = _empty_rows16(K, M, f8, device)
+            st = _empty_scales(-(-K // block_rows), -(-M // FP8_BLOCK), device)
+        _check(_L.gemm_quantize_fp8(h, M, K, types["float"][x.dtype], types["fp8"][f8], block_rows, 1 if pow2 else 0,
+                                    x.data_ptr(), _ld(x),
+                                    *((q.data_ptr(), _ld(q), s.data_ptr(), *s.stride()) if rows else (None, 0, None, 0, 0)),
+                                    *((qt.data_ptr(), _ld(qt), st.data_ptr(), *st.stride()) if transpose
+                                      else (None, 0, None, 0, 0)), raw), "gemm_quantize_fp8")
+        return ((q, s) if rows else ()) + ((qt, st) if transpose else ())
+
+    return _call(stream, device, enqueue)
+
+
+def _vector(t, what, dtypes, n, device):
+    if not isinstance(t, _types()["tensor"]):
+        raise ValueError("%s must be a torch tensor" % what)
+    if t.dtype not in dtypes or t.dim() != 1 or t.shape[0] != n or t.device != device or (n > 1 and t.stride(0) != 1):
+        raise ValueError("%s must be %d contiguous values of %s on %s (got %s %s)"
+                         % (what, n, " or ".join(str(d) for d in dtypes), device, t.dtype, tuple(t.shape)))
+
+
+def rms_fp8(x, weight, *, residual=None, eps=1e-6, fp8="e4m3", pow2=False, norm=False, h_out=None, stream=None):
+    """Root-mean-square norm of x + residual, to 8 bits, through gemm_rms_fp8:
+    (q, s, h, rstd), or (q, s, h, rstd, y) with norm=True.
+
+    x, residual: M x D of bfloat16, float16 or float32; weight: D values of
+    x's type or float32.  h = x + residual in x's type (x itself without a
+    residual), written into h_out where it is given, which may be x or
+    residual; rstd: M float32, what rms_backward takes; q, s: the normalised
+    rows in 8 bits, a scale for each 128 values; y: the same in x's type.
+    D up to 32768.  Streams and errors as run_fp8."""
+    import torch
+    types = _types()
+    _matrix(x, "x", types["float"])
+    device, (M, D) = x.device, x.shape
+    f8 = _fp8_dtype(fp8)
+    _vector(weight, "weight", (x.dtype, torch.float32), D, device)
+    if residual is not None:
+        _matrix(residual, "residual", (x.dtype,), device, (M, D))
+    if h_out is not None:
+        _matrix(h_out, "h_out", (x.dtype,), device, (M, D))
+    handle = _handle(device.index)
+
+    def enqueue(raw):
+        q = _empty_rows16(M, D, f8, device)
+        s = _empty_scales(M, -(-D // FP8_BLOCK), device)
+        rstd = torch.empty((M,), dtype=torch.float32, device=device)
+        write = h_out if h_out is not None else torch.empty((M, D), dtype=x.dtype, device=device) \
+            if residual is not None else None
+        y = torch.empty((M, D), dtype=x.dtype, device=device) if norm else None
+        ptr_ld = lambda t: (None, 0) if t is None else (t.data_ptr(), _ld(t))  # noqa: E731
+        _check(_L.gemm_rms_fp8(handle, M, D, types["float"][x.dtype], types["float"][weight.dtype], types["fp8"][f8],
+                               1 if pow2 else 0, eps, *ptr_ld(x), *ptr_ld(residual), weight.data_ptr(),
+                               *ptr_ld(write), *ptr_ld(y), *ptr_ld(q), s.data_ptr(), *s.stride(), rstd.data_ptr(),
+                               raw), "gemm_rms_fp8")
+        out = (q, s, x if write is None else write, rstd)
+        return out + (y,) if norm else out
+
+    return _call(stream, device, enqueue)
+
+
+def rms_backward(dy, h, weight, rstd, *, dh=None, dx_out=None, stream=None):
+    """The backward pass of rms_fp8's norm, through gemm_rms_backward: (dx, dw).
+
+    dy: the gradient of the normalised rows; h and rstd: what the forward pass
+    returned; dh: the gradient that reaches h from elsewhere (the residual
+    stream); all M x D of h's type.  dx, in that type, is the gradient of x and of
+    the residual; it is written into dx_out where given, which may be dy, h
+    or dh.  dw is float32, its rows added in a fixed order.  Streams and errors
+    as run_fp8."""
+    import torch
+    types = _types()
+    _matrix(h, "h", types["float"])
+    device, (M, D) = h.device, h.shape
+    _matrix(dy, "dy", (h.dtype,), device, (M, D))
+    for t, what in ((dh, "dh"), (dx_out, "dx_out")):
+        if t is not None:
+            _matrix(t, what, (h.dtype,), device, (M, D))
+    _vector(weight, "weight", (h.dtype, torch.float32), D, device)
+    _vector(rstd, "rstd", types["f32"], M, device)
+    handle = _handle(device.index)
+    nbytes = _L.gemm_rms_backward_workspace(M, D)
+
+    def enqueue(raw):
+        dx = torch.empty((M, D), dtype=h.dtype, device=device) if dx_out is None else dx_out
+        dw = torch.empty((D,), dtype=torch.float32, device=device)
+        # a workspace of this call's own: it belongs to the stream (and to the graph, under capture)
+        ws = torch.empty((nbytes,), dtype=torch.uint8, device=device)
+        _check(_L.gemm_rms_backward(handle, M, D, types["float"][h.dtype], types["float"][weight.dtype], dy.data_ptr(),
+                                    _ld(dy), h.data_ptr(), _ld(h), weight.data_ptr(), rstd.data_ptr(),
+                                    None if dh is None else dh.data_ptr(), 0 if dh is None else _ld(dh),
+                                    dx.data_ptr(), _ld(dx), dw.data_ptr(), ws.data_ptr(), nbytes, raw),
+               "gemm_rms_backward")
+        return dx, dw
+
+    return _call(stream, device, enqueue)
 
 
 class Gemm:

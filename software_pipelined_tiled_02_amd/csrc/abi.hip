@@ -9,15 +9,9 @@
 #include <mutex>
 
 #include "pipegemm.h"
+#include "handle.h"
 #include "kernel_args.h"
 #include "tile_layout.h"
-
-struct gemm_handle_s {
-    int device;
-    int num_cus;
-    int tile_override;  // GEMM_TILE_AUTO or a class
-    void* scratch;      // this device's address of `scratch` (below)
-};
 
 // The split-K workspace of gemm_run_splitk_noalloc: one static array per
 // device, for callers that cannot allocate device memory.  In host code its
@@ -28,9 +22,16 @@ struct gemm_handle_s {
 static __device__ __align__(256) uint8_t scratch[GEMM_NOALLOC_SCRATCH_BYTES];
 static_assert(GEMM_NOALLOC_SCRATCH_BYTES > pg::kSplitkCounterBytes, "scratch holds the counters");
 
+static thread_local int g_last_hip_error = 0;
+
+int pg::hip_fail(hipError_t e) {
+    g_last_hip_error = (int)e;
+    return GEMM_ERR_HIP;
+}
+
 namespace {
 
-thread_local int g_last_hip_error = 0;
+using pg::hip_fail;
 
 constexpr int kDefaultCus = 256;  // MI355X; used when no device is at hand
 
@@ -218,11 +219,6 @@ const Registry& registry() {
     return r;
 }
 
-int hip_fail(hipError_t e) {
-    g_last_hip_error = (int)e;
-    return GEMM_ERR_HIP;
-}
-
 // Writes zeros over n 32-bit words (clears the scratch counters with a
 // kernel rather than a memset).
 __global__ void zero_words(uint32_t* p, int n) {
@@ -291,22 +287,12 @@ int launch(gemm_handle_t h, const Plan& plan, int64_t M, int64_t N, int64_t K, i
     args.sk_tiles = plan.info.sk_tiles;
     args.ws = (plan.info.splits > 1 || plan.info.sk_tiles > 0) ? ws : nullptr;
 
-    int cur = -1;
-    hipError_t e = hipGetDevice(&cur);
-    if (e != hipSuccess) return hip_fail(e);
-    if (cur != h->device && (e = hipSetDevice(h->device)) != hipSuccess) return hip_fail(e);
     void* kargs[] = {&args};
-    e = hipLaunchKernel(fn, dim3((unsigned)plan.info.grid), dim3((unsigned)plan.info.threads), kargs, 0,
-                        (hipStream_t)stream);
-    if (e == hipSuccess) e = hipGetLastError();
-    if (cur != h->device) {
-        // put the caller's device back; a failure here is reported unless
-        // the launch itself already failed
-        const hipError_t r = hipSetDevice(cur);
-        if (e == hipSuccess) e = r;
-    }
-    if (e != hipSuccess) return hip_fail(e);
-    return GEMM_OK;
+    return pg::on_device(h, [&] {
+        const hipError_t e = hipLaunchKernel(fn, dim3((unsigned)plan.info.grid), dim3((unsigned)plan.info.threads),
+                                             kargs, 0, (hipStream_t)stream);
+        return e == hipSuccess ? hipGetLastError() : e;
+    });
 }
 
 }  // namespace

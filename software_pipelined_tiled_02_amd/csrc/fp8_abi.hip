@@ -1,0 +1,294 @@
+// fp8_abi.hip -- the C ABI of the 8-bit operators (include/pipegemm.h):
+// argument checks, choice of kernel, launch.  Host code only.
+#include <hip/hip_runtime.h>
+#include <limits.h>
+#include <stdint.h>
+#include <string.h>
+
+#include "pipegemm.h"
+#include "handle.h"
+#include "fp8_common.h"
+#include "fp8_gemm.h"
+
+namespace {
+
+constexpr int kDefaultCus = 256;  // MI355X; used when no device is at hand
+constexpr int64_t kBlock = pg::kBlock;
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+bool aligned(const void* p, int64_t n) { return (uintptr_t)p % (uintptr_t)n == 0; }
+bool is_fp8(int t) { return t == GEMM_E4M3 || t == GEMM_E5M2; }
+bool is_float(int t) { return t == GEMM_F16 || t == GEMM_BF16 || t == GEMM_F32; }
+int size_of(int t) { return t == GEMM_F32 ? 4 : 2; }
+int fp8_of(int t) { return t == GEMM_E5M2 ? pg::FP8_E5M2 : pg::FP8_E4M3; }
+
+struct Plan {
+    gemm_fp8_info_t info;
+    const void* fn;
+    int64_t tiles_m, tiles_n;
+    bool vec_c;
+};
+
+// Every check of the product, then its kernel.  No HIP call.
+int plan_product(int64_t M, int64_t N, int64_t K, int a_type, int b_type, int c_dtype, int b_scale_rows, int accumulate,
+                 int tile, const void* A, int64_t lda, const void* SA, int64_t sa_row, int64_t sa_blk, const void* B,
+                 int64_t ldb, const void* SB, int64_t sb_row, int64_t sb_blk, const void* C, int64_t ldc, int num_cus,
+                 bool query, Plan* plan) {
+    if (!is_fp8(a_type) || !is_fp8(b_type) || !is_float(c_dtype)) return GEMM_ERR_INVALID_ARG;
+    if (b_scale_rows != 1 && b_scale_rows != kBlock) return GEMM_ERR_INVALID_ARG;
+    if (tile < GEMM_FP8_TILE_AUTO || tile >= pg::FP8_TILE_COUNT) return GEMM_ERR_INVALID_ARG;
+    if (accumulate != 0 && accumulate != 1) return GEMM_ERR_INVALID_ARG;
+    if (M < 0 || N < 0 || K < 0 || lda < 0 || ldb < 0 || ldc < 0) return GEMM_ERR_INVALID_ARG;
+    if (sa_row < 0 || sa_blk < 0 || sb_row < 0 || sb_blk < 0) return GEMM_ERR_INVALID_ARG;
+    const bool has_c = M > 0 && N > 0, reads = has_c && K > 0;
+    if (reads && !query && (A == nullptr || B == nullptr || SA == nullptr || SB == nullptr)) return GEMM_ERR_INVALID_ARG;
+    if (reads && (lda < K || ldb < K)) return GEMM_ERR_INVALID_ARG;
+    if (has_c && ((C == nullptr && !query) || ldc < N)) return GEMM_ERR_INVALID_ARG;
+    if (accumulate && c_dtype != GEMM_F32) return GEMM_ERR_UNSUPPORTED;
+    if (!aligned(C, size_of(c_dtype)) || !aligned(SA, 4) || !aligned(SB, 4)) return GEMM_ERR_ALIGNMENT;
+    if (M > INT_MAX || N > INT_MAX || K > INT_MAX - kBlock) return GEMM_ERR_UNSUPPORTED;
+
+    // Rows that start on 16 bytes can be staged through LDS whatever K is (a
+    // chunk that holds one byte of a row lies in one page with it); rows at
+    // any address, and pieces of chunks, are read into registers.
+    const bool rows16 = !reads || (aligned(A, 16) && aligned(B, 16) && lda % 16 == 0 && ldb % 16 == 0);
+    const bool exact = c_dtype == GEMM_F32;
+    const bool bytes = reads && (!rows16 || K % 16 != 0);
+    const int at = fp8_of(a_type), bt = fp8_of(b_type);
+    auto kernel = [&](int t) -> const void* {
+        if (!pg::fp8_staged(t)) return pg::fp8_stream_kernel(t, at, bt, b_scale_rows == 1, exact, bytes);
+        return rows16 ? pg::fp8_staged_kernel(t, at, bt, b_scale_rows == 1, exact) : nullptr;
+    };
+    // The largest tile that is at least half full of rows and still gives
+    // every CU a workgroup.
+    int tc = tile;
+    if (tc == GEMM_FP8_TILE_AUTO) {
+        tc = pg::FP8_TILE_16;
+        for (int t = 0; t < pg::FP8_TILE_COUNT; ++t) {
+            const pg::Fp8Shape sh = pg::fp8_shape(t);
+            if (kernel(t) == nullptr || sh.bm >= 2 * M) continue;
+            if (ceil_div(M, sh.bm) * ceil_div(N, sh.bn) >= num_cus) { tc = t; break; }
+        }
+    }
+    plan->fn = kernel(tc);
+    if (plan->fn == nullptr) return tile == GEMM_FP8_TILE_AUTO || rows16 ? GEMM_ERR_UNSUPPORTED : GEMM_ERR_ALIGNMENT;
+    const pg::Fp8Shape sh = pg::fp8_shape(tc);
+
+    // 32-bit offsets inside a tile, and of a block's scales
+    const int64_t lim = (int64_t)1 << 31, kb = ceil_div(K, kBlock);
+    const int64_t sb_rows_of_tile = b_scale_rows == 1 ? sh.bn : ceil_div(sh.bn, kBlock);
+    if (reads && (lda >= lim / sh.bm || ldb >= lim / sh.bn || sa_row >= lim / (4 * sh.bm) ||
+                  sb_row >= lim / (4 * sb_rows_of_tile) || sa_blk >= lim / (4 * kb) || sb_blk >= lim / (4 * kb)))
+        return GEMM_ERR_UNSUPPORTED;
+    plan->tiles_m = has_c ? ceil_div(M, sh.bm) : 0;
+    plan->tiles_n = has_c ? ceil_div(N, sh.bn) : 0;
+    const int64_t grid = plan->tiles_m * plan->tiles_n;
+    if (grid >= ((int64_t)1 << 32) / (64 * sh.waves)) return GEMM_ERR_UNSUPPORTED;
+    plan->vec_c = aligned(C, 4 * size_of(c_dtype)) && ldc % 4 == 0;
+    gemm_fp8_info_t& in = plan->info;
+    memset(&in, 0, sizeof in);
+    in.tile = tc;
+    in.block_m = sh.bm;
+    in.block_n = sh.bn;
+    in.waves_k = sh.wk;
+    in.threads = 64 * sh.waves;
+    in.staged = pg::fp8_staged(tc) ? 1 : 0;
+    in.widened = exact ? 1 : 0;
+    in.grid = grid;
+    in.k_blocks = kb;
+    return GEMM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int gemm_query_fp8(int64_t M, int64_t N, int64_t K, int a_type, int b_type, int c_dtype, int b_scale_rows,
+                   int accumulate, int tile, const void* A, int64_t lda, const float* SA, int64_t sa_row,
+                   int64_t sa_blk, const void* B, int64_t ldb, const float* SB, int64_t sb_row, int64_t sb_blk,
+                   const void* C, int64_t ldc, gemm_fp8_info_t* info) {
+    if (info == nullptr) return GEMM_ERR_INVALID_ARG;
+    Plan plan;
+    const int rc = plan_product(M, N, K, a_type, b_type, c_dtype, b_scale_rows, accumulate, tile, A, lda, SA, sa_row,
+                                sa_blk, B, ldb, SB, sb_row, sb_blk, C, ldc, kDefaultCus, true, &plan);
+    if (rc == GEMM_OK) *info = plan.info;
+    return rc;
+}
+
+int gemm_run_fp8(gemm_handle_t h, int64_t M, int64_t N, int64_t K, int a_type, int b_type, int c_dtype,
+                 int b_scale_rows, int accumulate, int tile, const void* A, int64_t lda, const float* SA,
+                 int64_t sa_row, int64_t sa_blk, const void* B, int64_t ldb, const float* SB, int64_t sb_row,
+                 int64_t sb_blk, void* C, int64_t ldc, void* stream) {
+    if (h == nullptr) return GEMM_ERR_INVALID_ARG;
+    Plan plan;
+    const int rc = plan_product(M, N, K, a_type, b_type, c_dtype, b_scale_rows, accumulate, tile, A, lda, SA, sa_row,
+                                sa_blk, B, ldb, SB, sb_row, sb_blk, C, ldc, h->num_cus, false, &plan);
+    if (rc != GEMM_OK) return rc;
+    if (plan.info.grid == 0) return GEMM_OK;
+    pg::Fp8Args a;
+    a.A = (const uint8_t*)A;
+    a.B = (const uint8_t*)B;
+    a.SA = SA;
+    a.SB = SB;
+    a.C = C;
+    a.lda = lda;
+    a.ldb = ldb;
+    a.ldc = ldc;
+    a.sa_row = sa_row;
+    a.sa_blk = sa_blk;
+    a.sb_row = sb_row;
+    a.sb_blk = sb_blk;
+    a.M = (int32_t)M;
+    a.N = (int32_t)N;
+    a.K = (int32_t)K;
+    a.tiles_m = (int32_t)plan.tiles_m;
+    a.tiles_n = (int32_t)plan.tiles_n;
+    a.c_type = c_dtype;
+    a.accumulate = accumulate;
+    a.vec_c = plan.vec_c;
+    void* kargs[] = {&a};
+    return pg::on_device(h, [&] {
+        const hipError_t e = hipLaunchKernel(plan.fn, dim3((unsigned)plan.info.grid), dim3((unsigned)plan.info.threads),
+                                             kargs, 0, (hipStream_t)stream);
+        return e == hipSuccess ? hipGetLastError() : e;
+    });
+}
+
+int gemm_quantize_fp8(gemm_handle_t h, int64_t M, int64_t K, int x_dtype, int fp8_type, int block_rows, int pow2,
+                      const void* X, int64_t ldx, void* Q, int64_t ldq, float* S, int64_t s_row, int64_t s_blk,
+                      void* QT, int64_t ldqt, float* ST, int64_t st_row, int64_t st_blk, void* stream) {
+    if (h == nullptr || !is_float(x_dtype) || !is_fp8(fp8_type)) return GEMM_ERR_INVALID_ARG;
+    if (block_rows != 1 && block_rows != kBlock) return GEMM_ERR_INVALID_ARG;
+    if (pow2 != 0 && pow2 != 1) return GEMM_ERR_INVALID_ARG;
+    if (M < 0 || K < 0 || ldx < 0 || ldq < 0 || ldqt < 0) return GEMM_ERR_INVALID_ARG;
+    if (s_row < 0 || s_blk < 0 || st_row < 0 || st_blk < 0) return GEMM_ERR_INVALID_ARG;
+    const bool any = M > 0 && K > 0;
+    if (any && Q == nullptr && QT == nullptr) return GEMM_ERR_INVALID_ARG;
+    if (any && (X == nullptr || ldx < K)) return GEMM_ERR_INVALID_ARG;
+    if (any && Q != nullptr && (S == nullptr || ldq < K)) return GEMM_ERR_INVALID_ARG;
+    if (any && QT != nullptr && (ST == nullptr || ldqt < M)) return GEMM_ERR_INVALID_ARG;
+    const int sz = size_of(x_dtype);
+    if (!aligned(X, sz) || !aligned(S, 4) || !aligned(ST, 4)) return GEMM_ERR_ALIGNMENT;
+    if (M > INT_MAX || K > INT_MAX) return GEMM_ERR_UNSUPPORTED;
+    const bool tile = block_rows == kBlock;
+    const int64_t rows = pg::quantize_rows_per_group(M, K, tile || QT != nullptr);
+    if (ceil_div(M, rows) * ceil_div(K, kBlock) >= ((int64_t)1 << 24)) return GEMM_ERR_UNSUPPORTED;
+    if (!any) return GEMM_OK;
+    pg::QuantizeArgs a;
+    a.X = X;
+    a.Q = (uint8_t*)Q;
+    a.S = S;
+    a.QT = (uint8_t*)QT;
+    a.ST = ST;
+    a.ldx = ldx;
+    a.ldq = ldq;
+    a.ldqt = ldqt;
+    a.s_row = s_row;
+    a.s_blk = s_blk;
+    a.st_row = st_row;
+    a.st_blk = st_blk;
+    a.M = (int32_t)M;
+    a.K = (int32_t)K;
+    a.e5m2 = fp8_type == GEMM_E5M2;
+    a.pow2 = pow2;
+    a.vec = aligned(X, 16) && ldx * sz % 16 == 0;
+    a.vecq = aligned(Q, 8) && ldq % 8 == 0;
+    a.vecqt = aligned(QT, 16) && ldqt % 16 == 0;
+    return pg::on_device(h, [&] { return pg::launch_quantize(a, x_dtype, tile, (hipStream_t)stream); });
+}
+
+int gemm_rms_fp8(gemm_handle_t h, int64_t M, int64_t D, int x_dtype, int w_dtype, int fp8_type, int pow2, float eps,
+                 const void* X, int64_t ldx, const void* R, int64_t ldr, const void* W, void* H, int64_t ldh, void* Y,
+                 int64_t ldy, void* Q, int64_t ldq, float* S, int64_t s_row, int64_t s_blk, float* rstd, void* stream) {
+    if (h == nullptr || !is_float(x_dtype) || !is_fp8(fp8_type)) return GEMM_ERR_INVALID_ARG;
+    if (w_dtype != x_dtype && w_dtype != GEMM_F32) return GEMM_ERR_INVALID_ARG;
+    if (pow2 != 0 && pow2 != 1) return GEMM_ERR_INVALID_ARG;
+    if (!(eps >= 0.0f)) return GEMM_ERR_INVALID_ARG;
+    if (M < 0 || D < 0 || ldx < 0 || ldr < 0 || ldh < 0 || ldy < 0 || ldq < 0 || s_row < 0 || s_blk < 0)
+        return GEMM_ERR_INVALID_ARG;
+    const bool any = M > 0 && D > 0;
+    if (any && Q == nullptr && Y == nullptr) return GEMM_ERR_INVALID_ARG;
+    if (any && (X == nullptr || ldx < D || W == nullptr)) return GEMM_ERR_INVALID_ARG;
+    if (any && ((R != nullptr && ldr < D) || (H != nullptr && ldh < D) || (Y != nullptr && ldy < D)))
+        return GEMM_ERR_INVALID_ARG;
+    if (any && Q != nullptr && (S == nullptr || ldq < D)) return GEMM_ERR_INVALID_ARG;
+    const int sz = size_of(x_dtype);
+    if (!aligned(X, sz) || !aligned(R, sz) || !aligned(H, sz) || !aligned(Y, sz) || !aligned(W, size_of(w_dtype)) ||
+        !aligned(S, 4) || !aligned(rstd, 4))
+        return GEMM_ERR_ALIGNMENT;
+    if (M > GEMM_RMS_MAX_ROWS || D > GEMM_RMS_MAX_D) return GEMM_ERR_UNSUPPORTED;
+    if (!any) return GEMM_OK;
+    pg::RmsArgs a;
+    a.X = X;
+    a.R = R;
+    a.W = W;
+    a.H = H;
+    a.Y = Y;
+    a.Q = (uint8_t*)Q;
+    a.S = S;
+    a.rstd = rstd;
+    a.ldx = ldx;
+    a.ldr = ldr;
+    a.ldh = ldh;
+    a.ldy = ldy;
+    a.ldq = ldq;
+    a.s_row = s_row;
+    a.s_blk = s_blk;
+    a.M = (int32_t)M;
+    a.D = (int32_t)D;
+    a.eps = eps;
+    a.e5m2 = fp8_type == GEMM_E5M2;
+    a.pow2 = pow2;
+    a.w_f32 = w_dtype == GEMM_F32;
+    auto rows16 = [&](const void* p, int64_t ld) { return p == nullptr || (aligned(p, 16) && ld * sz % 16 == 0); };
+    a.vec = rows16(X, ldx) && rows16(R, ldr) && rows16(H, ldh) && rows16(Y, ldy) && aligned(W, 16) &&
+            (Q == nullptr || (aligned(Q, 8) && ldq % 8 == 0));
+    return pg::on_device(h, [&] { return pg::launch_rms(a, x_dtype, (hipStream_t)stream); });
+}
+
+int64_t gemm_rms_backward_workspace(int64_t M, int64_t D) {
+    if (M < 0 || D < 0 || M > GEMM_RMS_MAX_ROWS || D > GEMM_RMS_MAX_D) return 0;
+    return (int64_t)pg::rms_backward_groups(M, D, kDefaultCus) * D * 4;
+}
+
+int gemm_rms_backward(gemm_handle_t h, int64_t M, int64_t D, int x_dtype, int w_dtype, const void* DY, int64_t lddy,
+                      const void* H, int64_t ldh, const void* W, const float* rstd, const void* DH, int64_t lddh,
+                      void* DX, int64_t lddx, float* DW, void* workspace, int64_t workspace_bytes, void* stream) {
+    if (h == nullptr || !is_float(x_dtype)) return GEMM_ERR_INVALID_ARG;
+    if (w_dtype != x_dtype && w_dtype != GEMM_F32) return GEMM_ERR_INVALID_ARG;
+    if (M < 0 || D < 0 || lddy < 0 || ldh < 0 || lddh < 0 || lddx < 0 || workspace_bytes < 0) return GEMM_ERR_INVALID_ARG;
+    const bool any = M > 0 && D > 0;
+    if (D > 0 && DW == nullptr) return GEMM_ERR_INVALID_ARG;
+    if (any && (DY == nullptr || H == nullptr || W == nullptr || rstd == nullptr || DX == nullptr))
+        return GEMM_ERR_INVALID_ARG;
+    if (any && (lddy < D || ldh < D || lddx < D || (DH != nullptr && lddh < D))) return GEMM_ERR_INVALID_ARG;
+    const int sz = size_of(x_dtype);
+    if (!aligned(DY, sz) || !aligned(H, sz) || !aligned(DH, sz) || !aligned(DX, sz) || !aligned(W, size_of(w_dtype)) ||
+        !aligned(rstd, 4) || !aligned(DW, 4) || !aligned(workspace, 16))
+        return GEMM_ERR_ALIGNMENT;
+    if (M > GEMM_RMS_MAX_ROWS || D > GEMM_RMS_MAX_D) return GEMM_ERR_UNSUPPORTED;
+    if (any && (workspace == nullptr || workspace_bytes < gemm_rms_backward_workspace(M, D))) return GEMM_ERR_INVALID_ARG;
+    if (D == 0) return GEMM_OK;
+    pg::RmsBackwardArgs a;
+    a.DY = DY;
+    a.H = H;
+    a.W = W;
+    a.rstd = rstd;
+    a.DH = DH;
+    a.DX = DX;
+    a.parts = (float*)workspace;
+    a.DW = DW;
+    a.lddy = lddy;
+    a.ldh = ldh;
+    a.lddh = lddh;
+    a.lddx = lddx;
+    a.M = (int32_t)M;
+    a.D = (int32_t)D;
+    a.groups = pg::rms_backward_groups(M, D, kDefaultCus);
+    a.w_f32 = w_dtype == GEMM_F32;
+    auto rows16 = [&](const void* p, int64_t ld) { return p == nullptr || (aligned(p, 16) && ld * sz % 16 == 0); };
+    a.vec = rows16(DY, lddy) && rows16(H, ldh) && rows16(DH, lddh) && rows16(DX, lddx) && aligned(W, 16);
+    return pg::on_device(h, [&] { return pg::launch_rms_backward(a, x_dtype, (hipStream_t)stream); });
+}
+
+}  // extern "C"

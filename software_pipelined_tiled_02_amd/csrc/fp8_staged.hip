@@ -1,0 +1,244 @@
+// fp8_staged.hip -- 8-bit products of many rows: tiles staged through LDS.
+//
+// A workgroup computes a BM x BN tile of C; a K-tile is one block of 128, so
+// each block's scales are applied exactly once per piece of C.  Operands and
+// scales go from memory straight into LDS (16 and 4 bytes per lane) into a
+// ring of SLOTS, swizzled as tile_layout.h describes; one barrier per K-tile.
+#include "fp8_gemm.h"
+
+namespace pg {
+
+namespace {
+
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+    static_assert(N >= 0 && N < 64, "vmcnt range");
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
+    asm volatile("" ::: "memory");
+}
+// Barrier behind this wave's LDS accesses.
+__device__ __forceinline__ void barrier() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4) | (0 << 8));
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+template <int AT, int BT, bool SBROW, bool EXACT, int BM, int BN, int WM, int WN, int SLOTS>
+struct Staged {
+    static constexpr int T = WM * WN * 64;
+    static constexpr int WTM = BM / WM, WTN = BN / WN, FM = WTM / 16, FN = WTN / 16;
+    static constexpr int CPR = kBlock / kChunk;                  // 8 chunks of 16 bytes per row
+    static constexpr int LA = BM * CPR / T, LB = BN * CPR / T;   // chunks per lane and K-tile
+    static constexpr int LPT = LA + LB + 1;                      // loads per lane and K-tile, one of them scales
+    static constexpr int A_BYTES = BM * kBlock, B_BYTES = BN * kBlock, S_OFF = A_BYTES + B_BYTES;
+    static constexpr int SLOT = S_OFF + (BM + BN) * 4;
+    static constexpr int LDS = SLOTS * SLOT;
+    static_assert(BM + BN == T, "one scale per lane");
+    static_assert(LDS <= kLdsBudget, "LDS");
+    static_assert(WTN <= kBlock && kBlock % WTN == 0 && BN % kBlock == 0, "a wave's columns share a tile scale");
+
+    struct State {
+        __amdgpu_buffer_rsrc_t ra, rb, rs;
+        uint32_t offa[LA], offb[LB], offs;
+        uint32_t s_blk;                      // bytes from one block's scale to the next, of this wave's operand
+        int kc;                              // first k of the lane's chunks
+        int wave, K, KB, ragged;
+    };
+
+    // K-tiles in the order they are multiplied: a ragged last one first.
+    __device__ static __forceinline__ int block_of(const State& s, int t) {
+        return s.ragged ? (t == 0 ? s.KB - 1 : t - 1) : t;
+    }
+
+    // Loads of K-tile t into its slot.  One at or past KB moves nothing
+    // (every offset is out of range: zeros into a slot no later tile reads),
+    // so the number of loads in flight is the same at each boundary.
+    template <bool FIRST>
+    __device__ static __forceinline__ void issue(const State& s, uint8_t PG_LDS* smem, int t, int slot) {
+        const int kb = block_of(s, t);
+        uint8_t PG_LDS* base = smem + slot * SLOT;
+        const uint32_t so = __builtin_amdgcn_readfirstlane(t < s.KB ? (uint32_t)kb * kBlock : kOutside);
+        const uint32_t ss = __builtin_amdgcn_readfirstlane(t < s.KB ? (uint32_t)kb * s.s_blk : kOutside);
+        const uint32_t out = FIRST && kb * kBlock + s.kc >= s.K ? kOutside : 0u;   // chunks past K
+#pragma unroll
+        for (int j = 0; j < LA; ++j)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(s.ra, (void PG_LDS*)(base + (j * T + 64 * s.wave) * kChunk), 16,
+                                                     s.offa[j] | out, so, 0, 0);
+#pragma unroll
+        for (int j = 0; j < LB; ++j)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(s.rb, (void PG_LDS*)(base + A_BYTES + (j * T + 64 * s.wave) * kChunk),
+                                                     16, s.offb[j] | out, so, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(s.rs, (void PG_LDS*)(base + S_OFF + 256 * s.wave), 4, s.offs, ss, 0, 0);
+    }
+
+    // K not a multiple of 16: the bytes at and past K of the chunk that holds
+    // K - 1 become zero, in both operands (what lies there may be a NaN).
+    __device__ static __forceinline__ void clear_tail(const State& s, uint8_t PG_LDS* smem) {
+        const int k = s.K % kBlock, c = k / 16, keep = k % 16;
+        const int row = threadIdx.x;         // one row per lane: A's, then B's
+        i32x4 PG_LDS* p = (i32x4 PG_LDS*)(smem + (row * CPR + (c ^ swz(CPR, row))) * kChunk);
+        i32x4 v = *p;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const int left = keep - 4 * w;
+            v[w] = left >= 4 ? v[w] : left <= 0 ? 0 : v[w] & (int)((1u << (8 * left)) - 1u);
+        }
+        *p = v;
+    }
+
+    __device__ static __forceinline__ i32x4 chunk(const uint8_t PG_LDS* rows, uint32_t off) {
+        return *(const i32x4 PG_LDS*)(rows + off);
+    }
+
+    __device__ static __forceinline__ void run(const Fp8Args& a, uint8_t PG_LDS* smem) {
+        const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
+        State s;
+        s.wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+        const int wm = s.wave / WN, wn = s.wave % WN;
+        // Each XCD gets a run of tiles, in bands of 4 tile rows, so that what
+        // it holds at a time shares rows of A and of B in its L2.
+        const int ntiles = a.tiles_m * a.tiles_n;
+        int w = blockIdx.x;
+        if ((ntiles & 7) == 0) w = (w & 7) * (ntiles >> 3) + (w >> 3);
+        constexpr int kBand = 4;
+        const int band = kBand * a.tiles_n, gi = w / band, first = gi * kBand;
+        const int rows = min(a.tiles_m - first, kBand), in = w - gi * band;
+        const int m0 = (first + in % rows) * BM, n0 = in / rows * BN;
+
+        s.K = a.K;
+        s.KB = (a.K + kBlock - 1) / kBlock;
+        s.ragged = a.K % kBlock != 0;
+        s.ra = buffer_at(a.A + (int64_t)m0 * a.lda);
+        s.rb = buffer_at(a.B + (int64_t)n0 * a.ldb);
+        // Chunk p = j T + tid of a tile lies in row p / 8; the swizzle has
+        // period 16 in the row, so a lane's k is the same for each j.
+        const int c = (tid % CPR) ^ swz(CPR, tid / CPR);
+        s.kc = c * kChunk;
+#pragma unroll
+        for (int j = 0; j < LA; ++j) {
+            const int row = (j * T + tid) / CPR;
+            s.offa[j] = (uint32_t)(m0 + row < a.M ? row : 0) * (uint32_t)a.lda + c * kChunk;
+        }
+#pragma unroll
+        for (int j = 0; j < LB; ++j) {
+            const int row = (j * T + tid) / CPR;
+            s.offb[j] = (uint32_t)(n0 + row < a.N ? row : 0) * (uint32_t)a.ldb + c * kChunk;
+        }
+        // Scales: lane i < BM takes row i of A, lane BM + j column j (whole
+        // waves either way).
+        if (s.wave < BM / 64) {
+            s.rs = buffer_at(a.SA + (int64_t)m0 * a.sa_row);
+            s.offs = (uint32_t)(m0 + tid < a.M ? tid : 0) * (uint32_t)(a.sa_row * 4);
+            s.s_blk = (uint32_t)(a.sa_blk * 4);
+        } else {
+            const int col = tid - BM, n = n0 + col < a.N ? col : 0;
+            s.rs = buffer_at(a.SB + (int64_t)(SBROW ? n0 : n0 / kBlock) * a.sb_row);
+            s.offs = (uint32_t)(SBROW ? n : n / kBlock) * (uint32_t)(a.sb_row * 4);
+            s.s_blk = (uint32_t)(a.sb_blk * 4);
+        }
+
+        f32x4 acc[FM][FN];
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+        // LDS offsets of the lane's two chunks of a 16-row fragment at row 0
+        // of a tile (fragments start at multiples of 16, the swizzle's period)
+        const uint32_t rd0 = (uint32_t)(r * CPR + (g ^ swz(CPR, r))) * kChunk;
+        const uint32_t rd1 = (uint32_t)(r * CPR + ((4 + g) ^ swz(CPR, r))) * kChunk;
+
+        issue<true>(s, smem, 0, 0);
+#pragma unroll
+        for (int t = 1; t < SLOTS - 1; ++t) issue<false>(s, smem, t, t);
+        wait_loads<(SLOTS - 2) * LPT>();
+        barrier();
+        if (a.K % 16 != 0) {
+            clear_tail(s, smem);
+            barrier();
+        }
+        int slot = 0;
+        for (int t = 0; t < s.KB; ++t) {
+            const int free_slot = slot == 0 ? SLOTS - 1 : slot - 1;
+            issue<false>(s, smem, t + SLOTS - 1, free_slot);
+            const uint8_t PG_LDS* ta = smem + slot * SLOT + wm * WTM * kBlock;
+            const uint8_t PG_LDS* tb = smem + slot * SLOT + A_BYTES + wn * WTN * kBlock;
+            const float PG_LDS* sa = (const float PG_LDS*)(smem + slot * SLOT + S_OFF) + wm * WTM;
+            const float PG_LDS* sb = (const float PG_LDS*)(smem + slot * SLOT + S_OFF) + BM + wn * WTN;
+            Frag<BT, EXACT> fb[FN];
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+                fb[j] = fragment<BT, EXACT>(chunk(tb, j * 16 * kBlock + rd0), chunk(tb, j * 16 * kBlock + rd1));
+            f32x4 sbv[SBROW ? FN : 1];
+            if constexpr (SBROW) {
+#pragma unroll
+                for (int j = 0; j < FN; ++j) sbv[j] = *(const f32x4 PG_LDS*)(sb + 16 * j + 4 * g);
+            } else {
+                sbv[0][0] = sb[0];
+            }
+#pragma unroll
+            for (int i = 0; i < FM; ++i) {
+                const Frag<AT, EXACT> fa =
+                    fragment<AT, EXACT>(chunk(ta, i * 16 * kBlock + rd0), chunk(ta, i * 16 * kBlock + rd1));
+                const float sai = sa[16 * i + r];
+                const float sc = SBROW ? sai : sai * sbv[0][0];
+#pragma unroll
+                for (int j = 0; j < FN; ++j) {
+                    const f32x4 v = block_sum<AT, BT, EXACT>(fb[j], fa);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        acc[i][j][e] = fmaf(v[e], SBROW ? sc * sbv[j][e] : sc, acc[i][j][e]);
+                }
+            }
+            wait_loads<(SLOTS - 2) * LPT>();   // K-tile t + 1 has landed (this wave's part)
+            barrier();                         // ... everyone's, and slot t is free
+            slot = slot + 1 == SLOTS ? 0 : slot + 1;
+        }
+        wait_loads<0>();                       // no write into LDS outlives the workgroup
+
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+            const int64_t m = m0 + wm * WTM + 16 * i + r;
+            if (m >= a.M) continue;
+#pragma unroll
+            for (int j = 0; j < FN; ++j) {
+                const int64_t n = n0 + wn * WTN + 16 * j + 4 * g;
+                if (n < a.N) store_c<EXACT>(a, m, n, acc[i][j]);
+            }
+        }
+    }
+};
+
+template <int AT, int BT, bool SBROW, bool EXACT, int BM, int BN, int WM, int WN, int SLOTS>
+__global__ void __launch_bounds__(WM * WN * 64) fp8_staged_tile(Fp8Args a) {
+    typedef Staged<AT, BT, SBROW, EXACT, BM, BN, WM, WN, SLOTS> S;
+    __shared__ __attribute__((aligned(16))) uint8_t smem[S::LDS];
+    S::run(a, (uint8_t PG_LDS*)smem);
+}
+
+template <int AT, int BT>
+const void* by_mode(int tile, bool sb_rows, bool exact) {
+    if (tile == FP8_TILE_256 && !exact)
+        return sb_rows ? (const void*)&fp8_staged_tile<AT, BT, true, false, 256, 256, 2, 4, 2>
+                       : (const void*)&fp8_staged_tile<AT, BT, false, false, 256, 256, 2, 4, 2>;
+    if (tile != FP8_TILE_128) return nullptr;
+    if (exact)
+        return sb_rows ? (const void*)&fp8_staged_tile<AT, BT, true, true, 128, 128, 2, 2, 2>
+                       : (const void*)&fp8_staged_tile<AT, BT, false, true, 128, 128, 2, 2, 2>;
+    return sb_rows ? (const void*)&fp8_staged_tile<AT, BT, true, false, 128, 128, 2, 2, 2>
+                   : (const void*)&fp8_staged_tile<AT, BT, false, false, 128, 128, 2, 2, 2>;
+}
+
+}  // namespace
+
+const void* fp8_staged_kernel(int tile, int a_type, int b_type, bool sb_rows, bool exact) {
+    if (a_type == FP8_E4M3)
+        return b_type == FP8_E4M3 ? by_mode<FP8_E4M3, FP8_E4M3>(tile, sb_rows, exact)
+                                  : by_mode<FP8_E4M3, FP8_E5M2>(tile, sb_rows, exact);
+    return b_type == FP8_E4M3 ? by_mode<FP8_E5M2, FP8_E4M3>(tile, sb_rows, exact)
+                              : by_mode<FP8_E5M2, FP8_E5M2>(tile, sb_rows, exact);
+}
+
+}  // namespace pg

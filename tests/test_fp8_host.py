@@ -1,0 +1,247 @@
+"""The 8-bit operators on the CPU: the 64-bit reference against hand-checked
+values and torch's conversions, and every refusal of the C entry points and of
+the binding (all of them before any HIP call)."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from software_pipelined_tiled_02_amd import binding
+from tests import fp8_ref as R
+
+BAD, ALIGN, UNSUP, OK = (binding.GEMM_ERR_INVALID_ARG, binding.GEMM_ERR_ALIGNMENT, binding.GEMM_ERR_UNSUPPORTED,
+                         binding.GEMM_OK)
+TORCH = {"e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2}
+
+
+# ---- the reference ----------------------------------------------------------
+
+@pytest.mark.parametrize("fp8", ("e4m3", "e5m2"))
+def test_decode_is_torchs_for_every_bit_pattern(fp8):
+    raw = np.arange(256, dtype=np.uint8)
+    t = torch.from_numpy(raw).view(TORCH[fp8]).double().numpy()
+    assert np.array_equal(R.decode(raw, fp8), t, equal_nan=True)
+    assert R.decode([0x38 if fp8 == "e4m3" else 0x3C], fp8)[0] == 1.0
+
+
+@pytest.mark.parametrize("fp8", ("e4m3", "e5m2"))
+def test_encode_is_torchs(fp8):
+    rng = np.random.default_rng(1)
+    x = np.concatenate([rng.standard_normal(20000) * np.exp2(rng.integers(-20, 8, 20000)),
+                        R._table(fp8)[0], -R._table(fp8)[0],
+                        (R._table(fp8)[0][1:] + R._table(fp8)[0][:-1]) / 2])      # ties
+    x = np.clip(x, -R.TOP[fp8], R.TOP[fp8]).astype(np.float32)
+    t = torch.from_numpy(x).to(TORCH[fp8]).view(torch.uint8).numpy()
+    assert np.array_equal(R.encode(x.astype(np.float64), fp8), t)
+
+
+def test_quantize_by_hand():
+    x = np.zeros((2, 200), dtype=np.float32)
+    x[0, 3], x[0, 4], x[0, 130] = 448.0, -224.0, 1.0
+    q, s = R.quantize_fp32(x, "e4m3", 1)
+    assert s.shape == (2, 2) and s[0, 0] == 1.0 and s[0, 1] == np.float32(1 / 448.0) and s[1, 0] == np.float32(2.0 ** -126)
+    v = R.decode(q, "e4m3")
+    assert v[0, 3] == 448 and v[0, 4] == -224 and v[0, 130] == 448 and (v[1] == 0).all()
+    q, s = R.quantize_fp32(x, "e4m3", 128, pow2=True)
+    assert s.shape == (1, 2) and s[0, 0] == 1.0 and s[0, 1] == 2.0 ** -8
+    assert R.decode(q, "e4m3")[0, 130] == 256
+
+
+def test_product_by_hand():
+    a, b = np.zeros((1, 256)), np.zeros((2, 256))
+    a[0, 0], a[0, 200] = 2.0, 3.0
+    b[1, 0], b[1, 200] = 5.0, 7.0
+    C, _, _ = R.product(a, np.array([[10.0, 100.0]]), b, np.array([[1.0, 2.0]]), 128)
+    assert C[0, 0] == 0 and C[0, 1] == 2 * 5 * 10 + 3 * 7 * 200
+    C, _, _ = R.product(a, np.array([[10.0, 100.0]]), b, np.array([[1.0, 2.0], [0.5, 0.25]]), 1)
+    assert C[0, 1] == 2 * 5 * 5 + 3 * 7 * 25
+
+
+@pytest.mark.parametrize("with_dh", (False, True))
+def test_rms_backward_is_the_forwards_derivative(with_dh):
+    """The backward formula against central differences of the forward one, in 64 bits."""
+    rng = np.random.default_rng(2)
+    M, D, eps = 3, 37, 1e-3
+    h, w, dy = rng.standard_normal((M, D)), rng.standard_normal(D), rng.standard_normal((M, D))
+    dh = rng.standard_normal((M, D)) if with_dh else None
+
+    def loss(h, w):
+        return (R.rms(h, None, w, eps)[0] * dy).sum() + ((h * dh).sum() if with_dh else 0.0)
+
+    dx, dw = R.rms_backward(dy, h, w, R.rms(h, None, w, eps)[1], dh)
+    step = 1e-5      # truncation ~ step^2, rounding ~ 1e-16 * |loss| / step: both below 1e-9
+    for i, j in ((0, 0), (1, 17), (2, 36)):
+        d = np.zeros_like(h)
+        d[i, j] = step
+        assert abs((loss(h + d, w) - loss(h - d, w)) / (2 * step) - dx[i, j]) < 1e-8
+    for j in (0, 20):
+        d = np.zeros_like(w)
+        d[j] = step
+        assert abs((loss(h, w + d) - loss(h, w - d)) / (2 * step) - dw[j]) < 1e-8
+
+
+# ---- the product's plan and refusals ----------------------------------------
+
+def q(M=512, N=512, K=512, **kw):
+    return binding.gemm_query_fp8(M, N, K, check=False, **kw)
+
+
+def test_product_plan():
+    """The largest tile that the rows fill at least half and that gives 256 CUs a workgroup."""
+    T = binding.FP8_TILES
+    for M, N, K, tile in ((1, 4096, 4096, "16x16"), (16, 8192, 512, "16x16"), (17, 8192, 512, "32x32"),
+                          (64, 8192, 8192, "64x32"), (500, 4104, 4100, "64x64"), (2048, 2048, 128, "128x128"),
+                          (4096, 4096, 4096, "256x256")):
+        rc, info = q(M, N, K)
+        assert rc == OK and info["tile"] == T[tile], (M, N, K, info)
+        assert info["grid"] == -(-M // info["block_m"]) * -(-N // info["block_n"])
+        assert info["k_blocks"] == -(-K // 128)
+    assert q(4096, 4096, 4096, c_dtype="f32")[1]["tile"] == T["128x128"]       # fp32 outputs: widened
+    assert q(4096, 4096, 4096, c_dtype="f32")[1]["widened"] == 1
+    assert q(4096, 4096, 4100, lda=4100)[1]["staged"] == 0                      # rows at any address
+    assert q(4096, 4096, 4100, A=8)[1]["staged"] == 0
+    assert q(4096, 4096, 4100)[1]["staged"] == 1                                # any K with rows on 16 bytes
+
+
+def test_product_refusals():
+    assert q(a_type=1)[0] == BAD and q(b_type=18)[0] == BAD and q(c_dtype="i8")[0] == BAD
+    assert q(b_scale_rows=64)[0] == BAD and q(tile=6)[0] == BAD and q(tile=-2)[0] == BAD
+    assert q(accumulate=2)[0] == BAD and q(accumulate=1)[0] == UNSUP
+    assert q(accumulate=1, c_dtype="f32")[0] == OK
+    assert q(M=-1)[0] == BAD and q(N=-1)[0] == BAD and q(K=-1)[0] == BAD
+    assert q(lda=511)[0] == BAD and q(ldb=511)[0] == BAD and q(ldc=511)[0] == BAD
+    assert q(sa_row=-1)[0] == BAD and q(sb_blk=-1)[0] == BAD
+    assert q(C=1)[0] == ALIGN and q(SA=2)[0] == ALIGN and q(SB=6)[0] == ALIGN
+    assert q(C=2)[0] == OK and q(C=2, c_dtype="f32")[0] == ALIGN
+    assert q(tile="256x256", lda=520)[0] == ALIGN                               # rows not on 16 bytes
+    assert q(tile="256x256", c_dtype="f32")[0] == UNSUP
+    assert q(K=2 ** 31 - 1, lda=2 ** 31)[0] == UNSUP
+    assert q(lda=1 << 28)[0] == UNSUP and q(ldb=1 << 28)[0] == UNSUP            # a tile's rows: 2^31 bytes
+    assert q(sa_row=1 << 24)[0] == UNSUP and q(sb_blk=1 << 28)[0] == UNSUP      # a tile's, a row's scales
+    assert q(sa_row=0, sa_blk=0, sb_row=0, sb_blk=0)[0] == OK                   # expanded scales
+    assert q(M=0)[0] == OK and q(N=0)[0] == OK and q(K=0)[0] == OK and q(K=0, tile="128x128")[0] == OK
+    assert q(M=0)[1]["grid"] == 0
+    rc = binding.gemm_run_fp8(None, 16, 16, 16, "e4m3", "e4m3", "bf16", 128, 0, "auto", 0, 16, 0, 1, 16, 0, 16, 0, 1, 1,
+                              0, 16, stream=0, check=False)
+    assert rc == BAD
+    with pytest.raises(binding.GemmError):
+        binding.gemm_query_fp8(16, 16, 16, lda=8)
+
+
+class FakeHandle:
+    """Enough of a handle for calls that are refused before it is used: the
+    entry points check every argument before any HIP call."""
+
+    def __init__(self):
+        self.block = (ctypes.c_byte * 64)()
+        self.h = ctypes.addressof(self.block)
+
+
+H = FakeHandle().h
+P = 4096                   # an aligned address; refused calls never read it
+
+
+def run(**kw):
+    a = dict(M=512, N=512, K=512, a="e4m3", b="e4m3", c="bf16", rows=128, acc=0, tile="auto", A=P, lda=512, SA=P,
+             sa_row=1, sa_blk=512, B=P, ldb=512, SB=P, sb_row=1, sb_blk=4, C=P, ldc=512)
+    a.update(kw)
+    return binding.gemm_run_fp8(H, *a.values(), stream=0, check=False)
+
+
+def test_product_null_pointers():
+    for name in ("A", "B", "SA", "SB", "C"):
+        assert run(**{name: None}) == BAD, name
+    assert run(K=0, A=None, B=None, SA=None, SB=None, C=None) == BAD            # C = 0 has to go somewhere
+    for zero in ("M", "N"):
+        assert run(**{zero: 0, "A": None, "B": None, "SA": None, "SB": None, "C": None}) == OK
+
+
+def quant(**kw):
+    a = dict(M=256, K=256, x="bf16", f="e4m3", rows=1, pow2=0, X=P, ldx=256, Q=P, ldq=256, S=P, s_row=1, s_blk=256,
+             QT=P, ldqt=256, ST=P, st_row=1, st_blk=256)
+    a.update(kw)
+    return binding.gemm_quantize_fp8(H, *a.values(), stream=0, check=False)
+
+
+def test_quantize_refusals():
+    assert quant(x="i8") == BAD and quant(f=0) == BAD and quant(rows=2) == BAD and quant(pow2=2) == BAD
+    assert quant(M=-1) == BAD and quant(K=-1) == BAD and quant(s_row=-1) == BAD and quant(st_blk=-1) == BAD
+    assert quant(ldx=255) == BAD and quant(ldq=255) == BAD and quant(ldqt=255) == BAD
+    assert quant(X=None) == BAD and quant(S=None) == BAD and quant(ST=None) == BAD
+    assert quant(Q=None, QT=None) == BAD
+    assert quant(X=P + 1) == ALIGN and quant(S=P + 2) == ALIGN and quant(x="f32", X=P + 2) == ALIGN
+    assert quant(M=2 ** 31, ldqt=2 ** 31) == UNSUP
+    assert quant(M=2 ** 30, K=2 ** 14, ldx=2 ** 14, ldq=2 ** 14, ldqt=2 ** 30) == UNSUP     # 2^30 workgroups
+    assert quant(M=0, X=None) == OK and quant(K=0, X=None) == OK
+    assert binding.gemm_quantize_fp8(None, 1, 1, "bf16", "e4m3", 1, 0, P, 1, P, 1, P, 1, 1, stream=0, check=False) == BAD
+
+
+def rms(**kw):
+    a = dict(M=4, D=256, x="bf16", w="bf16", f="e4m3", pow2=0, eps=1e-6, X=P, ldx=256, R=P, ldr=256, W=P, H=P, ldh=256,
+             Y=P, ldy=256, Q=P, ldq=256, S=P, s_row=1, s_blk=4, rstd=P)
+    a.update(kw)
+    return binding.gemm_rms_fp8(H, *a.values(), stream=0, check=False)
+
+
+def test_rms_refusals():
+    assert rms(x="i8") == BAD and rms(w="f16") == BAD and rms(f=3) == BAD and rms(pow2=-1) == BAD
+    assert rms(eps=-1.0) == BAD and rms(eps=float("nan")) == BAD
+    assert rms(M=-1) == BAD and rms(D=-1) == BAD and rms(s_row=-1) == BAD
+    for ld in ("ldx", "ldr", "ldh", "ldy", "ldq"):
+        assert rms(**{ld: 255}) == BAD, ld
+    assert rms(X=None) == BAD and rms(W=None) == BAD and rms(S=None) == BAD and rms(Q=None, Y=None) == BAD
+    for p in ("X", "R", "H", "Y", "W"):
+        assert rms(**{p: P + 1}) == ALIGN, p
+    assert rms(S=P + 2) == ALIGN and rms(rstd=P + 2) == ALIGN and rms(w="f32", W=P + 2) == ALIGN
+    big = binding.GEMM_RMS_MAX_D + 1
+    assert rms(D=big, ldx=big, ldr=big, ldh=big, ldy=big, ldq=big) == UNSUP
+    assert rms(M=binding.GEMM_RMS_MAX_ROWS + 1) == UNSUP
+    assert rms(M=0, X=None, W=None) == OK and rms(D=0, X=None) == OK
+
+
+def rms_back(**kw):
+    a = dict(M=4, D=256, x="bf16", w="f32", DY=P, lddy=256, Hm=P, ldh=256, W=P, rstd=P, DH=P, lddh=256, DX=P, lddx=256,
+             DW=P, ws=P, nbytes=1 << 20)
+    a.update(kw)
+    return binding.gemm_rms_backward(H, *a.values(), stream=0, check=False)
+
+
+def test_rms_backward_refusals():
+    assert rms_back(x="i8") == BAD and rms_back(w="f16") == BAD and rms_back(M=-1) == BAD and rms_back(D=-1) == BAD
+    for ld in ("lddy", "ldh", "lddh", "lddx"):
+        assert rms_back(**{ld: 255}) == BAD, ld
+    for p in ("DY", "Hm", "W", "rstd", "DX", "DW", "ws"):
+        assert rms_back(**{p: None}) == BAD, p
+    assert rms_back(nbytes=binding.gemm_rms_backward_workspace(4, 256) - 1) == BAD and rms_back(nbytes=-1) == BAD
+    for p in ("DY", "Hm", "DH", "DX"):
+        assert rms_back(**{p: P + 1}) == ALIGN, p
+    assert rms_back(ws=P + 8) == ALIGN and rms_back(DW=P + 2) == ALIGN
+    assert rms_back(M=binding.GEMM_RMS_MAX_ROWS + 1) == UNSUP
+    big = binding.GEMM_RMS_MAX_D + 1
+    assert rms_back(D=big, lddy=big, ldh=big, lddh=big, lddx=big) == UNSUP
+    assert rms_back(D=0, DW=None) == OK
+
+
+def test_rms_backward_workspace():
+    assert binding.gemm_rms_backward_workspace(4, 256) == 4 * 256 * 4
+    assert binding.gemm_rms_backward_workspace(0, 256) == 0
+    assert binding.gemm_rms_backward_workspace(-1, 256) == 0
+    assert binding.gemm_rms_backward_workspace(1, binding.GEMM_RMS_MAX_D + 1) == 0
+    most = binding.gemm_rms_backward_workspace(1 << 20, 8192)
+    assert most == binding.gemm_rms_backward_workspace(1 << 21, 8192)            # bounded
+
+
+# ---- the torch functions' refusals (CPU tensors: nothing is enqueued) --------
+
+def test_binding_refuses_what_is_no_device_matrix():
+    x = torch.zeros(4, 256, dtype=torch.bfloat16)
+    q8 = torch.zeros(4, 256, dtype=torch.float8_e4m3fn)
+    s = torch.ones(4, 2)
+    for call in (lambda: binding.run_fp8(q8, s, q8, s), lambda: binding.run_fp8(x, s, q8, s),
+                 lambda: binding.run_fp8([1], s, q8, s), lambda: binding.run_fp8(q8[0], s, q8, s),
+                 lambda: binding.quantize_fp8(x), lambda: binding.quantize_fp8(x.to(torch.int8)),
+                 lambda: binding.quantize_fp8(None), lambda: binding.rms_fp8(x, x[0]),
+                 lambda: binding.rms_fp8(x[0], x[0]), lambda: binding.rms_backward(x, x, x[0], s[:, 0])):
+        with pytest.raises(ValueError):
+            call()
