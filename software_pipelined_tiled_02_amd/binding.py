@@ -411,27 +411,6 @@ def _rows16(n):
     return (n + 15) // 16 * 16
 
 
-def _ld(t):
-    """Elements from one row to the next; a single row's is free, and taken
-    as the next multiple of 16."""
-    return t.stride(0) if t.shape[0] > 1 else _rows16(t.shape[1])
-
-
-def _matrix(t, what, dtypes, device=None, shape=None):
-    """Argument check: t is a 2-D CUDA tensor of one of dtypes with unit
-    stride along its last axis and rows that do not overlap."""
-    if not isinstance(t, _types()["tensor"]) or t.dim() != 2:
-        raise ValueError("%s must be a 2-D torch tensor" % what)
-    if t.dtype not in dtypes:
-        raise ValueError("%s must be %s (got %s)" % (what, " or ".join(str(d) for d in dtypes), t.dtype))
-    if not t.is_cuda or (device is not None and t.device != device):
-        raise ValueError("all tensors must be CUDA tensors on one device (%s is on %s)" % (what, t.device))
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError("%s must be %s (got %s)" % (what, " x ".join(map(str, shape)), tuple(t.shape)))
-    if (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
-        raise ValueError("%s must have unit stride along its last axis, and rows that do not overlap" % what)
-
-
 _T = {}   # torch's types by role, filled on first use (torch is not imported with this module)
 
 
@@ -440,10 +419,71 @@ def _types():
         import torch
         _T["fp8"] = {torch.float8_e4m3fn: GEMM_E4M3, torch.float8_e5m2: GEMM_E5M2}
         _T["float"] = {torch.bfloat16: GEMM_BF16, torch.float16: GEMM_F16, torch.float32: GEMM_F32}
-        _T["tensor"], _T["f32"] = torch.Tensor, (torch.float32,)
         _T["named"] = {"e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2,
                        torch.float8_e4m3fn: torch.float8_e4m3fn, torch.float8_e5m2: torch.float8_e5m2}
+        _T["float32"], _T["bfloat16"], _T["uint8"] = torch.float32, torch.bfloat16, torch.uint8
+        _T["new"] = torch.empty_strided
+        # the current stream of a device as its raw handle, without a Stream
+        # object (2 us of a 10 us call)
+        _T["raw stream"] = getattr(torch._C, "_cuda_getCurrentRawStream",
+                                   lambda index: torch.cuda.current_stream(index).cuda_stream)
     return _T
+
+
+def _refuse(t, what, dtypes, device, shape):
+    """Raises ValueError, naming what _matrix found wrong with t."""
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError("%s must be a 2-D torch tensor" % what)
+    if t.dtype not in dtypes:
+        raise ValueError("%s must be %s (got %s)" % (what, " or ".join(str(d) for d in dtypes), t.dtype))
+    if not t.is_cuda or (device is not None and t.get_device() != device):
+        raise ValueError("all tensors must be CUDA tensors on one device (%s is on %s)" % (what, t.device))
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError("%s must be %s (got %s)" % (what, " x ".join(map(str, shape)), tuple(t.shape)))
+    raise ValueError("%s must have unit stride along its last axis, and rows that do not overlap" % what)
+
+
+def _matrix(t, what, dtypes, device=None, shape=None):
+    """Argument check: t is a 2-D CUDA tensor (on device number `device`, of
+    `shape`) of one of dtypes, with unit stride along its last axis and rows
+    that do not overlap.  Returns rows, columns, leading dimension (a single row's is free:
+    the next multiple of 16) and the type's GEMM_* value."""
+    try:
+        rows, cols = t.shape
+        ld, unit = t.stride()
+        code = dtypes.get(t.dtype)
+        index = t.get_device()
+        if (code is not None and (index == device or (device is None and index >= 0 and t.is_cuda))
+                and (unit == 1 or cols <= 1) and (ld >= cols or rows <= 1)
+                and (shape is None or (rows == shape[0] and cols == shape[1]))):
+            return rows, cols, ld if rows > 1 else _rows16(cols), code
+    except (AttributeError, TypeError, ValueError, RuntimeError):
+        pass
+    _refuse(t, what, dtypes, device, shape)
+
+
+def _vector(t, what, dtypes, n, device):
+    """Argument check: n contiguous values of one of dtypes; returns the type's GEMM_* value."""
+    try:
+        code = dtypes.get(t.dtype)
+        if code is not None and t.dim() == 1 and t.shape[0] == n and t.get_device() == device and (
+                n <= 1 or t.stride(0) == 1):
+            return code
+    except (AttributeError, TypeError, RuntimeError):
+        pass
+    raise ValueError("%s must be a torch tensor of %d contiguous values of %s on the other tensors' device"
+                     % (what, n, " or ".join(str(d) for d in dtypes)))
+
+
+def _scales(t, what, index):
+    """Argument check: a 2-D float32 tensor on device `index`, any strides."""
+    try:
+        if t.dtype is _T["float32"] and t.dim() == 2 and t.get_device() == index:
+            return t.shape
+    except (AttributeError, RuntimeError):
+        pass
+    raise ValueError("%s must be a 2-D float32 torch tensor on the matrices' device" % what)
 
 
 def _fp8_dtype(fp8):
@@ -453,46 +493,26 @@ def _fp8_dtype(fp8):
     return named[fp8]
 
 
-class _Target:
-    """Where a call is enqueued: the raw stream, and the stream that what the
-    call allocates belongs to."""
-
-    def __init__(self, stream, device):
-        import torch
-        if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream, device=device)
-        if stream.device != device:
-            raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, device))
-        self.raw, self.context = stream.cuda_stream, torch.cuda.stream(stream)
-
-
-def _call(stream, device, fn):
-    """fn(raw stream), with what it allocates belonging to that stream."""
+def _on_stream(stream, device):
+    """The context in which `stream` (a torch stream or a raw handle) is the
+    current one: what a call allocates in it belongs to that stream."""
     import torch
-    if stream is None:
-        return fn(torch.cuda.current_stream(device).cuda_stream)
-    target = _Target(stream, device)
-    with target.context:
-        return fn(target.raw)
-
-
-def _check(rc, where):
-    if rc != GEMM_OK:
-        raise GemmError(rc, where)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    if stream.device != device:
+        raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, device))
+    return torch.cuda.stream(stream)
 
 
 def _empty_rows16(rows, cols, dtype, device):
-    """rows x cols whose rows start on 16 bytes (8-bit types)."""
-    import torch
-    t = torch.empty((rows, _rows16(cols)), dtype=dtype, device=device)
-    return t if t.shape[1] == cols else t[:, :cols]
+    """rows x cols of 8-bit values whose rows start on 16 bytes."""
+    return _T["new"]((rows, cols), (_rows16(cols), 1), dtype=dtype, device=device)
 
 
 def _empty_scales(rows, blocks, device):
     """rows x blocks scales, one block's after another (the order the
     product reads them in)."""
-    import torch
-    return torch.empty((blocks, rows), dtype=torch.float32, device=device).t()
+    return _T["new"]((rows, blocks), (1, rows), dtype=_T["float32"], device=device)
 
 
 def run_fp8(a, sa, b, sb, *, out=None, out_dtype=None, accumulate=False, tile="auto", stream=None):
@@ -510,52 +530,49 @@ def run_fp8(a, sa, b, sb, *, out=None, out_dtype=None, accumulate=False, tile="a
 
     Rows that start on 16 bytes (as quantize_fp8 and rms_fp8 lay them out) are
     the fast case."""
-    import torch
     types = _types()
-    _matrix(a, "a", types["fp8"])
-    device = a.device
-    M, K = a.shape
-    _matrix(b, "b", types["fp8"], device)
-    N = b.shape[0]
-    if b.shape[1] != K:
-        raise ValueError("inner dimensions differ: a has K = %d, b has %d" % (K, b.shape[1]))
+    M, K, lda, a_type = _matrix(a, "a", types["fp8"])
+    index = a.get_device()
+    if stream is not None:
+        with _on_stream(stream, a.device):
+            return run_fp8(a, sa, b, sb, out=out, out_dtype=out_dtype, accumulate=accumulate, tile=tile)
+    N, Kb, ldb, b_type = _matrix(b, "b", types["fp8"], index)
+    if Kb != K:
+        raise ValueError("inner dimensions differ: a has K = %d, b has %d" % (K, Kb))
     blocks = (K + 127) // 128
-    for t, what in ((sa, "sa"), (sb, "sb")):
-        if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32 or t.dim() != 2 or t.device != device:
-            raise ValueError("%s must be a 2-D float32 tensor on a's device" % what)
-    if sa.shape[0] != M or sa.shape[1] != blocks:
-        raise ValueError("sa must be M x ceil(K / 128) = %d x %d (got %s)" % (M, blocks, tuple(sa.shape)))
-    b_scale_rows = 128 if sb.shape[0] == (N + 127) // 128 else 1
-    if (b_scale_rows == 1 and sb.shape[0] != N) or sb.shape[1] != blocks:
-        raise ValueError("sb must be ceil(N / 128) or N rows of ceil(K / 128) = %d scales (got %s)"
-                         % (blocks, tuple(sb.shape)))
-    if out is not None:
-        _matrix(out, "out", types["float"], device, (M, N))
-        if out_dtype is not None and out.dtype != out_dtype:
-            raise ValueError("out is %s, out_dtype %s" % (out.dtype, out_dtype))
-        out_dtype = out.dtype
-    else:
+    rows, cols = _scales(sa, "sa", index)
+    if rows != M or cols != blocks:
+        raise ValueError("sa must be M x ceil(K / 128) = %d x %d (got %d x %d)" % (M, blocks, rows, cols))
+    rows, cols = _scales(sb, "sb", index)
+    b_scale_rows = 128 if rows == (N + 127) // 128 else 1
+    if (b_scale_rows == 1 and rows != N) or cols != blocks:
+        raise ValueError("sb must be ceil(N / 128) or N rows of ceil(K / 128) = %d scales (got %d x %d)"
+                         % (blocks, rows, cols))
+    if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
-        out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
-        if out_dtype not in types["float"]:
+        if out_dtype is None:
+            out_dtype = types["bfloat16"]
+        c_type, ldc = types["float"].get(out_dtype), N
+        if c_type is None:
             raise ValueError("out_dtype must be bfloat16, float16 or float32 (got %s)" % out_dtype)
-    if accumulate and out_dtype is not torch.float32:
-        raise ValueError("accumulate needs a float32 out")
-    h = _handle(device.index)
-
-    def enqueue(raw):
-        c = torch.empty((M, N), dtype=out_dtype, device=device) if out is None else out
-        rc = _L.gemm_run_fp8(h, M, N, K, types["fp8"][a.dtype], types["fp8"][b.dtype], types["float"][out_dtype],
-                             b_scale_rows, 1 if accumulate else 0, _enum(tile, FP8_TILES),
-                             a.data_ptr(), _ld(a), sa.data_ptr(), *sa.stride(),
-                             b.data_ptr(), _ld(b), sb.data_ptr(), *sb.stride(),
-                             c.data_ptr(), _ld(c), raw)
-        if rc != GEMM_OK:
-            raise GemmError(rc, "gemm_run_fp8")
-        return c
-
-    return _call(stream, device, enqueue)
+    else:
+        _, _, ldc, c_type = _matrix(out, "out", types["float"], index, (M, N))
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise ValueError("out is %s, out_dtype %s" % (out.dtype, out_dtype))
+        if accumulate and c_type != GEMM_F32:
+            raise ValueError("accumulate needs a float32 out")
+    h = _handle(index)
+    if out is None:
+        out = types["new"]((M, N), (N, 1), dtype=out_dtype, device=a.device)
+    sa0, sa1 = sa.stride()
+    sb0, sb1 = sb.stride()
+    rc = _L.gemm_run_fp8(h, M, N, K, a_type, b_type, c_type, b_scale_rows, 1 if accumulate else 0, _enum(tile, FP8_TILES),
+                         a.data_ptr(), lda, sa.data_ptr(), sa0, sa1, b.data_ptr(), ldb, sb.data_ptr(), sb0, sb1,
+                         out.data_ptr(), ldc, types["raw stream"](index))
+    if rc != GEMM_OK:
+        raise GemmError(rc, "gemm_run_fp8")
+    return out
 
 
 def quantize_fp8(x, *, block="row", fp8="e4m3", pow2=False, rows=True, transpose=False, stream=None):
@@ -570,40 +587,37 @@ def quantize_fp8(x, *, block="row", fp8="e4m3", pow2=False, rows=True, transpose
     or "e5m2".  pow2: scales are powers of two.  Rows of q and qt start on 16
     bytes.  Streams and errors as run_fp8."""
     types = _types()
-    _matrix(x, "x", types["float"])
+    M, K, ldx, x_type = _matrix(x, "x", types["float"])
+    device = x.device
+    if stream is not None:
+        with _on_stream(stream, device):
+            return quantize_fp8(x, block=block, fp8=fp8, pow2=pow2, rows=rows, transpose=transpose)
     f8 = _fp8_dtype(fp8)
     if block not in BLOCK_ROWS:
         raise ValueError("block must be 'row' or 'tile' (got %r)" % (block,))
     if not rows and not transpose:
         raise ValueError("rows or transpose must be asked for")
-    device, (M, K) = x.device, x.shape
     block_rows = BLOCK_ROWS[block]
-    h = _handle(device.index)
-
-    def enqueue(raw):
-        q = s = qt = st = None
-        if rows:
-            q = _empty_rows16(M, K, f8, device)
-            s = _empty_scales(-(-M // block_rows), -(-K // FP8_BLOCK), device)
-        if transpose:
-            qt = _empty_rows16(K, M, f8, device)
-            st = _empty_scales(-(-K // block_rows), -(-M // FP8_BLOCK), device)
-        _check(_L.gemm_quantize_fp8(h, M, K, types["float"][x.dtype], types["fp8"][f8], block_rows, 1 if pow2 else 0,
-                                    x.data_ptr(), _ld(x),
-                                    *((q.data_ptr(), _ld(q), s.data_ptr(), *s.stride()) if rows else (None, 0, None, 0, 0)),
-                                    *((qt.data_ptr(), _ld(qt), st.data_ptr(), *st.stride()) if transpose
-                                      else (None, 0, None, 0, 0)), raw), "gemm_quantize_fp8")
-        return ((q, s) if rows else ()) + ((qt, st) if transpose else ())
-
-    return _call(stream, device, enqueue)
-
-
-def _vector(t, what, dtypes, n, device):
-    if not isinstance(t, _types()["tensor"]):
-        raise ValueError("%s must be a torch tensor" % what)
-    if t.dtype not in dtypes or t.dim() != 1 or t.shape[0] != n or t.device != device or (n > 1 and t.stride(0) != 1):
-        raise ValueError("%s must be %d contiguous values of %s on %s (got %s %s)"
-                         % (what, n, " or ".join(str(d) for d in dtypes), device, t.dtype, tuple(t.shape)))
+    index = x.get_device()
+    h = _handle(index)
+    out, given = (), ()
+    if rows:
+        n = -(-M // block_rows)
+        q, s = _empty_rows16(M, K, f8, device), _empty_scales(n, -(-K // FP8_BLOCK), device)
+        out, given = (q, s), (q.data_ptr(), _rows16(K), s.data_ptr(), 1, n)
+    else:
+        given = (None, 0, None, 0, 0)
+    if transpose:
+        n = -(-K // block_rows)
+        q, s = _empty_rows16(K, M, f8, device), _empty_scales(n, -(-M // FP8_BLOCK), device)
+        out, given = out + (q, s), given + (q.data_ptr(), _rows16(M), s.data_ptr(), 1, n)
+    else:
+        given += (None, 0, None, 0, 0)
+    rc = _L.gemm_quantize_fp8(h, M, K, x_type, types["fp8"][f8], block_rows, 1 if pow2 else 0, x.data_ptr(), ldx, *given,
+                              types["raw stream"](index))
+    if rc != GEMM_OK:
+        raise GemmError(rc, "gemm_quantize_fp8")
+    return out
 
 
 def rms_fp8(x, weight, *, residual=None, eps=1e-6, fp8="e4m3", pow2=False, norm=False, h_out=None, stream=None):
@@ -616,34 +630,42 @@ def rms_fp8(x, weight, *, residual=None, eps=1e-6, fp8="e4m3", pow2=False, norm=
     residual; rstd: M float32, what rms_backward takes; q, s: the normalised
     rows in 8 bits, a scale for each 128 values; y: the same in x's type.
     D up to 32768.  Streams and errors as run_fp8."""
-    import torch
     types = _types()
-    _matrix(x, "x", types["float"])
-    device, (M, D) = x.device, x.shape
+    M, D, ldx, x_type = _matrix(x, "x", types["float"])
+    device = x.device
+    if stream is not None:
+        with _on_stream(stream, device):
+            return rms_fp8(x, weight, residual=residual, eps=eps, fp8=fp8, pow2=pow2, norm=norm, h_out=h_out)
+    index = x.get_device()
     f8 = _fp8_dtype(fp8)
-    _vector(weight, "weight", (x.dtype, torch.float32), D, device)
+    own, f32, new = {x.dtype: x_type}, types["float32"], types["new"]
+    w_type = _vector(weight, "weight", own if x.dtype is f32 else {x.dtype: x_type, f32: GEMM_F32}, D, index)
+    r, ldr, h, ldh, y, ldy = None, 0, None, 0, None, 0
     if residual is not None:
-        _matrix(residual, "residual", (x.dtype,), device, (M, D))
+        ldr = _matrix(residual, "residual", own, index, (M, D))[2]
+        r = residual.data_ptr()
     if h_out is not None:
-        _matrix(h_out, "h_out", (x.dtype,), device, (M, D))
-    handle = _handle(device.index)
-
-    def enqueue(raw):
-        q = _empty_rows16(M, D, f8, device)
-        s = _empty_scales(M, -(-D // FP8_BLOCK), device)
-        rstd = torch.empty((M,), dtype=torch.float32, device=device)
-        write = h_out if h_out is not None else torch.empty((M, D), dtype=x.dtype, device=device) \
-            if residual is not None else None
-        y = torch.empty((M, D), dtype=x.dtype, device=device) if norm else None
-        ptr_ld = lambda t: (None, 0) if t is None else (t.data_ptr(), _ld(t))  # noqa: E731
-        _check(_L.gemm_rms_fp8(handle, M, D, types["float"][x.dtype], types["float"][weight.dtype], types["fp8"][f8],
-                               1 if pow2 else 0, eps, *ptr_ld(x), *ptr_ld(residual), weight.data_ptr(),
-                               *ptr_ld(write), *ptr_ld(y), *ptr_ld(q), s.data_ptr(), *s.stride(), rstd.data_ptr(),
-                               raw), "gemm_rms_fp8")
-        out = (q, s, x if write is None else write, rstd)
-        return out + (y,) if norm else out
-
-    return _call(stream, device, enqueue)
+        ldh = _matrix(h_out, "h_out", own, index, (M, D))[2]
+        h = h_out.data_ptr()
+    handle = _handle(index)
+    blocks = -(-D // FP8_BLOCK)
+    q, s = _empty_rows16(M, D, f8, device), _empty_scales(M, blocks, device)
+    rstd = new((M,), (1,), dtype=f32, device=device)
+    if h_out is None:
+        h_out = x
+        if residual is not None:
+            h_out = new((M, D), (D, 1), dtype=x.dtype, device=device)
+            h, ldh = h_out.data_ptr(), D
+    out = (q, s, h_out, rstd)
+    if norm:
+        out += (new((M, D), (D, 1), dtype=x.dtype, device=device),)
+        y, ldy = out[4].data_ptr(), D
+    rc = _L.gemm_rms_fp8(handle, M, D, x_type, w_type, types["fp8"][f8], 1 if pow2 else 0, eps, x.data_ptr(), ldx, r, ldr,
+                         weight.data_ptr(), h, ldh, y, ldy, q.data_ptr(), _rows16(D), s.data_ptr(), 1, M,
+                         rstd.data_ptr(), types["raw stream"](index))
+    if rc != GEMM_OK:
+        raise GemmError(rc, "gemm_rms_fp8")
+    return out
 
 
 def rms_backward(dy, h, weight, rstd, *, dh=None, dx_out=None, stream=None):
@@ -655,32 +677,38 @@ def rms_backward(dy, h, weight, rstd, *, dh=None, dx_out=None, stream=None):
     the residual; it is written into dx_out where given, which may be dy, h
     or dh.  dw is float32, its rows added in a fixed order.  Streams and errors
     as run_fp8."""
-    import torch
     types = _types()
-    _matrix(h, "h", types["float"])
-    device, (M, D) = h.device, h.shape
-    _matrix(dy, "dy", (h.dtype,), device, (M, D))
-    for t, what in ((dh, "dh"), (dx_out, "dx_out")):
-        if t is not None:
-            _matrix(t, what, (h.dtype,), device, (M, D))
-    _vector(weight, "weight", (h.dtype, torch.float32), D, device)
-    _vector(rstd, "rstd", types["f32"], M, device)
-    handle = _handle(device.index)
+    M, D, ldh, x_type = _matrix(h, "h", types["float"])
+    device = h.device
+    if stream is not None:
+        with _on_stream(stream, device):
+            return rms_backward(dy, h, weight, rstd, dh=dh, dx_out=dx_out)
+    index = h.get_device()
+    own, f32, new = {h.dtype: x_type}, types["float32"], types["new"]
+    lddy = _matrix(dy, "dy", own, index, (M, D))[2]
+    w_type = _vector(weight, "weight", own if h.dtype is f32 else {h.dtype: x_type, f32: GEMM_F32}, D, index)
+    _vector(rstd, "rstd", {f32: GEMM_F32}, M, index)
+    dhp, lddh = None, 0
+    if dh is not None:
+        lddh = _matrix(dh, "dh", own, index, (M, D))[2]
+        dhp = dh.data_ptr()
+    if dx_out is None:
+        lddx = D
+    else:
+        lddx = _matrix(dx_out, "dx_out", own, index, (M, D))[2]
+    handle = _handle(index)
+    if dx_out is None:
+        dx_out = new((M, D), (D, 1), dtype=h.dtype, device=device)
+    dw = new((D,), (1,), dtype=f32, device=device)
+    # a workspace of this call's own: it belongs to the stream (and to the graph, under capture)
     nbytes = _L.gemm_rms_backward_workspace(M, D)
-
-    def enqueue(raw):
-        dx = torch.empty((M, D), dtype=h.dtype, device=device) if dx_out is None else dx_out
-        dw = torch.empty((D,), dtype=torch.float32, device=device)
-        # a workspace of this call's own: it belongs to the stream (and to the graph, under capture)
-        ws = torch.empty((nbytes,), dtype=torch.uint8, device=device)
-        _check(_L.gemm_rms_backward(handle, M, D, types["float"][h.dtype], types["float"][weight.dtype], dy.data_ptr(),
-                                    _ld(dy), h.data_ptr(), _ld(h), weight.data_ptr(), rstd.data_ptr(),
-                                    None if dh is None else dh.data_ptr(), 0 if dh is None else _ld(dh),
-                                    dx.data_ptr(), _ld(dx), dw.data_ptr(), ws.data_ptr(), nbytes, raw),
-               "gemm_rms_backward")
-        return dx, dw
-
-    return _call(stream, device, enqueue)
+    ws = new((nbytes,), (1,), dtype=_T["uint8"], device=device)
+    rc = _L.gemm_rms_backward(handle, M, D, x_type, w_type, dy.data_ptr(), lddy, h.data_ptr(), ldh, weight.data_ptr(),
+                              rstd.data_ptr(), dhp, lddh, dx_out.data_ptr(), lddx, dw.data_ptr(), ws.data_ptr(), nbytes,
+                              types["raw stream"](index))
+    if rc != GEMM_OK:
+        raise GemmError(rc, "gemm_rms_backward")
+    return dx_out, dw
 
 
 class Gemm:

@@ -52,25 +52,42 @@ struct Staged {
         return s.ragged ? (t == 0 ? s.KB - 1 : t - 1) : t;
     }
 
-    // Loads of K-tile t into its slot.  One at or past KB moves nothing
-    // (every offset is out of range: zeros into a slot no later tile reads),
-    // so the number of loads in flight is the same at each boundary.
+    // Where the loads of K-tile t go and start.  One at or past KB moves
+    // nothing (every offset is out of range: zeros into a slot no later tile
+    // reads), so the number of loads in flight is the same at each boundary.
+    struct Issue {
+        uint8_t PG_LDS* base;
+        uint32_t so, ss;                     // byte offsets of the K-tile, and of its scales
+        uint32_t out;                        // the out-of-range bit for chunks past K
+    };
+    template <bool FIRST>
+    __device__ static __forceinline__ Issue start(const State& s, uint8_t PG_LDS* smem, int t, int slot) {
+        const int kb = block_of(s, t);
+        Issue x;
+        x.base = smem + slot * SLOT;
+        x.so = __builtin_amdgcn_readfirstlane(t < s.KB ? (uint32_t)kb * kBlock : kOutside);
+        x.ss = __builtin_amdgcn_readfirstlane(t < s.KB ? (uint32_t)kb * s.s_blk : kOutside);
+        x.out = FIRST && kb * kBlock + s.kc >= s.K ? kOutside : 0u;
+        return x;
+    }
+    // Load q of a K-tile's LPT: chunks of A, chunks of B, then the scales.
+    __device__ static __forceinline__ void load(const State& s, const Issue& x, int q) {
+        if (q < LA)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(s.ra, (void PG_LDS*)(x.base + (q * T + 64 * s.wave) * kChunk), 16,
+                                                     s.offa[q] | x.out, x.so, 0, 0);
+        else if (q < LA + LB)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                s.rb, (void PG_LDS*)(x.base + A_BYTES + ((q - LA) * T + 64 * s.wave) * kChunk), 16,
+                s.offb[q - LA] | x.out, x.so, 0, 0);
+        else
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(s.rs, (void PG_LDS*)(x.base + S_OFF + 256 * s.wave), 4, s.offs,
+                                                     x.ss, 0, 0);
+    }
     template <bool FIRST>
     __device__ static __forceinline__ void issue(const State& s, uint8_t PG_LDS* smem, int t, int slot) {
-        const int kb = block_of(s, t);
-        uint8_t PG_LDS* base = smem + slot * SLOT;
-        const uint32_t so = __builtin_amdgcn_readfirstlane(t < s.KB ? (uint32_t)kb * kBlock : kOutside);
-        const uint32_t ss = __builtin_amdgcn_readfirstlane(t < s.KB ? (uint32_t)kb * s.s_blk : kOutside);
-        const uint32_t out = FIRST && kb * kBlock + s.kc >= s.K ? kOutside : 0u;   // chunks past K
+        const Issue x = start<FIRST>(s, smem, t, slot);
 #pragma unroll
-        for (int j = 0; j < LA; ++j)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(s.ra, (void PG_LDS*)(base + (j * T + 64 * s.wave) * kChunk), 16,
-                                                     s.offa[j] | out, so, 0, 0);
-#pragma unroll
-        for (int j = 0; j < LB; ++j)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(s.rb, (void PG_LDS*)(base + A_BYTES + (j * T + 64 * s.wave) * kChunk),
-                                                     16, s.offb[j] | out, so, 0, 0);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(s.rs, (void PG_LDS*)(base + S_OFF + 256 * s.wave), 4, s.offs, ss, 0, 0);
+        for (int q = 0; q < LPT; ++q) load(s, x, q);
     }
 
     // K not a multiple of 16: the bytes at and past K of the chunk that holds
@@ -159,43 +176,80 @@ struct Staged {
             clear_tail(s, smem);
             barrier();
         }
+        // The K loop, one unit per 16x16 piece of the wave's block.  A unit
+        // issues its matrix instruction, then adds the sum that the unit LAG
+        // before it left (so the instruction's latency passes under the
+        // others'), then its share of the next fragment's LDS reads and of
+        // the next K-tile's loads; a fence keeps that order.  The last LAG
+        // sums of a K-tile are added under the next one's first reads.
+        constexpr int NU = FM * FN, LAG = NU > 3 ? 3 : 1, RING = LAG + 1;
+        f32x4 sum[RING];                     // sums not added yet: unit u's in u % RING
+        f32x4 sbv[SBROW ? FN : 1];
+        float sa[FM];
+#pragma unroll
+        for (int q = 0; q < RING; ++q) sum[q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int j = 0; j < (SBROW ? FN : 1); ++j) sbv[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < FM; ++i) sa[i] = 0.0f;
+        auto add = [&](int u) {
+            const int i = u / FN, j = u % FN;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                acc[i][j][e] = fmaf(sum[u % RING][e], SBROW ? sa[i] * sbv[SBROW ? j : 0][e] : sa[i], acc[i][j][e]);
+        };
+        static_assert(NU % RING == 0, "units of the next K-tile start at ring slot 0");
         int slot = 0;
         for (int t = 0; t < s.KB; ++t) {
             const int free_slot = slot == 0 ? SLOTS - 1 : slot - 1;
-            issue<false>(s, smem, t + SLOTS - 1, free_slot);
+            const Issue next = start<false>(s, smem, t + SLOTS - 1, free_slot);
             const uint8_t PG_LDS* ta = smem + slot * SLOT + wm * WTM * kBlock;
             const uint8_t PG_LDS* tb = smem + slot * SLOT + A_BYTES + wn * WTN * kBlock;
-            const float PG_LDS* sa = (const float PG_LDS*)(smem + slot * SLOT + S_OFF) + wm * WTM;
-            const float PG_LDS* sb = (const float PG_LDS*)(smem + slot * SLOT + S_OFF) + BM + wn * WTN;
+            const float PG_LDS* psa = (const float PG_LDS*)(smem + slot * SLOT + S_OFF) + wm * WTM;
+            const float PG_LDS* psb = (const float PG_LDS*)(smem + slot * SLOT + S_OFF) + BM + wn * WTN;
             Frag<BT, EXACT> fb[FN];
+            Frag<AT, EXACT> fa[2];
+            auto read_a = [&](int i) {
+                return fragment<AT, EXACT>(chunk(ta, i * 16 * kBlock + rd0), chunk(ta, i * 16 * kBlock + rd1));
+            };
+            fa[0] = read_a(0);
 #pragma unroll
             for (int j = 0; j < FN; ++j)
                 fb[j] = fragment<BT, EXACT>(chunk(tb, j * 16 * kBlock + rd0), chunk(tb, j * 16 * kBlock + rd1));
-            f32x4 sbv[SBROW ? FN : 1];
+            float sa_next[FM], sb_next = 0.0f;
+            f32x4 sbv_next[SBROW ? FN : 1];
+#pragma unroll
+            for (int i = 0; i < FM; ++i) sa_next[i] = psa[16 * i + r];
             if constexpr (SBROW) {
 #pragma unroll
-                for (int j = 0; j < FN; ++j) sbv[j] = *(const f32x4 PG_LDS*)(sb + 16 * j + 4 * g);
+                for (int j = 0; j < FN; ++j) sbv_next[j] = *(const f32x4 PG_LDS*)(psb + 16 * j + 4 * g);
             } else {
-                sbv[0][0] = sb[0];
+                sb_next = psb[0];
+            }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int u = NU - LAG; u < NU; ++u) add(u);      // the K-tile before's last
+#pragma unroll
+            for (int i = 0; i < FM; ++i) sa[i] = SBROW ? sa_next[i] : sa_next[i] * sb_next;
+            if constexpr (SBROW) {
+#pragma unroll
+                for (int j = 0; j < FN; ++j) sbv[j] = sbv_next[j];
             }
 #pragma unroll
-            for (int i = 0; i < FM; ++i) {
-                const Frag<AT, EXACT> fa =
-                    fragment<AT, EXACT>(chunk(ta, i * 16 * kBlock + rd0), chunk(ta, i * 16 * kBlock + rd1));
-                const float sai = sa[16 * i + r];
-                const float sc = SBROW ? sai : sai * sbv[0][0];
-#pragma unroll
-                for (int j = 0; j < FN; ++j) {
-                    const f32x4 v = block_sum<AT, BT, EXACT>(fb[j], fa);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        acc[i][j][e] = fmaf(v[e], SBROW ? sc * sbv[j][e] : sc, acc[i][j][e]);
-                }
+            for (int u = 0; u < NU; ++u) {
+                const int i = u / FN, j = u % FN;
+                sum[u % RING] = block_sum<AT, BT, EXACT>(fb[j], fa[i & 1]);
+                if (u >= LAG) add(u - LAG);
+                if (j == 0 && i + 1 < FM) fa[(i + 1) & 1] = read_a(i + 1);
+                if (u < LPT) load(s, next, u);
+                __builtin_amdgcn_sched_barrier(0);
             }
             wait_loads<(SLOTS - 2) * LPT>();   // K-tile t + 1 has landed (this wave's part)
             barrier();                         // ... everyone's, and slot t is free
             slot = slot + 1 == SLOTS ? 0 : slot + 1;
         }
+#pragma unroll
+        for (int u = NU - LAG; u < NU; ++u) add(u);
         wait_loads<0>();                       // no write into LDS outlives the workgroup
 
 #pragma unroll
