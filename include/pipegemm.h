@@ -355,12 +355,12 @@ int gemm_occupancy(gemm_handle_t h, int64_t M, int64_t N, int64_t K, int dtype, 
  * inputs or one another, but where stated.  Sizes of zero are accepted. */
 enum { GEMM_E4M3 = 16, GEMM_E5M2 = 17 };
 
-/* Part of C that one workgroup of gemm_run_fp8 computes.  The first two stage
- * operands through LDS and need rows that start on 16 bytes; the others take
- * any address.  GEMM_FP8_TILE_AUTO: the largest one that the call's rows fill at
- * least half and that gives every compute unit a workgroup. */
+/* Part of C that one workgroup of gemm_run_fp8 computes.  Those down to
+ * 64x32 stage operands through LDS and need rows that start on 16 bytes; the
+ * others take any address.  GEMM_FP8_TILE_AUTO: the one that takes the least time
+ * by what each cost in measurements. */
 enum { GEMM_FP8_TILE_AUTO = -1, GEMM_FP8_TILE_256x256 = 0, GEMM_FP8_TILE_128x128 = 1, GEMM_FP8_TILE_64x64 = 2,
-       GEMM_FP8_TILE_64x32 = 3, GEMM_FP8_TILE_32x32 = 4, GEMM_FP8_TILE_16x16 = 5 };
+       GEMM_FP8_TILE_64x32 = 3, GEMM_FP8_TILE_32x32 = 4, GEMM_FP8_TILE_16x32 = 5, GEMM_FP8_TILE_16x16 = 6 };
 
 typedef struct {
     int32_t tile;        /* GEMM_FP8_TILE_* chosen */

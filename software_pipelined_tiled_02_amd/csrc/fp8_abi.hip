@@ -26,7 +26,7 @@ struct Plan {
     gemm_fp8_info_t info;
     const void* fn;
     int64_t tiles_m, tiles_n;
-    bool vec_c;
+    bool vec_c, vec16_c;
 };
 
 // Every check of the product, then its kernel.  No HIP call.
@@ -59,15 +59,19 @@ int plan_product(int64_t M, int64_t N, int64_t K, int a_type, int b_type, int c_
         if (!pg::fp8_staged(t)) return pg::fp8_stream_kernel(t, at, bt, b_scale_rows == 1, exact, bytes);
         return rows16 ? pg::fp8_staged_kernel(t, at, bt, b_scale_rows == 1, exact) : nullptr;
     };
-    // The largest tile that is at least half full of rows and still gives
-    // every CU a workgroup.
+    // The class that takes the least time by the measured costs.
     int tc = tile;
     if (tc == GEMM_FP8_TILE_AUTO) {
-        tc = pg::FP8_TILE_16;
+        double best = 0.0;
         for (int t = 0; t < pg::FP8_TILE_COUNT; ++t) {
+            if (kernel(t) == nullptr) continue;
             const pg::Fp8Shape sh = pg::fp8_shape(t);
-            if (kernel(t) == nullptr || sh.bm >= 2 * M) continue;
-            if (ceil_div(M, sh.bm) * ceil_div(N, sh.bn) >= num_cus) { tc = t; break; }
+            const double time =
+                pg::fp8_time(t, exact, ceil_div(M, sh.bm) * ceil_div(N, sh.bn), ceil_div(K, kBlock), num_cus);
+            if (tc == GEMM_FP8_TILE_AUTO || time < best) {
+                tc = t;
+                best = time;
+            }
         }
     }
     plan->fn = kernel(tc);
@@ -85,6 +89,7 @@ int plan_product(int64_t M, int64_t N, int64_t K, int a_type, int b_type, int c_
     const int64_t grid = plan->tiles_m * plan->tiles_n;
     if (grid >= ((int64_t)1 << 32) / (64 * sh.waves)) return GEMM_ERR_UNSUPPORTED;
     plan->vec_c = aligned(C, 4 * size_of(c_dtype)) && ldc % 4 == 0;
+    plan->vec16_c = aligned(C, 16) && ldc * size_of(c_dtype) % 16 == 0;
     gemm_fp8_info_t& in = plan->info;
     memset(&in, 0, sizeof in);
     in.tile = tc;
@@ -146,6 +151,7 @@ int gemm_run_fp8(gemm_handle_t h, int64_t M, int64_t N, int64_t K, int a_type, i
     a.c_type = c_dtype;
     a.accumulate = accumulate;
     a.vec_c = plan.vec_c;
+    a.vec16_c = plan.vec16_c;
     void* kargs[] = {&a};
     return pg::on_device(h, [&] {
         const hipError_t e = hipLaunchKernel(plan.fn, dim3((unsigned)plan.info.grid), dim3((unsigned)plan.info.threads),

@@ -46,23 +46,53 @@ struct Fp8Args {
     int32_t c_type;          // XT_*
     int32_t accumulate;      // C += (fp32)
     int32_t vec_c;           // four neighbouring outputs are one aligned store
+    int32_t vec16_c;         // C's rows start on 16 bytes
 };
 
-// Tile classes: the workgroup's part of C, and the waves that share its K.
+// Tile classes: the workgroup's part of C, its waves, and how many of them
+// share each piece of C, every one with blocks of K of its own.
 enum Fp8Tile : int { FP8_TILE_256 = 0, FP8_TILE_128 = 1, FP8_TILE_64 = 2, FP8_TILE_64x32 = 3, FP8_TILE_32 = 4,
-                     FP8_TILE_16 = 5, FP8_TILE_COUNT = 6 };
+                     FP8_TILE_16x32 = 5, FP8_TILE_16 = 6, FP8_TILE_COUNT = 7 };
 struct Fp8Shape { int bm, bn, waves, wk; };
 constexpr Fp8Shape fp8_shape(int t) {
     return t == FP8_TILE_256 ? Fp8Shape{256, 256, 8, 1}
-         : t == FP8_TILE_128 ? Fp8Shape{128, 128, 4, 1}
-         : t == FP8_TILE_64 ? Fp8Shape{64, 64, 8, 8}
-         : t == FP8_TILE_64x32 ? Fp8Shape{64, 32, 8, 8}
+         : t == FP8_TILE_128 ? Fp8Shape{128, 128, 8, 1}
+         : t == FP8_TILE_64 ? Fp8Shape{64, 64, 4, 1}
+         : t == FP8_TILE_64x32 ? Fp8Shape{64, 32, 4, 1}
          : t == FP8_TILE_32 ? Fp8Shape{32, 32, 8, 8}
-                            : Fp8Shape{16, 16, 16, 16};
+         : t == FP8_TILE_16x32 ? Fp8Shape{16, 32, 8, 8}
+                               : Fp8Shape{16, 16, 16, 16};
 }
 // Tiles staged through LDS (whole 16-byte chunks); the others read operands
 // straight into registers.
-constexpr bool fp8_staged(int t) { return t == FP8_TILE_256 || t == FP8_TILE_128; }
+constexpr bool fp8_staged(int t) { return t <= FP8_TILE_64x32; }
+
+// What a tile class costs, for the choice between them: workgroups a CU holds
+// at a time, and microseconds per block of 128 of a round of workgroups that
+// gives no CU more than one (`some`) or fills every CU (`all`), and per round
+// besides.  Measured on an MI355X with operands in the caches, at N = 4096
+// and M = 1 to 4096, K = 1024 and 4096 (fp32 outputs, whose blocks cost about
+// twice the time, at 1024^2 x 4096 and 4096^2 x 8200); microseconds there by
+// the class chosen and the next best:
+//   M = 128: 64x32 9.8, 64x64 11.4         M = 512: 64x64 17.6, 128x128 19.5
+//   M = 640: 128x128 19.9, 64x64 25.1      M = 1024: 128x128 24.0, 64x64 31.4
+//   M = 1536: 128x128 39.8, 256x256 45.0   M = 2560: 256x256 46.4, 128x128 61.5
+struct Fp8Cost { int per_cu; double some, all, round; };
+constexpr Fp8Cost fp8_cost(int t, bool exact) {
+    return t == FP8_TILE_256 ? Fp8Cost{1, 1.30, 1.65, 6.0}
+         : t == FP8_TILE_128 ? (exact ? Fp8Cost{1, 1.00, 1.16, 4.0} : Fp8Cost{1, 0.50, 0.60, 4.0})
+         : t == FP8_TILE_64 ? (exact ? Fp8Cost{2, 0.45, 0.78, 2.5} : Fp8Cost{2, 0.24, 0.42, 2.5})
+         : t == FP8_TILE_64x32 ? (exact ? Fp8Cost{2, 0.30, 0.55, 2.5} : Fp8Cost{2, 0.19, 0.28, 2.5})
+         : t == FP8_TILE_32 ? Fp8Cost{2, 0.20, 0.30, 2.5}
+         : t == FP8_TILE_16x32 ? Fp8Cost{2, 0.15, 0.27, 2.5}
+                               : Fp8Cost{2, 0.12, 0.21, 2.5};
+}
+constexpr double fp8_time(int t, bool exact, int64_t workgroups, int64_t blocks, int64_t cus) {
+    const Fp8Cost c = fp8_cost(t, exact);
+    const int64_t slots = cus * c.per_cu, full = workgroups / slots, rest = workgroups % slots;
+    const double last = rest == 0 ? 0.0 : rest <= cus ? c.some : c.all;
+    return blocks * (full * c.all + last) + (full + (rest > 0 ? 1 : 0)) * c.round;
+}
 
 // The kernel for a call: a_type, b_type, row scales of B, fp32 output, and
 // (register-fed tiles) rows that do not start or end on 16 bytes.
@@ -87,6 +117,22 @@ constexpr uint32_t kOutside = 0x80000000u;
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_at(const void* p) {
     return __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, 0x7fffffff, kBufferWord3);
+}
+
+// At most N of this wave's loads are still in flight (vmcnt; loads retire in order).
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+    static_assert(N >= 0 && N < 64, "vmcnt range");
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
+    asm volatile("" ::: "memory");
+}
+// Barrier behind this wave's LDS accesses.
+__device__ __forceinline__ void barrier() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4) | (0 << 8));
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
 }
 
 // Eight 8-bit floats (two words) as bf16, exactly.
@@ -139,6 +185,16 @@ __device__ __forceinline__ f32x4 block_sum(const Frag<BT, EXACT>& x, const Frag<
     return t;
 }
 
+// Four values rounded to bf16 or fp16 (nearest even).
+__device__ __forceinline__ i32x2 to_16(f32x4 v, int type) {
+    if (type == XT_BF16)
+        return i32x2{__builtin_bit_cast(int, bf16x2{(__bf16)v[0], (__bf16)v[1]}),
+                     __builtin_bit_cast(int, bf16x2{(__bf16)v[2], (__bf16)v[3]})};
+    typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+    return i32x2{__builtin_bit_cast(int, f16x2{(_Float16)v[0], (_Float16)v[1]}),
+                 __builtin_bit_cast(int, f16x2{(_Float16)v[2], (_Float16)v[3]})};
+}
+
 // C[m][n .. n+3], rounded once to C's type; columns at or past N are left.
 template <bool EXACT>
 __device__ __forceinline__ void store_c(const Fp8Args& a, int64_t m, int64_t n, f32x4 v) {
@@ -154,21 +210,66 @@ __device__ __forceinline__ void store_c(const Fp8Args& a, int64_t m, int64_t n, 
         }
     } else {
         uint16_t* p = (uint16_t*)a.C + m * a.ldc + n;
-        i32x2 w;
-        if (a.c_type == XT_BF16) {
-            w = i32x2{__builtin_bit_cast(int, bf16x2{(__bf16)v[0], (__bf16)v[1]}),
-                      __builtin_bit_cast(int, bf16x2{(__bf16)v[2], (__bf16)v[3]})};
-        } else {
-            typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
-            w = i32x2{__builtin_bit_cast(int, f16x2{(_Float16)v[0], (_Float16)v[1]}),
-                      __builtin_bit_cast(int, f16x2{(_Float16)v[2], (_Float16)v[3]})};
-        }
+        const i32x2 w = to_16(v, a.c_type);
         if (a.vec_c && n + 4 <= a.N) {
             *(i32x2*)p = w;
         } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 if (n + e < a.N) p[e] = (uint16_t)((uint32_t)w[e >> 1] >> (16 * (e & 1)));
+        }
+    }
+}
+
+// The epilogue's LDS: per wave, two strips of 16 rows of its block of C, each
+// row padded by 16 bytes (so that the rows of a column fall in different banks).
+constexpr int strip_row(int fn, int size) { return 16 * fn * size + 16; }
+constexpr int epilogue_lds(int waves, int fn, int size) { return waves * 2 * 16 * strip_row(fn, size); }
+
+// A wave's block of FM x FN pieces at (m0, n0).  A lane holds 4 neighbouring
+// columns, 8 or 16 bytes, of a row; stored like that, an instruction would
+// write 32-byte runs of 16 rows.  A strip of 16 rows goes through the wave's
+// own part of LDS instead and leaves 16 bytes per lane, whole rows of the block
+// at a time (256x256 tiles, 4096^3: 4 us less, at 8192^3 30 us less of 490).
+// STREAM: past the caches (C is far larger than they are).
+template <bool EXACT, int FM, int FN, bool STREAM>
+__device__ __forceinline__ void store_block(const Fp8Args& a, uint8_t PG_LDS* smem, int wave, int m0, int n0,
+                                            const f32x4 (&acc)[FM][FN]) {
+    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+    constexpr int SIZE = EXACT ? 4 : 2, ROW = strip_row(FN, SIZE), CHUNKS = FN * SIZE;   // 16-byte chunks of a row
+    if (a.vec16_c && m0 + 16 * FM <= a.M && n0 + 16 * FN <= a.N) {
+        uint8_t PG_LDS* strips = smem + wave * 2 * 16 * ROW;
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+            uint8_t PG_LDS* strip = strips + (i & 1) * 16 * ROW;
+#pragma unroll
+            for (int j = 0; j < FN; ++j) {
+                uint8_t PG_LDS* p = strip + r * ROW + (16 * j + 4 * g) * SIZE;
+                if constexpr (EXACT) *(f32x4 PG_LDS*)p = acc[i][j];
+                else *(i32x2 PG_LDS*)p = to_16(acc[i][j], a.c_type);
+            }
+#pragma unroll
+            for (int q = 0; q < (16 * CHUNKS + 63) / 64; ++q) {
+                const int row = (q * 64 + lane) / CHUNKS, c = (q * 64 + lane) % CHUNKS;
+                if (row >= 16) break;
+                i32x4 v = *(const i32x4 PG_LDS*)(strip + row * ROW + c * 16);
+                i32x4* dst = (i32x4*)((uint8_t*)a.C + ((int64_t)(m0 + 16 * i + row) * a.ldc + n0) * SIZE + c * 16);
+                if constexpr (EXACT)
+                    if (a.accumulate) v = __builtin_bit_cast(i32x4, __builtin_bit_cast(f32x4, v) + *(const f32x4*)dst);
+                if constexpr (STREAM) __builtin_nontemporal_store(v, dst);
+                else *dst = v;
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+        const int64_t m = m0 + 16 * i + r;
+        if (m >= a.M) continue;
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+            const int64_t n = n0 + 16 * j + 4 * g;
+            if (n < a.N) store_c<EXACT>(a, m, n, acc[i][j]);
         }
     }
 }

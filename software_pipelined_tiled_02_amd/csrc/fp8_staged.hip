@@ -10,21 +10,6 @@ namespace pg {
 
 namespace {
 
-template <int N>
-__device__ __forceinline__ void wait_loads() {
-    static_assert(N >= 0 && N < 64, "vmcnt range");
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
-    asm volatile("" ::: "memory");
-}
-// Barrier behind this wave's LDS accesses.
-__device__ __forceinline__ void barrier() {
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4) | (0 << 8));
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-}
-
 template <int AT, int BT, bool SBROW, bool EXACT, int BM, int BN, int WM, int WN, int SLOTS>
 struct Staged {
     static constexpr int T = WM * WN * 64;
@@ -33,11 +18,12 @@ struct Staged {
     static constexpr int LA = BM * CPR / T, LB = BN * CPR / T;   // chunks per lane and K-tile
     static constexpr int LPT = LA + LB + 1;                      // loads per lane and K-tile, one of them scales
     static constexpr int A_BYTES = BM * kBlock, B_BYTES = BN * kBlock, S_OFF = A_BYTES + B_BYTES;
-    static constexpr int SLOT = S_OFF + (BM + BN) * 4;
-    static constexpr int LDS = SLOTS * SLOT;
-    static_assert(BM + BN == T, "one scale per lane");
+    static constexpr int SLOT = S_OFF + T * 4;
+    static constexpr int LDS = max3(SLOTS * SLOT, epilogue_lds(WM * WN, FN, EXACT ? 4 : 2), 0);
+    static_assert(BM + BN <= T && BM % 64 == 0, "a scale per lane, whole waves of A's");
     static_assert(LDS <= kLdsBudget, "LDS");
-    static_assert(WTN <= kBlock && kBlock % WTN == 0 && BN % kBlock == 0, "a wave's columns share a tile scale");
+    static_assert(WTN <= kBlock && kBlock % WTN == 0 && (BN % kBlock == 0 || kBlock % BN == 0),
+                  "a wave's columns share a tile scale");
 
     struct State {
         __amdgpu_buffer_rsrc_t ra, rb, rs;
@@ -95,6 +81,7 @@ struct Staged {
     __device__ static __forceinline__ void clear_tail(const State& s, uint8_t PG_LDS* smem) {
         const int k = s.K % kBlock, c = k / 16, keep = k % 16;
         const int row = threadIdx.x;         // one row per lane: A's, then B's
+        if (row >= BM + BN) return;
         i32x4 PG_LDS* p = (i32x4 PG_LDS*)(smem + (row * CPR + (c ^ swz(CPR, row))) * kChunk);
         i32x4 v = *p;
 #pragma unroll
@@ -143,14 +130,14 @@ struct Staged {
             const int row = (j * T + tid) / CPR;
             s.offb[j] = (uint32_t)(n0 + row < a.N ? row : 0) * (uint32_t)a.ldb + c * kChunk;
         }
-        // Scales: lane i < BM takes row i of A, lane BM + j column j (whole
-        // waves either way).
+        // Scales: lane i < BM takes row i of A, lane BM + j column j (lanes
+        // past them column 0's again, so that every wave issues one load).
         if (s.wave < BM / 64) {
             s.rs = buffer_at(a.SA + (int64_t)m0 * a.sa_row);
             s.offs = (uint32_t)(m0 + tid < a.M ? tid : 0) * (uint32_t)(a.sa_row * 4);
             s.s_blk = (uint32_t)(a.sa_blk * 4);
         } else {
-            const int col = tid - BM, n = n0 + col < a.N ? col : 0;
+            const int col = tid - BM, n = col < BN && n0 + col < a.N ? col : 0;
             s.rs = buffer_at(a.SB + (int64_t)(SBROW ? n0 : n0 / kBlock) * a.sb_row);
             s.offs = (uint32_t)(SBROW ? n : n / kBlock) * (uint32_t)(a.sb_row * 4);
             s.s_blk = (uint32_t)(a.sb_blk * 4);
@@ -183,6 +170,7 @@ struct Staged {
         // the next K-tile's loads; a fence keeps that order.  The last LAG
         // sums of a K-tile are added under the next one's first reads.
         constexpr int NU = FM * FN, LAG = NU > 3 ? 3 : 1, RING = LAG + 1;
+        constexpr int PER = (LPT + NU - 1) / NU;         // loads per unit, from the first on
         f32x4 sum[RING];                     // sums not added yet: unit u's in u % RING
         f32x4 sbv[SBROW ? FN : 1];
         float sa[FM];
@@ -241,7 +229,8 @@ struct Staged {
                 sum[u % RING] = block_sum<AT, BT, EXACT>(fb[j], fa[i & 1]);
                 if (u >= LAG) add(u - LAG);
                 if (j == 0 && i + 1 < FM) fa[(i + 1) & 1] = read_a(i + 1);
-                if (u < LPT) load(s, next, u);
+#pragma unroll
+                for (int q = u * PER; q < (u + 1) * PER && q < LPT; ++q) load(s, next, q);
                 __builtin_amdgcn_sched_barrier(0);
             }
             wait_loads<(SLOTS - 2) * LPT>();   // K-tile t + 1 has landed (this wave's part)
@@ -250,18 +239,9 @@ struct Staged {
         }
 #pragma unroll
         for (int u = NU - LAG; u < NU; ++u) add(u);
-        wait_loads<0>();                       // no write into LDS outlives the workgroup
-
-#pragma unroll
-        for (int i = 0; i < FM; ++i) {
-            const int64_t m = m0 + wm * WTM + 16 * i + r;
-            if (m >= a.M) continue;
-#pragma unroll
-            for (int j = 0; j < FN; ++j) {
-                const int64_t n = n0 + wn * WTN + 16 * j + 4 * g;
-                if (n < a.N) store_c<EXACT>(a, m, n, acc[i][j]);
-            }
-        }
+        wait_loads<0>();                       // no write into LDS outlives the K loop,
+        barrier();                             // whose slots the epilogue takes
+        store_block<EXACT, FM, FN, BM == 256>(a, smem, s.wave, m0 + wm * WTM, n0 + wn * WTN, acc);
     }
 };
 
@@ -272,17 +252,24 @@ __global__ void __launch_bounds__(WM * WN * 64) fp8_staged_tile(Fp8Args a) {
     S::run(a, (uint8_t PG_LDS*)smem);
 }
 
+// Waves and slots of each tile class.  More slots than two hide the memory's
+// latency where a K-tile is multiplied in less time than it takes to arrive.
+template <int AT, int BT, bool SBROW, bool EXACT>
+const void* by_tile(int tile) {
+    switch (tile) {
+    case FP8_TILE_256:
+        if constexpr (EXACT) return nullptr;     // the widened fragments leave no registers for 128 accumulators
+        else return (const void*)&fp8_staged_tile<AT, BT, SBROW, EXACT, 256, 256, 2, 4, 2>;
+    case FP8_TILE_128: return (const void*)&fp8_staged_tile<AT, BT, SBROW, EXACT, 128, 128, 2, 4, 4>;
+    case FP8_TILE_64: return (const void*)&fp8_staged_tile<AT, BT, SBROW, EXACT, 64, 64, 2, 2, 4>;
+    case FP8_TILE_64x32: return (const void*)&fp8_staged_tile<AT, BT, SBROW, EXACT, 64, 32, 2, 2, 6>;
+    default: return nullptr;
+    }
+}
 template <int AT, int BT>
 const void* by_mode(int tile, bool sb_rows, bool exact) {
-    if (tile == FP8_TILE_256 && !exact)
-        return sb_rows ? (const void*)&fp8_staged_tile<AT, BT, true, false, 256, 256, 2, 4, 2>
-                       : (const void*)&fp8_staged_tile<AT, BT, false, false, 256, 256, 2, 4, 2>;
-    if (tile != FP8_TILE_128) return nullptr;
-    if (exact)
-        return sb_rows ? (const void*)&fp8_staged_tile<AT, BT, true, true, 128, 128, 2, 2, 2>
-                       : (const void*)&fp8_staged_tile<AT, BT, false, true, 128, 128, 2, 2, 2>;
-    return sb_rows ? (const void*)&fp8_staged_tile<AT, BT, true, false, 128, 128, 2, 2, 2>
-                   : (const void*)&fp8_staged_tile<AT, BT, false, false, 128, 128, 2, 2, 2>;
+    if (sb_rows) return exact ? by_tile<AT, BT, true, true>(tile) : by_tile<AT, BT, true, false>(tile);
+    return exact ? by_tile<AT, BT, false, true>(tile) : by_tile<AT, BT, false, false>(tile);
 }
 
 }  // namespace

@@ -29,6 +29,7 @@ struct Stream {
         uint32_t offsa[MB], offsb[SBROW ? NB : 1][SBROW ? 4 : 1];
         uint32_t sa_blk, sb_blk;           // bytes from one block's scale to the next
         int K, KB, kc;                     // kc: first k of the lane's first chunk
+        int rot;                           // the block that is multiplied first
     };
 
     // 16 bytes of a row from k on, of which only those before K are read:
@@ -49,8 +50,10 @@ struct Stream {
         return v;
     }
 
-    // Block kb; one at or past KB gives zeros, scales too.
-    __device__ static __forceinline__ void load(const State& s, Block& x, int kb) {
+    // The k-th block in the order they are multiplied; one at or past KB gives
+    // zeros, scales too.
+    __device__ static __forceinline__ void load(const State& s, Block& x, int k) {
+        const int kb = k >= s.KB ? k : k + s.rot >= s.KB ? k + s.rot - s.KB : k + s.rot;
         const uint32_t soff = __builtin_amdgcn_readfirstlane((uint32_t)kb * kBlock);
         const int rem = s.K - (kb * kBlock + s.kc);        // bytes of the row from the lane's first chunk on
         if (BYTES && kb == s.KB - 1) {
@@ -121,6 +124,9 @@ struct Stream {
         s.K = a.K;
         s.KB = (a.K + kBlock - 1) / kBlock;
         s.kc = 16 * g;
+        // XCD x starts at block 9 x: with every row read at the same k, the
+        // rows' equal distances would gather the reads on a few channels.
+        s.rot = s.KB > 0 ? (int)((blockIdx.x & 7) * 9u % (unsigned)s.KB) : 0;
         s.ra = buffer_at(a.A + (int64_t)m0 * a.lda);
         s.rb = buffer_at(a.B + (int64_t)n0 * a.ldb);
         s.rsa = buffer_at(a.SA + (int64_t)m0 * a.sa_row);
@@ -155,19 +161,30 @@ struct Stream {
 #pragma unroll
             for (int j = 0; j < NB; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-        // Two blocks in flight: the next one's loads are issued before the
-        // current one is multiplied.
-        Block x, y;
-        int kb = wave;
-        load(s, x, kb);
-        while (kb < s.KB) {
-            load(s, y, kb + WK);
-            add(x, acc);
-            kb += WK;
-            if (kb >= s.KB) break;
-            load(s, x, kb + WK);
-            add(y, acc);
-            kb += WK;
+        if constexpr (BYTES) {
+            Block x;
+            for (int k = wave; k < s.KB; k += WK) {
+                load(s, x, k);
+                add(x, acc);
+            }
+        } else {
+            // Two blocks in flight: the next one's loads are issued before the
+            // current one is multiplied (the fences keep the compiler from
+            // moving them next to their use).  Three and four were slower: the
+            // registers they take cost waves (1x1024x8192: 7.5, 8.2, 8.6 us).
+            Block x[2];
+            load(s, x[0], wave);
+            for (int k = wave; k < s.KB;) {
+#pragma unroll
+                for (int d = 0; d < 2; ++d) {
+                    if (d > 0 && k >= s.KB) break;
+                    load(s, x[d ^ 1], k + WK);
+                    __builtin_amdgcn_sched_barrier(0);
+                    add(x[d], acc);
+                    __builtin_amdgcn_sched_barrier(0);
+                    k += WK;
+                }
+            }
         }
 
         // Partial sums to LDS, [wave][piece][lane]; then each thread adds
@@ -197,9 +214,8 @@ __global__ void __launch_bounds__(64 * WK) fp8_stream(Fp8Args a) {
 template <int AT, int BT, bool SBROW, bool EXACT, bool BYTES>
 const void* by_tile(int tile) {
     switch (tile) {
-    case FP8_TILE_64: return (const void*)&fp8_stream<AT, BT, SBROW, EXACT, BYTES, 4, 4, 8>;
-    case FP8_TILE_64x32: return (const void*)&fp8_stream<AT, BT, SBROW, EXACT, BYTES, 4, 2, 8>;
     case FP8_TILE_32: return (const void*)&fp8_stream<AT, BT, SBROW, EXACT, BYTES, 2, 2, 8>;
+    case FP8_TILE_16x32: return (const void*)&fp8_stream<AT, BT, SBROW, EXACT, BYTES, 1, 2, 8>;
     case FP8_TILE_16: return (const void*)&fp8_stream<AT, BT, SBROW, EXACT, BYTES, 1, 1, 16>;
     default: return nullptr;
     }

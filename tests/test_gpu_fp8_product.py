@@ -9,7 +9,7 @@ from tests.fp8_util import F8, FT, check_product, f8_of, operand, place_bytes, r
 
 pytestmark = pytest.mark.gpu
 
-TILES = ("256x256", "128x128", "64x64", "64x32", "32x32", "16x16")
+TILES = ("256x256", "128x128", "64x64", "64x32", "32x32", "16x32", "16x16")
 
 
 def case(M, N, K, at="e4m3", bt="e4m3", rows=128, seed=0):
