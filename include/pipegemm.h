@@ -359,8 +359,9 @@ enum { GEMM_E4M3 = 16, GEMM_E5M2 = 17 };
  * 64x32 stage operands through LDS and need rows that start on 16 bytes; the
  * others take any address.  GEMM_FP8_TILE_AUTO: the one that takes the least time
  * by what each cost in measurements. */
-enum { GEMM_FP8_TILE_AUTO = -1, GEMM_FP8_TILE_256x256 = 0, GEMM_FP8_TILE_128x128 = 1, GEMM_FP8_TILE_64x64 = 2,
-       GEMM_FP8_TILE_64x32 = 3, GEMM_FP8_TILE_32x32 = 4, GEMM_FP8_TILE_16x32 = 5, GEMM_FP8_TILE_16x16 = 6 };
+enum { GEMM_FP8_TILE_AUTO = -1, GEMM_FP8_TILE_256x256 = 0, GEMM_FP8_TILE_256x128 = 1, GEMM_FP8_TILE_128x128 = 2,
+       GEMM_FP8_TILE_64x64 = 3, GEMM_FP8_TILE_64x32 = 4, GEMM_FP8_TILE_32x32 = 5, GEMM_FP8_TILE_16x32 = 6,
+       GEMM_FP8_TILE_16x16 = 7 };
 
 typedef struct {
     int32_t tile;        /* GEMM_FP8_TILE_* chosen */

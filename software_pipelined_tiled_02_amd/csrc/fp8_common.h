@@ -69,27 +69,38 @@ template <int XT> struct XTypeOf { typedef float type; };
 template <> struct XTypeOf<XT_F16> { typedef _Float16 type; };
 template <> struct XTypeOf<XT_BF16> { typedef __bf16 type; };
 
-// Eight consecutive elements as fp32; those at or past `n` give 0.
+// Eight consecutive elements as they lie in memory; those at or past `n` are 0.
+template <int XT> struct Raw8 { typename XTypeOf<XT>::type v __attribute__((ext_vector_type(8))); };
+template <> struct Raw8<XT_F32> { float v __attribute__((ext_vector_type(8))); };
+
 template <int XT>
-__device__ __forceinline__ void load8(const void* base, int64_t at, int n, bool vec, float (&f)[8]) {
+__device__ __forceinline__ Raw8<XT> load_raw8(const void* base, int64_t at, int n, bool vec) {
     typedef typename XTypeOf<XT>::type T;
     const T* p = (const T*)base + at;
+    Raw8<XT> r;
     if (vec && n >= 8) {
         if constexpr (XT == XT_F32) {
             typedef float f32x4v __attribute__((ext_vector_type(4)));
             const f32x4v a = *(const f32x4v*)p, b = *(const f32x4v*)(p + 4);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) { f[e] = a[e]; f[4 + e] = b[e]; }
+            for (int e = 0; e < 4; ++e) { r.v[e] = a[e]; r.v[4 + e] = b[e]; }
         } else {
             typedef T tx8 __attribute__((ext_vector_type(8)));
-            const tx8 v = *(const tx8*)p;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = (float)v[e];
+            r.v = *(const tx8*)p;
         }
     } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = e < n ? (float)p[e] : 0.0f;
+        for (int e = 0; e < 8; ++e) r.v[e] = e < n ? p[e] : (T)0.0f;
     }
+    return r;
+}
+
+// The same as fp32.
+template <int XT>
+__device__ __forceinline__ void load8(const void* base, int64_t at, int n, bool vec, float (&f)[8]) {
+    const Raw8<XT> r = load_raw8<XT>(base, at, n, vec);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = (float)r.v[e];
 }
 
 // Eight consecutive elements rounded to the type (nearest even), those

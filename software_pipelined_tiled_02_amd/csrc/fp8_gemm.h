@@ -51,11 +51,12 @@ struct Fp8Args {
 
 // Tile classes: the workgroup's part of C, its waves, and how many of them
 // share each piece of C, every one with blocks of K of its own.
-enum Fp8Tile : int { FP8_TILE_256 = 0, FP8_TILE_128 = 1, FP8_TILE_64 = 2, FP8_TILE_64x32 = 3, FP8_TILE_32 = 4,
-                     FP8_TILE_16x32 = 5, FP8_TILE_16 = 6, FP8_TILE_COUNT = 7 };
+enum Fp8Tile : int { FP8_TILE_256 = 0, FP8_TILE_256x128 = 1, FP8_TILE_128 = 2, FP8_TILE_64 = 3, FP8_TILE_64x32 = 4,
+                     FP8_TILE_32 = 5, FP8_TILE_16x32 = 6, FP8_TILE_16 = 7, FP8_TILE_COUNT = 8 };
 struct Fp8Shape { int bm, bn, waves, wk; };
 constexpr Fp8Shape fp8_shape(int t) {
     return t == FP8_TILE_256 ? Fp8Shape{256, 256, 8, 1}
+         : t == FP8_TILE_256x128 ? Fp8Shape{256, 128, 8, 1}
          : t == FP8_TILE_128 ? Fp8Shape{128, 128, 8, 1}
          : t == FP8_TILE_64 ? Fp8Shape{64, 64, 4, 1}
          : t == FP8_TILE_64x32 ? Fp8Shape{64, 32, 4, 1}
@@ -75,11 +76,12 @@ constexpr bool fp8_staged(int t) { return t <= FP8_TILE_64x32; }
 // twice the time, at 1024^2 x 4096 and 4096^2 x 8200); microseconds there by
 // the class chosen and the next best:
 //   M = 128: 64x32 9.8, 64x64 11.4         M = 512: 64x64 17.6, 128x128 19.5
-//   M = 640: 128x128 19.9, 64x64 25.1      M = 1024: 128x128 24.0, 64x64 31.4
-//   M = 1536: 128x128 39.8, 256x256 45.0   M = 2560: 256x256 46.4, 128x128 61.5
+//   M = 640: 128x128 19.9, 64x64 25.1      M = 1024: 128x128 23.3, 256x128 28.8
+//   M = 2048: 256x128 34.6, 128x128 42.1   M = 4096: 256x256 58.5, 256x128 68.4
 struct Fp8Cost { int per_cu; double some, all, round; };
 constexpr Fp8Cost fp8_cost(int t, bool exact) {
     return t == FP8_TILE_256 ? Fp8Cost{1, 1.30, 1.65, 6.0}
+         : t == FP8_TILE_256x128 ? (exact ? Fp8Cost{1, 1.75, 1.95, 5.0} : Fp8Cost{1, 0.78, 0.93, 5.0})
          : t == FP8_TILE_128 ? (exact ? Fp8Cost{1, 1.00, 1.16, 4.0} : Fp8Cost{1, 0.50, 0.60, 4.0})
          : t == FP8_TILE_64 ? (exact ? Fp8Cost{2, 0.45, 0.78, 2.5} : Fp8Cost{2, 0.24, 0.42, 2.5})
          : t == FP8_TILE_64x32 ? (exact ? Fp8Cost{2, 0.30, 0.55, 2.5} : Fp8Cost{2, 0.19, 0.28, 2.5})
@@ -117,6 +119,13 @@ constexpr uint32_t kOutside = 0x80000000u;
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_at(const void* p) {
     return __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, 0x7fffffff, kBufferWord3);
+}
+
+// Workgroup b of n runs on XCD b mod 8, each of which has an L2 of its own.
+// The tile it takes: every XCD gets a run of neighbouring tiles.
+__device__ __forceinline__ int by_xcd(unsigned b, unsigned n) {
+    const unsigned x = b & 7, each = n >> 3, more = n & 7;
+    return (int)(x * each + (x < more ? x : more) + (b >> 3));
 }
 
 // At most N of this wave's loads are still in flight (vmcnt; loads retire in order).

@@ -103,9 +103,7 @@ struct Staged {
         const int wm = s.wave / WN, wn = s.wave % WN;
         // Each XCD gets a run of tiles, in bands of 4 tile rows, so that what
         // it holds at a time shares rows of A and of B in its L2.
-        const int ntiles = a.tiles_m * a.tiles_n;
-        int w = blockIdx.x;
-        if ((ntiles & 7) == 0) w = (w & 7) * (ntiles >> 3) + (w >> 3);
+        const int w = by_xcd(blockIdx.x, gridDim.x);
         constexpr int kBand = 4;
         const int band = kBand * a.tiles_n, gi = w / band, first = gi * kBand;
         const int rows = min(a.tiles_m - first, kBand), in = w - gi * band;
@@ -260,6 +258,7 @@ const void* by_tile(int tile) {
     case FP8_TILE_256:
         if constexpr (EXACT) return nullptr;     // the widened fragments leave no registers for 128 accumulators
         else return (const void*)&fp8_staged_tile<AT, BT, SBROW, EXACT, 256, 256, 2, 4, 2>;
+    case FP8_TILE_256x128: return (const void*)&fp8_staged_tile<AT, BT, SBROW, EXACT, 256, 128, 4, 2, 3>;
     case FP8_TILE_128: return (const void*)&fp8_staged_tile<AT, BT, SBROW, EXACT, 128, 128, 2, 4, 4>;
     case FP8_TILE_64: return (const void*)&fp8_staged_tile<AT, BT, SBROW, EXACT, 64, 64, 2, 2, 4>;
     case FP8_TILE_64x32: return (const void*)&fp8_staged_tile<AT, BT, SBROW, EXACT, 64, 32, 2, 2, 6>;

@@ -113,11 +113,8 @@ struct Stream {
     __device__ static __forceinline__ void run(const Fp8Args& a, f32x4 PG_LDS* sums) {
         const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         const int r = lane & 15, g = lane >> 4;
-        // Tiles of one column strip are neighbours (they share B); where the
-        // grid divides, workgroup w runs on XCD w % 8, and each XCD gets a
-        // run of neighbours.
-        const unsigned n = gridDim.x;
-        const unsigned w = (n & 7) == 0 ? (blockIdx.x & 7) * (n >> 3) + (blockIdx.x >> 3) : blockIdx.x;
+        // tiles of one column strip are neighbours: they share B
+        const unsigned w = by_xcd(blockIdx.x, gridDim.x);
         const int m0 = (int)(w % (unsigned)a.tiles_m) * BM, n0 = (int)(w / (unsigned)a.tiles_m) * BN;
 
         State s;
