@@ -373,6 +373,7 @@ typedef struct {
     int32_t reserved;
     int64_t grid;        /* workgroups */
     int64_t k_blocks;    /* ceil(K / 128) */
+    int64_t c_tiles;     /* tiles of C; above grid where workgroups take several in turn */
 } gemm_fp8_info_t;
 
 /* C = A * B of 8-bit matrices, each block of products times its scales:
@@ -386,7 +387,8 @@ typedef struct {
  * The sum inside a block is the matrix core's: for 16-bit outputs that of
  * the 8-bit instructions (about 2e-5 off on normal data); for
  * fp32 outputs both operands are widened to bf16, exactly, and it is fp32's
- * (half the rate).  The order of the sums is fixed for a tile class.
+ * (half the rate).  The order of the sums is fixed for a
+ * call's sizes and tile class.
  * accumulate = 1 (fp32 only): C += instead.
  * Leading dimensions are in elements, C may have any; an operand whose base
  * and leading dimension are not multiples of 16 bytes is read into

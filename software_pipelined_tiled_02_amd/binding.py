@@ -74,7 +74,7 @@ class Occupancy(ctypes.Structure):
 class Fp8Info(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in (
         "tile", "block_m", "block_n", "waves_k", "threads", "staged", "widened", "reserved")] + [
-        ("grid", ctypes.c_int64), ("k_blocks", ctypes.c_int64)]
+        ("grid", ctypes.c_int64), ("k_blocks", ctypes.c_int64), ("c_tiles", ctypes.c_int64)]
 
     def as_dict(self):
         return {n: getattr(self, n) for n, _ in self._fields_}

@@ -99,7 +99,9 @@ int plan_product(int64_t M, int64_t N, int64_t K, int a_type, int b_type, int c_
     in.threads = 64 * sh.waves;
     in.staged = pg::fp8_staged(tc) ? 1 : 0;
     in.widened = exact ? 1 : 0;
-    in.grid = grid;
+    // 256x256: one workgroup per CU stays and takes tile after tile
+    in.grid = tc == pg::FP8_TILE_256 && grid > num_cus ? num_cus : grid;
+    in.c_tiles = grid;
     in.k_blocks = kb;
     return GEMM_OK;
 }

@@ -230,10 +230,10 @@ __device__ __forceinline__ void store_c(const Fp8Args& a, int64_t m, int64_t n, 
     }
 }
 
-// The epilogue's LDS: per wave, two strips of 16 rows of its block of C, each
-// row padded by 16 bytes (so that the rows of a column fall in different banks).
+// The epilogue's LDS: per wave, a strip of 16 rows of its block of C, each row
+// padded by 16 bytes (so that the rows of a column fall in different banks).
 constexpr int strip_row(int fn, int size) { return 16 * fn * size + 16; }
-constexpr int epilogue_lds(int waves, int fn, int size) { return waves * 2 * 16 * strip_row(fn, size); }
+constexpr int epilogue_lds(int waves, int fn, int size) { return waves * 16 * strip_row(fn, size); }
 
 // A wave's block of FM x FN pieces at (m0, n0).  A lane holds 4 neighbouring
 // columns, 8 or 16 bytes, of a row; stored like that, an instruction would
@@ -247,10 +247,9 @@ __device__ __forceinline__ void store_block(const Fp8Args& a, uint8_t PG_LDS* sm
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     constexpr int SIZE = EXACT ? 4 : 2, ROW = strip_row(FN, SIZE), CHUNKS = FN * SIZE;   // 16-byte chunks of a row
     if (a.vec16_c && m0 + 16 * FM <= a.M && n0 + 16 * FN <= a.N) {
-        uint8_t PG_LDS* strips = smem + wave * 2 * 16 * ROW;
+        uint8_t PG_LDS* strip = smem + wave * 16 * ROW;     // (a wave's LDS accesses keep their order)
 #pragma unroll
         for (int i = 0; i < FM; ++i) {
-            uint8_t PG_LDS* strip = strips + (i & 1) * 16 * ROW;
 #pragma unroll
             for (int j = 0; j < FN; ++j) {
                 uint8_t PG_LDS* p = strip + r * ROW + (16 * j + 4 * g) * SIZE;

@@ -10,7 +10,7 @@ namespace pg {
 
 namespace {
 
-template <int AT, int BT, bool SBROW, bool EXACT, int BM, int BN, int WM, int WN, int SLOTS>
+template <int AT, int BT, bool SBROW, bool EXACT, int BM, int BN, int WM, int WN, int SLOTS, bool LOOP>
 struct Staged {
     static constexpr int T = WM * WN * 64;
     static constexpr int WTM = BM / WM, WTN = BN / WN, FM = WTM / 16, FN = WTN / 16;
@@ -19,7 +19,10 @@ struct Staged {
     static constexpr int LPT = LA + LB + 1;                      // loads per lane and K-tile, one of them scales
     static constexpr int A_BYTES = BM * kBlock, B_BYTES = BN * kBlock, S_OFF = A_BYTES + B_BYTES;
     static constexpr int SLOT = S_OFF + T * 4;
-    static constexpr int LDS = max3(SLOTS * SLOT, epilogue_lds(WM * WN, FN, EXACT ? 4 : 2), 0);
+    // The epilogue's strips take the ring's place, or (LOOP) lie behind it, so
+    // that the next tile's first loads can go out before the stores.
+    static constexpr int STRIPS = LOOP ? SLOTS * SLOT : 0;
+    static constexpr int LDS = max3(SLOTS * SLOT, STRIPS + epilogue_lds(WM * WN, FN, EXACT ? 4 : 2), 0);
     static_assert(BM + BN <= T && BM % 64 == 0, "a scale per lane, whole waves of A's");
     static_assert(LDS <= kLdsBudget, "LDS");
     static_assert(WTN <= kBlock && kBlock % WTN == 0 && (BN % kBlock == 0 || kBlock % BN == 0),
@@ -30,12 +33,15 @@ struct Staged {
         uint32_t offa[LA], offb[LB], offs;
         uint32_t s_blk;                      // bytes from one block's scale to the next, of this wave's operand
         int kc;                              // first k of the lane's chunks
-        int wave, K, KB, ragged;
+        int wave, K, KB, ragged, rot;
+        int m0, n0;                          // the tile
     };
 
-    // K-tiles in the order they are multiplied: a ragged last one first.
+    // K-tiles in the order they are multiplied: a ragged last one first, the
+    // others from `rot` on.
     __device__ static __forceinline__ int block_of(const State& s, int t) {
-        return s.ragged ? (t == 0 ? s.KB - 1 : t - 1) : t;
+        const int nb = s.KB - s.ragged, q = t - s.ragged + s.rot;
+        return t < s.ragged ? s.KB - 1 : q >= nb ? q - nb : q;
     }
 
     // Where the loads of K-tile t go and start.  One at or past KB moves
@@ -96,22 +102,24 @@ struct Staged {
         return *(const i32x4 PG_LDS*)(rows + off);
     }
 
-    __device__ static __forceinline__ void run(const Fp8Args& a, uint8_t PG_LDS* smem) {
-        const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
-        State s;
-        s.wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-        const int wm = s.wave / WN, wn = s.wave % WN;
+    // Tile number `tile`: where it is, and where a lane's loads start.
+    __device__ static __forceinline__ void locate(const Fp8Args& a, State& s, int tile) {
+        const int tid = threadIdx.x, ntiles = a.tiles_m * a.tiles_n;
         // Each XCD gets a run of tiles, in bands of 4 tile rows, so that what
         // it holds at a time shares rows of A and of B in its L2.
-        const int w = by_xcd(blockIdx.x, gridDim.x);
+        const int w = by_xcd(tile, ntiles);
         constexpr int kBand = 4;
         const int band = kBand * a.tiles_n, gi = w / band, first = gi * kBand;
         const int rows = min(a.tiles_m - first, kBand), in = w - gi * band;
         const int m0 = (first + in % rows) * BM, n0 = in / rows * BN;
-
-        s.K = a.K;
-        s.KB = (a.K + kBlock - 1) / kBlock;
-        s.ragged = a.K % kBlock != 0;
+        s.m0 = m0;
+        s.n0 = n0;
+        // With more tiles than one round, XCD x starts at K-tile 9 x: read at
+        // one k by every XCD, rows at equal distances gather on a few memory
+        // channels (8192 x 8192 x 8200: 545 us without, 517 with; one round,
+        // whose operands the caches hold, gains nothing).
+        const int nb = s.KB - s.ragged;
+        s.rot = ntiles > 256 && nb > 0 ? (int)((tile & 7) * 9u % (unsigned)nb) : 0;
         s.ra = buffer_at(a.A + (int64_t)m0 * a.lda);
         s.rb = buffer_at(a.B + (int64_t)n0 * a.ldb);
         // Chunk p = j T + tid of a tile lies in row p / 8; the swizzle has
@@ -140,8 +148,46 @@ struct Staged {
             s.offs = (uint32_t)(SBROW ? n : n / kBlock) * (uint32_t)(a.sb_row * 4);
             s.s_blk = (uint32_t)(a.sb_blk * 4);
         }
+    }
 
+    // The first SLOTS - 1 K-tiles' loads.
+    __device__ static __forceinline__ void fill(const State& s, uint8_t PG_LDS* smem) {
+        issue<true>(s, smem, 0, 0);
+#pragma unroll
+        for (int t = 1; t < SLOTS - 1; ++t) issue<false>(s, smem, t, t);
+    }
+
+    __device__ static __forceinline__ void run(const Fp8Args& a, uint8_t PG_LDS* smem) {
+        State s;
+        s.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        s.K = a.K;
+        s.KB = (a.K + kBlock - 1) / kBlock;
+        s.ragged = a.K % kBlock != 0 ? 1 : 0;
+        const int wm = s.wave / WN, wn = s.wave % WN;
         f32x4 acc[FM][FN];
+        int tile = blockIdx.x;
+        locate(a, s, tile);
+        fill(s, smem);
+        while (true) {
+            multiply(a, s, smem, acc);
+            // (no write into LDS is left in flight, and every wave is here)
+            const int m0 = s.m0 + wm * WTM, n0 = s.n0 + wn * WTN;
+            tile += gridDim.x;
+            const bool more = LOOP && tile < a.tiles_m * a.tiles_n;
+            if (more) {
+                locate(a, s, tile);
+                fill(s, smem);
+            }
+            store_block<EXACT, FM, FN, BM * BN == 256 * 256>(a, smem + STRIPS, s.wave, m0, n0, acc);
+            if (!more) return;
+        }
+    }
+
+    // One tile's K loop, its first loads under way.
+    __device__ static __forceinline__ void multiply(const Fp8Args& a, const State& s, uint8_t PG_LDS* smem,
+                                                    f32x4 (&acc)[FM][FN]) {
+        const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+        const int wm = s.wave / WN, wn = s.wave % WN;
 #pragma unroll
         for (int i = 0; i < FM; ++i)
 #pragma unroll
@@ -152,9 +198,6 @@ struct Staged {
         const uint32_t rd0 = (uint32_t)(r * CPR + (g ^ swz(CPR, r))) * kChunk;
         const uint32_t rd1 = (uint32_t)(r * CPR + ((4 + g) ^ swz(CPR, r))) * kChunk;
 
-        issue<true>(s, smem, 0, 0);
-#pragma unroll
-        for (int t = 1; t < SLOTS - 1; ++t) issue<false>(s, smem, t, t);
         wait_loads<(SLOTS - 2) * LPT>();
         barrier();
         if (a.K % 16 != 0) {
@@ -237,31 +280,31 @@ struct Staged {
         }
 #pragma unroll
         for (int u = NU - LAG; u < NU; ++u) add(u);
-        wait_loads<0>();                       // no write into LDS outlives the K loop,
-        barrier();                             // whose slots the epilogue takes
-        store_block<EXACT, FM, FN, BM == 256>(a, smem, s.wave, m0 + wm * WTM, n0 + wn * WTN, acc);
+        wait_loads<0>();                       // no write into LDS outlives the K loop
+        barrier();
     }
 };
 
-template <int AT, int BT, bool SBROW, bool EXACT, int BM, int BN, int WM, int WN, int SLOTS>
+template <int AT, int BT, bool SBROW, bool EXACT, int BM, int BN, int WM, int WN, int SLOTS, bool LOOP>
 __global__ void __launch_bounds__(WM * WN * 64) fp8_staged_tile(Fp8Args a) {
-    typedef Staged<AT, BT, SBROW, EXACT, BM, BN, WM, WN, SLOTS> S;
+    typedef Staged<AT, BT, SBROW, EXACT, BM, BN, WM, WN, SLOTS, LOOP> S;
     __shared__ __attribute__((aligned(16))) uint8_t smem[S::LDS];
     S::run(a, (uint8_t PG_LDS*)smem);
 }
 
 // Waves and slots of each tile class.  More slots than two hide the memory's
 // latency where a K-tile is multiplied in less time than it takes to arrive.
+// The 256x256 tile's workgroups stay and take tile after tile.
 template <int AT, int BT, bool SBROW, bool EXACT>
 const void* by_tile(int tile) {
     switch (tile) {
     case FP8_TILE_256:
         if constexpr (EXACT) return nullptr;     // the widened fragments leave no registers for 128 accumulators
-        else return (const void*)&fp8_staged_tile<AT, BT, SBROW, EXACT, 256, 256, 2, 4, 2>;
-    case FP8_TILE_256x128: return (const void*)&fp8_staged_tile<AT, BT, SBROW, EXACT, 256, 128, 4, 2, 3>;
-    case FP8_TILE_128: return (const void*)&fp8_staged_tile<AT, BT, SBROW, EXACT, 128, 128, 2, 4, 4>;
-    case FP8_TILE_64: return (const void*)&fp8_staged_tile<AT, BT, SBROW, EXACT, 64, 64, 2, 2, 4>;
-    case FP8_TILE_64x32: return (const void*)&fp8_staged_tile<AT, BT, SBROW, EXACT, 64, 32, 2, 2, 6>;
+        else return (const void*)&fp8_staged_tile<AT, BT, SBROW, EXACT, 256, 256, 2, 4, 2, true>;
+    case FP8_TILE_256x128: return (const void*)&fp8_staged_tile<AT, BT, SBROW, EXACT, 256, 128, 4, 2, 3, false>;
+    case FP8_TILE_128: return (const void*)&fp8_staged_tile<AT, BT, SBROW, EXACT, 128, 128, 2, 4, 4, false>;
+    case FP8_TILE_64: return (const void*)&fp8_staged_tile<AT, BT, SBROW, EXACT, 64, 64, 2, 2, 4, false>;
+    case FP8_TILE_64x32: return (const void*)&fp8_staged_tile<AT, BT, SBROW, EXACT, 64, 32, 2, 2, 6, false>;
     default: return nullptr;
     }
 }

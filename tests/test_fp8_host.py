@@ -97,7 +97,8 @@ def test_product_plan():
                           (16, 16, 0, None)):
         rc, info = q(M, N, K)
         assert rc == OK and (tile is None or info["tile"] == T[tile]), (M, N, K, info)
-        assert info["grid"] == -(-M // info["block_m"]) * -(-N // info["block_n"])
+        assert info["c_tiles"] == -(-M // info["block_m"]) * -(-N // info["block_n"])
+        assert info["grid"] == min(info["c_tiles"], 256 if tile == "256x256" else 1 << 31)
         assert info["k_blocks"] == -(-K // 128)
     assert q(4096, 4096, 4096, c_dtype="f32")[1]["tile"] == T["256x128"]       # fp32 outputs: widened
     assert q(4096, 4096, 4096, c_dtype="f32")[1]["widened"] == 1

@@ -194,6 +194,21 @@ def test_offsets_past_32_bits(tile):
         check_product(ct[:, torch.from_numpy(rows).cuda()], b, np.repeat(sb, N, 0), a, sa, "e4m3", "e4m3", 1, "bf16", tile)
 
 
+@pytest.mark.parametrize("tile,rows", (("256x256", 128), ("256x256", 1), ("128x128", 128)))
+def test_more_tiles_than_one_round(tile, rows):
+    """More than 256 tiles: workgroups take several in turn, and K-tiles start at
+    a place that depends on the tile.  Sampled rows and columns, the edges' among them."""
+    M, N, K = 4353, 4100, 400
+    a, sa, b, sb = case(M, N, K, rows=rows)
+    c = run_product(a, sa, b, sb, "e4m3", "e4m3", tile=tile)
+    rng = np.random.default_rng(1)
+    i = np.unique(np.concatenate([[0, 255, 256, 4095, 4351, 4352], rng.integers(0, M, 60)]))
+    j = np.unique(np.concatenate([[0, 127, 128, 255, 256, 4095, 4096, 4099], rng.integers(0, N, 60)]))
+    part = c[torch.from_numpy(i).cuda()][:, torch.from_numpy(j).cuda()]
+    check_product(part, a[i], sa[i], b[j], np.repeat(sb, rows, 0)[j], "e4m3", "e4m3", 1, "bf16", tile)
+    assert torch.equal(c, run_product(a, sa, b, sb, "e4m3", "e4m3", tile=tile))       # the same bits each time
+
+
 def test_streams_and_reuse_of_freed_memory():
     """A call on another stream: what it allocates belongs to that stream."""
     a, sa, b, sb = case(128, 256, 512)
