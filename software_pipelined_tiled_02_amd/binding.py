@@ -2,12 +2,12 @@
 
 Argument marshalling only: every step of the GEMM runs in the HIP kernels.
 The functions keep the C names; device buffers are passed as torch CUDA
-tensors (their data_ptr) or plain integer addresses.  There is no fallback:
-if the library is missing, loading raises.
+tensors (their data_ptr) or plain integer addresses.  run_fp8, quantize_fp8,
+rms_fp8 and rms_backward are the 8-bit operators on torch tensors.  There is
+no fallback: if the library is missing, loading raises.
 """
 import ctypes
 import os
-import threading
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libpipegemm.so")
@@ -277,7 +277,7 @@ def gemm_query_streamk(M, N, K, dtype, layout, stages, variant, grid=0, tile="au
     return rc, info.as_dict()
 
 
-_HANDLES = {}   # device index -> Gemm, for run() and the 8-bit functions
+_HANDLES = {}   # device index -> Gemm, for run()
 
 
 def run(a, b, *, layout="RC", stages=2, variant="direct", out=None, stream=None):
@@ -390,130 +390,49 @@ def gemm_rms_backward(h, M, D, x_dtype, w_dtype, DY, lddy, H, ldh, W, rstd, DH, 
     return rc
 
 
-_HANDLES_LOCK = threading.Lock()
-
-
-def _handle(index):
-    """The handle of a device, made on first use (which waits for the device,
-    so it cannot be part of a graph capture)."""
-    g = _HANDLES.get(index)
-    if g is None:
-        import torch
-        if torch.cuda.is_current_stream_capturing():
-            raise RuntimeError("the first call on a device sets it up: make one before the graph capture")
-        with _HANDLES_LOCK:
-            g = _HANDLES.get(index)
-            if g is None:
-                g = _HANDLES[index] = Gemm(index)
-    return g.h
-
-
 def _rows16(n):
     return (n + 15) // 16 * 16
 
 
-_T = {}   # torch's types by role, filled on first use (torch is not imported with this module)
+# The functions below are the operators on torch tensors.  Their checks,
+# allocations and calls are compiled (csrc/torch_ops.cpp): the smallest calls
+# are bound by the host.
+_OPS = None
+_FP8_NAMES = dict(FP8_TYPES)    # and torch's dtypes, once torch is there
 
 
-def _types():
-    if not _T:
+def _ops():
+    global _OPS
+    if _OPS is None:
         import torch
-        _T["fp8"] = {torch.float8_e4m3fn: GEMM_E4M3, torch.float8_e5m2: GEMM_E5M2}
-        _T["float"] = {torch.bfloat16: GEMM_BF16, torch.float16: GEMM_F16, torch.float32: GEMM_F32}
-        _T["named"] = {"e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2,
-                       torch.float8_e4m3fn: torch.float8_e4m3fn, torch.float8_e5m2: torch.float8_e5m2}
-        _T["float32"], _T["bfloat16"], _T["uint8"] = torch.float32, torch.bfloat16, torch.uint8
-        _T["new"] = torch.empty_strided
-        # the current stream of a device as its raw handle, without a Stream
-        # object (2 us of a 10 us call)
-        _T["raw stream"] = getattr(torch._C, "_cuda_getCurrentRawStream",
-                                   lambda index: torch.cuda.current_stream(index).cuda_stream)
-    return _T
+        _lib()
+        path = os.path.join(HERE, "_torch_ops.so")
+        if not os.path.exists(path):
+            raise RuntimeError("_torch_ops.so is not built (%s); run __graft_entry__.build()" % path)
+        from . import _torch_ops
+        _FP8_NAMES.update({torch.float8_e4m3fn: GEMM_E4M3, torch.float8_e5m2: GEMM_E5M2})
+        _OPS = _torch_ops
+    return _OPS
 
 
-def _refuse(t, what, dtypes, device, shape):
-    """Raises ValueError, naming what _matrix found wrong with t."""
-    import torch
-    if not isinstance(t, torch.Tensor) or t.dim() != 2:
-        raise ValueError("%s must be a 2-D torch tensor" % what)
-    if t.dtype not in dtypes:
-        raise ValueError("%s must be %s (got %s)" % (what, " or ".join(str(d) for d in dtypes), t.dtype))
-    if not t.is_cuda or (device is not None and t.get_device() != device):
-        raise ValueError("all tensors must be CUDA tensors on one device (%s is on %s)" % (what, t.device))
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError("%s must be %s (got %s)" % (what, " x ".join(map(str, shape)), tuple(t.shape)))
-    raise ValueError("%s must have unit stride along its last axis, and rows that do not overlap" % what)
-
-
-def _matrix(t, what, dtypes, device=None, shape=None):
-    """Argument check: t is a 2-D CUDA tensor (on device number `device`, of
-    `shape`) of one of dtypes, with unit stride along its last axis and rows
-    that do not overlap.  Returns rows, columns, leading dimension (a single row's is free:
-    the next multiple of 16) and the type's GEMM_* value."""
+def _named(x, table, what):
     try:
-        rows, cols = t.shape
-        ld, unit = t.stride()
-        code = dtypes.get(t.dtype)
-        index = t.get_device()
-        if (code is not None and (index == device or (device is None and index >= 0 and t.is_cuda))
-                and (unit == 1 or cols <= 1) and (ld >= cols or rows <= 1)
-                and (shape is None or (rows == shape[0] and cols == shape[1]))):
-            return rows, cols, ld if rows > 1 else _rows16(cols), code
-    except (AttributeError, TypeError, ValueError, RuntimeError):
-        pass
-    _refuse(t, what, dtypes, device, shape)
+        return table[x]
+    except (KeyError, TypeError):
+        raise ValueError("%s must be one of %s (got %r)" % (what, ", ".join(map(str, table)), x)) from None
 
 
-def _vector(t, what, dtypes, n, device):
-    """Argument check: n contiguous values of one of dtypes; returns the type's GEMM_* value."""
-    try:
-        code = dtypes.get(t.dtype)
-        if code is not None and t.dim() == 1 and t.shape[0] == n and t.get_device() == device and (
-                n <= 1 or t.stride(0) == 1):
-            return code
-    except (AttributeError, TypeError, RuntimeError):
-        pass
-    raise ValueError("%s must be a torch tensor of %d contiguous values of %s on the other tensors' device"
-                     % (what, n, " or ".join(str(d) for d in dtypes)))
-
-
-def _scales(t, what, index):
-    """Argument check: a 2-D float32 tensor on device `index`, any strides."""
-    try:
-        if t.dtype is _T["float32"] and t.dim() == 2 and t.get_device() == index:
-            return t.shape
-    except (AttributeError, RuntimeError):
-        pass
-    raise ValueError("%s must be a 2-D float32 torch tensor on the matrices' device" % what)
-
-
-def _fp8_dtype(fp8):
-    named = _types()["named"]
-    if fp8 not in named:
-        raise ValueError("fp8 must be e4m3 or e5m2 (got %r)" % (fp8,))
-    return named[fp8]
-
-
-def _on_stream(stream, device):
+def _on_stream(stream, t):
     """The context in which `stream` (a torch stream or a raw handle) is the
     current one: what a call allocates in it belongs to that stream."""
     import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError("all tensors must be CUDA tensors")
     if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=device)
-    if stream.device != device:
-        raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, device))
+        stream = torch.cuda.ExternalStream(stream, device=t.device)
+    if stream.device != t.device:
+        raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, t.device))
     return torch.cuda.stream(stream)
-
-
-def _empty_rows16(rows, cols, dtype, device):
-    """rows x cols of 8-bit values whose rows start on 16 bytes."""
-    return _T["new"]((rows, cols), (_rows16(cols), 1), dtype=dtype, device=device)
-
-
-def _empty_scales(rows, blocks, device):
-    """rows x blocks scales, one block's after another (the order the
-    product reads them in)."""
-    return _T["new"]((rows, blocks), (1, rows), dtype=_T["float32"], device=device)
 
 
 def run_fp8(a, sa, b, sb, *, out=None, out_dtype=None, accumulate=False, tile="auto", stream=None):
@@ -524,56 +443,20 @@ def run_fp8(a, sa, b, sb, *, out=None, out_dtype=None, accumulate=False, tile="a
     ("tile" scales) or N x ceil(K / 128) ("row" scales).  Scales may have any
     strides (expanded ones too).  C is M x N of out_dtype: bfloat16 (the
     default), float16 or float32; `out` is written in place, else a new tensor
-    is allocated; accumulate=True adds to a float32 `out`.  The call is
-    enqueued on `stream` (a torch stream or its raw handle; the current stream
-    of A's device by default).  Argument errors raise ValueError, or GemmError
-    with the C status, before anything is enqueued.
+    is allocated; accumulate=True adds to a float32 `out`.
 
-    Rows that start on 16 bytes (as quantize_fp8 and rms_fp8 lay them out) are
-    the fast case."""
-    types = _types()
-    M, K, lda, a_type = _matrix(a, "a", types["fp8"])
-    index = a.get_device()
+    The call is enqueued on `stream` (a torch stream or its raw handle; the
+    current stream of A's device by default).  Argument errors raise
+    ValueError, or GemmError with the C status, before anything is enqueued.
+    The first call on a device sets it up, which a graph capture cannot hold
+    (RuntimeError).
+
+    Rows that start on 16 bytes are the fast case, on 128 the fastest
+    (quantize_fp8 and rms_fp8 lay them out so)."""
     if stream is not None:
-        with _on_stream(stream, a.device):
+        with _on_stream(stream, a):
             return run_fp8(a, sa, b, sb, out=out, out_dtype=out_dtype, accumulate=accumulate, tile=tile)
-    N, Kb, ldb, b_type = _matrix(b, "b", types["fp8"], index)
-    if Kb != K:
-        raise ValueError("inner dimensions differ: a has K = %d, b has %d" % (K, Kb))
-    blocks = (K + 127) // 128
-    rows, cols = _scales(sa, "sa", index)
-    if rows != M or cols != blocks:
-        raise ValueError("sa must be M x ceil(K / 128) = %d x %d (got %d x %d)" % (M, blocks, rows, cols))
-    rows, cols = _scales(sb, "sb", index)
-    b_scale_rows = 128 if rows == (N + 127) // 128 else 1
-    if (b_scale_rows == 1 and rows != N) or cols != blocks:
-        raise ValueError("sb must be ceil(N / 128) or N rows of ceil(K / 128) = %d scales (got %d x %d)"
-                         % (blocks, rows, cols))
-    if out is None:
-        if accumulate:
-            raise ValueError("accumulate needs out")
-        if out_dtype is None:
-            out_dtype = types["bfloat16"]
-        c_type, ldc = types["float"].get(out_dtype), N
-        if c_type is None:
-            raise ValueError("out_dtype must be bfloat16, float16 or float32 (got %s)" % out_dtype)
-    else:
-        _, _, ldc, c_type = _matrix(out, "out", types["float"], index, (M, N))
-        if out_dtype is not None and out.dtype != out_dtype:
-            raise ValueError("out is %s, out_dtype %s" % (out.dtype, out_dtype))
-        if accumulate and c_type != GEMM_F32:
-            raise ValueError("accumulate needs a float32 out")
-    h = _handle(index)
-    if out is None:
-        out = types["new"]((M, N), (N, 1), dtype=out_dtype, device=a.device)
-    sa0, sa1 = sa.stride()
-    sb0, sb1 = sb.stride()
-    rc = _L.gemm_run_fp8(h, M, N, K, a_type, b_type, c_type, b_scale_rows, 1 if accumulate else 0, _enum(tile, FP8_TILES),
-                         a.data_ptr(), lda, sa.data_ptr(), sa0, sa1, b.data_ptr(), ldb, sb.data_ptr(), sb0, sb1,
-                         out.data_ptr(), ldc, types["raw stream"](index))
-    if rc != GEMM_OK:
-        raise GemmError(rc, "gemm_run_fp8")
-    return out
+    return (_OPS or _ops()).run_fp8(a, sa, b, sb, out, out_dtype, accumulate, _named(tile, FP8_TILES, "tile"))
 
 
 def quantize_fp8(x, *, block="row", fp8="e4m3", pow2=False, rows=True, transpose=False, stream=None):
@@ -585,40 +468,14 @@ def quantize_fp8(x, *, block="row", fp8="e4m3", pow2=False, rows=True, transpose
     "tile": one for each 128 x 128; s is ceil(M / 128) x ceil(K / 128).
     qt (K x M) is x transposed, quantised along its own rows (by tiles: the
     same values and scales as q, transposed); st are its scales.  fp8: "e4m3"
-    or "e5m2".  pow2: scales are powers of two.  Rows of q and qt start on 16
-    bytes.  Streams and errors as run_fp8."""
-    types = _types()
-    M, K, ldx, x_type = _matrix(x, "x", types["float"])
-    device = x.device
+    or "e5m2", or torch's dtype.  pow2: scales are powers of two.  Rows of q
+    and qt start on 16 bytes, from 1024 columns on on 128.  Streams and errors
+    as run_fp8."""
     if stream is not None:
-        with _on_stream(stream, device):
+        with _on_stream(stream, x):
             return quantize_fp8(x, block=block, fp8=fp8, pow2=pow2, rows=rows, transpose=transpose)
-    f8 = _fp8_dtype(fp8)
-    if block not in BLOCK_ROWS:
-        raise ValueError("block must be 'row' or 'tile' (got %r)" % (block,))
-    if not rows and not transpose:
-        raise ValueError("rows or transpose must be asked for")
-    block_rows = BLOCK_ROWS[block]
-    index = x.get_device()
-    h = _handle(index)
-    out, given = (), ()
-    if rows:
-        n = -(-M // block_rows)
-        q, s = _empty_rows16(M, K, f8, device), _empty_scales(n, -(-K // FP8_BLOCK), device)
-        out, given = (q, s), (q.data_ptr(), _rows16(K), s.data_ptr(), 1, n)
-    else:
-        given = (None, 0, None, 0, 0)
-    if transpose:
-        n = -(-K // block_rows)
-        q, s = _empty_rows16(K, M, f8, device), _empty_scales(n, -(-M // FP8_BLOCK), device)
-        out, given = out + (q, s), given + (q.data_ptr(), _rows16(M), s.data_ptr(), 1, n)
-    else:
-        given += (None, 0, None, 0, 0)
-    rc = _L.gemm_quantize_fp8(h, M, K, x_type, types["fp8"][f8], block_rows, 1 if pow2 else 0, x.data_ptr(), ldx, *given,
-                              types["raw stream"](index))
-    if rc != GEMM_OK:
-        raise GemmError(rc, "gemm_quantize_fp8")
-    return out
+    ops = _OPS or _ops()
+    return ops.quantize_fp8(x, _named(block, BLOCK_ROWS, "block"), _named(fp8, _FP8_NAMES, "fp8"), pow2, rows, transpose)
 
 
 def rms_fp8(x, weight, *, residual=None, eps=1e-6, fp8="e4m3", pow2=False, norm=False, h_out=None, stream=None):
@@ -631,42 +488,11 @@ def rms_fp8(x, weight, *, residual=None, eps=1e-6, fp8="e4m3", pow2=False, norm=
     residual; rstd: M float32, what rms_backward takes; q, s: the normalised
     rows in 8 bits, a scale for each 128 values; y: the same in x's type.
     D up to 32768.  Streams and errors as run_fp8."""
-    types = _types()
-    M, D, ldx, x_type = _matrix(x, "x", types["float"])
-    device = x.device
     if stream is not None:
-        with _on_stream(stream, device):
+        with _on_stream(stream, x):
             return rms_fp8(x, weight, residual=residual, eps=eps, fp8=fp8, pow2=pow2, norm=norm, h_out=h_out)
-    index = x.get_device()
-    f8 = _fp8_dtype(fp8)
-    own, f32, new = {x.dtype: x_type}, types["float32"], types["new"]
-    w_type = _vector(weight, "weight", own if x.dtype is f32 else {x.dtype: x_type, f32: GEMM_F32}, D, index)
-    r, ldr, h, ldh, y, ldy = None, 0, None, 0, None, 0
-    if residual is not None:
-        ldr = _matrix(residual, "residual", own, index, (M, D))[2]
-        r = residual.data_ptr()
-    if h_out is not None:
-        ldh = _matrix(h_out, "h_out", own, index, (M, D))[2]
-        h = h_out.data_ptr()
-    handle = _handle(index)
-    blocks = -(-D // FP8_BLOCK)
-    q, s = _empty_rows16(M, D, f8, device), _empty_scales(M, blocks, device)
-    rstd = new((M,), (1,), dtype=f32, device=device)
-    if h_out is None:
-        h_out = x
-        if residual is not None:
-            h_out = new((M, D), (D, 1), dtype=x.dtype, device=device)
-            h, ldh = h_out.data_ptr(), D
-    out = (q, s, h_out, rstd)
-    if norm:
-        out += (new((M, D), (D, 1), dtype=x.dtype, device=device),)
-        y, ldy = out[4].data_ptr(), D
-    rc = _L.gemm_rms_fp8(handle, M, D, x_type, w_type, types["fp8"][f8], 1 if pow2 else 0, eps, x.data_ptr(), ldx, r, ldr,
-                         weight.data_ptr(), h, ldh, y, ldy, q.data_ptr(), _rows16(D), s.data_ptr(), 1, M,
-                         rstd.data_ptr(), types["raw stream"](index))
-    if rc != GEMM_OK:
-        raise GemmError(rc, "gemm_rms_fp8")
-    return out
+    ops = _OPS or _ops()
+    return ops.rms_fp8(x, weight, residual, eps, _named(fp8, _FP8_NAMES, "fp8"), pow2, norm, h_out)
 
 
 def rms_backward(dy, h, weight, rstd, *, dh=None, dx_out=None, stream=None):
@@ -678,38 +504,10 @@ def rms_backward(dy, h, weight, rstd, *, dh=None, dx_out=None, stream=None):
     the residual; it is written into dx_out where given, which may be dy, h
     or dh.  dw is float32, its rows added in a fixed order.  Streams and errors
     as run_fp8."""
-    types = _types()
-    M, D, ldh, x_type = _matrix(h, "h", types["float"])
-    device = h.device
     if stream is not None:
-        with _on_stream(stream, device):
+        with _on_stream(stream, dy):
             return rms_backward(dy, h, weight, rstd, dh=dh, dx_out=dx_out)
-    index = h.get_device()
-    own, f32, new = {h.dtype: x_type}, types["float32"], types["new"]
-    lddy = _matrix(dy, "dy", own, index, (M, D))[2]
-    w_type = _vector(weight, "weight", own if h.dtype is f32 else {h.dtype: x_type, f32: GEMM_F32}, D, index)
-    _vector(rstd, "rstd", {f32: GEMM_F32}, M, index)
-    dhp, lddh = None, 0
-    if dh is not None:
-        lddh = _matrix(dh, "dh", own, index, (M, D))[2]
-        dhp = dh.data_ptr()
-    if dx_out is None:
-        lddx = D
-    else:
-        lddx = _matrix(dx_out, "dx_out", own, index, (M, D))[2]
-    handle = _handle(index)
-    if dx_out is None:
-        dx_out = new((M, D), (D, 1), dtype=h.dtype, device=device)
-    dw = new((D,), (1,), dtype=f32, device=device)
-    # a workspace of this call's own: it belongs to the stream (and to the graph, under capture)
-    nbytes = _L.gemm_rms_backward_workspace(M, D)
-    ws = new((nbytes,), (1,), dtype=_T["uint8"], device=device)
-    rc = _L.gemm_rms_backward(handle, M, D, x_type, w_type, dy.data_ptr(), lddy, h.data_ptr(), ldh, weight.data_ptr(),
-                              rstd.data_ptr(), dhp, lddh, dx_out.data_ptr(), lddx, dw.data_ptr(), ws.data_ptr(), nbytes,
-                              types["raw stream"](index))
-    if rc != GEMM_OK:
-        raise GemmError(rc, "gemm_rms_backward")
-    return dx_out, dw
+    return (_OPS or _ops()).rms_backward(dy, h, weight, rstd, dh, dx_out)
 
 
 class Gemm:

@@ -1,10 +1,12 @@
-"""Build libpipegemm.so (gfx950) in-tree with hipcc.
+"""Build libpipegemm.so (gfx950) in-tree with hipcc, and _torch_ops.so with g++.
 
 Each translation unit under csrc/ is compiled on its own (in parallel) and
 the objects are linked into software_pipelined_tiled_02_amd/libpipegemm.so.
 Each kernel's register, LDS and occupancy figures, as the compiler reports
 them (its kernel-resource-usage remarks), are written to
-kernel_resources.json beside the library.  Two standalone measurement
+kernel_resources.json beside the library.  csrc/torch_ops.cpp (host code: the
+8-bit operators on torch tensors) becomes the module _torch_ops, linked to
+the library.  Two standalone measurement
 programs are built beside it: `ceiling_probe`
 (csrc/ceiling_probe.hip: MFMA and HBM rates of the chip, no GEMM code) and
 `lds_layout_probe` (csrc/lds_layout_probe.hip: LDS bank conflicts of the
@@ -27,6 +29,8 @@ SOURCES = ["kernels_i8.hip", "kernels_f16.hip", "kernels_bf16.hip", "kernels_f32
            "fp8_abi.hip", "fp8_stream.hip", "fp8_staged.hip", "fp8_quantize.hip", "fp8_rms.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
+CXX = os.environ.get("CXX", "g++")
+TORCH_OPS = os.path.join(HERE, "_torch_ops.so")
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
     # packed-fp32 instructions are kept out of every kernel
@@ -35,11 +39,35 @@ FLAGS = [
 ]
 
 
+def torch_ops_object():
+    """The compile of csrc/torch_ops.cpp, started: (process, object)."""
+    import sysconfig
+
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    obj = os.path.join(BUILD, "torch_ops.o")
+    cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1", "-I" + inc,
+           "-I" + os.path.join(inc, "torch", "csrc", "api", "include"), "-I/opt/rocm/include",
+           "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(ROOT, "include"), "-c",
+           os.path.join(CSRC, "torch_ops.cpp"), "-o", obj]
+    return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT), obj
+
+
+def link_torch_ops(obj):
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = TORCH_OPS + ".tmp%d" % os.getpid()
+    subprocess.run([CXX, "-shared", "-o", tmp, obj, "-L" + lib, "-ltorch_python", "-ltorch", "-ltorch_cpu",
+                    "-ltorch_hip", "-lc10", "-lc10_hip", "-L" + HERE, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib], check=True)
+    os.replace(tmp, TORCH_OPS)
+
+
 def build(jobs=None, verbose=False):
     """Compile every HIP source and link the shared library; returns its path."""
     os.makedirs(BUILD, exist_ok=True)
     jobs = jobs or min(len(SOURCES), os.cpu_count() or 1)
     objs, procs, logs = [], [], {}
+    ops, ops_obj = torch_ops_object()
     pending = list(SOURCES)
     while pending or procs:
         while pending and len(procs) < jobs:
@@ -63,6 +91,10 @@ def build(jobs=None, verbose=False):
     cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objs]
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
+    out, _ = ops.communicate()
+    if ops.returncode != 0:
+        raise RuntimeError("%s failed on torch_ops.cpp:\n%s" % (CXX, out.decode(errors="replace")))
+    link_torch_ops(ops_obj)
     for name in PROBES:
         exe = os.path.join(HERE, name)
         tmp = exe + ".tmp%d" % os.getpid()

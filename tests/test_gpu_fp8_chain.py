@@ -2,12 +2,16 @@
 and a decoding step use it: every stage against its definition on what the
 stage before it gave, the whole against unquantised arithmetic, and the same
 captured in a graph and replayed."""
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
 
 from software_pipelined_tiled_02_amd import binding
 from tests import fp8_ref as R
+from tests.conftest import ROOT
 from tests.fp8_util import check_product, raw_of
 
 pytestmark = pytest.mark.gpu
@@ -91,23 +95,32 @@ def test_training_step_captured_and_replayed():
                                    eager[name].view(torch.uint8) if name == "q" else eager[name]), name
 
 
-def test_first_call_under_capture_is_refused():
-    """A device's first call sets it up, which a capture cannot hold: an error, not a broken graph."""
-    x = torch.ones((4, 256), device="cuda")
-    kept = dict(binding._HANDLES)
-    binding.quantize_fp8(x)
-    torch.cuda.synchronize()
-    saved = dict(binding._HANDLES)
+FIRST_CALL = """
+import torch
+from software_pipelined_tiled_02_amd import binding
+x = torch.ones((4, 256), device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
     try:
-        binding._HANDLES.clear()
-        g = torch.cuda.CUDAGraph()
-        with torch.cuda.graph(g):
-            with pytest.raises(RuntimeError, match="before the graph capture"):
-                binding.quantize_fp8(x)
-            x.add_(1.0)
-    finally:
-        binding._HANDLES.update(saved)
-        binding._HANDLES.update(kept)
+        binding.quantize_fp8(x)
+        raise SystemExit("not refused")
+    except RuntimeError as e:
+        assert "before the graph capture" in str(e), e
+    y = x + 1
+g.replay()
+q, s = binding.quantize_fp8(y)
+torch.cuda.synchronize()
+assert bool((q.float() * s.repeat_interleave(128, 1) == 2).all())
+print("refused, then fine")
+"""
+
+
+def test_first_call_under_capture_is_refused():
+    """A process's first call on a device sets it up, which a capture cannot
+    hold: an error, and neither a broken graph nor a broken process."""
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=ROOT, capture_output=True, text=True, timeout=100)
+    assert r.returncode == 0 and "refused, then fine" in r.stdout, r.stdout + r.stderr
 
 
 def test_threads_at_once():

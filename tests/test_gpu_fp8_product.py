@@ -255,7 +255,7 @@ def test_refusals():
         args.update(kw)
         with pytest.raises(ValueError):
             binding.run_fp8(**args)
-    with pytest.raises(KeyError):
+    with pytest.raises(ValueError):
         binding.run_fp8(a, s, a, s1, tile="1x1")
     with pytest.raises(binding.GemmError):
         binding.run_fp8(a, s, a, s1, out_dtype=torch.float32, tile="256x256")

@@ -93,7 +93,7 @@ def test_rows_at_any_address_and_nothing_else_written(ld, offset):
     buffer, of which only the rows change."""
     M, K = 35, 140
     rng = np.random.default_rng(ld + offset)
-    h = binding._handle(0)
+    g = binding.Gemm(0)
     for x in ("bf16", "f32"):
         t, x32 = source(rng, M, K, x)
         flat = torch.full((offset + M * (K + ld),), float("nan"), dtype=FT[x])
@@ -106,7 +106,7 @@ def test_rows_at_any_address_and_nothing_else_written(ld, offset):
             qb = torch.full((offset + (M + 1) * ldq,), 0x55, dtype=torch.uint8, device="cuda")
             tb = torch.full((offset + (K + 1) * ldqt,), 0x55, dtype=torch.uint8, device="cuda")
             sb, stb = torch.full((M + 1, nb + 1), 9.0, device="cuda"), torch.full((K + 1, mb + 1), 9.0, device="cuda")
-            binding.gemm_quantize_fp8(h, M, K, x, "e4m3", rows, 0, src, K + ld, qb.data_ptr() + offset, ldq, sb, nb + 1,
+            binding.gemm_quantize_fp8(g.h, M, K, x, "e4m3", rows, 0, src, K + ld, qb.data_ptr() + offset, ldq, sb, nb + 1,
                                       1, tb.data_ptr() + offset, ldqt, stb, mb + 1, 1)
             qv, tv = qb[offset:].as_strided((M, K), (ldq, 1)), tb[offset:].as_strided((K, M), (ldqt, 1))
             n, nt = (M, K) if rows == 1 else (1, nb)
