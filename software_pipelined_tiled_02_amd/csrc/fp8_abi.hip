@@ -26,7 +26,6 @@ struct Plan {
     gemm_fp8_info_t info;
     const void* fn;
     int64_t tiles_m, tiles_n;
-    bool vec_c, vec16_c;
 };
 
 // Every check of the product, then its kernel.  No HIP call.
@@ -88,8 +87,6 @@ int plan_product(int64_t M, int64_t N, int64_t K, int a_type, int b_type, int c_
     plan->tiles_n = has_c ? ceil_div(N, sh.bn) : 0;
     const int64_t grid = plan->tiles_m * plan->tiles_n;
     if (grid >= ((int64_t)1 << 32) / (64 * sh.waves)) return GEMM_ERR_UNSUPPORTED;
-    plan->vec_c = aligned(C, 4 * size_of(c_dtype)) && ldc % 4 == 0;
-    plan->vec16_c = aligned(C, 16) && ldc * size_of(c_dtype) % 16 == 0;
     gemm_fp8_info_t& in = plan->info;
     memset(&in, 0, sizeof in);
     in.tile = tc;
@@ -152,8 +149,6 @@ int gemm_run_fp8(gemm_handle_t h, int64_t M, int64_t N, int64_t K, int a_type, i
     a.tiles_n = (int32_t)plan.tiles_n;
     a.c_type = c_dtype;
     a.accumulate = accumulate;
-    a.vec_c = plan.vec_c;
-    a.vec16_c = plan.vec16_c;
     void* kargs[] = {&a};
     return pg::on_device(h, [&] {
         const hipError_t e = hipLaunchKernel(plan.fn, dim3((unsigned)plan.info.grid), dim3((unsigned)plan.info.threads),
@@ -199,9 +194,6 @@ int gemm_quantize_fp8(gemm_handle_t h, int64_t M, int64_t K, int x_dtype, int fp
     a.K = (int32_t)K;
     a.e5m2 = fp8_type == GEMM_E5M2;
     a.pow2 = pow2;
-    a.vec = aligned(X, 16) && ldx * sz % 16 == 0;
-    a.vecq = aligned(Q, 8) && ldq % 8 == 0;
-    a.vecqt = aligned(QT, 16) && ldqt % 16 == 0;
     return pg::on_device(h, [&] { return pg::launch_quantize(a, x_dtype, tile, (hipStream_t)stream); });
 }
 
@@ -248,15 +240,12 @@ int gemm_rms_fp8(gemm_handle_t h, int64_t M, int64_t D, int x_dtype, int w_dtype
     a.e5m2 = fp8_type == GEMM_E5M2;
     a.pow2 = pow2;
     a.w_f32 = w_dtype == GEMM_F32;
-    auto rows16 = [&](const void* p, int64_t ld) { return p == nullptr || (aligned(p, 16) && ld * sz % 16 == 0); };
-    a.vec = rows16(X, ldx) && rows16(R, ldr) && rows16(H, ldh) && rows16(Y, ldy) && aligned(W, 16) &&
-            (Q == nullptr || (aligned(Q, 8) && ldq % 8 == 0));
     return pg::on_device(h, [&] { return pg::launch_rms(a, x_dtype, (hipStream_t)stream); });
 }
 
 int64_t gemm_rms_backward_workspace(int64_t M, int64_t D) {
     if (M < 0 || D < 0 || M > GEMM_RMS_MAX_ROWS || D > GEMM_RMS_MAX_D) return 0;
-    return (int64_t)pg::rms_backward_groups(M, D, kDefaultCus) * D * 4;
+    return pg::rms_backward_groups(M, D, kDefaultCus) * pg::rms_parts_row(D) * 4;
 }
 
 int gemm_rms_backward(gemm_handle_t h, int64_t M, int64_t D, int x_dtype, int w_dtype, const void* DY, int64_t lddy,
@@ -294,8 +283,6 @@ int gemm_rms_backward(gemm_handle_t h, int64_t M, int64_t D, int x_dtype, int w_
     a.D = (int32_t)D;
     a.groups = pg::rms_backward_groups(M, D, kDefaultCus);
     a.w_f32 = w_dtype == GEMM_F32;
-    auto rows16 = [&](const void* p, int64_t ld) { return p == nullptr || (aligned(p, 16) && ld * sz % 16 == 0); };
-    a.vec = rows16(DY, lddy) && rows16(H, ldh) && rows16(DH, lddh) && rows16(DX, lddx) && aligned(W, 16);
     return pg::on_device(h, [&] { return pg::launch_rms_backward(a, x_dtype, (hipStream_t)stream); });
 }
 

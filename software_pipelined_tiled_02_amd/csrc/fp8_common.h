@@ -27,8 +27,7 @@ struct QuantizeArgs {
     float* ST;               // scale (row k or row block, m block) at k * st_row + mb * st_blk
     int64_t ldx, ldq, ldqt, s_row, s_blk, st_row, st_blk;
     int32_t M, K;
-    int32_t e5m2, pow2, vec; // vec: X's rows start on 16 bytes
-    int32_t vecq, vecqt;     // Q's rows start on 8 bytes, QT's on 16
+    int32_t e5m2, pow2;
 };
 
 struct RmsArgs {
@@ -43,7 +42,7 @@ struct RmsArgs {
     int64_t ldx, ldr, ldh, ldy, ldq, s_row, s_blk;
     int32_t M, D;
     float eps;
-    int32_t e5m2, pow2, vec, w_f32;   // vec: every row starts on 16 bytes (Q's on 8)
+    int32_t e5m2, pow2, w_f32;
 };
 
 struct RmsBackwardArgs {
@@ -53,11 +52,11 @@ struct RmsBackwardArgs {
     const float* rstd;
     const void* DH;          // gradient that reaches h from elsewhere, or NULL
     void* DX;
-    float* parts;            // [groups][D] partial sums of dw
+    float* parts;            // [groups][D rounded up to 4] partial sums of dw
     float* DW;
     int64_t lddy, ldh, lddh, lddx;
     int32_t M, D, groups;
-    int32_t vec, w_f32;
+    int32_t w_f32;
 };
 
 #if defined(__HIPCC__)
@@ -69,24 +68,26 @@ template <int XT> struct XTypeOf { typedef float type; };
 template <> struct XTypeOf<XT_F16> { typedef _Float16 type; };
 template <> struct XTypeOf<XT_BF16> { typedef __bf16 type; };
 
+// Accesses of 8 and 16 bytes at any address: gfx950 reads and writes them
+// whole, so rows need no alignment beyond their elements' (8192 x 9300 bf16
+// rows, 4 bytes off 16, element by element: three times the time).
+typedef i32x4q i32x4u __attribute__((aligned(1)));
+typedef i32x2q i32x2u __attribute__((aligned(1)));
+
 // Eight consecutive elements as they lie in memory; those at or past `n` are 0.
 template <int XT> struct Raw8 { typename XTypeOf<XT>::type v __attribute__((ext_vector_type(8))); };
-template <> struct Raw8<XT_F32> { float v __attribute__((ext_vector_type(8))); };
 
 template <int XT>
-__device__ __forceinline__ Raw8<XT> load_raw8(const void* base, int64_t at, int n, bool vec) {
+__device__ __forceinline__ Raw8<XT> load_raw8(const void* base, int64_t at, int n) {
     typedef typename XTypeOf<XT>::type T;
     const T* p = (const T*)base + at;
     Raw8<XT> r;
-    if (vec && n >= 8) {
+    if (n >= 8) {
         if constexpr (XT == XT_F32) {
-            typedef float f32x4v __attribute__((ext_vector_type(4)));
-            const f32x4v a = *(const f32x4v*)p, b = *(const f32x4v*)(p + 4);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) { r.v[e] = a[e]; r.v[4 + e] = b[e]; }
+            struct Two { i32x4q a, b; } two = {*(const i32x4u*)p, *(const i32x4u*)(p + 4)};
+            r = __builtin_bit_cast(Raw8<XT>, two);
         } else {
-            typedef T tx8 __attribute__((ext_vector_type(8)));
-            r.v = *(const tx8*)p;
+            r = __builtin_bit_cast(Raw8<XT>, (i32x4q)*(const i32x4u*)p);
         }
     } else {
 #pragma unroll
@@ -97,29 +98,29 @@ __device__ __forceinline__ Raw8<XT> load_raw8(const void* base, int64_t at, int 
 
 // The same as fp32.
 template <int XT>
-__device__ __forceinline__ void load8(const void* base, int64_t at, int n, bool vec, float (&f)[8]) {
-    const Raw8<XT> r = load_raw8<XT>(base, at, n, vec);
+__device__ __forceinline__ void load8(const void* base, int64_t at, int n, float (&f)[8]) {
+    const Raw8<XT> r = load_raw8<XT>(base, at, n);
 #pragma unroll
     for (int e = 0; e < 8; ++e) f[e] = (float)r.v[e];
 }
 
 // Eight consecutive elements rounded to the type (nearest even), those
-// before `n`; f receives the rounded values.
+// before `n`.
 template <int XT>
-__device__ __forceinline__ void store8(void* base, int64_t at, int n, bool vec, const float (&f)[8]) {
+__device__ __forceinline__ void store8(void* base, int64_t at, int n, const float (&f)[8]) {
     typedef typename XTypeOf<XT>::type T;
     T* p = (T*)base + at;
-    if (vec && n >= 8) {
-        if constexpr (XT == XT_F32) {
-            typedef float f32x4v __attribute__((ext_vector_type(4)));
-            *(f32x4v*)p = f32x4v{f[0], f[1], f[2], f[3]};
-            *(f32x4v*)(p + 4) = f32x4v{f[4], f[5], f[6], f[7]};
-        } else {
-            typedef T tx8 __attribute__((ext_vector_type(8)));
-            tx8 v;
+    if (n >= 8) {
+        Raw8<XT> r;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = (T)f[e];
-            *(tx8*)p = v;
+        for (int e = 0; e < 8; ++e) r.v[e] = (T)f[e];
+        if constexpr (XT == XT_F32) {
+            struct Two { i32x4q a, b; };
+            const Two two = __builtin_bit_cast(Two, r);
+            *(i32x4u*)p = two.a;
+            *(i32x4u*)(p + 4) = two.b;
+        } else {
+            *(i32x4u*)p = __builtin_bit_cast(i32x4q, r);
         }
     } else {
 #pragma unroll
@@ -192,9 +193,9 @@ __device__ __forceinline__ float amax8(const float (&f)[8]) {
 }
 
 // Eight 8-bit values to a row, those before `n`.
-__device__ __forceinline__ void store_fp8x8(uint8_t* p, int n, bool vec, i32x2q v) {
-    if (vec && n >= 8) {
-        *(i32x2q*)p = v;
+__device__ __forceinline__ void store_fp8x8(uint8_t* p, int n, i32x2q v) {
+    if (n >= 8) {
+        *(i32x2u*)p = v;
     } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
@@ -211,6 +212,7 @@ int quantize_rows_per_group(int64_t M, int64_t K, bool tile);
 hipError_t launch_rms(const RmsArgs& a, int xtype, hipStream_t stream);
 hipError_t launch_rms_backward(const RmsBackwardArgs& a, int xtype, hipStream_t stream);
 int rms_backward_groups(int64_t M, int64_t D, int num_cus);
+constexpr int64_t rms_parts_row(int64_t D) { return (D + 3) / 4 * 4; }
 
 }  // namespace pg
 

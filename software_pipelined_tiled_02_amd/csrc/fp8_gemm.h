@@ -45,8 +45,6 @@ struct Fp8Args {
     int32_t tiles_m, tiles_n;
     int32_t c_type;          // XT_*
     int32_t accumulate;      // C += (fp32)
-    int32_t vec_c;           // four neighbouring outputs are one aligned store
-    int32_t vec16_c;         // C's rows start on 16 bytes
 };
 
 // Tile classes: the workgroup's part of C, its waves, and how many of them
@@ -209,9 +207,9 @@ template <bool EXACT>
 __device__ __forceinline__ void store_c(const Fp8Args& a, int64_t m, int64_t n, f32x4 v) {
     if constexpr (EXACT) {
         float* p = (float*)a.C + m * a.ldc + n;
-        if (a.vec_c && n + 4 <= a.N) {
-            if (a.accumulate) v += *(const f32x4*)p;
-            *(f32x4*)p = v;
+        if (n + 4 <= a.N) {
+            if (a.accumulate) v += __builtin_bit_cast(f32x4, (i32x4q)*(const i32x4u*)p);
+            *(i32x4u*)p = __builtin_bit_cast(i32x4q, v);
         } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
@@ -220,8 +218,8 @@ __device__ __forceinline__ void store_c(const Fp8Args& a, int64_t m, int64_t n, 
     } else {
         uint16_t* p = (uint16_t*)a.C + m * a.ldc + n;
         const i32x2 w = to_16(v, a.c_type);
-        if (a.vec_c && n + 4 <= a.N) {
-            *(i32x2*)p = w;
+        if (n + 4 <= a.N) {
+            *(i32x2u*)p = w;
         } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
@@ -246,7 +244,7 @@ __device__ __forceinline__ void store_block(const Fp8Args& a, uint8_t PG_LDS* sm
                                             const f32x4 (&acc)[FM][FN]) {
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     constexpr int SIZE = EXACT ? 4 : 2, ROW = strip_row(FN, SIZE), CHUNKS = FN * SIZE;   // 16-byte chunks of a row
-    if (a.vec16_c && m0 + 16 * FM <= a.M && n0 + 16 * FN <= a.N) {
+    if (m0 + 16 * FM <= a.M && n0 + 16 * FN <= a.N) {
         uint8_t PG_LDS* strip = smem + wave * 16 * ROW;     // (a wave's LDS accesses keep their order)
 #pragma unroll
         for (int i = 0; i < FM; ++i) {
@@ -261,9 +259,9 @@ __device__ __forceinline__ void store_block(const Fp8Args& a, uint8_t PG_LDS* sm
                 const int row = (q * 64 + lane) / CHUNKS, c = (q * 64 + lane) % CHUNKS;
                 if (row >= 16) break;
                 i32x4 v = *(const i32x4 PG_LDS*)(strip + row * ROW + c * 16);
-                i32x4* dst = (i32x4*)((uint8_t*)a.C + ((int64_t)(m0 + 16 * i + row) * a.ldc + n0) * SIZE + c * 16);
+                i32x4u* dst = (i32x4u*)((uint8_t*)a.C + ((int64_t)(m0 + 16 * i + row) * a.ldc + n0) * SIZE + c * 16);
                 if constexpr (EXACT)
-                    if (a.accumulate) v = __builtin_bit_cast(i32x4, __builtin_bit_cast(f32x4, v) + *(const f32x4*)dst);
+                    if (a.accumulate) v = __builtin_bit_cast(i32x4, __builtin_bit_cast(f32x4, v) + __builtin_bit_cast(f32x4, (i32x4)*dst));
                 if constexpr (STREAM) __builtin_nontemporal_store(v, dst);
                 else *dst = v;
             }

@@ -26,7 +26,7 @@ __global__ void __launch_bounds__(256) quantize_rows(QuantizeArgs a) {
 #pragma unroll
     for (int i = 0; i < R; ++i) {
         const int64_t m = m0 + 16 * i;
-        load8<XT>(a.X, m < a.M ? m * a.ldx + k0 : 0, m < a.M ? n : 0, a.vec, f[i]);
+        load8<XT>(a.X, m < a.M ? m * a.ldx + k0 : 0, m < a.M ? n : 0, f[i]);
     }
 #pragma unroll
     for (int i = 0; i < R; ++i) {
@@ -34,73 +34,84 @@ __global__ void __launch_bounds__(256) quantize_rows(QuantizeArgs a) {
         const float s = block_scale(max16(amax8(f[i])), a.e5m2, a.pow2);
         const i32x2q v = to_fp8x8(f[i], 1.0f / s, a.e5m2);
         if (m < a.M) {
-            store_fp8x8(a.Q + m * a.ldq + k0, n, a.vecq, v);
+            store_fp8x8(a.Q + m * a.ldq + k0, n, v);
             if (c == 0) a.S[m * a.s_row + kb * a.s_blk] = s;
         }
     }
 }
 
-// A 128 x 128 tile per workgroup: thread (c, g) holds the 8 x 8 values of
-// rows 8 g .. and columns 8 c ...  The 16 threads of a row block are lanes of
+// A 128 x 128 tile per workgroup: thread (c, g) holds the R x 8 values of
+// rows R g .. and columns 8 c ...  The 16 threads of a row block are lanes of
 // one 16-lane row, those of a column are spread over the waves, so column
 // (and tile) maxima pass through LDS.  The transposed bytes pass through LDS
-// too: written 8 at a time, they leave in rows of 128.
-template <int XT, bool TILE>
-__global__ void __launch_bounds__(256) quantize_tile(QuantizeArgs a) {
+// too: written R at a time, they leave in rows of 128.
+// Measured with both directions, bf16, rows: 8192^2 48.3 us at R = 4 (5.6
+// TB/s), 50.8 at 8, 64.6 at 2; but with one tile per CU or fewer a thread's own
+// arithmetic counts (66 x 320: 9.8 us at R = 8, 6.2 at 2).
+template <int XT, bool TILE, int R>
+__global__ void __launch_bounds__(2048 / R) quantize_tile(QuantizeArgs a) {
     constexpr int LD = kBlock + 16;              // a transposed row in LDS
+    constexpr int T = 2048 / R, WAVES = T / 64;
     __shared__ __attribute__((aligned(16))) uint8_t tr[kBlock * LD];
-    __shared__ float part[4][kBlock];
+    __shared__ float part[WAVES][kBlock];
     const int tid = threadIdx.x, c = tid & 15, g = tid >> 4, wave = tid >> 6, lane = tid & 63;
     const unsigned kblocks = (unsigned)((a.K + kBlock - 1) / kBlock);
     const int64_t kb = blockIdx.x % kblocks, mb = blockIdx.x / kblocks;
-    const int64_t k0 = kb * kBlock + c * 8, m0 = mb * kBlock + g * 8;
+    const int64_t k0 = kb * kBlock + c * 8, m0 = mb * kBlock + g * R;
     const int n = (int)min((int64_t)8, max((int64_t)0, a.K - k0));
-    float f[8][8];
+    float f[R][8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < R; ++i) {
         const int64_t m = m0 + i;
-        load8<XT>(a.X, m < a.M ? m * a.ldx + k0 : 0, m < a.M ? n : 0, a.vec, f[i]);
+        load8<XT>(a.X, m < a.M ? m * a.ldx + k0 : 0, m < a.M ? n : 0, f[i]);
     }
-    float s_tile = 0.0f, col[8];
+    float r_tile = 0.0f, col[8];                 // reciprocal scales
     if constexpr (TILE) {
         float m = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m = fmaxf(m, amax8(f[i]));
+        for (int i = 0; i < R; ++i) m = fmaxf(m, amax8(f[i]));
         m = max16(m);
         m = fmaxf(m, __shfl_xor(m, 16));
         m = fmaxf(m, __shfl_xor(m, 32));
         if (lane == 0) part[0][wave] = m;
         __syncthreads();
-        m = fmaxf(fmaxf(part[0][0], part[0][1]), fmaxf(part[0][2], part[0][3]));
-        s_tile = block_scale(m, a.e5m2, a.pow2);
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) m = fmaxf(m, part[0][w]);
+        const float s = block_scale(m, a.e5m2, a.pow2);
+        r_tile = 1.0f / s;
         if (tid == 0) {
-            if (a.Q != nullptr) a.S[mb * a.s_row + kb * a.s_blk] = s_tile;
-            if (a.QT != nullptr) a.ST[kb * a.st_row + mb * a.st_blk] = s_tile;
+            if (a.Q != nullptr) a.S[mb * a.s_row + kb * a.s_blk] = s;
+            if (a.QT != nullptr) a.ST[kb * a.st_row + mb * a.st_blk] = s;
         }
     } else {
+        // a column's maximum over the wave's rows, then over the waves: one
+        // thread per column finishes it, and leaves the reciprocal for all
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             float m = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(f[i][j]));
+            for (int i = 0; i < R; ++i) m = fmaxf(m, fabsf(f[i][j]));
             m = fmaxf(m, __shfl_xor(m, 16));
             m = fmaxf(m, __shfl_xor(m, 32));
             if (lane < 16) part[wave][c * 8 + j] = m;
         }
         __syncthreads();
+        if (tid < kBlock) {
+            float m = part[0][tid];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int k = c * 8 + j;
-            col[j] = block_scale(fmaxf(fmaxf(part[0][k], part[1][k]), fmaxf(part[2][k], part[3][k])), a.e5m2, a.pow2);
-            if (g == 0 && j < n) a.ST[(k0 + j) * a.st_row + mb * a.st_blk] = col[j];
-            col[j] = 1.0f / col[j];
+            for (int w = 1; w < WAVES; ++w) m = fmaxf(m, part[w][tid]);
+            const float s = block_scale(m, a.e5m2, a.pow2);
+            const int64_t k = kb * kBlock + tid;
+            if (k < a.K) a.ST[k * a.st_row + mb * a.st_blk] = s;
+            part[0][tid] = 1.0f / s;
         }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) col[j] = part[0][c * 8 + j];
     }
-    const float r_tile = TILE ? 1.0f / s_tile : 0.0f;
-    uint32_t lo[8], hi[8];                       // TILE: the rows' bytes, for the transposed copy
     if (a.Q != nullptr) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < R; ++i) {
             const int64_t m = m0 + i;
             float r = r_tile;
             if constexpr (!TILE) {
@@ -109,29 +120,35 @@ __global__ void __launch_bounds__(256) quantize_tile(QuantizeArgs a) {
                 if (c == 0 && m < a.M) a.S[m * a.s_row + kb * a.s_blk] = s;
             }
             const i32x2q v = to_fp8x8(f[i], r, a.e5m2);
-            if (m < a.M) store_fp8x8(a.Q + m * a.ldq + k0, n, a.vecq, v);
+            if (m < a.M) store_fp8x8(a.Q + m * a.ldq + k0, n, v);
         }
     }
     if (a.QT == nullptr) return;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         const float r = TILE ? r_tile : col[j];
-        lo[j] = to_fp8x4(f[0][j] * r, f[1][j] * r, f[2][j] * r, f[3][j] * r, a.e5m2);
-        hi[j] = to_fp8x4(f[4][j] * r, f[5][j] * r, f[6][j] * r, f[7][j] * r, a.e5m2);
-        *(i32x2q*)(tr + (c * 8 + j) * LD + g * 8) = i32x2q{(int)lo[j], (int)hi[j]};
+        uint8_t* to = tr + (c * 8 + j) * LD + g * R;
+        if constexpr (R == 2) {
+            *(uint16_t*)to = (uint16_t)to_fp8x4(f[0][j] * r, f[1][j] * r, 0.0f, 0.0f, a.e5m2);
+        } else {
+#pragma unroll
+            for (int q = 0; q < R / 4; ++q)
+                *(int*)(to + 4 * q) = to_fp8x4(f[4 * q][j] * r, f[4 * q + 1][j] * r, f[4 * q + 2][j] * r,
+                                               f[4 * q + 3][j] * r, a.e5m2);
+        }
     }
     __syncthreads();
     const int64_t mt = mb * kBlock + (tid & 7) * 16;
     const int nt = (int)min((int64_t)16, a.M - mt);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int row = i * 32 + (tid >> 3);
+    for (int i = 0; i < kBlock * 8 / T; ++i) {
+        const int row = i * (T / 8) + (tid >> 3);
         const int64_t k = kb * kBlock + row;
         if (k >= a.K || nt <= 0) continue;
         const i32x4q v = *(const i32x4q*)(tr + row * LD + (tid & 7) * 16);
         uint8_t* dst = a.QT + k * a.ldqt + mt;
-        if (a.vecqt && nt == 16) {
-            *(i32x4q*)dst = v;
+        if (nt == 16) {
+            *(i32x4u*)dst = v;
         } else {
 #pragma unroll
             for (int e = 0; e < 16; ++e)
@@ -140,15 +157,23 @@ __global__ void __launch_bounds__(256) quantize_tile(QuantizeArgs a) {
     }
 }
 
+constexpr unsigned kFewTiles = 256;      // one per CU (4096 x 2048, 512 tiles: 10.3 us at R = 4, 12.2 at 2)
+
 template <int XT>
 hipError_t launch(const QuantizeArgs& a, bool tile, hipStream_t stream) {
     const int rows = quantize_rows_per_group(a.M, a.K, tile || a.QT != nullptr);
     const dim3 grid((unsigned)(((int64_t)a.K + kBlock - 1) / kBlock * (((int64_t)a.M + rows - 1) / rows)));
-    if (tile)
-        hipLaunchKernelGGL((quantize_tile<XT, true>), grid, dim3(256), 0, stream, a);
-    else if (a.QT != nullptr)
-        hipLaunchKernelGGL((quantize_tile<XT, false>), grid, dim3(256), 0, stream, a);
-    else if (rows == 16)
+    if (tile || a.QT != nullptr) {
+        const bool few = grid.x <= kFewTiles;
+        if (tile && few)
+            hipLaunchKernelGGL((quantize_tile<XT, true, 2>), grid, dim3(1024), 0, stream, a);
+        else if (tile)
+            hipLaunchKernelGGL((quantize_tile<XT, true, 4>), grid, dim3(512), 0, stream, a);
+        else if (few)
+            hipLaunchKernelGGL((quantize_tile<XT, false, 2>), grid, dim3(1024), 0, stream, a);
+        else
+            hipLaunchKernelGGL((quantize_tile<XT, false, 4>), grid, dim3(512), 0, stream, a);
+    } else if (rows == 16)
         hipLaunchKernelGGL((quantize_rows<XT, 1>), grid, dim3(256), 0, stream, a);
     else
         hipLaunchKernelGGL((quantize_rows<XT, 4>), grid, dim3(256), 0, stream, a);

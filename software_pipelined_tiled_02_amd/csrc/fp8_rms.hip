@@ -34,11 +34,11 @@ __device__ __forceinline__ float row_sum(float x, float* red) {
 }
 
 template <int XT>
-__device__ __forceinline__ void load_w(const void* W, int64_t at, int n, bool vec, bool w_f32, float (&w)[8]) {
+__device__ __forceinline__ void load_w(const void* W, int64_t at, int n, bool w_f32, float (&w)[8]) {
     if (w_f32)
-        load8<XT_F32>(W, at, n, vec, w);
+        load8<XT_F32>(W, at, n, w);
     else
-        load8<XT>(W, at, n, vec, w);
+        load8<XT>(W, at, n, w);
 }
 
 template <int XT, int TPR, int NC>
@@ -54,14 +54,14 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rms_kernel(RmsArgs a) {
     for (int i = 0; i < NC; ++i) {
         const int64_t k = ((int64_t)i * TPR + t) * 8;
         const int n = (int)min((int64_t)8, max((int64_t)0, a.D - k));
-        load8<XT>(a.X, n > 0 ? m * a.ldx + k : 0, n, a.vec, f[i]);
+        load8<XT>(a.X, n > 0 ? m * a.ldx + k : 0, n, f[i]);
         if (a.R != nullptr) {
             float r[8];
-            load8<XT>(a.R, n > 0 ? m * a.ldr + k : 0, n, a.vec, r);
+            load8<XT>(a.R, n > 0 ? m * a.ldr + k : 0, n, r);
 #pragma unroll
             for (int e = 0; e < 8; ++e) f[i][e] = rounded<XT>(f[i][e] + r[e]);
         }
-        if (a.H != nullptr && n > 0) store8<XT>(a.H, m * a.ldh + k, n, a.vec, f[i]);
+        if (a.H != nullptr && n > 0) store8<XT>(a.H, m * a.ldh + k, n, f[i]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) sq += f[i][e] * f[i][e];
     }
@@ -73,52 +73,66 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rms_kernel(RmsArgs a) {
         const int64_t k = ((int64_t)i * TPR + t) * 8;
         const int n = (int)min((int64_t)8, max((int64_t)0, a.D - k));
         float w[8];
-        load_w<XT>(a.W, n > 0 ? k : 0, n, a.vec, a.w_f32, w);
+        load_w<XT>(a.W, n > 0 ? k : 0, n, a.w_f32, w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[i][e] = f[i][e] * rstd * w[e];
-        if (a.Y != nullptr && n > 0) store8<XT>(a.Y, m * a.ldy + k, n, a.vec, f[i]);
+        if (a.Y != nullptr && n > 0) store8<XT>(a.Y, m * a.ldy + k, n, f[i]);
         if (a.Q != nullptr) {
             const float s = block_scale(max16(amax8(f[i])), a.e5m2, a.pow2);
             const i32x2q v = to_fp8x8(f[i], 1.0f / s, a.e5m2);
             if (n > 0) {
-                store_fp8x8(a.Q + m * a.ldq + k, n, a.vec, v);
+                store_fp8x8(a.Q + m * a.ldq + k, n, v);
                 if ((t & 15) == 0) a.S[m * a.s_row + (k / kBlock) * a.s_blk] = s;
             }
         }
     }
 }
 
+// How a backward pass holds its rows.  kAhead: in registers, the next row
+// loaded before the current one's sum, so that two rows per group are on
+// their way (8192 x 4096 bf16: 86 us without, 53 with).  kHold: in registers,
+// one at a time.  kTwice: read for the sum and again (from the caches) for dx.
+// The longer the row, the fewer registers a thread has for each value of it:
+// 8192 values and fewer go ahead (16-bit ones up to 12288); a form that spills
+// costs more than it gives (4096 x 16384 bf16: 242 us ahead, 116 held).
+enum Holding { kAhead, kHold, kTwice };
+
 // Row group g of `groups` takes rows g, g + groups, ...: it keeps its part
-// of dw in registers over them and writes it once, to parts[g].  AHEAD: the
-// next row is loaded before the current one's sum, so that two rows per
-// group are on their way (8192 x 4096: 86 us without it, 53 with it).  Rows of more
-// than 8192 values leave a thread no registers for that, and have loads enough in flight.
-template <int XT, int TPR, int NC, bool AHEAD>
+// of dw in registers over them and writes it once, to parts[g].
+template <int XT, int TPR, int NC, int HOLDING>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rms_backward_kernel(RmsBackwardArgs a) {
     __shared__ float red[2][TPR > 64 ? TPR / 64 : 1];
     constexpr int RPW = TPR < 256 ? 256 / TPR : 1;
+    constexpr bool KEEP = HOLDING == kAhead;                 // the weight stays in registers too
+    constexpr int NH = HOLDING == kTwice ? 1 : NC;
     const int t = threadIdx.x % TPR;
     const int group = blockIdx.x * RPW + threadIdx.x / TPR;
     if (group >= a.groups) return;                           // whole waves, RPW > 1 only
     struct Row {
-        Raw8<XT> dy[NC], h[NC], dh[NC];
+        Raw8<XT> dy[NH], h[NH], dh[NH];
         float rstd;
+    };
+    auto load_part = [&](Row& x, int64_t m, int i, bool with_dh) {
+        const int k = (i * TPR + t) * 8, n = min(8, max(0, a.D - k)), q = HOLDING == kTwice ? 0 : i;
+        x.dy[q] = load_raw8<XT>(a.DY, n > 0 ? m * a.lddy + k : 0, n);
+        x.h[q] = load_raw8<XT>(a.H, n > 0 ? m * a.ldh + k : 0, n);
+        if (with_dh && a.DH != nullptr) x.dh[q] = load_raw8<XT>(a.DH, n > 0 ? m * a.lddh + k : 0, n);
     };
     auto load_row = [&](Row& x, int64_t m) {
         x.rstd = a.rstd[m];
+        if constexpr (HOLDING != kTwice) {
 #pragma unroll
-        for (int i = 0; i < NC; ++i) {
-            const int k = (i * TPR + t) * 8, n = min(8, max(0, a.D - k));
-            x.dy[i] = load_raw8<XT>(a.DY, n > 0 ? m * a.lddy + k : 0, n, a.vec);
-            x.h[i] = load_raw8<XT>(a.H, n > 0 ? m * a.ldh + k : 0, n, a.vec);
-            if (a.DH != nullptr) x.dh[i] = load_raw8<XT>(a.DH, n > 0 ? m * a.lddh + k : 0, n, a.vec);
+            for (int i = 0; i < NC; ++i) load_part(x, m, i, true);
         }
     };
-    float w[NC][8], dw[NC][8];
+    auto weight = [&](int i, float (&w)[8]) {
+        const int k = (i * TPR + t) * 8, n = min(8, max(0, a.D - k));
+        load_w<XT>(a.W, n > 0 ? k : 0, n, a.w_f32, w);
+    };
+    float kept[KEEP ? NC : 1][8], dw[NC][8];
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-        const int k = (i * TPR + t) * 8, n = min(8, max(0, a.D - k));
-        load_w<XT>(a.W, n > 0 ? k : 0, n, a.vec, a.w_f32, w[i]);
+        if constexpr (KEEP) weight(i, kept[i]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) dw[i][e] = 0.0f;
     }
@@ -128,40 +142,47 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rms_backward_kernel(Rms
     for (int64_t m = group; m < a.M; m += a.groups) {
         Row next;
         const bool more = m + a.groups < a.M;
-        if (AHEAD && more) load_row(next, m + a.groups);
+        if (HOLDING == kAhead && more) load_row(next, m + a.groups);
         float dot = 0.0f;
 #pragma unroll
-        for (int i = 0; i < NC; ++i)
+        for (int i = 0; i < NC; ++i) {
+            const int q = HOLDING == kTwice ? 0 : i;
+            if constexpr (HOLDING == kTwice) load_part(x, m, i, false);
+            if constexpr (!KEEP) weight(i, kept[0]);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float dy = (float)x.dy[i].v[e], h = (float)x.h[i].v[e];
+                const float dy = (float)x.dy[q].v[e], h = (float)x.h[q].v[e];
                 dw[i][e] += dy * (h * x.rstd);
-                dot += dy * w[i][e] * h;
+                dot += dy * kept[KEEP ? i : 0][e] * h;
             }
+            if constexpr (HOLDING == kTwice) __builtin_amdgcn_sched_barrier(0);
+        }
         dot = row_sum<TPR>(dot, red[turn]);
         turn ^= 1;
         const float c = x.rstd * x.rstd * (dot / (float)a.D);
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
-            const int k = (i * TPR + t) * 8, n = min(8, max(0, a.D - k));
+            const int k = (i * TPR + t) * 8, n = min(8, max(0, a.D - k)), q = HOLDING == kTwice ? 0 : i;
             float dx[8];
+            if constexpr (HOLDING == kTwice) load_part(x, m, i, true);
+            if constexpr (!KEEP) weight(i, kept[0]);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                dx[e] = x.rstd * ((float)x.dy[i].v[e] * w[i][e] - (float)x.h[i].v[e] * c);
-                if (a.DH != nullptr) dx[e] += (float)x.dh[i].v[e];
+                dx[e] = x.rstd * ((float)x.dy[q].v[e] * kept[KEEP ? i : 0][e] - (float)x.h[q].v[e] * c);
+                if (a.DH != nullptr) dx[e] += (float)x.dh[q].v[e];
             }
-            if (n > 0) store8<XT>(a.DX, m * a.lddx + k, n, a.vec, dx);
+            if (n > 0) store8<XT>(a.DX, m * a.lddx + k, n, dx);
+            if constexpr (HOLDING == kTwice) __builtin_amdgcn_sched_barrier(0);
         }
         if (more) {
-            if constexpr (AHEAD) x = next;
+            if constexpr (HOLDING == kAhead) x = next;
             else load_row(x, m + a.groups);
         }
     }
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
         const int k = (i * TPR + t) * 8, n = min(8, max(0, a.D - k));
-        // parts' rows are D values: on 16 bytes where D is a multiple of 4
-        if (n > 0) store8<XT_F32>(a.parts, (int64_t)group * a.D + k, n, (a.D & 3) == 0, dw[i]);
+        if (n > 0) store8<XT_F32>(a.parts, group * rms_parts_row(a.D) + k, n, dw[i]);
     }
 }
 
@@ -174,16 +195,10 @@ __global__ void __launch_bounds__(256) rms_backward_sum(RmsBackwardArgs a) {
     const int c = threadIdx.x & 3, g = threadIdx.x >> 2;
     const int k = blockIdx.x * 16 + c * 4;
     f32x4v s = {0.0f, 0.0f, 0.0f, 0.0f};
-    if ((a.D & 3) == 0) {
-        if (k < a.D) {
+    if (k < a.D) {       // (past D, to the row's end, whatever lies there goes into sums that nobody stores)
+        const int64_t row = rms_parts_row(a.D);
 #pragma unroll 8
-            for (int p = g; p < a.groups; p += 64) s += *(const f32x4v*)(a.parts + (int64_t)p * a.D + k);
-        }
-    } else {
-        for (int p = g; p < a.groups; p += 64)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (k + e < a.D) s[e] += a.parts[(int64_t)p * a.D + k + e];
+        for (int p = g; p < a.groups; p += 64) s += *(const f32x4v*)(a.parts + p * row + k);
     }
     red[g][c] = s;
     __syncthreads();
@@ -215,11 +230,11 @@ hipError_t forward_for(const RmsArgs& a, hipStream_t stream) {
     return forward<XT, 1024, 4>(a, stream);
 }
 
-template <int XT, int TPR, int NC, bool AHEAD>
+template <int XT, int TPR, int NC, int HOLDING>
 hipError_t backward(const RmsBackwardArgs& a, hipStream_t stream) {
     constexpr int RPW = TPR < 256 ? 256 / TPR : 1;
     if (a.groups > 0) {                  // no rows: dw is zero
-        hipLaunchKernelGGL((rms_backward_kernel<XT, TPR, NC, AHEAD>), dim3((unsigned)((a.groups + RPW - 1) / RPW)),
+        hipLaunchKernelGGL((rms_backward_kernel<XT, TPR, NC, HOLDING>), dim3((unsigned)((a.groups + RPW - 1) / RPW)),
                            dim3(TPR < 256 ? 256 : TPR), 0, stream, a);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
@@ -230,13 +245,14 @@ hipError_t backward(const RmsBackwardArgs& a, hipStream_t stream) {
 
 template <int XT>
 hipError_t backward_for(const RmsBackwardArgs& a, hipStream_t stream) {
-    if (a.D <= 512) return backward<XT, 64, 1, true>(a, stream);
-    if (a.D <= 1024) return backward<XT, 64, 2, true>(a, stream);
-    if (a.D <= 2048) return backward<XT, 256, 1, true>(a, stream);
-    if (a.D <= 4096) return backward<XT, 256, 2, true>(a, stream);
-    if (a.D <= 8192) return backward<XT, 512, 2, true>(a, stream);
-    if (a.D <= 16384) return backward<XT, 1024, 2, false>(a, stream);
-    return backward<XT, 1024, 4, false>(a, stream);
+    if (a.D <= 512) return backward<XT, 64, 1, kAhead>(a, stream);
+    if (a.D <= 1024) return backward<XT, 64, 2, kAhead>(a, stream);
+    if (a.D <= 2048) return backward<XT, 256, 1, kAhead>(a, stream);
+    if (a.D <= 4096) return backward<XT, 256, 2, kAhead>(a, stream);
+    if (a.D <= 8192) return backward<XT, 512, 2, kAhead>(a, stream);
+    if (a.D <= 12288 && XT != XT_F32) return backward<XT, 512, 3, XT == XT_F32 ? kHold : kAhead>(a, stream);
+    if (a.D <= 16384) return backward<XT, 1024, 2, kHold>(a, stream);
+    return backward<XT, 1024, 4, kTwice>(a, stream);
 }
 
 }  // namespace
