@@ -349,7 +349,7 @@ int gemm_occupancy(gemm_handle_t h, int64_t M, int64_t N, int64_t K, int dtype, 
  * its block an infinite scale (every value of it then stands for NaN).
  *
  * All of these are asynchronous, allocate nothing, and enqueue one kernel
- * (gemm_rms_backward: two) on `stream`, on the handle's device; any
+ * (gemm_rms_backward: up to two) on `stream`, on the handle's device; any
  * number of calls may overlap, on any streams (gemm_rms_backward: each with its own
  * workspace).  A captured graph can hold them.  Outputs must not overlap
  * inputs or one another, but where stated.  Sizes of zero are accepted. */
@@ -445,7 +445,8 @@ int gemm_rms_fp8(gemm_handle_t h, int64_t M, int64_t D, int x_dtype, int w_dtype
  * DH (may be NULL): the gradient that reaches h from elsewhere.  dx is the
  * gradient of x and of the residual alike; DX may be DY, DH or H (in place).  DW: D
  * fp32 values, overwritten; rows are added in a fixed order.  workspace:
- * gemm_rms_backward_workspace bytes of device memory, 16-byte aligned, any contents. */
+ * gemm_rms_backward_workspace bytes of device memory, 16-byte aligned, any
+ * contents (few rows take none: 0, NULL). */
 int gemm_rms_backward(gemm_handle_t h, int64_t M, int64_t D, int x_dtype, int w_dtype,
                       const void *DY, int64_t lddy, const void *H, int64_t ldh, const void *W, const float *rstd,
                       const void *DH, int64_t lddh, void *DX, int64_t lddx, float *DW,

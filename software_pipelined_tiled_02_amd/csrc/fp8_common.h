@@ -55,8 +55,10 @@ struct RmsBackwardArgs {
     float* parts;            // [groups][D rounded up to 4] partial sums of dw
     float* DW;
     int64_t lddy, ldh, lddh, lddx;
-    int32_t M, D, groups;
+    int32_t M, D, groups;    // groups: parts of dw
     int32_t w_f32;
+    int32_t in_place;        // DX's bytes meet DY's or H's
+    int32_t by_columns;
 };
 
 #if defined(__HIPCC__)
@@ -74,34 +76,63 @@ template <> struct XTypeOf<XT_BF16> { typedef __bf16 type; };
 typedef i32x4q i32x4u __attribute__((aligned(1)));
 typedef i32x2q i32x2u __attribute__((aligned(1)));
 
-// Eight consecutive elements as they lie in memory; those at or past `n` are 0.
+// Eight consecutive elements as they lie in memory.
 template <int XT> struct Raw8 { typename XTypeOf<XT>::type v __attribute__((ext_vector_type(8))); };
 
+// Elements k .. k + 7 of a row, of which the row has the first `n`; element k
+// lies at base + at.  Where the row ends among them the access moves back to
+// end with it, and settle8, called when the values are needed, moves them to
+// their places: element by element, each load is waited for on the spot
+// (norm's backward pass in bf16, 7763 x 276: 21.6 us against 16.0).  The
+// elements in front are dropped, so they may be changing.
 template <int XT>
-__device__ __forceinline__ Raw8<XT> load_raw8(const void* base, int64_t at, int n) {
+__device__ __forceinline__ Raw8<XT> fetch8(const void* base, int64_t at, int64_t k, int n) {
     typedef typename XTypeOf<XT>::type T;
     const T* p = (const T*)base + at;
     Raw8<XT> r;
-    if (n >= 8) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) r.v[e] = (T)0.0f;
+    if (n >= 8 || (n > 0 && k >= 8)) {
+        p -= 8 - min(n, 8);
         if constexpr (XT == XT_F32) {
             struct Two { i32x4q a, b; } two = {*(const i32x4u*)p, *(const i32x4u*)(p + 4)};
             r = __builtin_bit_cast(Raw8<XT>, two);
         } else {
             r = __builtin_bit_cast(Raw8<XT>, (i32x4q)*(const i32x4u*)p);
         }
-    } else {
+    } else if (n > 0) {                      // a row of less than 8
 #pragma unroll
-        for (int e = 0; e < 8; ++e) r.v[e] = e < n ? p[e] : (T)0.0f;
+        for (int e = 0; e < 7; ++e)
+            if (e < n) r.v[e] = p[e];
     }
     return r;
 }
 
-// The same as fp32.
+// The n elements at their places, zeros behind them.
 template <int XT>
-__device__ __forceinline__ void load8(const void* base, int64_t at, int n, float (&f)[8]) {
-    const Raw8<XT> r = load_raw8<XT>(base, at, n);
+__device__ __forceinline__ void settle8(Raw8<XT>& r, int64_t k, int n) {
+    typedef typename XTypeOf<XT>::type T;
+    if (n <= 0 || n >= 8 || k < 8) return;
+#pragma unroll
+    for (int by = 4; by > 0; by >>= 1)
+        if ((8 - n) & by) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) r.v[e] = e + by < 8 ? r.v[e + by < 8 ? e + by : 0] : (T)0.0f;
+        }
+}
+
+template <int XT>
+__device__ __forceinline__ void to_f32(const Raw8<XT>& r, float (&f)[8]) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) f[e] = (float)r.v[e];
+}
+
+// Both, and the values as fp32.
+template <int XT>
+__device__ __forceinline__ void load8(const void* base, int64_t at, int64_t k, int n, float (&f)[8]) {
+    Raw8<XT> r = fetch8<XT>(base, at, k, n);
+    settle8<XT>(r, k, n);
+    to_f32<XT>(r, f);
 }
 
 // Eight consecutive elements rounded to the type (nearest even), those
@@ -211,7 +242,13 @@ hipError_t launch_quantize(const QuantizeArgs& a, int xtype, bool tile, hipStrea
 int quantize_rows_per_group(int64_t M, int64_t K, bool tile);
 hipError_t launch_rms(const RmsArgs& a, int xtype, hipStream_t stream);
 hipError_t launch_rms_backward(const RmsBackwardArgs& a, int xtype, hipStream_t stream);
-int rms_backward_groups(int64_t M, int64_t D, int num_cus);
+// A backward pass's form, and how many parts of dw it leaves in the workspace
+// (0: it needs none).
+struct RmsBackwardPlan {
+    bool by_columns;
+    int parts;
+};
+RmsBackwardPlan rms_backward_plan(int64_t M, int64_t D, int num_cus);
 constexpr int64_t rms_parts_row(int64_t D) { return (D + 3) / 4 * 4; }
 
 }  // namespace pg

@@ -23,10 +23,16 @@ __global__ void __launch_bounds__(256) quantize_rows(QuantizeArgs a) {
     const int64_t m0 = (int64_t)(blockIdx.x / kblocks) * (16 * R) + g;
     const int n = (int)min((int64_t)8, max((int64_t)0, a.K - k0));
     float f[R][8];
+    Raw8<XT> raw[R];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
         const int64_t m = m0 + 16 * i;
-        load8<XT>(a.X, m < a.M ? m * a.ldx + k0 : 0, m < a.M ? n : 0, f[i]);
+        raw[i] = fetch8<XT>(a.X, m * a.ldx + k0, k0, m < a.M ? n : 0);
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        settle8<XT>(raw[i], k0, n);
+        to_f32<XT>(raw[i], f[i]);
     }
 #pragma unroll
     for (int i = 0; i < R; ++i) {
@@ -60,10 +66,16 @@ __global__ void __launch_bounds__(2048 / R) quantize_tile(QuantizeArgs a) {
     const int64_t k0 = kb * kBlock + c * 8, m0 = mb * kBlock + g * R;
     const int n = (int)min((int64_t)8, max((int64_t)0, a.K - k0));
     float f[R][8];
+    Raw8<XT> raw[R];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
         const int64_t m = m0 + i;
-        load8<XT>(a.X, m < a.M ? m * a.ldx + k0 : 0, m < a.M ? n : 0, f[i]);
+        raw[i] = fetch8<XT>(a.X, m * a.ldx + k0, k0, m < a.M ? n : 0);
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        settle8<XT>(raw[i], k0, n);
+        to_f32<XT>(raw[i], f[i]);
     }
     float r_tile = 0.0f, col[8];                 // reciprocal scales
     if constexpr (TILE) {

@@ -11,6 +11,8 @@
 // (fp32) between its statistics and its output: TPR threads hold it, 8
 // consecutive values per thread and step, NC steps.  A block of 128 is 16
 // neighbouring lanes.
+#include <algorithm>
+
 #include "fp8_common.h"
 
 namespace pg {
@@ -34,11 +36,11 @@ __device__ __forceinline__ float row_sum(float x, float* red) {
 }
 
 template <int XT>
-__device__ __forceinline__ void load_w(const void* W, int64_t at, int n, bool w_f32, float (&w)[8]) {
+__device__ __forceinline__ void load_w(const void* W, int64_t k, int n, bool w_f32, float (&w)[8]) {
     if (w_f32)
-        load8<XT_F32>(W, at, n, w);
+        load8<XT_F32>(W, k, k, n, w);
     else
-        load8<XT>(W, at, n, w);
+        load8<XT>(W, k, k, n, w);
 }
 
 template <int XT, int TPR, int NC>
@@ -54,10 +56,10 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rms_kernel(RmsArgs a) {
     for (int i = 0; i < NC; ++i) {
         const int64_t k = ((int64_t)i * TPR + t) * 8;
         const int n = (int)min((int64_t)8, max((int64_t)0, a.D - k));
-        load8<XT>(a.X, n > 0 ? m * a.ldx + k : 0, n, f[i]);
+        load8<XT>(a.X, m * a.ldx + k, k, n, f[i]);
         if (a.R != nullptr) {
             float r[8];
-            load8<XT>(a.R, n > 0 ? m * a.ldr + k : 0, n, r);
+            load8<XT>(a.R, m * a.ldr + k, k, n, r);
 #pragma unroll
             for (int e = 0; e < 8; ++e) f[i][e] = rounded<XT>(f[i][e] + r[e]);
         }
@@ -73,7 +75,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rms_kernel(RmsArgs a) {
         const int64_t k = ((int64_t)i * TPR + t) * 8;
         const int n = (int)min((int64_t)8, max((int64_t)0, a.D - k));
         float w[8];
-        load_w<XT>(a.W, n > 0 ? k : 0, n, a.w_f32, w);
+        load_w<XT>(a.W, k, n, a.w_f32, w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[i][e] = f[i][e] * rstd * w[e];
         if (a.Y != nullptr && n > 0) store8<XT>(a.Y, m * a.ldy + k, n, f[i]);
@@ -88,46 +90,40 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rms_kernel(RmsArgs a) {
     }
 }
 
-// How a backward pass holds its rows.  kAhead: in registers, the next row
-// loaded before the current one's sum, so that two rows per group are on
-// their way (8192 x 4096 bf16: 86 us without, 53 with).  kHold: in registers,
-// one at a time.  kTwice: read for the sum and again (from the caches) for dx.
-// The longer the row, the fewer registers a thread has for each value of it:
-// 8192 values and fewer go ahead (16-bit ones up to 12288); a form that spills
-// costs more than it gives (4096 x 16384 bf16: 242 us ahead, 116 held).
-enum Holding { kAhead, kHold, kTwice };
+// How a backward pass of many rows holds them.  Ahead: in registers, the next
+// row loaded before the current one's sum, so that two rows per group are on
+// their way (8192 x 4096 bf16: 86 us without, 53 with).  Otherwise one at a
+// time: the longer the row, the fewer registers a thread has for each value
+// of it, and a form that spills costs more than it gives (4096 x 16384 bf16:
+// 242 us ahead, 112 held).
 
 // Row group g of `groups` takes rows g, g + groups, ...: it keeps its part
 // of dw in registers over them and writes it once, to parts[g].
-template <int XT, int TPR, int NC, int HOLDING>
+template <int XT, int TPR, int NC, bool AHEAD>       // AHEAD: any D, else multiples of 8
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rms_backward_kernel(RmsBackwardArgs a) {
     __shared__ float red[2][TPR > 64 ? TPR / 64 : 1];
     constexpr int RPW = TPR < 256 ? 256 / TPR : 1;
-    constexpr bool KEEP = HOLDING == kAhead;                 // the weight stays in registers too
-    constexpr int NH = HOLDING == kTwice ? 1 : NC;
+    constexpr bool KEEP = AHEAD;                             // the weight stays in registers too
     const int t = threadIdx.x % TPR;
     const int group = blockIdx.x * RPW + threadIdx.x / TPR;
     if (group >= a.groups) return;                           // whole waves, RPW > 1 only
     struct Row {
-        Raw8<XT> dy[NH], h[NH], dh[NH];
+        Raw8<XT> dy[NC], h[NC], dh[NC];
         float rstd;
-    };
-    auto load_part = [&](Row& x, int64_t m, int i, bool with_dh) {
-        const int k = (i * TPR + t) * 8, n = min(8, max(0, a.D - k)), q = HOLDING == kTwice ? 0 : i;
-        x.dy[q] = load_raw8<XT>(a.DY, n > 0 ? m * a.lddy + k : 0, n);
-        x.h[q] = load_raw8<XT>(a.H, n > 0 ? m * a.ldh + k : 0, n);
-        if (with_dh && a.DH != nullptr) x.dh[q] = load_raw8<XT>(a.DH, n > 0 ? m * a.lddh + k : 0, n);
     };
     auto load_row = [&](Row& x, int64_t m) {
         x.rstd = a.rstd[m];
-        if constexpr (HOLDING != kTwice) {
 #pragma unroll
-            for (int i = 0; i < NC; ++i) load_part(x, m, i, true);
+        for (int i = 0; i < NC; ++i) {
+            const int k = (i * TPR + t) * 8, n = AHEAD ? min(8, max(0, a.D - k)) : k < a.D ? 8 : 0;
+            x.dy[i] = fetch8<XT>(a.DY, m * a.lddy + k, k, n);
+            x.h[i] = fetch8<XT>(a.H, m * a.ldh + k, k, n);
+            if (a.DH != nullptr) x.dh[i] = fetch8<XT>(a.DH, m * a.lddh + k, k, n);
         }
     };
     auto weight = [&](int i, float (&w)[8]) {
-        const int k = (i * TPR + t) * 8, n = min(8, max(0, a.D - k));
-        load_w<XT>(a.W, n > 0 ? k : 0, n, a.w_f32, w);
+        const int k = (i * TPR + t) * 8, n = AHEAD ? min(8, max(0, a.D - k)) : k < a.D ? 8 : 0;
+        load_w<XT>(a.W, k, n, a.w_f32, w);
     };
     float kept[KEEP ? NC : 1][8], dw[NC][8];
 #pragma unroll
@@ -142,40 +138,41 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rms_backward_kernel(Rms
     for (int64_t m = group; m < a.M; m += a.groups) {
         Row next;
         const bool more = m + a.groups < a.M;
-        if (HOLDING == kAhead && more) load_row(next, m + a.groups);
+        if (AHEAD && more) load_row(next, m + a.groups);
         float dot = 0.0f;
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
-            const int q = HOLDING == kTwice ? 0 : i;
-            if constexpr (HOLDING == kTwice) load_part(x, m, i, false);
+            const int k = (i * TPR + t) * 8, n = min(8, max(0, a.D - k));
+            if constexpr (AHEAD) {
+                settle8<XT>(x.dy[i], k, n);
+                settle8<XT>(x.h[i], k, n);
+            }
             if constexpr (!KEEP) weight(i, kept[0]);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float dy = (float)x.dy[q].v[e], h = (float)x.h[q].v[e];
+                const float dy = (float)x.dy[i].v[e], h = (float)x.h[i].v[e];
                 dw[i][e] += dy * (h * x.rstd);
                 dot += dy * kept[KEEP ? i : 0][e] * h;
             }
-            if constexpr (HOLDING == kTwice) __builtin_amdgcn_sched_barrier(0);
         }
         dot = row_sum<TPR>(dot, red[turn]);
         turn ^= 1;
         const float c = x.rstd * x.rstd * (dot / (float)a.D);
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
-            const int k = (i * TPR + t) * 8, n = min(8, max(0, a.D - k)), q = HOLDING == kTwice ? 0 : i;
+            const int k = (i * TPR + t) * 8, n = AHEAD ? min(8, max(0, a.D - k)) : k < a.D ? 8 : 0;
             float dx[8];
-            if constexpr (HOLDING == kTwice) load_part(x, m, i, true);
+            if (AHEAD && a.DH != nullptr) settle8<XT>(x.dh[i], k, n);
             if constexpr (!KEEP) weight(i, kept[0]);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                dx[e] = x.rstd * ((float)x.dy[q].v[e] * kept[KEEP ? i : 0][e] - (float)x.h[q].v[e] * c);
-                if (a.DH != nullptr) dx[e] += (float)x.dh[q].v[e];
+                dx[e] = x.rstd * ((float)x.dy[i].v[e] * kept[KEEP ? i : 0][e] - (float)x.h[i].v[e] * c);
+                if (a.DH != nullptr) dx[e] += (float)x.dh[i].v[e];
             }
             if (n > 0) store8<XT>(a.DX, m * a.lddx + k, n, dx);
-            if constexpr (HOLDING == kTwice) __builtin_amdgcn_sched_barrier(0);
         }
         if (more) {
-            if constexpr (HOLDING == kAhead) x = next;
+            if constexpr (AHEAD) x = next;
             else load_row(x, m + a.groups);
         }
     }
@@ -211,6 +208,100 @@ __global__ void __launch_bounds__(256) rms_backward_sum(RmsBackwardArgs a) {
     }
 }
 
+// The other form of the backward pass, for fewer rows and for the longest:
+// dw takes only the rows' rstd, which is given, not their sums, so it needs
+// nothing from dx.  The first workgroups take a row each (TPR threads per
+// row), the others 64 or 128 columns of dw over a part of the rows each: 8 or
+// 16 lanes across, the other threads down, their sums added in turn.  dy and h
+// are read twice, mostly from the caches, but dw's parts are few, none for
+// 512 rows and fewer, which take one launch (bf16 with dh, 16 x 4096: 5.1 us,
+// 8.3 in groups and two launches; 512 x 4096: 6.9 and 14.8).
+// 64 columns give short rows more workgroups (512 x 1024: 5.6 us against 8.2), 128
+// read longer pieces (1024 x 8192: 25 us against 21).
+// Where dx takes the place of dy or h the dw workgroups go first, in a launch
+// of their own: side by side they would read what a row has overwritten.
+constexpr int columns_lanes(int TPR) { return TPR <= 256 ? 8 : 16; }
+
+template <int XT, int TPR, int NC>
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rms_backward_columns(RmsBackwardArgs a, int first) {
+    constexpr int T = TPR < 256 ? 256 : TPR, RPW = T / TPR, LANES = columns_lanes(TPR), COLUMNS = LANES * 8, DOWN = T / LANES;
+    constexpr int AT_ONCE = XT == XT_F32 || LANES == 16 ? 4 : 8;   // rows on their way per thread
+    __shared__ float sums[DOWN][COLUMNS + 4];
+    const int row_groups = (a.M + RPW - 1) / RPW, block = (int)blockIdx.x + first;
+    if (block >= row_groups) {
+        const int c = threadIdx.x % LANES, g = threadIdx.x / LANES;
+        const int blocks = (a.D + COLUMNS - 1) / COLUMNS, part = (block - row_groups) / blocks;
+        const int k0 = (block - row_groups) % blocks * COLUMNS, k = k0 + c * 8, n = min(8, max(0, a.D - k));
+        const int parts = max(1, a.groups), rows = (a.M + parts - 1) / parts;
+        const int64_t to = min((int64_t)a.M, (int64_t)(part + 1) * rows);
+        float dw[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dw[e] = 0.0f;
+        for (int64_t m0 = (int64_t)part * rows + g; m0 < to; m0 += AT_ONCE * DOWN) {
+            Raw8<XT> dy[AT_ONCE], h[AT_ONCE];
+            float rstd[AT_ONCE];
+#pragma unroll
+            for (int i = 0; i < AT_ONCE; ++i) {
+                const int64_t m = m0 + i * DOWN;
+                dy[i] = fetch8<XT>(a.DY, m * a.lddy + k, k, m < to ? n : 0);
+                h[i] = fetch8<XT>(a.H, m * a.ldh + k, k, m < to ? n : 0);
+                rstd[i] = m < to ? a.rstd[m] : 0.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < AT_ONCE; ++i) {
+                settle8<XT>(dy[i], k, n);
+                settle8<XT>(h[i], k, n);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) dw[e] += (float)dy[i].v[e] * ((float)h[i].v[e] * rstd[i]);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sums[g][c * 8 + e] = dw[e];
+        __syncthreads();
+        const int col = k0 + (int)threadIdx.x;
+        if (threadIdx.x < COLUMNS && col < a.D) {
+            float s = 0.0f;
+#pragma unroll
+            for (int i = 0; i < DOWN; ++i) s += sums[i][threadIdx.x];
+            (a.groups > 0 ? a.parts + part * rms_parts_row(a.D) : a.DW)[col] = s;
+        }
+        return;
+    }
+    const int t = threadIdx.x % TPR;
+    const int64_t m = (int64_t)block * RPW + threadIdx.x / TPR;
+    if (m >= a.M) return;                                    // whole waves, RPW > 1 only
+    const float rstd = a.rstd[m];
+    float dy[NC][8], h[NC][8];
+    float dot = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+        const int k = (i * TPR + t) * 8, n = min(8, max(0, a.D - k));
+        float w[8];
+        load8<XT>(a.DY, m * a.lddy + k, k, n, dy[i]);
+        load8<XT>(a.H, m * a.ldh + k, k, n, h[i]);
+        load_w<XT>(a.W, k, n, a.w_f32, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            dy[i][e] *= w[e];
+            dot += dy[i][e] * h[i][e];
+        }
+    }
+    dot = row_sum<TPR>(dot, sums[0]);
+    const float c = rstd * rstd * (dot / (float)a.D);
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+        const int k = (i * TPR + t) * 8, n = min(8, max(0, a.D - k));
+        float dx[8], dh[8];
+        if (a.DH != nullptr) load8<XT>(a.DH, m * a.lddh + k, k, n, dh);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            dx[e] = rstd * (dy[i][e] - h[i][e] * c);
+            if (a.DH != nullptr) dx[e] += dh[e];
+        }
+        if (n > 0) store8<XT>(a.DX, m * a.lddx + k, n, dx);
+    }
+}
+
 template <int XT, int TPR, int NC>
 hipError_t forward(const RmsArgs& a, hipStream_t stream) {
     constexpr int RPW = TPR < 256 ? 256 / TPR : 1;
@@ -230,38 +321,72 @@ hipError_t forward_for(const RmsArgs& a, hipStream_t stream) {
     return forward<XT, 1024, 4>(a, stream);
 }
 
-template <int XT, int TPR, int NC, int HOLDING>
-hipError_t backward(const RmsBackwardArgs& a, hipStream_t stream) {
-    constexpr int RPW = TPR < 256 ? 256 / TPR : 1;
-    if (a.groups > 0) {                  // no rows: dw is zero
-        hipLaunchKernelGGL((rms_backward_kernel<XT, TPR, NC, HOLDING>), dim3((unsigned)((a.groups + RPW - 1) / RPW)),
-                           dim3(TPR < 256 ? 256 : TPR), 0, stream, a);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-    }
+hipError_t sum_parts(const RmsBackwardArgs& a, hipStream_t stream) {
     hipLaunchKernelGGL(rms_backward_sum, dim3((unsigned)((a.D + 15) / 16)), dim3(256), 0, stream, a);
     return hipGetLastError();
 }
 
+template <int XT, int TPR, int NC, bool AHEAD>
+hipError_t backward(const RmsBackwardArgs& a, hipStream_t stream) {
+    constexpr int RPW = TPR < 256 ? 256 / TPR : 1;
+    hipLaunchKernelGGL((rms_backward_kernel<XT, TPR, NC, AHEAD>), dim3((unsigned)((a.groups + RPW - 1) / RPW)),
+                       dim3(TPR < 256 ? 256 : TPR), 0, stream, a);
+    const hipError_t e = hipGetLastError();
+    return e != hipSuccess ? e : sum_parts(a, stream);
+}
+
+template <int XT, int TPR, int NC>
+hipError_t backward_columns(const RmsBackwardArgs& a, hipStream_t stream) {
+    constexpr int T = TPR < 256 ? 256 : TPR, RPW = T / TPR, COLUMNS = columns_lanes(TPR) * 8;
+    const int rows = (int)((a.M + RPW - 1) / RPW);
+    const int columns = (a.D + COLUMNS - 1) / COLUMNS * (a.groups > 0 ? a.groups : 1);
+    const bool apart = a.in_place && rows > 0;
+    if (apart) {
+        hipLaunchKernelGGL((rms_backward_columns<XT, TPR, NC>), dim3((unsigned)columns), dim3(T), 0, stream, a, rows);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL((rms_backward_columns<XT, TPR, NC>), dim3((unsigned)(apart ? rows : rows + columns)), dim3(T),
+                       0, stream, a, 0);
+    const hipError_t e = hipGetLastError();
+    return e != hipSuccess || a.groups == 0 ? e : sum_parts(a, stream);
+}
+
 template <int XT>
 hipError_t backward_for(const RmsBackwardArgs& a, hipStream_t stream) {
-    if (a.D <= 512) return backward<XT, 64, 1, kAhead>(a, stream);
-    if (a.D <= 1024) return backward<XT, 64, 2, kAhead>(a, stream);
-    if (a.D <= 2048) return backward<XT, 256, 1, kAhead>(a, stream);
-    if (a.D <= 4096) return backward<XT, 256, 2, kAhead>(a, stream);
-    if (a.D <= 8192) return backward<XT, 512, 2, kAhead>(a, stream);
-    if (a.D <= 12288 && XT != XT_F32) return backward<XT, 512, 3, XT == XT_F32 ? kHold : kAhead>(a, stream);
-    if (a.D <= 16384) return backward<XT, 1024, 2, kHold>(a, stream);
-    return backward<XT, 1024, 4, kTwice>(a, stream);
+    if (a.by_columns) {
+        if (a.D <= 512) return backward_columns<XT, 64, 1>(a, stream);
+        if (a.D <= 1024) return backward_columns<XT, 64, 2>(a, stream);
+        if (a.D <= 2048) return backward_columns<XT, 256, 1>(a, stream);
+        if (a.D <= 4096) return backward_columns<XT, 256, 2>(a, stream);
+        if (a.D <= 8192) return backward_columns<XT, 512, 2>(a, stream);
+        if (a.D <= 16384) return backward_columns<XT, 1024, 2>(a, stream);
+        return backward_columns<XT, 1024, 4>(a, stream);
+    }
+    if (a.D <= 512) return backward<XT, 64, 1, true>(a, stream);
+    if (a.D <= 1024) return backward<XT, 64, 2, true>(a, stream);
+    if (a.D <= 2048) return backward<XT, 256, 1, true>(a, stream);
+    if (a.D <= 4096) return backward<XT, 256, 2, true>(a, stream);
+    if (a.D <= 8192) return backward<XT, 512, 2, true>(a, stream);
+    if constexpr (XT != XT_F32)
+        if (a.D <= 12288) return backward<XT, 512, 3, true>(a, stream);
+    return backward<XT, 1024, 2, false>(a, stream);
 }
 
 }  // namespace
 
-int rms_backward_groups(int64_t M, int64_t D, int num_cus) {
-    // two workgroups of 256 threads per CU (one of 1024), each with as many
-    // groups as it holds rows at a time
-    const int64_t most = (int64_t)num_cus * (D <= 1024 ? 8 : D <= 8192 ? 2 : 1);
-    return (int)(M < most ? M : most);
+RmsBackwardPlan rms_backward_plan(int64_t M, int64_t D, int num_cus) {
+    // us in groups and by columns, bf16 with dh: 560 x 8192 20 and 15, 1024 x
+    // 8192 27.5 and 21.3, 2000 x 8192 39.6 and 36.2, 4000 x 8192 63 and 73; 1024 x 4096 16.2 and
+    // 13.6, 1500 x 4096 17.3 and 17.5; 2000 x 1024 12.7 and 8.8, 8192 x 1024
+    // 20.3 and 20.9.  Groups hold 16384 columns at most (1500 x 20000, read
+    // twice with registers in scratch: 171 us, by columns 77), and above 12288 multiples of 8.
+    if (M <= 1024 || (D <= 1024 && M <= 4096) || D > 16384 || (D > 12288 && D % 8 != 0))
+        return {true, M <= 512 ? 0 : (int)std::min<int64_t>((M + 255) / 256, 64)};
+    // two workgroups of 256 or 512 threads per CU (one of 1024), each with as
+    // many groups as it holds rows at a time
+    const int64_t most = (int64_t)num_cus * (D <= 1024 ? 4 : D <= 8192 ? 2 : 1);
+    return {false, (int)std::min(M, most)};
 }
 
 hipError_t launch_rms(const RmsArgs& a, int xtype, hipStream_t stream) {

@@ -338,12 +338,13 @@ PyObject* rms_backward_(PyObject* const* arg, Py_ssize_t n) {
     const at::Tensor dw = empty({D}, {1}, at::kFloat, hm.device);
     // a workspace of this call's own: it belongs to the stream (and, under capture, to the graph)
     const int64_t bytes = gemm_rms_backward_workspace(M, D);
-    const at::Tensor ws = empty({bytes}, {1}, at::kByte, hm.device);
+    at::Tensor ws;
+    if (bytes > 0) ws = empty({bytes}, {1}, at::kByte, hm.device);
     void* const stream = raw_stream(hm.device);
     const int rc = enqueue([&] {
         return gemm_rms_backward(h, M, D, hm.type, w_type, dy.p, dy.ld, hm.p, hm.ld, w.data_ptr(),
                                  (const float*)rstd.data_ptr(), dh.p, dh.ld, dx.p, dx.ld, (float*)dw.data_ptr(),
-                                 ws.data_ptr(), bytes, stream);
+                                 bytes > 0 ? ws.data_ptr() : nullptr, bytes, stream);
     });
     if (rc != GEMM_OK) return gemm_error(rc, "gemm_rms_backward");
     return tuple_of({dxt, dw});

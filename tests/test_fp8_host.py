@@ -216,9 +216,10 @@ def test_rms_backward_refusals():
     assert rms_back(x="i8") == BAD and rms_back(w="f16") == BAD and rms_back(M=-1) == BAD and rms_back(D=-1) == BAD
     for ld in ("lddy", "ldh", "lddh", "lddx"):
         assert rms_back(**{ld: 255}) == BAD, ld
-    for p in ("DY", "Hm", "W", "rstd", "DX", "DW", "ws"):
+    for p in ("DY", "Hm", "W", "rstd", "DX", "DW"):
         assert rms_back(**{p: None}) == BAD, p
-    assert rms_back(nbytes=binding.gemm_rms_backward_workspace(4, 256) - 1) == BAD and rms_back(nbytes=-1) == BAD
+    need = binding.gemm_rms_backward_workspace(4096, 256)
+    assert rms_back(M=4096, ws=None) == BAD and rms_back(M=4096, nbytes=need - 1) == BAD and rms_back(nbytes=-1) == BAD
     for p in ("DY", "Hm", "DH", "DX"):
         assert rms_back(**{p: P + 1}) == ALIGN, p
     assert rms_back(ws=P + 8) == ALIGN and rms_back(DW=P + 2) == ALIGN
@@ -229,12 +230,12 @@ def test_rms_backward_refusals():
 
 
 def test_rms_backward_workspace():
-    assert binding.gemm_rms_backward_workspace(4, 256) == 4 * 256 * 4
-    assert binding.gemm_rms_backward_workspace(0, 256) == 0
-    assert binding.gemm_rms_backward_workspace(-1, 256) == 0
-    assert binding.gemm_rms_backward_workspace(1, binding.GEMM_RMS_MAX_D + 1) == 0
-    most = binding.gemm_rms_backward_workspace(1 << 20, 8192)
-    assert most == binding.gemm_rms_backward_workspace(1 << 21, 8192)            # bounded
+    ws = binding.gemm_rms_backward_workspace
+    assert ws(4, 256) == ws(512, 8192) == ws(0, 256) == 0                       # few rows: none
+    assert ws(513, 2048) % (2048 * 4) == 0 and ws(513, 2046) == ws(513, 2048) > 0
+    assert ws(-1, 256) == 0 and ws(1, binding.GEMM_RMS_MAX_D + 1) == 0
+    assert ws(1 << 20, 8192) == ws(1 << 21, 8192) > 0                           # bounded
+    assert ws(1 << 20, 20000) == ws(1 << 21, 20000) > 0
 
 
 # ---- the torch functions' refusals (CPU tensors: nothing is enqueued) --------

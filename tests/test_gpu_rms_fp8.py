@@ -128,7 +128,8 @@ def check_backward(dy, h, w, rstd, dh, dx, dw, x):
     R.assert_within(d(dw), rw, err + 2.0 ** -126, "dw")
 
 
-@pytest.mark.parametrize("M,D", SIZES + ((0, 64), (2100, 72), (1500, 1032), (600, 2560)))
+@pytest.mark.parametrize("M,D", SIZES + ((0, 64), (2100, 72), (1500, 1032), (600, 2560), (512, 136), (513, 136), (1100, 4104), (4100, 520), (4096, 200),
+                                         (1030, 9000), (1030, 12296), (1030, 12300), (513, 16392), (1025, 7)))
 def test_backward_sizes(M, D):
     t, _, w = inputs(M, D, "bf16", "f32", False)
     dy, dh, _ = inputs(M, D, "bf16", "f32", True, seed=5)
@@ -141,8 +142,8 @@ def test_backward_sizes(M, D):
 
 
 @pytest.mark.parametrize("x,w", (("bf16", "bf16"), ("f16", "f16"), ("f16", "f32"), ("f32", "f32")))
-def test_backward_types_strides_and_in_place(x, w):
-    M, D = 40, 1100
+@pytest.mark.parametrize("M,D", ((40, 1100), (1030, 300)))
+def test_backward_types_strides_and_in_place(M, D, x, w):
     t, _, wt = inputs(M, D, x, w, False)
     dy, dh, _ = inputs(M, D, x, w, True, seed=5)
     rstd = torch.rsqrt(t.double().square().mean(1) + 1e-6).float()
