@@ -27,6 +27,10 @@ Before anything touches the GPU the chip's attainable rates are measured
 by ceiling_probe (a child process), so every fraction is also given against
 the ceiling of the same box.
 
+--workload fp8_linear is not one of the five: its step is one linear layer
+behind a norm, forward and backward, through the 8-bit operators, on bf16
+tokens; `value` is TFLOP/s of its three products, over all the step's time.
+
 Prints one JSON line.  `value` is TOP/s (int8) or TFLOP/s (fp) counting
 2*M*N*K operations (the convention of the pipelining study's benchmark
 table), or GB/s of algorithmic bytes for the memory-bound skinny shape.
@@ -85,8 +89,11 @@ WORKLOADS = {
 FIVE = ["fp32_256", "int8_4096", "fp16_4096", "bf16_skinny", "bf16_8192x8200"]
 HEADLINE = "int8_4096"
 
+# The 8-bit linear layer: tokens, inputs and outputs.
+FP8_LINEAR = (8192, 4096, 4096)
+
 # MI355X published dense peaks (per GPU)
-PEAK = {"i8": 5033.2, "f16": 2516.6, "bf16": 2516.6, "f32": 157.3}   # TOP/s, TFLOP/s
+PEAK = {"i8": 5033.2, "f16": 2516.6, "bf16": 2516.6, "f32": 157.3, "fp8": 5033.2}   # TOP/s, TFLOP/s
 HBM_PEAK_GBS = 8000.0
 ROTATE_BYTES = 512 * 2 ** 20
 
@@ -97,12 +104,13 @@ def flops(M, N, K):
 
 
 def kernel_source_hash():
-    """Hash of the library's sources with comments and white space removed,
-    so that only a change of code marks measured counters as stale."""
+    """Hash of the GEMM's sources (not of the 8-bit operators', which have no
+    part in it) with comments and white space removed, so that only a change
+    of code marks measured counters as stale."""
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "software_pipelined_tiled_02_amd", "csrc")
     for name in sorted(os.listdir(csrc)):
-        if name.endswith((".h", ".hip")) and not name.endswith("_probe.hip"):   # probes are no GEMM source
+        if name.endswith((".h", ".hip")) and not name.endswith("_probe.hip") and not name.startswith("fp8_"):
             text = open(os.path.join(csrc, name), encoding="utf-8").read()
             text = re.sub(r"/\*.*?\*/", " ", text, flags=re.S)
             text = re.sub(r"//[^\n]*", " ", text)
@@ -435,13 +443,110 @@ def measure_workload(name, args, g, ceilings, res_table, pairs):
     return record
 
 
+def fp8_linear_step(x, r, wn, w, dc, dh, grad, mark=lambda name: None):
+    """c = norm(x + r) w^T in 8 bits, and the gradients of x (and r), of the
+    norm's weight and, added to `grad`, of w.  mark(name) is called behind
+    every operator."""
+    from software_pipelined_tiled_02_amd import binding
+
+    wq, ws, wqt, wst = binding.quantize_fp8(w, block="tile", transpose=True)
+    mark("quantize w, both ways")
+    q, s, h, rstd, y = binding.rms_fp8(x, wn, residual=r, norm=True)
+    mark("norm")
+    c = binding.run_fp8(q, s, wq, ws)
+    mark("product forward")
+    dq, ds, dqt, dst = binding.quantize_fp8(dc, transpose=True)
+    mark("quantize dc, both ways")
+    dy = binding.run_fp8(dq, ds, wqt, wst)
+    mark("product for dy")
+    yqt, yst = binding.quantize_fp8(y, rows=False, transpose=True)
+    mark("quantize y, transposed")
+    binding.run_fp8(dqt, dst, yqt, yst, out=grad, accumulate=True)
+    mark("product for dw (fp32, added)")
+    dx, dwn = binding.rms_backward(dy, h, wn, rstd, dh=dh)
+    mark("norm backward")
+    return c, dx, dwn
+
+
+def measure_fp8_linear(args):
+    """Times fp8_linear_step; returns the line's figures."""
+    import torch
+
+    M, D, N = FP8_LINEAR
+    g = torch.Generator(device="cuda").manual_seed(0)
+
+    def normal(*shape):
+        return torch.randn(shape, generator=g, device="cuda")
+
+    sets = []
+    for _ in range(2):                       # a set's tensors and the step's own exceed ROTATE_BYTES
+        sets.append([normal(M, D).bfloat16(), normal(M, D).bfloat16(), (1 + 0.2 * normal(D)).bfloat16(),
+                     normal(N, D) / D ** 0.5, normal(M, N).bfloat16(), normal(M, D).bfloat16(),
+                     torch.zeros((N, D), device="cuda")])
+    stream = torch.cuda.current_stream()
+    deadline = time.monotonic() + 0.5        # settle the clocks
+    while time.monotonic() < deadline:
+        fp8_linear_step(*sets[0])
+        torch.cuda.synchronize()
+    rounds = []
+    for _ in range(args.rounds):
+        for i in range(args.warmup):
+            fp8_linear_step(*sets[i % 2])
+        torch.cuda.synchronize()
+        t0, t1 = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        t0.record(stream)
+        for i in range(args.steps):
+            fp8_linear_step(*sets[i % 2])
+        t1.record(stream)
+        torch.cuda.synchronize()
+        rounds.append(t0.elapsed_time(t1) / args.steps)
+    ms = sorted(rounds)[len(rounds) // 2]
+    spent = {}                               # a last pass, an event behind every operator
+    for i in range(args.steps):
+        last = torch.cuda.Event(enable_timing=True)
+        last.record(stream)
+        marks = [("", last)]
+
+        def mark(name):
+            e = torch.cuda.Event(enable_timing=True)
+            e.record(stream)
+            marks.append((name, e))
+
+        fp8_linear_step(*sets[i % 2], mark=mark)
+        torch.cuda.synchronize()
+        for (_, a), (name, b) in zip(marks, marks[1:]):
+            spent.setdefault(name, []).append(a.elapsed_time(b) * 1e3)
+    return ms, rounds, {k: round(sorted(v)[len(v) // 2], 2) for k, v in spent.items()}
+
+
+def fp8_linear(args):
+    import torch
+
+    if not torch.cuda.is_available():
+        print("bench.py needs a GPU", file=sys.stderr)
+        sys.exit(1)
+    ms, rounds, spent = measure_fp8_linear(args)
+    M, D, N = FP8_LINEAR
+    ops = 3 * flops(M, N, D)
+    value = ops / (ms * 1e-3) / 1e12
+    print(json.dumps({
+        "metric": "8-bit linear layer, forward and backward: TFLOP/s of its products over the whole step, 1 GPU",
+        "value": round(value, 2), "unit": "TFLOP/s", "n_gpus": 1, "steps": args.steps, "warmup": args.warmup,
+        "ms_per_step": round(ms, 5), "higher_is_better": True, "scaling": "weak", "vs_baseline": None,
+        "dtype": "fp8 (e4m3, block scales), bf16 tokens, fp32 weights and their gradient",
+        "data": "synthetic (seeded)",
+        "config": {"workload": "fp8_linear", "tokens": M, "inputs": D, "outputs": N},
+        "roofline": {"bound": "mfma", "peak_TFLOP/s": PEAK["fp8"], "frac_peak": round(value / PEAK["fp8"], 4)},
+        "rounds_ms": [round(t, 5) for t in rounds], "operators_us": spent}), flush=True)
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--gpus", type=int, default=1)
     ap.add_argument("--steps", type=int, default=20)
     ap.add_argument("--warmup", type=int, default=15)
     ap.add_argument("--rounds", type=int, default=3, help="rounds over all pairs; each pair reports its median")
-    ap.add_argument("--workload", default="all", choices=["all"] + sorted(WORKLOADS),
+    ap.add_argument("--workload", default="all", choices=["all", "fp8_linear"] + sorted(WORKLOADS),
                     help="one workload, or all: the five benchmark workloads (headline int8 4096^3)")
     ap.add_argument("--pairs", default="all", help="comma list like 3:direct,2:reg, or all")
     ap.add_argument("--tile", default="auto", help="tile class: auto, 256x256, 256x256w8, 128x128, 32x64")
@@ -465,6 +570,8 @@ def main():
               file=sys.stderr)
         sys.exit(2)
 
+    if args.workload == "fp8_linear":
+        return fp8_linear(args)
     names = FIVE if args.workload == "all" else [args.workload]
 
     # The ceiling probe runs first, as a child process, before this process
