@@ -29,8 +29,8 @@ TILES = {"auto": GEMM_TILE_AUTO, "256x256": GEMM_TILE_256x256, "128x128": GEMM_T
          "32x64": GEMM_TILE_32x64, "256x256w8": GEMM_TILE_256x256_W8}
 
 FP8_TYPES = {"e4m3": GEMM_E4M3, "e5m2": GEMM_E5M2}
-FP8_TILES = {"auto": -1, "256x256": 0, "256x128": 1, "128x128": 2, "64x64": 3, "64x32": 4, "32x32": 5,
-             "16x32": 6, "16x16": 7}
+FP8_TILES = {"auto": -1, "256x256": 0, "256x128": 1, "128x128": 2, "64x64": 3, "64x64k4": 4,
+             "64x32": 5, "32x32": 6, "16x32": 7, "16x16": 8}
 FP8_BLOCK = 128   # values of a row that share a scale
 BLOCK_ROWS = {"row": 1, "tile": FP8_BLOCK}
 

@@ -26,7 +26,7 @@ LIB = os.path.join(HERE, "libpipegemm.so")
 RESOURCES = os.path.join(HERE, "kernel_resources.json")
 PROBES = ["ceiling_probe", "lds_layout_probe"]
 SOURCES = ["kernels_i8.hip", "kernels_f16.hip", "kernels_bf16.hip", "kernels_f32.hip", "abi.hip",
-           "fp8_abi.hip", "fp8_stream.hip", "fp8_staged.hip", "fp8_quantize.hip", "fp8_rms.hip"]
+           "fp8_abi.hip", "fp8_stream.hip", "fp8_staged.hip", "fp8_waves.hip", "fp8_quantize.hip", "fp8_rms.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 CXX = os.environ.get("CXX", "g++")

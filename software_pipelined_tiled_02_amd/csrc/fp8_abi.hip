@@ -56,7 +56,9 @@ int plan_product(int64_t M, int64_t N, int64_t K, int a_type, int b_type, int c_
     const int at = fp8_of(a_type), bt = fp8_of(b_type);
     auto kernel = [&](int t) -> const void* {
         if (!pg::fp8_staged(t)) return pg::fp8_stream_kernel(t, at, bt, b_scale_rows == 1, exact, bytes);
-        return rows16 ? pg::fp8_staged_kernel(t, at, bt, b_scale_rows == 1, exact) : nullptr;
+        if (!rows16) return nullptr;
+        const void* fn = pg::fp8_staged_kernel(t, at, bt, b_scale_rows == 1, exact);
+        return fn != nullptr ? fn : pg::fp8_waves_kernel(t, at, bt, b_scale_rows == 1, exact);
     };
     // The class that takes the least time by the measured costs.
     int tc = tile;

@@ -48,16 +48,18 @@ struct Fp8Args {
 };
 
 // Tile classes: the workgroup's part of C, its waves, and how many of them
-// share each piece of C, every one with blocks of K of its own.
-enum Fp8Tile : int { FP8_TILE_256 = 0, FP8_TILE_256x128 = 1, FP8_TILE_128 = 2, FP8_TILE_64 = 3, FP8_TILE_64x32 = 4,
-                     FP8_TILE_32 = 5, FP8_TILE_16x32 = 6, FP8_TILE_16 = 7, FP8_TILE_COUNT = 8 };
+// share each piece of C, every one with blocks of K of its own (64K4: 64 x 64
+// like 64, but its four waves do).
+enum Fp8Tile : int { FP8_TILE_256 = 0, FP8_TILE_256x128 = 1, FP8_TILE_128 = 2, FP8_TILE_64 = 3, FP8_TILE_64K4 = 4,
+                     FP8_TILE_64x32 = 5, FP8_TILE_32 = 6, FP8_TILE_16x32 = 7, FP8_TILE_16 = 8, FP8_TILE_COUNT = 9 };
 struct Fp8Shape { int bm, bn, waves, wk; };
 constexpr Fp8Shape fp8_shape(int t) {
     return t == FP8_TILE_256 ? Fp8Shape{256, 256, 8, 1}
          : t == FP8_TILE_256x128 ? Fp8Shape{256, 128, 8, 1}
          : t == FP8_TILE_128 ? Fp8Shape{128, 128, 8, 1}
          : t == FP8_TILE_64 ? Fp8Shape{64, 64, 4, 1}
-         : t == FP8_TILE_64x32 ? Fp8Shape{64, 32, 4, 1}
+         : t == FP8_TILE_64K4 ? Fp8Shape{64, 64, 4, 4}
+         : t == FP8_TILE_64x32 ? Fp8Shape{64, 32, 4, 4}
          : t == FP8_TILE_32 ? Fp8Shape{32, 32, 8, 8}
          : t == FP8_TILE_16x32 ? Fp8Shape{16, 32, 8, 8}
                                : Fp8Shape{16, 16, 16, 16};
@@ -70,21 +72,26 @@ constexpr bool fp8_staged(int t) { return t <= FP8_TILE_64x32; }
 // at a time, and microseconds per block of 128 of a round of workgroups that
 // gives no CU more than one (`some`) or fills every CU (`all`), and per round
 // besides.  Measured on an MI355X with operands in the caches, at N = 4096
-// and M = 1 to 4096, K = 1024 and 4096 (fp32 outputs, whose blocks cost about
-// twice the time, at 1024^2 x 4096 and 4096^2 x 8200); microseconds there by
+// and M = 32 to 4096, K = 512 to 8192 (fp32 outputs, whose blocks cost more,
+// there too and at 1024^2 x 4096 and 4096^2 x 8200); microseconds at K = 4096 by
 // the class chosen and the next best:
-//   M = 128: 64x32 9.8, 64x64 11.4         M = 512: 64x64 17.6, 128x128 19.5
-//   M = 640: 128x128 19.9, 64x64 25.1      M = 1024: 128x128 23.3, 256x128 28.8
-//   M = 2048: 256x128 34.6, 128x128 42.1   M = 4096: 256x256 58.5, 256x128 68.4
+//   M = 32: 64x32 7.4, 16x32 8.4           M = 64: 64x32 8.1, 64x64k4 9.4
+//   M = 128: 64x32 8.2, 64x64k4 9.4        M = 256: 64x64k4 10.4, 64x64 11.7
+//   M = 512: 64x64 17.3, 64x64k4 18.4      M = 640: 128x128 18.9, 64x64 24.9
+//   M = 1024: 128x128 22.3, 256x128 28.8   M = 2048: 256x128 34.6, 128x128 42.1
+//   M = 4096: 256x256 57.8, 256x128 68.4
+// and in fp32 M = 32: 16x32 8.9, 64x32 10.5; M = 128: 64x32 11.2, 64x64k4
+// 14.4; M = 256: 64x64k4 15.1, 64x64 19.9.
 struct Fp8Cost { int per_cu; double some, all, round; };
 constexpr Fp8Cost fp8_cost(int t, bool exact) {
     return t == FP8_TILE_256 ? Fp8Cost{1, 1.30, 1.65, 6.0}
          : t == FP8_TILE_256x128 ? (exact ? Fp8Cost{1, 1.75, 1.95, 5.0} : Fp8Cost{1, 0.78, 0.93, 5.0})
          : t == FP8_TILE_128 ? (exact ? Fp8Cost{1, 1.00, 1.16, 4.0} : Fp8Cost{1, 0.50, 0.60, 4.0})
-         : t == FP8_TILE_64 ? (exact ? Fp8Cost{2, 0.45, 0.78, 2.5} : Fp8Cost{2, 0.24, 0.42, 2.5})
-         : t == FP8_TILE_64x32 ? (exact ? Fp8Cost{2, 0.30, 0.55, 2.5} : Fp8Cost{2, 0.19, 0.28, 2.5})
-         : t == FP8_TILE_32 ? Fp8Cost{2, 0.20, 0.30, 2.5}
-         : t == FP8_TILE_16x32 ? Fp8Cost{2, 0.15, 0.27, 2.5}
+         : t == FP8_TILE_64 ? (exact ? Fp8Cost{2, 0.50, 0.75, 2.8} : Fp8Cost{2, 0.24, 0.42, 2.5})
+         : t == FP8_TILE_64K4 ? (exact ? Fp8Cost{1, 0.31, 0.31, 3.8} : Fp8Cost{1, 0.18, 0.18, 3.4})
+         : t == FP8_TILE_64x32 ? (exact ? Fp8Cost{1, 0.21, 0.21, 3.2} : Fp8Cost{1, 0.13, 0.13, 2.9})
+         : t == FP8_TILE_32 ? (exact ? Fp8Cost{2, 0.22, 0.47, 3.5} : Fp8Cost{2, 0.20, 0.44, 2.6})
+         : t == FP8_TILE_16x32 ? Fp8Cost{2, 0.16, 0.34, 2.2}
                                : Fp8Cost{2, 0.12, 0.21, 2.5};
 }
 constexpr double fp8_time(int t, bool exact, int64_t workgroups, int64_t blocks, int64_t cus) {
@@ -98,6 +105,7 @@ constexpr double fp8_time(int t, bool exact, int64_t workgroups, int64_t blocks,
 // (register-fed tiles) rows that do not start or end on 16 bytes.
 const void* fp8_stream_kernel(int tile, int a_type, int b_type, bool sb_rows, bool exact, bool bytes);
 const void* fp8_staged_kernel(int tile, int a_type, int b_type, bool sb_rows, bool exact);
+const void* fp8_waves_kernel(int tile, int a_type, int b_type, bool sb_rows, bool exact);
 
 #if defined(__HIPCC__)
 
@@ -126,6 +134,18 @@ __device__ __forceinline__ int by_xcd(unsigned b, unsigned n) {
     return (int)(x * each + (x < more ? x : more) + (b >> 3));
 }
 
+// Tile number `tile`: each XCD gets a run of tiles, in bands of 4 tile rows,
+// so that what it holds at a time shares rows of A and of B in its L2.
+template <int BM, int BN>
+__device__ __forceinline__ void place_tile(const Fp8Args& a, int tile, int& m0, int& n0) {
+    constexpr int kBand = 4;
+    const int w = by_xcd(tile, a.tiles_m * a.tiles_n);
+    const int band = kBand * a.tiles_n, gi = w / band, first = gi * kBand;
+    const int rows = min(a.tiles_m - first, kBand), in = w - gi * band;
+    m0 = (first + in % rows) * BM;
+    n0 = in / rows * BN;
+}
+
 // At most N of this wave's loads are still in flight (vmcnt; loads retire in order).
 template <int N>
 __device__ __forceinline__ void wait_loads() {
@@ -139,6 +159,13 @@ __device__ __forceinline__ void barrier() {
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4) | (0 << 8));
     __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// This wave's LDS accesses are done.
+__device__ __forceinline__ void wait_lds() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4) | (0 << 8));
     asm volatile("" ::: "memory");
 }
 

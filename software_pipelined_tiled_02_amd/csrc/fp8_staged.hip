@@ -105,13 +105,8 @@ struct Staged {
     // Tile number `tile`: where it is, and where a lane's loads start.
     __device__ static __forceinline__ void locate(const Fp8Args& a, State& s, int tile) {
         const int tid = threadIdx.x, ntiles = a.tiles_m * a.tiles_n;
-        // Each XCD gets a run of tiles, in bands of 4 tile rows, so that what
-        // it holds at a time shares rows of A and of B in its L2.
-        const int w = by_xcd(tile, ntiles);
-        constexpr int kBand = 4;
-        const int band = kBand * a.tiles_n, gi = w / band, first = gi * kBand;
-        const int rows = min(a.tiles_m - first, kBand), in = w - gi * band;
-        const int m0 = (first + in % rows) * BM, n0 = in / rows * BN;
+        int m0, n0;
+        place_tile<BM, BN>(a, tile, m0, n0);
         s.m0 = m0;
         s.n0 = n0;
         // With more tiles than one round, XCD x starts at K-tile 9 x: read at
@@ -304,7 +299,6 @@ const void* by_tile(int tile) {
     case FP8_TILE_256x128: return (const void*)&fp8_staged_tile<AT, BT, SBROW, EXACT, 256, 128, 4, 2, 3, false>;
     case FP8_TILE_128: return (const void*)&fp8_staged_tile<AT, BT, SBROW, EXACT, 128, 128, 2, 4, 4, false>;
     case FP8_TILE_64: return (const void*)&fp8_staged_tile<AT, BT, SBROW, EXACT, 64, 64, 2, 2, 4, false>;
-    case FP8_TILE_64x32: return (const void*)&fp8_staged_tile<AT, BT, SBROW, EXACT, 64, 32, 2, 2, 6, false>;
     default: return nullptr;
     }
 }

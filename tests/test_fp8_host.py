@@ -90,8 +90,8 @@ def q(M=512, N=512, K=512, **kw):
 def test_product_plan():
     """The class that takes the least time by the measured costs, for 256 CUs."""
     T = binding.FP8_TILES
-    for M, N, K, tile in ((1, 4096, 4096, "16x16"), (16, 4096, 8192, "16x16"), (1, 8192, 8192, "16x32"),
-                          (64, 8192, 8192, "64x32"), (128, 4096, 4096, "64x32"), (512, 4096, 4096, "64x64"),
+    for M, N, K, tile in ((1, 4096, 4096, "16x16"), (16, 4096, 8192, "16x16"), (1, 8192, 8192, "64x32"),
+                          (64, 8192, 8192, "64x32"), (128, 4096, 4096, "64x32"), (256, 4096, 4096, "64x64k4"), (512, 4096, 4096, "64x64"),
                           (500, 4104, 4100, "128x128"), (1024, 4096, 4096, "128x128"), (2048, 4096, 4096, "256x128"),
                           (4096, 4096, 4096, "256x256"), (8192, 8192, 8200, "256x256"), (0, 16, 16, None),
                           (16, 16, 0, None)):
@@ -102,6 +102,7 @@ def test_product_plan():
         assert info["k_blocks"] == -(-K // 128)
     assert q(4096, 4096, 4096, c_dtype="f32")[1]["tile"] == T["256x128"]       # fp32 outputs: widened
     assert q(4096, 4096, 4096, c_dtype="f32")[1]["widened"] == 1
+    assert q(1, 8192, 8192, c_dtype="f32")[1]["tile"] == T["16x32"]
     assert q(4096, 4096, 4100, lda=4100)[1]["staged"] == 0                      # rows at any address
     assert q(4096, 4096, 4100, A=8)[1]["staged"] == 0
     assert q(4096, 4096, 4100)[1]["staged"] == 1                                # any K with rows on 16 bytes
@@ -109,7 +110,7 @@ def test_product_plan():
 
 def test_product_refusals():
     assert q(a_type=1)[0] == BAD and q(b_type=18)[0] == BAD and q(c_dtype="i8")[0] == BAD
-    assert q(b_scale_rows=64)[0] == BAD and q(tile=8)[0] == BAD and q(tile=-2)[0] == BAD
+    assert q(b_scale_rows=64)[0] == BAD and q(tile=9)[0] == BAD and q(tile=-2)[0] == BAD
     assert q(accumulate=2)[0] == BAD and q(accumulate=1)[0] == UNSUP
     assert q(accumulate=1, c_dtype="f32")[0] == OK
     assert q(M=-1)[0] == BAD and q(N=-1)[0] == BAD and q(K=-1)[0] == BAD

@@ -9,7 +9,7 @@ from tests.fp8_util import F8, FT, check_product, f8_of, operand, place_bytes, r
 
 pytestmark = pytest.mark.gpu
 
-TILES = ("256x256", "256x128", "128x128", "64x64", "64x32", "32x32", "16x32", "16x16")
+TILES = ("256x256", "256x128", "128x128", "64x64", "64x64k4", "64x32", "32x32", "16x32", "16x16")
 
 
 def case(M, N, K, at="e4m3", bt="e4m3", rows=128, seed=0):
@@ -29,6 +29,18 @@ def test_every_tile(tile, rows, out):
         a, sa, b, sb = case(M, N, K, rows=rows)
         c = run_product(a, sa, b, sb, "e4m3", "e4m3", out_dtype=FT[out], tile=tile)
         check_product(c, a, sa, b, sb, "e4m3", "e4m3", rows, out, "%s %dx%dx%d" % (tile, M, N, K))
+
+
+@pytest.mark.parametrize("K", (2000, 2176, 3733))
+@pytest.mark.parametrize("tile", TILES)
+def test_many_blocks(tile, K):
+    """Blocks whose share among the waves is even and uneven, rings that are refilled often."""
+    for rows, out in ((128, "bf16"), (1, "f32")):
+        if tile == "256x256" and out == "f32":
+            continue
+        a, sa, b, sb = case(70, 65, K, rows=rows)
+        c = run_product(a, sa, b, sb, "e4m3", "e4m3", out_dtype=FT[out], tile=tile)
+        check_product(c, a, sa, b, sb, "e4m3", "e4m3", rows, out, "%s %d" % (tile, K))
 
 
 @pytest.mark.parametrize("at,bt", (("e4m3", "e5m2"), ("e5m2", "e4m3"), ("e5m2", "e5m2")))
@@ -170,7 +182,7 @@ def test_scales_of_any_strides():
                   "bf16", "expanded")
 
 
-@pytest.mark.parametrize("tile", ("256x256", "64x32"))
+@pytest.mark.parametrize("tile", ("256x256", "64x64", "64x32"))
 def test_offsets_past_32_bits(tile):
     """Rows of A, B and C more than 2^32 bytes from their base."""
     M, N, K, ld = 33000, 16, 144, 1 << 17
