@@ -76,18 +76,18 @@ constexpr bool fp8_staged(int t) { return t <= FP8_TILE_64x32; }
 // there too and at 1024^2 x 4096 and 4096^2 x 8200); microseconds at K = 4096 by
 // the class chosen and the next best:
 //   M = 32: 64x32 7.4, 16x32 8.4           M = 64: 64x32 8.1, 64x64k4 9.4
-//   M = 128: 64x32 8.2, 64x64k4 9.4        M = 256: 64x64k4 10.4, 64x64 11.7
-//   M = 512: 64x64 17.3, 64x64k4 18.4      M = 640: 128x128 18.9, 64x64 24.9
+//   M = 128: 64x32 8.2, 64x64k4 9.4        M = 256: 64x64k4 10.3, 64x64 11.1
+//   M = 512: 64x64 17.1, 64x64k4 18.4      M = 640: 128x128 18.9, 64x64 24.9
 //   M = 1024: 128x128 22.3, 256x128 28.8   M = 2048: 256x128 34.6, 128x128 42.1
 //   M = 4096: 256x256 57.8, 256x128 68.4
 // and in fp32 M = 32: 16x32 8.9, 64x32 10.5; M = 128: 64x32 11.2, 64x64k4
-// 14.4; M = 256: 64x64k4 15.1, 64x64 19.9.
+// 14.4; M = 256: 64x64k4 14.9, 64x64 18.8; M = 512: 64x64 26.8, 64x64k4 27.9.
 struct Fp8Cost { int per_cu; double some, all, round; };
 constexpr Fp8Cost fp8_cost(int t, bool exact) {
     return t == FP8_TILE_256 ? Fp8Cost{1, 1.30, 1.65, 6.0}
          : t == FP8_TILE_256x128 ? (exact ? Fp8Cost{1, 1.75, 1.95, 5.0} : Fp8Cost{1, 0.78, 0.93, 5.0})
          : t == FP8_TILE_128 ? (exact ? Fp8Cost{1, 1.00, 1.16, 4.0} : Fp8Cost{1, 0.50, 0.60, 4.0})
-         : t == FP8_TILE_64 ? (exact ? Fp8Cost{2, 0.50, 0.75, 2.8} : Fp8Cost{2, 0.24, 0.42, 2.5})
+         : t == FP8_TILE_64 ? (exact ? Fp8Cost{2, 0.47, 0.71, 2.8} : Fp8Cost{2, 0.24, 0.42, 2.5})
          : t == FP8_TILE_64K4 ? (exact ? Fp8Cost{1, 0.31, 0.31, 3.8} : Fp8Cost{1, 0.18, 0.18, 3.4})
          : t == FP8_TILE_64x32 ? (exact ? Fp8Cost{1, 0.21, 0.21, 3.2} : Fp8Cost{1, 0.13, 0.13, 2.9})
          : t == FP8_TILE_32 ? (exact ? Fp8Cost{2, 0.22, 0.47, 3.5} : Fp8Cost{2, 0.20, 0.44, 2.6})

@@ -23,7 +23,7 @@ struct Staged {
     // that the next tile's first loads can go out before the stores.
     static constexpr int STRIPS = LOOP ? SLOTS * SLOT : 0;
     static constexpr int LDS = max3(SLOTS * SLOT, STRIPS + epilogue_lds(WM * WN, FN, EXACT ? 4 : 2), 0);
-    static_assert(BM + BN <= T && BM % 64 == 0, "a scale per lane, whole waves of A's");
+    static_assert(T <= 512 && BM + BN <= T && BM % 64 == 0, "a scale per lane, whole waves of A's");
     static_assert(LDS <= kLdsBudget, "LDS");
     static_assert(WTN <= kBlock && kBlock % WTN == 0 && (BN % kBlock == 0 || kBlock % BN == 0),
                   "a wave's columns share a tile scale");
@@ -280,8 +280,12 @@ struct Staged {
     }
 };
 
+// A bound of 512 threads, for tiles of fewer too, keeps a kernel to 256
+// registers per thread: given more, the compiler leaves the matrix
+// instructions' sums in those that vector instructions cannot read, a copy
+// for each multiply-add (64 x 64 tiles, 256 x 4096 x 4096: 11.6 us, 11.1 so).
 template <int AT, int BT, bool SBROW, bool EXACT, int BM, int BN, int WM, int WN, int SLOTS, bool LOOP>
-__global__ void __launch_bounds__(WM * WN * 64) fp8_staged_tile(Fp8Args a) {
+__global__ void __launch_bounds__(512) fp8_staged_tile(Fp8Args a) {
     typedef Staged<AT, BT, SBROW, EXACT, BM, BN, WM, WN, SLOTS, LOOP> S;
     __shared__ __attribute__((aligned(16))) uint8_t smem[S::LDS];
     S::run(a, (uint8_t PG_LDS*)smem);

@@ -5,9 +5,10 @@
 // reads too, and (fp32 outputs) widens it again.  Here a wave takes a block of K
 // by itself: it waits only for its own loads, and reads and widens each byte
 // once.  Measured at 256 x 4096 x 4096, 64 x 64 tiles, against waves in 2 x 2
-// with a barrier per K-tile: 10.1 us against 11.7, fp32 15.1 against 19.9; 64 x 8192 x 8192,
-// 64 x 32 tiles: 14.1 against 16.7 (4.9 TB/s: bound by memory).  What is left in fp32 is
-// the widening: 276 vector instructions per 64 matrix instructions of a K-tile.
+// with a barrier per K-tile: 10.2 us against 11.1, fp32 14.9 against 18.8; 64 x
+// 8192 x 8192, 64 x 32 tiles: 14.1 against 16.7 (4.9 TB/s: bound by memory).
+// What is left in fp32 is the widening: 276 vector instructions to a K-tile's
+// 64 matrix instructions.
 #include "fp8_gemm.h"
 
 namespace pg {
@@ -242,10 +243,8 @@ struct Waves {
     }
 };
 
-// The bound is twice the threads it is launched with, which keeps it to 256
-// registers per thread: given more, the compiler leaves the matrix
-// instructions' sums in those that vector instructions cannot read, a copy
-// for each multiply-add.
+// Twice the threads: 256 registers each, as fp8_staged.hip explains
+// (256 x 4096 x 4096: 10.4 us without, 10.0 with).
 template <int AT, int BT, bool SBROW, bool EXACT, int BM, int BN, int W, int SLOTS>
 __global__ void __launch_bounds__(2 * W * 64) fp8_waves_tile(Fp8Args a) {
     typedef Waves<AT, BT, SBROW, EXACT, BM, BN, W, SLOTS> S;
