@@ -66,6 +66,10 @@ int plan_product(int64_t M, int64_t N, int64_t K, int a_type, int b_type, int c_
         double best = 0.0;
         for (int t = 0; t < pg::FP8_TILE_COUNT; ++t) {
             if (kernel(t) == nullptr) continue;
+            // A handful of rows leave a staged tile of 64 mostly loading copies
+            // of A (1 x 8192 x 8192, B not in the caches: 64x32 15.9 us, 16x32
+            // 13.9; 16 rows, in the caches: 13.0 and 14.2).
+            if (M <= 8 && pg::fp8_staged(t)) continue;
             const pg::Fp8Shape sh = pg::fp8_shape(t);
             const double time =
                 pg::fp8_time(t, exact, ceil_div(M, sh.bm) * ceil_div(N, sh.bn), ceil_div(K, kBlock), num_cus);

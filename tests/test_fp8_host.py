@@ -90,7 +90,7 @@ def q(M=512, N=512, K=512, **kw):
 def test_product_plan():
     """The class that takes the least time by the measured costs, for 256 CUs."""
     T = binding.FP8_TILES
-    for M, N, K, tile in ((1, 4096, 4096, "16x16"), (16, 4096, 8192, "16x16"), (1, 8192, 8192, "64x32"),
+    for M, N, K, tile in ((1, 4096, 4096, "16x16"), (16, 4096, 8192, "16x16"), (1, 8192, 8192, "16x32"), (32, 8192, 8192, "64x32"),
                           (64, 8192, 8192, "64x32"), (128, 4096, 4096, "64x32"), (256, 4096, 4096, "64x64k4"), (512, 4096, 4096, "64x64"),
                           (500, 4104, 4100, "128x128"), (1024, 4096, 4096, "128x128"), (2048, 4096, 4096, "256x128"),
                           (4096, 4096, 4096, "256x256"), (8192, 8192, 8200, "256x256"), (0, 16, 16, None),

@@ -142,7 +142,7 @@ def test_backward_sizes(M, D):
 
 
 @pytest.mark.parametrize("x,w", (("bf16", "bf16"), ("f16", "f16"), ("f16", "f32"), ("f32", "f32")))
-@pytest.mark.parametrize("M,D", ((40, 1100), (1030, 300)))
+@pytest.mark.parametrize("M,D", ((40, 1100), (1030, 300), (1030, 2052)))
 def test_backward_types_strides_and_in_place(M, D, x, w):
     t, _, wt = inputs(M, D, x, w, False)
     dy, dh, _ = inputs(M, D, x, w, True, seed=5)
