@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rms_kernel(RmsArgs a) {
 
 // How a backward pass of many rows holds them.  Ahead: in registers, the next
 // row loaded before the current one's sum, so that two rows per group are on
-// their way (8192 x 4096 bf16: 86 us without, 53 with).  Otherwise one at a
+// their way (8192 x 4096 bf16: 86 us without, 52 with).  Otherwise one at a
 // time: the longer the row, the fewer registers a thread has for each value
 // of it, and a form that spills costs more than it gives (4096 x 16384 bf16:
 // 242 us ahead, 112 held).
@@ -366,8 +366,8 @@ hipError_t backward_for(const RmsBackwardArgs& a, hipStream_t stream) {
     if (a.D <= 512) return backward<XT, 64, 1, true>(a, stream);
     if (a.D <= 1024) return backward<XT, 64, 2, true>(a, stream);
     if (a.D <= 2048) return backward<XT, 256, 1, true>(a, stream);
-    if (a.D <= 4096) return backward<XT, 256, 2, true>(a, stream);
-    if (a.D <= 8192) return backward<XT, 512, 2, true>(a, stream);
+    if (a.D <= 4096) return backward<XT, 512, 1, true>(a, stream);
+    if (a.D <= 8192) return backward<XT, 1024, 1, true>(a, stream);
     if constexpr (XT != XT_F32)
         if (a.D <= 12288) return backward<XT, 512, 3, true>(a, stream);
     return backward<XT, 1024, 2, false>(a, stream);
@@ -376,16 +376,19 @@ hipError_t backward_for(const RmsBackwardArgs& a, hipStream_t stream) {
 }  // namespace
 
 RmsBackwardPlan rms_backward_plan(int64_t M, int64_t D, int num_cus) {
-    // us in groups and by columns, bf16 with dh: 560 x 8192 20 and 15, 1024 x
-    // 8192 27.5 and 21.3, 2000 x 8192 39.6 and 36.2, 4000 x 8192 63 and 73; 1024 x 4096 16.2 and
-    // 13.6, 1500 x 4096 17.3 and 17.5; 2000 x 1024 12.7 and 8.8, 8192 x 1024
-    // 20.3 and 20.9.  Groups hold 16384 columns at most (1500 x 20000, read
-    // twice with registers in scratch: 171 us, by columns 77), and above 12288 multiples of 8.
+    // us in groups and by columns, bf16 with dh: 560 x 4096 14.3 and 9.2, 1024
+    // x 4096 15.6 and 13.5, 1300 x 4096 16.1 and 16.7; 560 x 8192 15.9 and
+    // 14.7, 1024 x 8192 20.0 and 21.3, 2000 x 8192 32.5 and 36; 2000 x 1024
+    // 12.7 and 8.8, 8192 x 1024 20.3 and 20.9.  Groups hold 16384 columns at
+    // most (1500 x 20000, read twice with registers in scratch: 171 us, by
+    // columns 77), and above 12288 multiples of 8.
     if (M <= 1024 || (D <= 1024 && M <= 4096) || D > 16384 || (D > 12288 && D % 8 != 0))
         return {true, M <= 512 ? 0 : (int)std::min<int64_t>((M + 255) / 256, 64)};
-    // two workgroups of 256 or 512 threads per CU (one of 1024), each with as
-    // many groups as it holds rows at a time
-    const int64_t most = (int64_t)num_cus * (D <= 1024 ? 4 : D <= 8192 ? 2 : 1);
+    // two workgroups of 256 or 512 threads per CU (one of more), each with as
+    // many groups as it holds rows at a time: more groups leave more parts
+    // (8192 x 8192: 512 groups 110 us, 256 105), fewer have too little on its
+    // way (8192 x 4096: 52 and 62)
+    const int64_t most = (int64_t)num_cus * (D <= 1024 ? 4 : D <= 4096 ? 2 : 1);
     return {false, (int)std::min(M, most)};
 }
 
