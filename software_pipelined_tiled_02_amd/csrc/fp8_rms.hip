@@ -364,7 +364,7 @@ hipError_t backward_for(const RmsBackwardArgs& a, hipStream_t stream) {
         return backward_columns<XT, 1024, 4>(a, stream);
     }
     if (a.D <= 512) return backward<XT, 64, 1, true>(a, stream);
-    if (a.D <= 1024) return backward<XT, 64, 2, true>(a, stream);
+    if (a.D <= 1024) return backward<XT, 128, 1, true>(a, stream);
     if (a.D <= 2048) return backward<XT, 256, 1, true>(a, stream);
     if (a.D <= 4096) return backward<XT, 512, 1, true>(a, stream);
     if (a.D <= 8192) return backward<XT, 1024, 1, true>(a, stream);
@@ -379,16 +379,17 @@ RmsBackwardPlan rms_backward_plan(int64_t M, int64_t D, int num_cus) {
     // us in groups and by columns, bf16 with dh: 560 x 4096 14.3 and 9.2, 1024
     // x 4096 15.6 and 13.5, 1300 x 4096 16.1 and 16.7; 560 x 8192 15.9 and
     // 14.7, 1024 x 8192 20.0 and 21.3, 2000 x 8192 32.5 and 36; 2000 x 1024
-    // 12.7 and 8.8, 8192 x 1024 20.3 and 20.9.  Groups hold 16384 columns at
+    // 12.7 and 8.8, 8192 x 1024 19.4 and 20.9.  Groups hold 16384 columns at
     // most (1500 x 20000, read twice with registers in scratch: 171 us, by
     // columns 77), and above 12288 multiples of 8.
     if (M <= 1024 || (D <= 1024 && M <= 4096) || D > 16384 || (D > 12288 && D % 8 != 0))
         return {true, M <= 512 ? 0 : (int)std::min<int64_t>((M + 255) / 256, 64)};
     // two workgroups of 256 or 512 threads per CU (one of more), each with as
     // many groups as it holds rows at a time: more groups leave more parts
-    // (8192 x 8192: 512 groups 110 us, 256 105), fewer have too little on its
-    // way (8192 x 4096: 52 and 62)
-    const int64_t most = (int64_t)num_cus * (D <= 1024 ? 4 : D <= 4096 ? 2 : 1);
+    // (8192 x 8192: 512 groups 110 us, 256 105; 8192 x 2048: 1024 39, 512 31),
+    // fewer have too little on the way (8192 x 4096: 512 52, 256 62; 16384 x
+    // 256: 1536 18.0, 1024 21.3)
+    const int64_t most = (int64_t)num_cus * (D <= 512 ? 6 : D <= 1024 ? 4 : D <= 4096 ? 2 : 1);
     return {false, (int)std::min(M, most)};
 }
 
