@@ -22,7 +22,7 @@ namespace {
 // Sum over the TPR threads of a row, the same in each (red: one slot per
 // wave; a caller in a loop alternates between two).
 template <int TPR>
-__device__ __forceinline__ float row_sum(float x, float* red) {
+__device__ __forceinline__ float row_sum(float x, float* red) {     // TPR > 64: the workgroup's only row
     x = sum64(x);
     if constexpr (TPR > 64) {
         const int wave = threadIdx.x >> 6;
@@ -100,9 +100,9 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rms_kernel(RmsArgs a) {
 // Row group g of `groups` takes rows g, g + groups, ...: it keeps its part
 // of dw in registers over them and writes it once, to parts[g].
 template <int XT, int TPR, int NC, bool AHEAD>       // AHEAD: any D, else multiples of 8
-__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rms_backward_kernel(RmsBackwardArgs a) {
+__global__ void __launch_bounds__(TPR == 64 ? 256 : TPR) rms_backward_kernel(RmsBackwardArgs a) {
     __shared__ float red[2][TPR > 64 ? TPR / 64 : 1];
-    constexpr int RPW = TPR < 256 ? 256 / TPR : 1;
+    constexpr int RPW = TPR == 64 ? 4 : 1;                   // rows of several waves meet at barriers: one each
     constexpr bool KEEP = AHEAD;                             // the weight stays in registers too
     const int t = threadIdx.x % TPR;
     const int group = blockIdx.x * RPW + threadIdx.x / TPR;
@@ -328,9 +328,9 @@ hipError_t sum_parts(const RmsBackwardArgs& a, hipStream_t stream) {
 
 template <int XT, int TPR, int NC, bool AHEAD>
 hipError_t backward(const RmsBackwardArgs& a, hipStream_t stream) {
-    constexpr int RPW = TPR < 256 ? 256 / TPR : 1;
+    constexpr int RPW = TPR == 64 ? 4 : 1;
     hipLaunchKernelGGL((rms_backward_kernel<XT, TPR, NC, AHEAD>), dim3((unsigned)((a.groups + RPW - 1) / RPW)),
-                       dim3(TPR < 256 ? 256 : TPR), 0, stream, a);
+                       dim3(TPR * RPW), 0, stream, a);
     const hipError_t e = hipGetLastError();
     return e != hipSuccess ? e : sum_parts(a, stream);
 }
