@@ -45,6 +45,7 @@ struct Fp8Args {
     int32_t tiles_m, tiles_n;
     int32_t c_type;          // XT_*
     int32_t accumulate;      // C += (fp32)
+    int32_t c_lines;         // C's rows start on 128 bytes
 };
 
 // Tile classes: the workgroup's part of C, its waves, and how many of them
@@ -265,7 +266,10 @@ constexpr int epilogue_lds(int waves, int fn, int size) { return waves * 16 * st
 // write 32-byte runs of 16 rows.  A strip of 16 rows goes through the wave's
 // own part of LDS instead and leaves 16 bytes per lane, whole rows of the block
 // at a time (256x256 tiles, 4096^3: 4 us less, at 8192^3 30 us less of 490).
-// STREAM: past the caches (C is far larger than they are).
+// STREAM: past the caches where C's rows start on whole lines (8192 x 4096 x
+// 256 fp32: 43.6 us, 49.0 through them; 2048 x 4096^2 bf16 35.7 and 37.3);
+// pieces of lines are joined there (8192 x 8190 x 512 bf16: 60.5 us, past them 76.6;
+// 6384 x 2731 x 128 fp32 23.7 and 30.4).
 template <bool EXACT, int FM, int FN, bool STREAM>
 __device__ __forceinline__ void store_block(const Fp8Args& a, uint8_t PG_LDS* smem, int wave, int m0, int n0,
                                             const f32x4 (&acc)[FM][FN]) {
@@ -289,8 +293,13 @@ __device__ __forceinline__ void store_block(const Fp8Args& a, uint8_t PG_LDS* sm
                 i32x4u* dst = (i32x4u*)((uint8_t*)a.C + ((int64_t)(m0 + 16 * i + row) * a.ldc + n0) * SIZE + c * 16);
                 if constexpr (EXACT)
                     if (a.accumulate) v = __builtin_bit_cast(i32x4, __builtin_bit_cast(f32x4, v) + __builtin_bit_cast(f32x4, (i32x4)*dst));
-                if constexpr (STREAM) __builtin_nontemporal_store(v, dst);
-                else *dst = v;
+                if (STREAM && a.c_lines) {
+                    asm volatile("" ::: "memory");       // (or the two stores become a plain one)
+                    __builtin_nontemporal_store(v, dst);
+                    asm volatile("" ::: "memory");
+                } else {
+                    *dst = v;
+                }
             }
         }
         return;

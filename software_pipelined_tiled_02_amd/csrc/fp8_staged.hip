@@ -59,7 +59,7 @@ struct Staged {
         x.base = smem + slot * SLOT;
         x.so = __builtin_amdgcn_readfirstlane(t < s.KB ? (uint32_t)kb * kBlock : kOutside);
         x.ss = __builtin_amdgcn_readfirstlane(t < s.KB ? (uint32_t)kb * s.s_blk : kOutside);
-        x.out = FIRST && kb * kBlock + s.kc >= s.K ? kOutside : 0u;
+        x.out = FIRST && t < s.KB && kb * kBlock + s.kc >= s.K ? kOutside : 0u;     // (never on top of x.so's)
         return x;
     }
     // Load q of a K-tile's LPT: chunks of A, chunks of B, then the scales.
@@ -173,7 +173,7 @@ struct Staged {
                 locate(a, s, tile);
                 fill(s, smem);
             }
-            store_block<EXACT, FM, FN, BM * BN == 256 * 256>(a, smem + STRIPS, s.wave, m0, n0, acc);
+            store_block<EXACT, FM, FN, (BM * BN >= 128 * 128)>(a, smem + STRIPS, s.wave, m0, n0, acc);
             if (!more) return;
         }
     }

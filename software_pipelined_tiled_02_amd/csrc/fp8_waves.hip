@@ -57,7 +57,8 @@ struct Waves {
         x.ssa = __builtin_amdgcn_readfirstlane(t < s.KB ? (uint32_t)kb * s.sa_blk : kOutside);
         x.ssb = __builtin_amdgcn_readfirstlane(t < s.KB ? (uint32_t)kb * s.sb_blk : kOutside);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) x.out[h] = FIRST && kb * kBlock + (s.kc ^ (32 * h)) >= s.K ? kOutside : 0u;
+        for (int h = 0; h < 2; ++h)                          // (never on top of x.so's)
+            x.out[h] = FIRST && t < s.KB && kb * kBlock + (s.kc ^ (32 * h)) >= s.K ? kOutside : 0u;
         return x;
     }
     __device__ static __forceinline__ void load(const State& s, const Issue& x, int q) {

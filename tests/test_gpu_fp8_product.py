@@ -25,7 +25,7 @@ def case(M, N, K, at="e4m3", bt="e4m3", rows=128, seed=0):
 def test_every_tile(tile, rows, out):
     if tile == "256x256" and out == "f32":
         pytest.skip("refused: fp32 outputs stop at 256x128")
-    for M, N, K in ((33, 140, 300), (259, 131, 128), (16, 16, 1040)):
+    for M, N, K in ((33, 140, 300), (259, 131, 128), (256, 256, 272), (16, 16, 1040)):
         a, sa, b, sb = case(M, N, K, rows=rows)
         c = run_product(a, sa, b, sb, "e4m3", "e4m3", out_dtype=FT[out], tile=tile)
         check_product(c, a, sa, b, sb, "e4m3", "e4m3", rows, out, "%s %dx%dx%d" % (tile, M, N, K))
