@@ -155,7 +155,7 @@ int gemm_run_fp8(gemm_handle_t h, int64_t M, int64_t N, int64_t K, int a_type, i
     a.tiles_n = (int32_t)plan.tiles_n;
     a.c_type = c_dtype;
     a.accumulate = accumulate;
-    a.c_lines = aligned(C, 128) && ldc * size_of(c_dtype) % 128 == 0;
+    a.c_lines = !accumulate && aligned(C, 128) && ldc * size_of(c_dtype) % 128 == 0;
     void* kargs[] = {&a};
     return pg::on_device(h, [&] {
         const hipError_t e = hipLaunchKernel(plan.fn, dim3((unsigned)plan.info.grid), dim3((unsigned)plan.info.threads),

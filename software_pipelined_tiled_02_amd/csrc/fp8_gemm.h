@@ -45,7 +45,7 @@ struct Fp8Args {
     int32_t tiles_m, tiles_n;
     int32_t c_type;          // XT_*
     int32_t accumulate;      // C += (fp32)
-    int32_t c_lines;         // C's rows start on 128 bytes
+    int32_t c_lines;         // C's rows start on 128 bytes, and nothing is read from them
 };
 
 // Tile classes: the workgroup's part of C, its waves, and how many of them
@@ -277,8 +277,25 @@ __device__ __forceinline__ void store_block(const Fp8Args& a, uint8_t PG_LDS* sm
     constexpr int SIZE = EXACT ? 4 : 2, ROW = strip_row(FN, SIZE), CHUNKS = FN * SIZE;   // 16-byte chunks of a row
     if (m0 + 16 * FM <= a.M && n0 + 16 * FN <= a.N) {
         uint8_t PG_LDS* strip = smem + wave * 16 * ROW;     // (a wave's LDS accesses keep their order)
+        constexpr int Q = (16 * CHUNKS + 63) / 64;
+        const auto target = [&](int i, int q) {
+            const int row = (q * 64 + lane) / CHUNKS, c = (q * 64 + lane) % CHUNKS;
+            return (i32x4u*)((uint8_t*)a.C + ((int64_t)(m0 + 16 * i + row) * a.ldc + n0) * SIZE + c * 16);
+        };
+        // What C holds (accumulate), a strip ahead: behind the stores each
+        // load would be waited for in turn (8192 x 4096 x 512: 101 us, 89 so).
+        f32x4 old[2][Q];
+        const auto fetch = [&](int i) {
+            if constexpr (EXACT)
+                if (a.accumulate)
+#pragma unroll
+                    for (int q = 0; q < Q; ++q)
+                        if ((q * 64 + lane) / CHUNKS < 16) old[i & 1][q] = __builtin_bit_cast(f32x4, (i32x4)*target(i, q));
+        };
+        fetch(0);
 #pragma unroll
         for (int i = 0; i < FM; ++i) {
+            if (i + 1 < FM) fetch(i + 1);
 #pragma unroll
             for (int j = 0; j < FN; ++j) {
                 uint8_t PG_LDS* p = strip + r * ROW + (16 * j + 4 * g) * SIZE;
@@ -286,13 +303,13 @@ __device__ __forceinline__ void store_block(const Fp8Args& a, uint8_t PG_LDS* sm
                 else *(i32x2 PG_LDS*)p = to_16(acc[i][j], a.c_type);
             }
 #pragma unroll
-            for (int q = 0; q < (16 * CHUNKS + 63) / 64; ++q) {
+            for (int q = 0; q < Q; ++q) {
                 const int row = (q * 64 + lane) / CHUNKS, c = (q * 64 + lane) % CHUNKS;
                 if (row >= 16) break;
                 i32x4 v = *(const i32x4 PG_LDS*)(strip + row * ROW + c * 16);
-                i32x4u* dst = (i32x4u*)((uint8_t*)a.C + ((int64_t)(m0 + 16 * i + row) * a.ldc + n0) * SIZE + c * 16);
+                i32x4u* dst = target(i, q);
                 if constexpr (EXACT)
-                    if (a.accumulate) v = __builtin_bit_cast(i32x4, __builtin_bit_cast(f32x4, v) + __builtin_bit_cast(f32x4, (i32x4)*dst));
+                    if (a.accumulate) v = __builtin_bit_cast(i32x4, __builtin_bit_cast(f32x4, v) + old[i & 1][q]);
                 if (STREAM && a.c_lines) {
                     asm volatile("" ::: "memory");       // (or the two stores become a plain one)
                     __builtin_nontemporal_store(v, dst);
