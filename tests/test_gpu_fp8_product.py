@@ -103,8 +103,9 @@ def test_output_stays_inside_its_rows(tile, N, ldc, offset):
 
 
 @pytest.mark.parametrize("tile", TILES[1:])
-def test_accumulate(tile):
-    M, N, K = 70, 131, 400
+@pytest.mark.parametrize("M,N", ((70, 131), (300, 272)))
+def test_accumulate(tile, M, N):
+    K = 400
     a, sa, b, sb = case(M, N, K, rows=1)
     c = torch.randn((M, N), device="cuda")
     base = c.double().cpu().numpy()
