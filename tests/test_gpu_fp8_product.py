@@ -183,7 +183,7 @@ def test_scales_of_any_strides():
                   "bf16", "expanded")
 
 
-@pytest.mark.parametrize("tile", ("256x256", "64x64", "64x32"))
+@pytest.mark.parametrize("tile", ("256x256", "64x64", "64x64k4", "64x32"))
 def test_offsets_past_32_bits(tile):
     """Rows of A, B and C more than 2^32 bytes from their base."""
     M, N, K, ld = 33000, 16, 144, 1 << 17

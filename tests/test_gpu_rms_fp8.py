@@ -186,6 +186,54 @@ def test_backward_is_the_forwards_difference():
         assert abs((loss(x, w + d) - loss(x, w - d)) / (2 * step) - float(dw[j])) < 1e-3
 
 
+def test_offsets_past_32_bits():
+    """Rows 2^30 and more elements apart: row 2 lies past 2^31 elements."""
+    M, D, ld = 3, 520, 2 ** 30 + 24
+    buf = torch.empty(2 * ld + 8 * D, dtype=torch.bfloat16, device="cuda")
+    x, r, w = inputs(M, D, "bf16", "bf16", True)
+    dy, dh, _ = inputs(M, D, "bf16", "bf16", True, seed=5)
+
+    def far(i, values=None):
+        v = buf.as_strided((M, D), (ld, 1), i * D)
+        return v if values is None else v.copy_(values.cuda())
+
+    want = binding.rms_fp8(x.cuda(), w.cuda(), residual=r.cuda(), norm=True)
+    got = binding.rms_fp8(far(0, x), w.cuda(), residual=far(1, r), norm=True, h_out=far(2))
+    for a, b in zip(got, want):
+        assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
+    dx, dw = binding.rms_backward(dy.cuda(), want[2], w.cuda(), want[3], dh=dh.cuda())
+    for into in (far(5), far(3, dy)):                              # beside the others, and in place
+        gx, gw = binding.rms_backward(far(3, dy), got[2], w.cuda(), got[3], dh=far(4, dh), dx_out=into)
+        assert torch.equal(gx, dx) and torch.equal(gw, dw)
+
+
+@pytest.mark.parametrize("M,D", ((600, 1032), (1100, 1032)))
+def test_backward_captured_and_replayed(M, D):
+    """Two graphs of one pool, whose parts of dw share memory, replayed in turn between eager calls."""
+    t, _, w = inputs(M, D, "bf16", "bf16", False)
+    assert binding.gemm_rms_backward_workspace(M, D) > 0
+    dy, dh, _ = (v.cuda() if v is not None else v for v in inputs(M, D, "bf16", "bf16", True, seed=5))
+    h, w = t.cuda(), w.cuda()
+    rstd = torch.rsqrt(h.float().square().mean(1) + 1e-6)
+    binding.rms_backward(dy, h, w, rstd, dh=dh)                    # eager once: the library
+    torch.cuda.synchronize()
+    graphs, pool = [], None
+    for extra in (dh, None):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, pool=pool):
+            out = binding.rms_backward(dy, h, w, rstd, dh=extra)
+        pool = g.pool()
+        graphs.append((g, extra, out))
+    for i in range(4):
+        h.copy_(torch.roll(t, i, 0))
+        dy.mul_(-1.25)
+        for g, extra, out in graphs:
+            want = binding.rms_backward(dy, h, w, rstd, dh=extra)
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+
+
 def test_two_streams_at_once():
     """Calls that overlap share nothing: each has its own workspace."""
     M, D = 1500, 2048
