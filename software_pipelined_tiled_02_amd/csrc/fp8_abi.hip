@@ -9,6 +9,7 @@
 #include "handle.h"
 #include "fp8_common.h"
 #include "fp8_gemm.h"
+#include "fp8_rms_plan.h"
 
 namespace {
 
@@ -252,7 +253,7 @@ int gemm_rms_fp8(gemm_handle_t h, int64_t M, int64_t D, int x_dtype, int w_dtype
 
 int64_t gemm_rms_backward_workspace(int64_t M, int64_t D) {
     if (M < 0 || D < 0 || M > GEMM_RMS_MAX_ROWS || D > GEMM_RMS_MAX_D) return 0;
-    return pg::rms_backward_plan(M, D, kDefaultCus).parts * pg::rms_parts_row(D) * 4;
+    return pg::rms_backward_form(M, D, false, kDefaultCus).parts * pg::rms_parts_row(D) * 4;
 }
 
 int gemm_rms_backward(gemm_handle_t h, int64_t M, int64_t D, int x_dtype, int w_dtype, const void* DY, int64_t lddy,
@@ -289,16 +290,15 @@ int gemm_rms_backward(gemm_handle_t h, int64_t M, int64_t D, int x_dtype, int w_
     a.lddx = lddx;
     a.M = (int32_t)M;
     a.D = (int32_t)D;
-    const pg::RmsBackwardPlan plan = pg::rms_backward_plan(M, D, kDefaultCus);
-    a.groups = plan.parts;
-    a.by_columns = plan.by_columns;
+    const pg::RmsBackwardForm form = pg::rms_backward_form(M, D, x_dtype == GEMM_F32, kDefaultCus);
+    a.groups = form.parts;
     a.w_f32 = w_dtype == GEMM_F32;
     const auto meets = [&](const void* p, int64_t ld) {      // the byte ranges of DX and p
         const uintptr_t x = (uintptr_t)DX, y = (uintptr_t)p;
         return any && x < y + ((uintptr_t)(M - 1) * ld + D) * sz && y < x + ((uintptr_t)(M - 1) * lddx + D) * sz;
     };
     a.in_place = meets(DY, lddy) || meets(H, ldh);
-    return pg::on_device(h, [&] { return pg::launch_rms_backward(a, x_dtype, (hipStream_t)stream); });
+    return pg::on_device(h, [&] { return pg::launch_rms_backward(a, form, x_dtype, (hipStream_t)stream); });
 }
 
 }  // extern "C"

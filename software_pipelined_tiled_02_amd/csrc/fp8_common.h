@@ -58,7 +58,6 @@ struct RmsBackwardArgs {
     int32_t M, D, groups;    // groups: parts of dw
     int32_t w_f32;
     int32_t in_place;        // DX's bytes meet DY's or H's
-    int32_t by_columns;
 };
 
 #if defined(__HIPCC__)
@@ -241,15 +240,8 @@ hipError_t launch_quantize(const QuantizeArgs& a, int xtype, bool tile, hipStrea
 // Rows of one workgroup (blocks of 128 columns each).
 int quantize_rows_per_group(int64_t M, int64_t K, bool tile);
 hipError_t launch_rms(const RmsArgs& a, int xtype, hipStream_t stream);
-hipError_t launch_rms_backward(const RmsBackwardArgs& a, int xtype, hipStream_t stream);
-// A backward pass's form, and how many parts of dw it leaves in the workspace
-// (0: it needs none).
-struct RmsBackwardPlan {
-    bool by_columns;
-    int parts;
-};
-RmsBackwardPlan rms_backward_plan(int64_t M, int64_t D, int num_cus);
-constexpr int64_t rms_parts_row(int64_t D) { return (D + 3) / 4 * 4; }
+struct RmsBackwardForm;      // fp8_rms_plan.h
+hipError_t launch_rms_backward(const RmsBackwardArgs& a, const RmsBackwardForm& form, int xtype, hipStream_t stream);
 
 }  // namespace pg
 

@@ -11,9 +11,8 @@
 // (fp32) between its statistics and its output: TPR threads hold it, 8
 // consecutive values per thread and step, NC steps.  A block of 128 is 16
 // neighbouring lanes.
-#include <algorithm>
-
 #include "fp8_common.h"
+#include "fp8_rms_plan.h"
 
 namespace pg {
 
@@ -103,12 +102,13 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rms_kernel(RmsArgs a) {
 // row loaded before the current one's sum, so that two rows per group are on
 // their way (8192 x 4096 bf16: 86 us without, 52 with).  Otherwise one at a
 // time: the longer the row, the fewer registers a thread has for each value
-// of it, and a form that spills costs more than it gives (4096 x 16384 bf16:
-// 242 us ahead, 112 held).
+// of it, and two rows of 16384 go to scratch (4096 x 16384 bf16: 242 us ahead,
+// 112 held).  fp8_rms_plan.h chooses; the launches refuse a row that a form
+// does not take.
 
 // Row group g of `groups` takes rows g, g + groups, ...: it keeps its part
 // of dw in registers over them and writes it once, to parts[g].
-template <int XT, int TPR, int NC, bool AHEAD>       // AHEAD: any D, else multiples of 8
+template <int XT, int TPR, int NC, bool AHEAD, bool WHOLE>       // WHOLE: D is a multiple of 8
 __global__ void __launch_bounds__(TPR == 64 ? 256 : TPR) rms_backward_kernel(RmsBackwardArgs a) {
     __shared__ float red[2][TPR > 64 ? TPR / 64 : 1];
     constexpr int RPW = TPR == 64 ? 4 : 1;                   // rows of several waves meet at barriers: one each
@@ -124,14 +124,14 @@ __global__ void __launch_bounds__(TPR == 64 ? 256 : TPR) rms_backward_kernel(Rms
         x.rstd = a.rstd[m];
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
-            const int k = (i * TPR + t) * 8, n = AHEAD ? min(8, max(0, a.D - k)) : k < a.D ? 8 : 0;
+            const int k = (i * TPR + t) * 8, n = WHOLE ? (k < a.D ? 8 : 0) : min(8, max(0, a.D - k));
             x.dy[i] = fetch8<XT>(a.DY, m * a.lddy + k, k, n);
             x.h[i] = fetch8<XT>(a.H, m * a.ldh + k, k, n);
             if (a.DH != nullptr) x.dh[i] = fetch8<XT>(a.DH, m * a.lddh + k, k, n);
         }
     };
     auto weight = [&](int i, float (&w)[8]) {
-        const int k = (i * TPR + t) * 8, n = AHEAD ? min(8, max(0, a.D - k)) : k < a.D ? 8 : 0;
+        const int k = (i * TPR + t) * 8, n = WHOLE ? (k < a.D ? 8 : 0) : min(8, max(0, a.D - k));
         load_w<XT>(a.W, k, n, a.w_f32, w);
     };
     float kept[KEEP ? NC : 1][8], dw[NC][8];
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(TPR == 64 ? 256 : TPR) rms_backward_kernel(Rms
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int k = (i * TPR + t) * 8, n = min(8, max(0, a.D - k));
-            if constexpr (AHEAD) {
+            if constexpr (!WHOLE) {
                 settle8<XT>(x.dy[i], k, n);
                 settle8<XT>(x.h[i], k, n);
             }
@@ -169,9 +169,9 @@ __global__ void __launch_bounds__(TPR == 64 ? 256 : TPR) rms_backward_kernel(Rms
         const float c = x.rstd * x.rstd * (dot / (float)a.D);
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
-            const int k = (i * TPR + t) * 8, n = AHEAD ? min(8, max(0, a.D - k)) : k < a.D ? 8 : 0;
+            const int k = (i * TPR + t) * 8, n = WHOLE ? (k < a.D ? 8 : 0) : min(8, max(0, a.D - k));
             float dx[8];
-            if (AHEAD && a.DH != nullptr) settle8<XT>(x.dh[i], k, n);
+            if (!WHOLE && a.DH != nullptr) settle8<XT>(x.dh[i], k, n);
             if constexpr (!KEEP) weight(i, kept[0]);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
@@ -340,10 +340,11 @@ hipError_t sum_parts(const RmsBackwardArgs& a, hipStream_t stream) {
     return hipGetLastError();
 }
 
-template <int XT, int TPR, int NC, bool AHEAD>
+template <int XT, int TPR, int NC, bool AHEAD, bool WHOLE>
 hipError_t backward(const RmsBackwardArgs& a, hipStream_t stream) {
     constexpr int RPW = TPR == 64 ? 4 : 1;
-    hipLaunchKernelGGL((rms_backward_kernel<XT, TPR, NC, AHEAD>), dim3((unsigned)((a.groups + RPW - 1) / RPW)),
+    if ((WHOLE && a.D % 8 != 0) || a.D > TPR * NC * 8) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((rms_backward_kernel<XT, TPR, NC, AHEAD, WHOLE>), dim3((unsigned)((a.groups + RPW - 1) / RPW)),
                        dim3(TPR * RPW), 0, stream, a);
     const hipError_t e = hipGetLastError();
     return e != hipSuccess ? e : sum_parts(a, stream);
@@ -352,6 +353,7 @@ hipError_t backward(const RmsBackwardArgs& a, hipStream_t stream) {
 template <int XT, int TPR, int NC, int AT_ONCE>
 hipError_t launch_columns(const RmsBackwardArgs& a, hipStream_t stream) {
     constexpr int T = TPR < 256 ? 256 : TPR, RPW = T / TPR, COLUMNS = columns_lanes(TPR) * 8;
+    if (a.D > TPR * NC * 8) return hipErrorInvalidValue;
     const int rows = (int)((a.M + RPW - 1) / RPW);
     const int columns = (a.D + COLUMNS - 1) / COLUMNS * (a.groups > 0 ? a.groups : 1);
     const bool apart = a.in_place && rows > 0;
@@ -376,46 +378,41 @@ hipError_t backward_columns(const RmsBackwardArgs& a, hipStream_t stream) {
     return launch_columns<XT, TPR, NC, 4>(a, stream);
 }
 
+constexpr int form_key(int tpr, int nc) { return 8 * tpr + nc; }
+
 template <int XT>
-hipError_t backward_for(const RmsBackwardArgs& a, hipStream_t stream) {
-    if (a.by_columns) {
-        if (a.D <= 512) return backward_columns<XT, 64, 1>(a, stream);
-        if (a.D <= 1024) return backward_columns<XT, 64, 2>(a, stream);
-        if (a.D <= 2048) return backward_columns<XT, 256, 1>(a, stream);
-        if (a.D <= 4096) return backward_columns<XT, 256, 2>(a, stream);
-        if (a.D <= 8192) return backward_columns<XT, 512, 2>(a, stream);
-        if (a.D <= 16384) return backward_columns<XT, 1024, 2>(a, stream);
-        return backward_columns<XT, 1024, 4>(a, stream);
+hipError_t backward_for(const RmsBackwardArgs& a, const RmsBackwardForm& f, hipStream_t stream) {
+    const int key = form_key(f.tpr, f.nc);
+    if (f.by_columns) {
+        switch (key) {
+        case form_key(64, 1): return backward_columns<XT, 64, 1>(a, stream);
+        case form_key(64, 2): return backward_columns<XT, 64, 2>(a, stream);
+        case form_key(256, 1): return backward_columns<XT, 256, 1>(a, stream);
+        case form_key(256, 2): return backward_columns<XT, 256, 2>(a, stream);
+        case form_key(512, 2): return backward_columns<XT, 512, 2>(a, stream);
+        case form_key(1024, 2): return backward_columns<XT, 1024, 2>(a, stream);
+        case form_key(1024, 4): return backward_columns<XT, 1024, 4>(a, stream);
+        default: return hipErrorInvalidValue;
+        }
     }
-    if (a.D <= 512) return backward<XT, 64, 1, true>(a, stream);
-    if (a.D <= 1024) return backward<XT, 128, 1, true>(a, stream);
-    if (a.D <= 2048) return backward<XT, 256, 1, true>(a, stream);
-    if (a.D <= 4096) return backward<XT, 512, 1, true>(a, stream);
-    if (a.D <= 8192) return backward<XT, 1024, 1, true>(a, stream);
-    if constexpr (XT != XT_F32)
-        if (a.D <= 12288) return backward<XT, 512, 3, true>(a, stream);
-    return backward<XT, 1024, 2, false>(a, stream);
+    switch (key) {
+    case form_key(64, 1): return backward<XT, 64, 1, true, false>(a, stream);
+    case form_key(128, 1): return backward<XT, 128, 1, true, false>(a, stream);
+    case form_key(256, 1): return backward<XT, 256, 1, true, false>(a, stream);
+    case form_key(512, 1): return backward<XT, 512, 1, true, false>(a, stream);
+    case form_key(1024, 1): return backward<XT, 1024, 1, true, false>(a, stream);
+    case form_key(512, 3):
+        if constexpr (XT != XT_F32) return backward<XT, 512, 3, true, false>(a, stream);
+        else return hipErrorInvalidValue;
+    case form_key(1024, 2):
+        if (f.whole) return backward<XT, 1024, 2, false, true>(a, stream);
+        if constexpr (XT == XT_F32) return backward<XT, 1024, 2, false, false>(a, stream);
+        else return hipErrorInvalidValue;
+    default: return hipErrorInvalidValue;
+    }
 }
 
 }  // namespace
-
-RmsBackwardPlan rms_backward_plan(int64_t M, int64_t D, int num_cus) {
-    // us in groups and by columns, bf16 with dh: 560 x 4096 14.3 and 9.2, 1024
-    // x 4096 15.6 and 13.5, 1300 x 4096 16.1 and 16.7; 560 x 8192 15.9 and
-    // 14.7, 1024 x 8192 20.0 and 21.3, 2000 x 8192 32.5 and 36; 2000 x 1024
-    // 12.7 and 8.8, 8192 x 1024 19.4 and 20.9.  Groups hold 16384 columns at
-    // most (1500 x 20000, read twice with registers in scratch: 171 us, by
-    // columns 77), and above 12288 multiples of 8.
-    if (M <= 1024 || (D <= 1024 && M <= 4096) || D > 16384 || (D > 12288 && D % 8 != 0))
-        return {true, M <= 512 ? 0 : (int)std::min<int64_t>((M + 255) / 256, 64)};
-    // two workgroups of 256 or 512 threads per CU (one of more), each with as
-    // many groups as it holds rows at a time: more groups leave more parts
-    // (8192 x 8192: 512 groups 110 us, 256 105; 8192 x 2048: 1024 39, 512 31),
-    // fewer have too little on the way (8192 x 4096: 512 52, 256 62; 16384 x
-    // 256: 1536 18.0, 1024 21.3)
-    const int64_t most = (int64_t)num_cus * (D <= 512 ? 6 : D <= 1024 ? 4 : D <= 4096 ? 2 : 1);
-    return {false, (int)std::min(M, most)};
-}
 
 hipError_t launch_rms(const RmsArgs& a, int xtype, hipStream_t stream) {
     switch (xtype) {
@@ -425,11 +422,11 @@ hipError_t launch_rms(const RmsArgs& a, int xtype, hipStream_t stream) {
     }
 }
 
-hipError_t launch_rms_backward(const RmsBackwardArgs& a, int xtype, hipStream_t stream) {
+hipError_t launch_rms_backward(const RmsBackwardArgs& a, const RmsBackwardForm& form, int xtype, hipStream_t stream) {
     switch (xtype) {
-    case XT_F16: return backward_for<XT_F16>(a, stream);
-    case XT_BF16: return backward_for<XT_BF16>(a, stream);
-    default: return backward_for<XT_F32>(a, stream);
+    case XT_F16: return backward_for<XT_F16>(a, form, stream);
+    case XT_BF16: return backward_for<XT_BF16>(a, form, stream);
+    default: return backward_for<XT_F32>(a, form, stream);
     }
 }
 

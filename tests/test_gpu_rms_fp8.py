@@ -161,6 +161,31 @@ def test_backward_types_strides_and_in_place(M, D, x, w):
     assert torch.equal(got, dx) and torch.equal(gw, dw) and bool(wide[3, :, D:].isnan().all())
 
 
+@pytest.mark.parametrize("x", ("f32", "bf16", "f16"))
+@pytest.mark.parametrize("M,D", ((1030, 8196), (1030, 8193), (1030, 9300), (1030, 8200), (2000, 10001), (1030, 12284),
+                                 (1025, 12287), (1025, 12288), (1025, 12292)))
+def test_backward_long_rows_of_every_type(M, D, x):
+    """Rows of 8193 and more in groups, which end inside a thread's 8 values and at them:
+    contiguous, strided with NaNs between the rows, and in place."""
+    t, _, wt = inputs(M, D, x, "f32", False)
+    dy, dh, _ = inputs(M, D, x, "f32", True, seed=5)
+    rstd = torch.rsqrt(t.double().square().mean(1) + 1e-6).float()
+    wt, rs = wt.cuda(), rstd.cuda()
+    flat = torch.full(((M + 1) * D,), 7.0, dtype=FT[x], device="cuda")       # what lies behind the last row stays
+    dx, dw = binding.rms_backward(dy.cuda(), t.cuda(), wt, rs, dh=dh.cuda(), dx_out=flat[:M * D].view(M, D))
+    check_backward(dy, t, wt, rstd, dh, dx, dw, x)
+    assert bool((flat[M * D:] == 7.0).all())
+    wide = torch.full((4, M, D + 5), float("nan"), dtype=FT[x], device="cuda")
+    for i, v in enumerate((dy, t, dh)):
+        wide[i, :, :D] = v.cuda()
+    got, gw = binding.rms_backward(wide[0, :, :D], wide[1, :, :D], wt, rs, dh=wide[2, :, :D], dx_out=wide[3, :, :D])
+    assert torch.equal(got, dx) and torch.equal(gw, dw) and bool(wide[3, :, D:].isnan().all())
+    for into in range(3):
+        got, gw = binding.rms_backward(wide[0, :, :D], wide[1, :, :D], wt, rs, dh=wide[2, :, :D], dx_out=wide[into, :, :D])
+        assert torch.equal(got, dx) and torch.equal(gw, dw) and bool(wide[:, :, D:].isnan().all())
+        wide[into, :, :D] = (dy, t, dh)[into].cuda()
+
+
 def test_backward_is_the_forwards_difference():
     """dx and dw against differences of the forward pass itself, in fp32."""
     M, D, eps = 2, 64, 1e-2
