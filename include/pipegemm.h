@@ -399,7 +399,8 @@ typedef struct {
  * type, a leading dimension below K or N), GEMM_ERR_ALIGNMENT (C, SA or SB
  * not element-aligned, or a staged tile asked for with other rows than it
  * takes), GEMM_ERR_UNSUPPORTED (accumulate without GEMM_F32, the 256x256
- * tile with it, a tile's rows or a row's scales spanning 2^31 bytes),
+ * tile with it, a tile's rows, or the scales of all its blocks, spanning 2^31
+ * bytes),
  * GEMM_ERR_HIP. */
 int gemm_run_fp8(gemm_handle_t h, int64_t M, int64_t N, int64_t K,
                  int a_type, int b_type, int c_dtype, int b_scale_rows, int accumulate, int tile,

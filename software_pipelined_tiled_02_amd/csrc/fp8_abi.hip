@@ -5,6 +5,8 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <algorithm>
+
 #include "pipegemm.h"
 #include "handle.h"
 #include "fp8_common.h"
@@ -22,6 +24,12 @@ bool is_fp8(int t) { return t == GEMM_E4M3 || t == GEMM_E5M2; }
 bool is_float(int t) { return t == GEMM_F16 || t == GEMM_BF16 || t == GEMM_F32; }
 int size_of(int t) { return t == GEMM_F32 ? 4 : 2; }
 int fp8_of(int t) { return t == GEMM_E5M2 ? pg::FP8_E5M2 : pg::FP8_E4M3; }
+
+// rows x blocks scales span less than the buffer range, past which loads give
+// zero: a scale's address is the sum of its row's and its block's parts.
+bool scales_fit(int64_t rows, int64_t row, int64_t blocks, int64_t blk) {
+    return 4 * ((rows > 1 ? (__int128)rows * row : 0) + (blocks > 1 ? (__int128)blocks * blk : 0)) <= INT_MAX;
+}
 
 struct Plan {
     gemm_fp8_info_t info;
@@ -84,11 +92,11 @@ int plan_product(int64_t M, int64_t N, int64_t K, int a_type, int b_type, int c_
     if (plan->fn == nullptr) return tile == GEMM_FP8_TILE_AUTO || rows16 ? GEMM_ERR_UNSUPPORTED : GEMM_ERR_ALIGNMENT;
     const pg::Fp8Shape sh = pg::fp8_shape(tc);
 
-    // 32-bit offsets inside a tile, and of a block's scales
+    // 32-bit offsets inside a tile, and of the scales that a tile takes
     const int64_t lim = (int64_t)1 << 31, kb = ceil_div(K, kBlock);
-    const int64_t sb_rows_of_tile = b_scale_rows == 1 ? sh.bn : ceil_div(sh.bn, kBlock);
-    if (reads && (lda >= lim / sh.bm || ldb >= lim / sh.bn || sa_row >= lim / (4 * sh.bm) ||
-                  sb_row >= lim / (4 * sb_rows_of_tile) || sa_blk >= lim / (4 * kb) || sb_blk >= lim / (4 * kb)))
+    const int64_t sb_rows = b_scale_rows == 1 ? std::min<int64_t>(sh.bn, N) : ceil_div(std::min<int64_t>(sh.bn, N), kBlock);
+    if (reads && (lda >= lim / sh.bm || ldb >= lim / sh.bn || !scales_fit(std::min<int64_t>(sh.bm, M), sa_row, kb, sa_blk) ||
+                  !scales_fit(sb_rows, sb_row, kb, sb_blk)))
         return GEMM_ERR_UNSUPPORTED;
     plan->tiles_m = has_c ? ceil_div(M, sh.bm) : 0;
     plan->tiles_n = has_c ? ceil_div(N, sh.bn) : 0;

@@ -133,6 +133,22 @@ def test_product_refusals():
         binding.gemm_query_fp8(16, 16, 16, lda=8)
 
 
+def test_product_refuses_scales_past_the_buffers_range():
+    """A scale's address is the sum of its row's and its block's parts, which has to stay below 2^31
+    bytes (a load past it gives zero): both sides of the border, of A's and of B's scales."""
+    far = dict(M=256, N=256, K=256, tile="256x256")
+    assert q(sa_row=2 ** 21 - 1, sa_blk=2 ** 28 - 1, **far)[0] == UNSUP         # row 255, block 1: 3.2 GB
+    assert q(sa_row=2 ** 20, sa_blk=2 ** 27 - 1, **far)[0] == OK                # 256 rows and 2 blocks: 2^31 - 8
+    assert q(sa_row=2 ** 20, sa_blk=2 ** 27, **far)[0] == UNSUP
+    rows = dict(far, b_scale_rows=1)
+    assert q(sb_row=2 ** 20, sb_blk=2 ** 27 - 1, **rows)[0] == OK
+    assert q(sb_row=2 ** 20, sb_blk=2 ** 27, **rows)[0] == UNSUP
+    assert q(sb_row=2 ** 27, sb_blk=2 ** 27 - 1, **far)[0] == OK                # tiles: two rows of scales
+    assert q(sb_row=2 ** 27, sb_blk=2 ** 27, **far)[0] == UNSUP
+    assert q(sa_row=2 ** 62, sa_blk=2 ** 62, **far)[0] == UNSUP                 # (no overflow in the check)
+    assert q(M=1, N=256, K=128, sa_row=2 ** 62, sa_blk=2 ** 62)[0] == OK        # one scale: no stride counts
+
+
 class FakeHandle:
     """Enough of a handle for calls that are refused before it is used: the
     entry points check every argument before any HIP call.  (Device 0 with 256
