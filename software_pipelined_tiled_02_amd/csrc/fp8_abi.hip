@@ -31,6 +31,13 @@ bool scales_fit(int64_t rows, int64_t row, int64_t blocks, int64_t blk) {
     return 4 * ((rows > 1 ? (__int128)rows * row : 0) + (blocks > 1 ? (__int128)blocks * blk : 0)) <= INT_MAX;
 }
 
+// A tile's rows span less than 2^31 bytes, with 4096 to spare: the loops address
+// up to 16 blocks past K, with the bit that puts them out of range (2^31), and
+// so large an offset would carry out of 32 bits and come back in range.
+bool rows_fit(int64_t rows, int64_t ld, int64_t K) {
+    return (rows > 1 ? (__int128)rows * ld : K) + 4096 <= (int64_t)1 << 31;
+}
+
 struct Plan {
     gemm_fp8_info_t info;
     const void* fn;
@@ -93,10 +100,10 @@ int plan_product(int64_t M, int64_t N, int64_t K, int a_type, int b_type, int c_
     const pg::Fp8Shape sh = pg::fp8_shape(tc);
 
     // 32-bit offsets inside a tile, and of the scales that a tile takes
-    const int64_t lim = (int64_t)1 << 31, kb = ceil_div(K, kBlock);
-    const int64_t sb_rows = b_scale_rows == 1 ? std::min<int64_t>(sh.bn, N) : ceil_div(std::min<int64_t>(sh.bn, N), kBlock);
-    if (reads && (lda >= lim / sh.bm || ldb >= lim / sh.bn || !scales_fit(std::min<int64_t>(sh.bm, M), sa_row, kb, sa_blk) ||
-                  !scales_fit(sb_rows, sb_row, kb, sb_blk)))
+    const int64_t kb = ceil_div(K, kBlock);
+    const int64_t a_rows = std::min<int64_t>(sh.bm, M), b_rows = std::min<int64_t>(sh.bn, N);
+    if (reads && (!rows_fit(a_rows, lda, K) || !rows_fit(b_rows, ldb, K) || !scales_fit(a_rows, sa_row, kb, sa_blk) ||
+                  !scales_fit(b_scale_rows == 1 ? b_rows : ceil_div(b_rows, kBlock), sb_row, kb, sb_blk)))
         return GEMM_ERR_UNSUPPORTED;
     plan->tiles_m = has_c ? ceil_div(M, sh.bm) : 0;
     plan->tiles_n = has_c ? ceil_div(N, sh.bn) : 0;
@@ -150,13 +157,14 @@ int gemm_run_fp8(gemm_handle_t h, int64_t M, int64_t N, int64_t K, int a_type, i
     a.SA = SA;
     a.SB = SB;
     a.C = C;
-    a.lda = lda;
-    a.ldb = ldb;
+    const bool reads = K > 0;            // else strides are unchecked, and every load is out of range by its bit alone
+    a.lda = reads ? lda : 0;
+    a.ldb = reads ? ldb : 0;
     a.ldc = ldc;
-    a.sa_row = sa_row;
-    a.sa_blk = sa_blk;
-    a.sb_row = sb_row;
-    a.sb_blk = sb_blk;
+    a.sa_row = reads ? sa_row : 0;
+    a.sa_blk = reads ? sa_blk : 0;
+    a.sb_row = reads ? sb_row : 0;
+    a.sb_blk = reads ? sb_blk : 0;
     a.M = (int32_t)M;
     a.N = (int32_t)N;
     a.K = (int32_t)K;

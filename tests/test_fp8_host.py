@@ -149,6 +149,18 @@ def test_product_refuses_scales_past_the_buffers_range():
     assert q(M=1, N=256, K=128, sa_row=2 ** 62, sa_blk=2 ** 62)[0] == OK        # one scale: no stride counts
 
 
+def test_product_refuses_rows_whose_offsets_leave_32_bits():
+    """The loops address up to 16 blocks past K, out of range by a bit of their own: the rows' span
+    leaves room for them.  Both sides of the border, of A and of B."""
+    far = dict(M=32, N=32, tile="32x32", sa_blk=1, sb_blk=1)
+    assert q(K=2 ** 26 - 16, lda=2 ** 26 - 16, ldb=2 ** 26 - 16, **far)[0] == UNSUP
+    assert q(K=2 ** 26 - 128, lda=2 ** 26 - 128, ldb=2 ** 26 - 128, **far)[0] == OK
+    assert q(K=2 ** 26 - 128, lda=2 ** 26 - 112, ldb=2 ** 26 - 128, **far)[0] == UNSUP
+    assert q(K=2 ** 26 - 128, lda=2 ** 26 - 128, ldb=2 ** 26 - 112, **far)[0] == UNSUP
+    one = dict(M=1, N=1, tile="16x16", lda=2 ** 62, ldb=2 ** 62)                # one row: its K counts
+    assert q(K=2 ** 31 - 4096, **one)[0] == OK and q(K=2 ** 31 - 4095, **one)[0] == UNSUP
+
+
 class FakeHandle:
     """Enough of a handle for calls that are refused before it is used: the
     entry points check every argument before any HIP call.  (Device 0 with 256

@@ -133,6 +133,17 @@ def test_sizes_of_zero():
 
 
 @pytest.mark.parametrize("tile", TILES)
+def test_no_columns_and_far_rows(tile):
+    """K = 0: C is zeros, and the strides of rows and scales without elements do not matter."""
+    M, N, ld = 70, 130, 2 ** 31 - 16
+    a, b = (torch.empty(0, dtype=F8["e4m3"], device="cuda").as_strided((n, 0), (ld, 1)) for n in (M, N))
+    sa, sb = (torch.empty(0, device="cuda").as_strided((n, 0), (2 ** 29 - 1, 2 ** 29 - 1)) for n in (M, 2))
+    c = torch.full((M, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    binding.run_fp8(a, sa, b, sb, out=c, tile=tile)
+    assert bool((c == 0.0).all())
+
+
+@pytest.mark.parametrize("tile", TILES)
 def test_nan_infinity_and_scales(tile):
     """NaNs, infinities (e5m2) and scales of zero, infinity and NaN reach their row and column alone."""
     M, N, K = 20, 140, 272
@@ -205,6 +216,20 @@ def test_offsets_past_32_bits(tile):
         binding.run_fp8(f8_of(b, "e4m3"), torch.from_numpy(np.repeat(sb, N, 0)).cuda(), buf.view(F8["e4m3"])[:, :K], s,
                         out=ct, tile=tile)
         check_product(ct[:, torch.from_numpy(rows).cuda()], b, np.repeat(sb, N, 0), a, sa, "e4m3", "e4m3", 1, "bf16", tile)
+
+
+@pytest.mark.parametrize("tile", TILES)
+def test_a_very_long_k(tile):
+    """Two rows of 2^28 + 20 columns, all but a few of them zero: offsets near the border of what is taken."""
+    M, N, K = 1, 2, 2 ** 28 + 20
+    at, nb = (0, 2 ** 27 - 1, 2 ** 27, 2 ** 28 - 129, 2 ** 28, K - 1), -(-K // 128)
+    a, b = (torch.zeros((n, K + 12), dtype=torch.uint8, device="cuda") for n in (M, N))
+    for i, k in enumerate(at):
+        a[0, k], b[1, k] = 0x38 + i, 0x40                          # 1 + i / 8 and 2
+    b[0, K - 1] = 0x38
+    s = torch.ones((1, nb), device="cuda")
+    c = binding.run_fp8(a.view(F8["e4m3"])[:, :K], s, b.view(F8["e4m3"])[:, :K], s, tile=tile)
+    assert c.tolist() == [[1 + 5 / 8, 2 * (6 + 15 / 8)]]
 
 
 @pytest.mark.parametrize("tile,rows", (("256x256", 128), ("256x256", 1), ("128x128", 128)))
