@@ -359,7 +359,8 @@ enum { GEMM_E4M3 = 16, GEMM_E5M2 = 17 };
  * 64x32 stage operands through LDS and need rows that start on 16 bytes; the
  * others take any address.  From 64x64_K4 on each wave takes blocks of K of
  * its own (gemm_fp8_info_t's waves_k).  GEMM_FP8_TILE_AUTO: the one that takes the least time
- * by what each cost in measurements. */
+ * by what each cost in measurements, of those (of 32 rows and more) that can
+ * address the call's operands and scales. */
 enum { GEMM_FP8_TILE_AUTO = -1, GEMM_FP8_TILE_256x256 = 0, GEMM_FP8_TILE_256x128 = 1, GEMM_FP8_TILE_128x128 = 2,
        GEMM_FP8_TILE_64x64 = 3, GEMM_FP8_TILE_64x64_K4 = 4, GEMM_FP8_TILE_64x32 = 5, GEMM_FP8_TILE_32x32 = 6,
        GEMM_FP8_TILE_16x32 = 7, GEMM_FP8_TILE_16x16 = 8 };

@@ -76,39 +76,44 @@ int plan_product(int64_t M, int64_t N, int64_t K, int a_type, int b_type, int c_
         const void* fn = pg::fp8_staged_kernel(t, at, bt, b_scale_rows == 1, exact);
         return fn != nullptr ? fn : pg::fp8_waves_kernel(t, at, bt, b_scale_rows == 1, exact);
     };
-    // The class that takes the least time by the measured costs.
+    // A class's launch, and its 32-bit offsets inside a tile (of `rows` rows of
+    // A) and to the scales that a tile takes.
+    const int64_t kb = ceil_div(K, kBlock);
+    auto fits = [&](int t, int64_t rows) {
+        const pg::Fp8Shape sh = pg::fp8_shape(t);
+        if (has_c && ceil_div(M, sh.bm) * ceil_div(N, sh.bn) >= ((int64_t)1 << 32) / (64 * sh.waves)) return false;
+        const int64_t a_rows = std::min(rows, M), b_rows = std::min<int64_t>(sh.bn, N);
+        return !reads || (rows_fit(a_rows, lda, K) && rows_fit(b_rows, ldb, K) && scales_fit(a_rows, sa_row, kb, sa_blk) &&
+                          scales_fit(b_scale_rows == 1 ? b_rows : ceil_div(b_rows, kBlock), sb_row, kb, sb_blk));
+    };
+    // The class that takes the least time by the measured costs, of those that
+    // fit.  (Where only tiles of 16 rows do, which read B for each 16 rows of A,
+    // the caller has to ask for one.)
     int tc = tile;
     if (tc == GEMM_FP8_TILE_AUTO) {
         double best = 0.0;
         for (int t = 0; t < pg::FP8_TILE_COUNT; ++t) {
+            const pg::Fp8Shape sh = pg::fp8_shape(t);
             if (kernel(t) == nullptr) continue;
             // A handful of rows leave a staged tile of 64 mostly loading copies
             // of A (1 x 8192 x 8192, B not in the caches: 64x32 15.9 us, 16x32
             // 13.9; 16 rows, in the caches: 13.0 and 14.2).
             if (M <= 8 && pg::fp8_staged(t)) continue;
-            const pg::Fp8Shape sh = pg::fp8_shape(t);
-            const double time =
-                pg::fp8_time(t, exact, ceil_div(M, sh.bm) * ceil_div(N, sh.bn), ceil_div(K, kBlock), num_cus);
-            if (tc == GEMM_FP8_TILE_AUTO || time < best) {
+            const double time = pg::fp8_time(t, exact, ceil_div(M, sh.bm) * ceil_div(N, sh.bn), kb, num_cus);
+            if ((tc == GEMM_FP8_TILE_AUTO || time < best) && fits(t, std::max(sh.bm, 32))) {
                 tc = t;
                 best = time;
             }
         }
+        if (tc == GEMM_FP8_TILE_AUTO) return GEMM_ERR_UNSUPPORTED;
     }
     plan->fn = kernel(tc);
-    if (plan->fn == nullptr) return tile == GEMM_FP8_TILE_AUTO || rows16 ? GEMM_ERR_UNSUPPORTED : GEMM_ERR_ALIGNMENT;
+    if (plan->fn == nullptr) return rows16 ? GEMM_ERR_UNSUPPORTED : GEMM_ERR_ALIGNMENT;
     const pg::Fp8Shape sh = pg::fp8_shape(tc);
-
-    // 32-bit offsets inside a tile, and of the scales that a tile takes
-    const int64_t kb = ceil_div(K, kBlock);
-    const int64_t a_rows = std::min<int64_t>(sh.bm, M), b_rows = std::min<int64_t>(sh.bn, N);
-    if (reads && (!rows_fit(a_rows, lda, K) || !rows_fit(b_rows, ldb, K) || !scales_fit(a_rows, sa_row, kb, sa_blk) ||
-                  !scales_fit(b_scale_rows == 1 ? b_rows : ceil_div(b_rows, kBlock), sb_row, kb, sb_blk)))
-        return GEMM_ERR_UNSUPPORTED;
+    if (!fits(tc, sh.bm)) return GEMM_ERR_UNSUPPORTED;
     plan->tiles_m = has_c ? ceil_div(M, sh.bm) : 0;
     plan->tiles_n = has_c ? ceil_div(N, sh.bn) : 0;
     const int64_t grid = plan->tiles_m * plan->tiles_n;
-    if (grid >= ((int64_t)1 << 32) / (64 * sh.waves)) return GEMM_ERR_UNSUPPORTED;
     gemm_fp8_info_t& in = plan->info;
     memset(&in, 0, sizeof in);
     in.tile = tc;

@@ -161,6 +161,25 @@ def test_product_refuses_rows_whose_offsets_leave_32_bits():
     assert q(K=2 ** 31 - 4096, **one)[0] == OK and q(K=2 ** 31 - 4095, **one)[0] == UNSUP
 
 
+@pytest.mark.parametrize("size", ((4096, 4096, 4096), (512, 512, 512), (64, 8192, 8192), (5, 4096, 4096), (8192, 8192, 8200)))
+def test_auto_takes_what_some_class_takes(size):
+    """Strides too wide for the cheapest class go to the next one that reaches."""
+    M, N, K = size
+    wide = [dict(lda=1 << e) for e in range(14, 31)] + [dict(ldb=1 << e) for e in range(14, 31)]
+    wide += [dict(sa_row=1 << e, sa_blk=1) for e in range(10, 30)] + [dict(sb_row=1 << e, sb_blk=1) for e in range(10, 30)]
+    wide += [dict(b_scale_rows=1, sb_row=1 << e, sb_blk=1) for e in range(10, 30)]
+    for kw in wide:
+        rc, info = q(M, N, K, **kw)
+        takes = [t for t in range(9) if q(M, N, K, tile=t, **kw)[0] == OK]
+        if any(t <= 6 for t in takes) or (M <= 32 and takes):
+            assert rc == OK and info["tile"] in takes, (kw, takes)
+        elif not takes:
+            assert rc == UNSUP, kw
+    assert q(4096, 4096, 4096, lda=1 << 23)[1]["tile"] == binding.FP8_TILES["128x128"]
+    assert q(4096, 4096, 4096, sa_row=1 << 21, sa_blk=1)[0] == OK
+    assert q(4096, 4096, 4096)[1]["tile"] == binding.FP8_TILES["256x256"]
+
+
 class FakeHandle:
     """Enough of a handle for calls that are refused before it is used: the
     entry points check every argument before any HIP call.  (Device 0 with 256
