@@ -421,7 +421,8 @@ int gemm_query_fp8(int64_t M, int64_t N, int64_t K,
  * of block_rows x 128.  QT, ST: its transpose (K x M), by blocks of 1 x 128
  * along M, or 128 x 128 (the same values and scales as Q's, transposed).
  * Either pair may be NULL, not both.  Only columns before K (M) of Q (QT) are
- * written.  Errors as above; GEMM_ERR_UNSUPPORTED for 2^24 and more workgroups (about
+ * written.  Errors as above; GEMM_ERR_UNSUPPORTED for 2^24 and more workgroups
+ * of 64 x 128 values, 2^23 of 128 x 128 by tiles or with a transpose (about
  * 2^37 values). */
 int gemm_quantize_fp8(gemm_handle_t h, int64_t M, int64_t K, int x_dtype, int fp8_type, int block_rows, int pow2,
                       const void *X, int64_t ldx, void *Q, int64_t ldq, float *S, int64_t s_row, int64_t s_blk,

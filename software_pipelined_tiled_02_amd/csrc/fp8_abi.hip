@@ -203,8 +203,9 @@ int gemm_quantize_fp8(gemm_handle_t h, int64_t M, int64_t K, int x_dtype, int fp
     if (!aligned(X, sz) || !aligned(S, 4) || !aligned(ST, 4)) return GEMM_ERR_ALIGNMENT;
     if (M > INT_MAX || K > INT_MAX) return GEMM_ERR_UNSUPPORTED;
     const bool tile = block_rows == kBlock;
-    const int64_t rows = pg::quantize_rows_per_group(M, K, tile || QT != nullptr);
-    if (ceil_div(M, rows) * ceil_div(K, kBlock) >= ((int64_t)1 << 24)) return GEMM_ERR_UNSUPPORTED;
+    const bool both = tile || QT != nullptr;
+    const int64_t groups = ceil_div(M, pg::quantize_rows_per_group(M, K, both)) * ceil_div(K, kBlock);
+    if (groups >= ((int64_t)1 << 32) / pg::quantize_threads(both)) return GEMM_ERR_UNSUPPORTED;
     if (!any) return GEMM_OK;
     pg::QuantizeArgs a;
     a.X = X;

@@ -237,8 +237,10 @@ __device__ __forceinline__ void store_fp8x8(uint8_t* p, int n, i32x2q v) {
 
 // Launchers (fp8_quantize.hip, fp8_rms.hip); each enqueues on the current device.
 hipError_t launch_quantize(const QuantizeArgs& a, int xtype, bool tile, hipStream_t stream);
-// Rows of one workgroup (blocks of 128 columns each).
+// Rows of one workgroup (blocks of 128 columns each), and its threads where
+// there are many; a launch takes less than 2^32 threads.
 int quantize_rows_per_group(int64_t M, int64_t K, bool tile);
+constexpr int quantize_threads(bool tile) { return tile ? 512 : 256; }
 hipError_t launch_rms(const RmsArgs& a, int xtype, hipStream_t stream);
 struct RmsBackwardForm;      // fp8_rms_plan.h
 hipError_t launch_rms_backward(const RmsBackwardArgs& a, const RmsBackwardForm& form, int xtype, hipStream_t stream);

@@ -180,15 +180,15 @@ hipError_t launch(const QuantizeArgs& a, bool tile, hipStream_t stream) {
         if (tile && few)
             hipLaunchKernelGGL((quantize_tile<XT, true, 2>), grid, dim3(1024), 0, stream, a);
         else if (tile)
-            hipLaunchKernelGGL((quantize_tile<XT, true, 4>), grid, dim3(512), 0, stream, a);
+            hipLaunchKernelGGL((quantize_tile<XT, true, 4>), grid, dim3(quantize_threads(true)), 0, stream, a);
         else if (few)
             hipLaunchKernelGGL((quantize_tile<XT, false, 2>), grid, dim3(1024), 0, stream, a);
         else
-            hipLaunchKernelGGL((quantize_tile<XT, false, 4>), grid, dim3(512), 0, stream, a);
+            hipLaunchKernelGGL((quantize_tile<XT, false, 4>), grid, dim3(quantize_threads(true)), 0, stream, a);
     } else if (rows == 16)
-        hipLaunchKernelGGL((quantize_rows<XT, 1>), grid, dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((quantize_rows<XT, 1>), grid, dim3(quantize_threads(false)), 0, stream, a);
     else
-        hipLaunchKernelGGL((quantize_rows<XT, 4>), grid, dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((quantize_rows<XT, 4>), grid, dim3(quantize_threads(false)), 0, stream, a);
     return hipGetLastError();
 }
 

@@ -230,6 +230,17 @@ def test_quantize_refusals():
     assert binding.gemm_quantize_fp8(None, 1, 1, "bf16", "e4m3", 1, 0, P, 1, P, 1, P, 1, 1, stream=0, check=False) == BAD
 
 
+def test_quantize_refuses_launches_of_too_many_threads():
+    """A launch takes less than 2^32 threads: 2^24 workgroups of 256, or 2^23 of 512."""
+    M = 2 ** 30 - 127                                                           # 2^23 row blocks of 128
+    one = dict(K=1, ldx=1, ldq=1, s_blk=M, ldqt=M, st_blk=1)
+    assert quant(M=M, **one) == UNSUP and quant(M=M, rows=128, **one) == UNSUP
+    assert quant(M=M, rows=128, **dict(one, QT=None)) == UNSUP
+    wide = dict(K=2 ** 30 - 127, M=128, ldx=2 ** 30, ldq=2 ** 30, ldqt=128)     # 2^23 column blocks of 128
+    assert quant(rows=128, **wide) == UNSUP and quant(**wide) == UNSUP
+    assert quant(M=2 ** 30 - 63, K=1, QT=None) == UNSUP                         # rows alone: 2^24 of 64
+
+
 def rms(**kw):
     a = dict(M=4, D=256, x="bf16", w="bf16", f="e4m3", pow2=0, eps=1e-6, X=P, ldx=256, R=P, ldr=256, W=P, H=P, ldh=256,
              Y=P, ldy=256, Q=P, ldq=256, S=P, s_row=1, s_blk=4, rstd=P)
