@@ -246,7 +246,7 @@ int gemm_rms_fp8(gemm_handle_t h, int64_t M, int64_t D, int x_dtype, int w_dtype
     if (!aligned(X, sz) || !aligned(R, sz) || !aligned(H, sz) || !aligned(Y, sz) || !aligned(W, size_of(w_dtype)) ||
         !aligned(S, 4) || !aligned(rstd, 4))
         return GEMM_ERR_ALIGNMENT;
-    if (M > GEMM_RMS_MAX_ROWS || D > GEMM_RMS_MAX_D) return GEMM_ERR_UNSUPPORTED;
+    if (M > GEMM_RMS_MAX_ROWS || D > GEMM_RMS_MAX_D || !pg::rms_launches(M, D)) return GEMM_ERR_UNSUPPORTED;
     if (!any) return GEMM_OK;
     pg::RmsArgs a;
     a.X = X;
@@ -294,6 +294,8 @@ int gemm_rms_backward(gemm_handle_t h, int64_t M, int64_t D, int x_dtype, int w_
         !aligned(rstd, 4) || !aligned(DW, 4) || !aligned(workspace, 16))
         return GEMM_ERR_ALIGNMENT;
     if (M > GEMM_RMS_MAX_ROWS || D > GEMM_RMS_MAX_D) return GEMM_ERR_UNSUPPORTED;
+    const pg::RmsBackwardForm form = pg::rms_backward_form(M, D, x_dtype == GEMM_F32, kDefaultCus);
+    if (!pg::rms_backward_launches(form, M, D)) return GEMM_ERR_UNSUPPORTED;
     const int64_t needed = gemm_rms_backward_workspace(M, D);
     if (needed > 0 && (workspace == nullptr || workspace_bytes < needed)) return GEMM_ERR_INVALID_ARG;
     if (D == 0) return GEMM_OK;
@@ -312,7 +314,6 @@ int gemm_rms_backward(gemm_handle_t h, int64_t M, int64_t D, int x_dtype, int w_
     a.lddx = lddx;
     a.M = (int32_t)M;
     a.D = (int32_t)D;
-    const pg::RmsBackwardForm form = pg::rms_backward_form(M, D, x_dtype == GEMM_F32, kDefaultCus);
     a.groups = form.parts;
     a.w_f32 = w_dtype == GEMM_F32;
     const auto meets = [&](const void* p, int64_t ld) {      // the byte ranges of DX and p

@@ -43,7 +43,7 @@ __device__ __forceinline__ void load_w(const void* W, int64_t k, int n, bool w_f
 }
 
 template <int XT, int TPR, int NC>
-__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rms_kernel(RmsArgs a) {
+__global__ void __launch_bounds__(rms_group_threads(TPR)) rms_kernel(RmsArgs a) {
     __shared__ float red[TPR > 64 ? TPR / 64 : 1];
     constexpr int RPW = TPR < 256 ? 256 / TPR : 1;          // rows per workgroup
     const int t = threadIdx.x % TPR;
@@ -229,8 +229,6 @@ __global__ void __launch_bounds__(256) rms_backward_sum(RmsBackwardArgs a) {
 // read longer pieces (1024 x 8192: 25 us against 21).
 // Where dx takes the place of dy or h the dw workgroups go first, in a launch
 // of their own: side by side they would read what a row has overwritten.
-constexpr int columns_lanes(int TPR) { return TPR <= 256 ? 8 : 16; }
-
 template <int XT, int TPR, int NC, int AT_ONCE>      // rows on their way per thread
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rms_backward_columns(RmsBackwardArgs a, int first) {
     constexpr int T = TPR < 256 ? 256 : TPR, RPW = T / TPR, LANES = columns_lanes(TPR), COLUMNS = LANES * 8, DOWN = T / LANES;
@@ -310,29 +308,31 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rms_backward_columns(Rm
     }
 }
 
+constexpr int form_key(int tpr, int nc) { return 8 * tpr + nc; }
+
 template <int XT, int TPR, int NC>
 hipError_t forward(const RmsArgs& a, hipStream_t stream) {
-    constexpr int RPW = TPR < 256 ? 256 / TPR : 1;
-    hipLaunchKernelGGL((rms_kernel<XT, TPR, NC>), dim3((unsigned)((a.M + RPW - 1) / RPW)), dim3(TPR < 256 ? 256 : TPR),
-                       0, stream, a);
+    if (a.D > TPR * NC * 8) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((rms_kernel<XT, TPR, NC>), dim3((unsigned)rms_row_groups(a.M, TPR)), dim3(rms_group_threads(TPR)), 0,
+                       stream, a);
     return hipGetLastError();
 }
 
 template <int XT>
 hipError_t forward_for(const RmsArgs& a, hipStream_t stream) {
-    if (a.D <= 512) return forward<XT, 64, 1>(a, stream);
-    // Few rows: more threads each, a chunk per thread (us in a graph, 1 x 8192:
-    // 3.4, at four chunks 5.3; 256 x 8192 4.8 and 6.5; 1 x 1000 2.6 and 3.1);
-    // with many the bytes on their way count (8192 x 8192: 91 at four chunks).
-    if (a.M <= 512 && a.D <= 8192)
-        return a.D <= 2048 ? forward<XT, 256, 1>(a, stream)
-             : a.D <= 4096 ? forward<XT, 512, 1>(a, stream) : forward<XT, 1024, 1>(a, stream);
-    if (a.D <= 1024) return forward<XT, 64, 2>(a, stream);
-    if (a.D <= 2048) return forward<XT, 256, 1>(a, stream);
-    if (a.D <= 4096) return forward<XT, 256, 2>(a, stream);
-    if (a.D <= 8192) return forward<XT, 256, 4>(a, stream);
-    if (a.D <= 16384) return forward<XT, 1024, 2>(a, stream);
-    return forward<XT, 1024, 4>(a, stream);
+    const RmsForm f = rms_form(a.M, a.D);
+    switch (form_key(f.tpr, f.nc)) {
+    case form_key(64, 1): return forward<XT, 64, 1>(a, stream);
+    case form_key(64, 2): return forward<XT, 64, 2>(a, stream);
+    case form_key(256, 1): return forward<XT, 256, 1>(a, stream);
+    case form_key(256, 2): return forward<XT, 256, 2>(a, stream);
+    case form_key(256, 4): return forward<XT, 256, 4>(a, stream);
+    case form_key(512, 1): return forward<XT, 512, 1>(a, stream);
+    case form_key(1024, 1): return forward<XT, 1024, 1>(a, stream);
+    case form_key(1024, 2): return forward<XT, 1024, 2>(a, stream);
+    case form_key(1024, 4): return forward<XT, 1024, 4>(a, stream);
+    default: return hipErrorInvalidValue;
+    }
 }
 
 hipError_t sum_parts(const RmsBackwardArgs& a, hipStream_t stream) {
@@ -352,9 +352,9 @@ hipError_t backward(const RmsBackwardArgs& a, hipStream_t stream) {
 
 template <int XT, int TPR, int NC, int AT_ONCE>
 hipError_t launch_columns(const RmsBackwardArgs& a, hipStream_t stream) {
-    constexpr int T = TPR < 256 ? 256 : TPR, RPW = T / TPR, COLUMNS = columns_lanes(TPR) * 8;
+    constexpr int T = rms_group_threads(TPR), COLUMNS = columns_lanes(TPR) * 8;
     if (a.D > TPR * NC * 8) return hipErrorInvalidValue;
-    const int rows = (int)((a.M + RPW - 1) / RPW);
+    const int rows = (int)rms_row_groups(a.M, TPR);
     const int columns = (a.D + COLUMNS - 1) / COLUMNS * (a.groups > 0 ? a.groups : 1);
     const bool apart = a.in_place && rows > 0;
     const auto launch = [&](int workgroups, int first) {
@@ -377,8 +377,6 @@ hipError_t backward_columns(const RmsBackwardArgs& a, hipStream_t stream) {
         if (a.M > 128) return launch_columns<XT, TPR, NC, 8>(a, stream);
     return launch_columns<XT, TPR, NC, 4>(a, stream);
 }
-
-constexpr int form_key(int tpr, int nc) { return 8 * tpr + nc; }
 
 template <int XT>
 hipError_t backward_for(const RmsBackwardArgs& a, const RmsBackwardForm& f, hipStream_t stream) {

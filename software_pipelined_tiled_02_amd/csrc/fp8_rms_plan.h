@@ -1,6 +1,6 @@
-// fp8_rms_plan.h -- which form of its kernels the norm's backward pass takes.
-// Plain constexpr C++ with no HIP dependency: the launcher, the workspace's
-// size and a host test share it.
+// fp8_rms_plan.h -- which form of its kernels the norm and its backward pass
+// take.  Plain constexpr C++ with no HIP dependency: the launchers, the checks,
+// the workspace's size and a host test share it.
 #ifndef PIPEGEMM_FP8_RMS_PLAN_H
 #define PIPEGEMM_FP8_RMS_PLAN_H
 
@@ -9,6 +9,9 @@
 namespace pg {
 
 // `tpr` threads hold a row in `nc` steps of 8 values each.
+struct RmsForm {
+    int tpr, nc;
+};
 struct RmsBackwardForm {
     bool by_columns;         // dw by columns beside the rows, else in the rows' groups
     int parts;               // of dw, left in the workspace (0: it needs none)
@@ -19,7 +22,42 @@ struct RmsBackwardForm {
 
 constexpr int64_t rms_parts_row(int64_t D) { return (D + 3) / 4 * 4; }
 
-// The form for M rows of D values.  by_columns and parts, which the workspace
+constexpr RmsForm rms_form(int64_t M, int64_t D) {
+    if (D <= 512) return {64, 1};
+    // Few rows: more threads each, a chunk per thread (us in a graph, 1 x 8192:
+    // 3.4, at four chunks 5.3; 256 x 8192 4.8 and 6.5; 1 x 1000 2.6 and 3.1);
+    // with many the bytes on their way count (8192 x 8192: 91 at four chunks).
+    if (M <= 512 && D <= 8192) return D <= 2048 ? RmsForm{256, 1} : D <= 4096 ? RmsForm{512, 1} : RmsForm{1024, 1};
+    if (D <= 1024) return {64, 2};
+    if (D <= 2048) return {256, 1};
+    if (D <= 4096) return {256, 2};
+    if (D <= 8192) return {256, 4};
+    if (D <= 16384) return {1024, 2};
+    return {1024, 4};
+}
+
+// Workgroups hold whole rows, 256 threads at least.
+constexpr int rms_group_threads(int tpr) { return tpr < 256 ? 256 : tpr; }
+constexpr int64_t rms_row_groups(int64_t M, int tpr) {
+    return (M + rms_group_threads(tpr) / tpr - 1) / (rms_group_threads(tpr) / tpr);
+}
+// Lanes across the columns of dw that a workgroup of the form by columns takes.
+constexpr int columns_lanes(int tpr) { return tpr <= 256 ? 8 : 16; }
+
+// A launch takes less than 2^32 threads (the forms in groups have few).
+constexpr int64_t kLaunchThreads = (int64_t)1 << 32;
+constexpr bool rms_launches(int64_t M, int64_t D) {
+    const RmsForm f = rms_form(M, D);
+    return rms_row_groups(M, f.tpr) * rms_group_threads(f.tpr) < kLaunchThreads;
+}
+constexpr bool rms_backward_launches(const RmsBackwardForm& f, int64_t M, int64_t D) {
+    if (!f.by_columns) return true;
+    const int64_t across = 8 * columns_lanes(f.tpr);
+    return (rms_row_groups(M, f.tpr) + (D + across - 1) / across * (f.parts > 0 ? f.parts : 1)) * rms_group_threads(f.tpr) <
+           kLaunchThreads;
+}
+
+// The backward pass's form for M rows of D values.  by_columns and parts, which the workspace
 // goes by, do not depend on the type (`f32`).
 constexpr RmsBackwardForm rms_backward_form(int64_t M, int64_t D, bool f32, int num_cus) {
     // us in groups and by columns, bf16 with dh: 560 x 4096 14.3 and 9.2, 1024

@@ -1,4 +1,4 @@
-// The form the norm's backward pass takes, over both sides of every border of
+// The forms that the norm and its backward pass take, over both sides of every border of
 // M and D and both kinds of type: one that exists and takes the D it is given,
 // with parts of dw that fit the workspace whatever the type.
 #include <cstdio>
@@ -33,11 +33,20 @@ int main() {
     for (int64_t d : {8, 512, 1024, 2048, 4096, 8192, 9300, 10000, 12288, 16384, 20000, 32768})
         for (int64_t e = -9; e <= 9; ++e)
             if (d + e >= 1 && d + e <= 32768) ds.push_back(d + e);
-    long bad = 0, seen = 0;
+    // launches: one row below the last refused one, and everything of fewer rows or shorter ones
+    const int64_t most = 1 << 22;
+    bool launches = pg::rms_launches(most, 8192) && pg::rms_launches(most - 1, 32768) && !pg::rms_launches(most, 8193);
+    const auto back = [](int64_t m, int64_t d) {
+        return pg::rms_backward_launches(pg::rms_backward_form(m, d, false, 256), m, d);
+    };
+    launches = launches && back(most, 8192) && back(most, 16384) && back(most - 16385, 32768) && !back(most - 16384, 32768);
+    long bad = launches ? 0 : 1, seen = 0;
     for (int64_t m : ms)
         for (int64_t d : ds) {
             if (m > (1 << 22)) continue;
             const RmsBackwardForm half = pg::rms_backward_form(m, d, false, 256);
+            const pg::RmsForm fw = pg::rms_form(m, d);
+            if ((int64_t)fw.tpr * fw.nc * 8 < d) ++bad;
             for (bool f32 : {false, true}) {
                 const RmsBackwardForm f = pg::rms_backward_form(m, d, f32, 256);
                 ++seen;

@@ -288,6 +288,17 @@ def test_rms_backward_refusals():
     assert rms_back(D=0, DW=None) == OK
 
 
+def test_rms_refuses_launches_of_too_many_threads():
+    """A launch takes less than 2^32 threads; long rows have 1024 each."""
+    M = binding.GEMM_RMS_MAX_ROWS
+    for D in (8193, 8200, 16384, 32768):
+        assert rms(M=M, D=D, ldx=D, ldr=D, ldh=D, ldy=D, ldq=D) == UNSUP, D
+    for D in (12289, 16385, 32768):
+        for rows in (M, M - 1):                          # the columns of dw take workgroups too
+            assert rms_back(M=rows, D=D, lddy=D, ldh=D, lddh=D, lddx=D, nbytes=1 << 30) == UNSUP, D
+    assert rms_back(M=M - 16384, D=32768, lddy=32768, ldh=32768, lddh=32768, lddx=32768, nbytes=1 << 30) == UNSUP
+
+
 def test_rms_backward_workspace():
     ws = binding.gemm_rms_backward_workspace
     assert ws(4, 256) == ws(512, 8192) == ws(0, 256) == 0                       # few rows: none
