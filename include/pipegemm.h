@@ -438,10 +438,11 @@ int gemm_quantize_fp8(gemm_handle_t h, int64_t M, int64_t K, int x_dtype, int fp
  * values of w_dtype (x_dtype or GEMM_F32).  R may be NULL (h = x); H (h), Y
  * (y, rounded), Q with S, and rstd (M fp32 values) are written where they are
  * not NULL, and one of Q and Y must be given.  H may be X or R (in
- * place).  GEMM_ERR_UNSUPPORTED above GEMM_RMS_MAX_D or GEMM_RMS_MAX_ROWS,
- * and where the launch would have 2^32 threads: GEMM_RMS_MAX_ROWS rows of more
- * than 8192; for the backward pass within 16384 rows of GEMM_RMS_MAX_ROWS, of
- * more than 16384, or more than 12288 and no multiple of 8. */
+ * place).  With D = 0 nothing is written.  GEMM_ERR_UNSUPPORTED above
+ * GEMM_RMS_MAX_D or GEMM_RMS_MAX_ROWS, and where the launch would have 2^32
+ * threads: GEMM_RMS_MAX_ROWS rows of more than 8192; for the backward pass
+ * within 16384 rows of GEMM_RMS_MAX_ROWS, of more than 16384, or more than 12288
+ * and no multiple of 8. */
 int gemm_rms_fp8(gemm_handle_t h, int64_t M, int64_t D, int x_dtype, int w_dtype, int fp8_type, int pow2, float eps,
                  const void *X, int64_t ldx, const void *R, int64_t ldr, const void *W, void *H, int64_t ldh,
                  void *Y, int64_t ldy, void *Q, int64_t ldq, float *S, int64_t s_row, int64_t s_blk, float *rstd,

@@ -18,6 +18,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <limits>
 #include <mutex>
 #include <string>
 
@@ -303,6 +304,7 @@ PyObject* rms_fp8_(PyObject* const* arg, Py_ssize_t n) {
         ho.ld = D;
     }
     if (norm) y = empty({M, D}, {D, 1}, xt.scalar_type(), x.device);
+    if (D == 0) rstd.fill_(std::numeric_limits<double>::quiet_NaN());     // the mean of no values; the kernel writes nothing
     void* const stream = raw_stream(x.device);
     const int rc = enqueue([&] {
         return gemm_rms_fp8(h, M, D, x.type, w_type, (int)fp8, pow2, (float)eps, x.p, x.ld, r.p, r.ld, w.data_ptr(),

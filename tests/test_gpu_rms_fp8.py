@@ -114,6 +114,19 @@ def test_forward_zeros_and_what_is_not_finite():
     assert bool(z[3].isinf().all()) and np.isnan(R.decode(raw_of(z[0]), "e4m3")).all()
 
 
+def test_forward_rows_without_values():
+    """The mean of no values is NaN, as torch has it, whatever the memory held."""
+    junk = torch.full((1 << 16,), 3.0, device="cuda")
+    del junk
+    x, w = torch.empty((5, 0), device="cuda"), torch.empty(0, device="cuda")
+    q, s, h, rstd, y = binding.rms_fp8(x, w, norm=True)
+    assert q.shape == y.shape == (5, 0) and s.shape == (5, 0) and rstd.shape == (5,) and bool(rstd.isnan().all())
+    dx, dw = binding.rms_backward(x, h, w, rstd)
+    assert dx.shape == (5, 0) and dw.shape == (0,)
+    q, s, h, rstd = binding.rms_fp8(torch.empty((0, 64), device="cuda"), torch.ones(64, device="cuda"))
+    assert q.shape == (0, 64) and s.shape == (0, 1) and rstd.shape == (0,)
+
+
 def check_backward(dy, h, w, rstd, dh, dx, dw, x):
     d = lambda t: None if t is None else t.double().cpu().numpy()  # noqa: E731
     M, D = h.shape
