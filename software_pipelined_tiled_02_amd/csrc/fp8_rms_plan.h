@@ -88,7 +88,13 @@ constexpr RmsBackwardForm rms_backward_form(int64_t M, int64_t D, bool f32, int 
     if (D <= 2048) return {false, parts, 256, 1, true, false};
     if (D <= 4096) return {false, parts, 512, 1, true, false};
     if (D <= 8192) return {false, parts, 1024, 1, true, false};
-    if (!f32 && D <= 12288) return {false, parts, 512, 3, true, false};
+    // 16-bit rows up to 12288 in 512 threads, the next one ahead, take 11
+    // registers to scratch.  Rows that end inside a thread's 8 values gain by it
+    // (us at 1030, 2000 and 8192 x 9300: 36, 51 and 161; held, with 19 registers
+    // in scratch, 39, 55 and 166; by columns 35, 61 and 230), multiples of 8 do
+    // not (8192 x 8200: 147, held 118; 8192 x 10240: 149 and 135; 8192 x 12288: 178
+    // and 157; 2000 x 10240: 49 and 44; 1030 x 12288: 40 and 36).
+    if (!f32 && D <= 12288 && D % 8 != 0) return {false, parts, 512, 3, true, false};
     // fp32 rows that end inside a thread's 8 values: settling them takes 9
     // registers to scratch, and is still faster than by columns with many
     // rows (8192 x 9300: 254 us, 348 by columns; 2000 x 9300: 78 and 90; 1030 x

@@ -40,7 +40,10 @@ int main() {
         return pg::rms_backward_launches(pg::rms_backward_form(m, d, false, 256), m, d);
     };
     launches = launches && back(most, 8192) && back(most, 16384) && back(most - 16385, 32768) && !back(most - 16384, 32768);
-    long bad = launches ? 0 : 1, seen = 0;
+    // 16-bit rows of 8193 to 12288: only those that are no multiple of 8 spill
+    const bool spills = pg::rms_backward_form(2000, 10241, false, 256).ahead && !pg::rms_backward_form(2000, 10240, false, 256).ahead &&
+                        !pg::rms_backward_form(2000, 8200, false, 256).ahead && !pg::rms_backward_form(2000, 12288, false, 256).ahead;
+    long bad = launches && spills ? 0 : 1, seen = 0;
     for (int64_t m : ms)
         for (int64_t d : ds) {
             if (m > (1 << 22)) continue;
