@@ -349,10 +349,11 @@ int gemm_occupancy(gemm_handle_t h, int64_t M, int64_t N, int64_t K, int dtype, 
  * its block an infinite scale (every value of it then stands for NaN).
  *
  * All of these are asynchronous, allocate nothing, and enqueue one kernel
- * (gemm_rms_backward: up to two) on `stream`, on the handle's device; any
- * number of calls may overlap, on any streams (gemm_rms_backward: each with its own
- * workspace).  A captured graph can hold them.  Outputs must not overlap
- * inputs or one another, but where stated.  Sizes of zero are accepted. */
+ * (gemm_rms_backward: up to two, up to three where DX takes the place of DY or
+ * H) on `stream`, on the handle's device; any number of calls may overlap, on
+ * any streams (gemm_rms_backward: each with its own workspace).  A captured
+ * graph can hold them.  Outputs must not overlap inputs or one another, but
+ * where stated.  Sizes of zero are accepted. */
 enum { GEMM_E4M3 = 16, GEMM_E5M2 = 17 };
 
 /* Part of C that one workgroup of gemm_run_fp8 computes.  Those down to
