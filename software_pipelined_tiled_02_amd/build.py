@@ -127,7 +127,7 @@ def parse_resource_remarks(text):
 def write_resources(logs):
     table = {}
     for text in logs.values():
-        table.update({k: v for k, v in parse_resource_remarks(text).items() if "pipegemm_kernel" in k})
+        table.update(parse_resource_remarks(text))
     tmp = RESOURCES + ".tmp%d" % os.getpid()
     with open(tmp, "w") as f:
         json.dump(table, f, indent=0, sort_keys=True)
