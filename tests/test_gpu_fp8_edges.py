@@ -1,12 +1,16 @@
 """The 8-bit operators at the ends of what they take: strides at the border of
 the 32-bit offsets, the most rows, every class of the norm in every type, one
 tensor in several places, and other streams.  Bounds as in the tests of each operator."""
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
 
 from software_pipelined_tiled_02_amd import binding
 from tests import fp8_ref as R
+from tests.conftest import ROOT
 from tests.fp8_util import F8, FT, check_product, f8_of, operand, raw_of, values
 from tests.test_gpu_rms_fp8 import check_backward, check_forward, inputs
 
@@ -197,3 +201,35 @@ def test_two_graphs_of_the_product_and_the_quantiser_in_one_pool():
             g.replay()
             torch.cuda.synchronize()
             assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+ONE_EAGER_CALL = """
+import torch
+from software_pipelined_tiled_02_amd import binding
+x, r = (torch.randn((700, 520), device="cuda").bfloat16() for _ in range(2))
+w, weight = torch.ones(520, device="cuda").bfloat16(), torch.randn((200, 520), device="cuda")
+
+def layer():
+    wq, ws = binding.quantize_fp8(weight, block="tile")
+    q, s, h, rstd = binding.rms_fp8(x, w, residual=r)
+    return (binding.run_fp8(q, s, wq, ws), binding.run_fp8(q, s, wq, ws, out_dtype=torch.float32, tile="64x64"),
+            *binding.rms_backward(x, h, w, rstd, dh=r))
+
+binding.quantize_fp8(torch.ones((4, 256), device="cuda"))
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    out = layer()
+for i in range(3):
+    x.mul_(-1.5)
+    g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(out, layer()))
+print("captured at first use")
+"""
+
+
+def test_operators_captured_at_their_first_use():
+    """One eager call sets the device up; every other operator may meet a capture first."""
+    r = subprocess.run([sys.executable, "-c", ONE_EAGER_CALL], cwd=ROOT, capture_output=True, text=True, timeout=100)
+    assert r.returncode == 0 and "captured at first use" in r.stdout, r.stdout + r.stderr
