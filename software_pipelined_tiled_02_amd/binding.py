@@ -452,7 +452,9 @@ def run_fp8(a, sa, b, sb, *, out=None, out_dtype=None, accumulate=False, tile="a
     (RuntimeError).
 
     Rows that start on 16 bytes are the fast case, on 128 the fastest
-    (quantize_fp8 and rms_fp8 lay them out so)."""
+    (quantize_fp8 and rms_fp8 lay them out so); others take twice the time
+    with few rows and up to 20 times with thousands.  16-bit outputs take the
+    8-bit matrix instructions' sums, float32 ones fp32's."""
     if stream is not None:
         with _on_stream(stream, a):
             return run_fp8(a, sa, b, sb, out=out, out_dtype=out_dtype, accumulate=accumulate, tile=tile)

@@ -38,8 +38,8 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Elements from one row of an 8-bit matrix to the next: rows start on 16
 // bytes; wide ones on 128, the caches' lines, so that the product's loads of
-// 128 bytes touch one line each, not two (8192 x 8192 x 8200: 443 us, 506 with
-// rows on 16; 512 x 4096 x 4100: 16.7 and 21.0; at K = 520 no difference).
+// 128 bytes touch one line each, not two (8192 x 8192 x 8200: 447 us, 505 with
+// rows on 16; 512 x 4096 x 4100: 17.2 and 22.0; at K = 520 no difference).
 int64_t pitch(int64_t n) { return n < 1024 ? (n + 15) / 16 * 16 : (n + 127) / 128 * 128; }
 
 std::mutex g_mutex;
