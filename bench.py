@@ -104,13 +104,13 @@ def flops(M, N, K):
 
 
 def kernel_source_hash():
-    """Hash of the GEMM's sources (not of the 8-bit operators', which have no
-    part in it) with comments and white space removed, so that only a change
+    """Hash of the GEMM's sources (not of the 8-bit and the feed-forward
+    operators', which have no part in it) with comments and white space removed, so that only a change
     of code marks measured counters as stale."""
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "software_pipelined_tiled_02_amd", "csrc")
     for name in sorted(os.listdir(csrc)):
-        if name.endswith((".h", ".hip")) and not name.endswith("_probe.hip") and not name.startswith("fp8_"):
+        if name.endswith((".h", ".hip")) and not name.endswith("_probe.hip") and not name.startswith(("fp8_", "linear_")):
             text = open(os.path.join(csrc, name), encoding="utf-8").read()
             text = re.sub(r"/\*.*?\*/", " ", text, flags=re.S)
             text = re.sub(r"//[^\n]*", " ", text)

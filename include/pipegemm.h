@@ -464,6 +464,98 @@ int gemm_rms_backward(gemm_handle_t h, int64_t M, int64_t D, int x_dtype, int w_
                       void *workspace, int64_t workspace_bytes, void *stream);
 int64_t gemm_rms_backward_workspace(int64_t M, int64_t D);
 
+/* ---- a feed-forward block in 16 bits, forward and backward ------------------
+ *
+ * Products of bf16 or fp16 matrices (dtype GEMM_BF16 or GEMM_F16) with what
+ * stands next to them in a feed-forward block done in the same kernel:
+ *   H = gemm_gated(X, Wg, Wu), Y = gemm_linear(H, Wd, residual X) forward;
+ *   dG, dU, H = gemm_gated_backward(dY, Wd, G, U),
+ *   dX = gemm_linear(dG, Wg, dU, Wu, residual dY; layout RR),
+ *   dW = gemm_weight_gradient(dG, X), ... backward.
+ * Products are summed in fp32 and everything up to an output's rounding is
+ * fp32; each output is rounded once, to nearest even, to dtype (weight
+ * gradients stay fp32).  The order of the sums is fixed for a call's sizes,
+ * alignment and tile class.
+ *
+ * Activations: relu(z) = max(z, 0), its derivative 0 at 0; gelu(z) = z F(z),
+ * F the normal distribution's function; gelu_tanh(z) = z (1 + tanh(sqrt(2 /
+ * pi) (z + 0.044715 z^3))) / 2; silu(z) = z / (1 + exp(-z)).  Each is within
+ * 2^-16 of its value of z as summed.  A NaN stays one.
+ *
+ * Leading dimensions are in elements; all rows may lie at any address that is
+ * aligned to their elements.  Where every factor of a call has its base and
+ * leading dimension on 16 bytes, K-tiles go straight into LDS; where one has
+ * not, they pass through registers, which is slower.  No value of
+ * a factor outside its matrix counts, whatever it holds.
+ *
+ * Asynchronous: each enqueues one kernel on `stream`, on the handle's device,
+ * and nothing else; nothing is allocated; any number may overlap, and a graph
+ * can capture them.  Outputs must not overlap inputs or one another, but where
+ * stated.  Sizes of zero are accepted.  Errors: GEMM_ERR_INVALID_ARG (NULL, a
+ * negative size, an unknown type, a leading dimension below the row's length),
+ * GEMM_ERR_ALIGNMENT (a pointer not aligned to its elements; a tile class asked
+ * for that needs rows on 16 bytes), GEMM_ERR_UNSUPPORTED (256 rows of a factor
+ * with K along its rows, or 64 of one with K across them, that span 2^31 bytes;
+ * 2^32 threads), GEMM_ERR_HIP. */
+enum { GEMM_ACT_NONE = 0, GEMM_ACT_RELU = 1, GEMM_ACT_GELU = 2, GEMM_ACT_GELU_TANH = 3, GEMM_ACT_SILU = 4 };
+
+/* Part of the sums that one workgroup computes (gated: half of its columns are
+ * the second product's).  GEMM_LINEAR_TILE_AUTO: chosen by the call's sizes. */
+enum { GEMM_LINEAR_TILE_AUTO = -1, GEMM_LINEAR_TILE_256x256 = 0, GEMM_LINEAR_TILE_128x128 = 1, GEMM_LINEAR_TILE_64x64 = 2 };
+
+enum { GEMM_FORM_LINEAR_RC = 0, GEMM_FORM_LINEAR_RR = 1, GEMM_FORM_GATED = 2, GEMM_FORM_GATED_BACKWARD = 3,
+       GEMM_FORM_WEIGHT_GRADIENT = 4 };
+
+typedef struct {
+    int32_t tile;              /* GEMM_LINEAR_TILE_* chosen */
+    int32_t block_m, block_n;  /* outputs of one workgroup */
+    int32_t threads;           /* per workgroup */
+    int32_t rows16;            /* 1: K-tiles go straight into LDS */
+    int32_t reserved;
+    int64_t grid;              /* workgroups */
+    int64_t k_tiles;           /* ceil(K / 64), K the length of the sums */
+} gemm_linear_info_t;
+
+/* C = act(A B + A2 B2 + bias) + R, and Z = the activation's argument.
+ * A: M x K.  Layout RC: B is column-major (its N x K transpose, as a layer's
+ * weight lies); RR: row-major K x N.  A2 and B2: as A and B, both NULL or none.
+ * bias: N values of bias_dtype (dtype or GEMM_F32), R: M x N, Z: M x N, each may
+ * be NULL.  C, and only C, may take R's place (the same address and leading
+ * dimension). */
+int gemm_linear(gemm_handle_t h, int64_t M, int64_t N, int64_t K, int dtype, int layout, int activation, int bias_dtype,
+                int tile, const void *A, int64_t lda, const void *B, int64_t ldb, const void *A2, int64_t lda2,
+                const void *B2, int64_t ldb2, const void *bias, const void *R, int64_t ldr, void *Z, int64_t ldz,
+                void *C, int64_t ldc, void *stream);
+
+/* H = act(G) * U with G = X Wg + bg and U = X Wu + bu.  X: M x K; WG, WU: the
+ * N x K transposes of Wg and Wu; BG, BU: N values of bias_dtype, each may be
+ * NULL; G, U: M x N, both NULL or none; H: M x N.  H is formed of G and U
+ * before their rounding. */
+int gemm_gated(gemm_handle_t h, int64_t M, int64_t N, int64_t K, int dtype, int activation, int bias_dtype, int tile,
+               const void *X, int64_t ldx, const void *WG, int64_t ldwg, const void *WU, int64_t ldwu, const void *BG,
+               const void *BU, void *G, int64_t ldg, void *U, int64_t ldu, void *H, int64_t ldh, void *stream);
+
+/* With dH = DY W: DG = dH U act'(G), DU = dH act(G), and H = act(G) U again;
+ * U and DU NULL: DG = dH act'(G), H = act(G).  DY: M x K, W: row-major K x N (the
+ * weight of the layer that takes H, as it lies), the others M x N; H may be
+ * NULL.  dH is not rounded. */
+int gemm_gated_backward(gemm_handle_t h, int64_t M, int64_t N, int64_t K, int dtype, int activation, int tile,
+                        const void *DY, int64_t lddy, const void *W, int64_t ldw, const void *G, int64_t ldg,
+                        const void *U, int64_t ldu, void *DG, int64_t lddg, void *DU, int64_t lddu, void *H, int64_t ldh,
+                        void *stream);
+
+/* DW (N x K, fp32) = DC^T A, DC: M x N, A: M x K; DB: N fp32 values, the sums of
+ * DC's columns, or NULL.  accumulate = 1: DW += and DB +=.  DB needs K > 0. */
+int gemm_weight_gradient(gemm_handle_t h, int64_t M, int64_t N, int64_t K, int dtype, int accumulate, int tile,
+                         const void *DC, int64_t lddc, const void *A, int64_t lda, float *DW, int64_t lddw, float *DB,
+                         void *stream);
+
+/* What a call of these sizes would launch on a 256-CU device (rows_on_16:
+ * whether all its factors' rows start on 16 bytes); M, N and K as the call
+ * takes them.  No HIP call. */
+int gemm_query_linear(int form, int64_t M, int64_t N, int64_t K, int dtype, int rows_on_16, int tile,
+                      gemm_linear_info_t *info);
+
 /* Static text for a status code (never NULL). */
 const char *gemm_status_string(int status);
 

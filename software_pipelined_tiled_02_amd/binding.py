@@ -3,8 +3,9 @@
 Argument marshalling only: every step of the GEMM runs in the HIP kernels.
 The functions keep the C names; device buffers are passed as torch CUDA
 tensors (their data_ptr) or plain integer addresses.  run_fp8, quantize_fp8,
-rms_fp8 and rms_backward are the 8-bit operators on torch tensors.  There is
-no fallback: if the library is missing, loading raises.
+rms_fp8 and rms_backward are the 8-bit operators on torch tensors; linear,
+gated, gated_backward and weight_gradient those of a feed-forward block in 16
+bits.  There is no fallback: if the library is missing, loading raises.
 """
 import ctypes
 import os
@@ -33,13 +34,17 @@ FP8_TILES = {"auto": -1, "256x256": 0, "256x128": 1, "128x128": 2, "64x64": 3, "
              "64x32": 5, "32x32": 6, "16x32": 7, "16x16": 8}
 FP8_BLOCK = 128   # values of a row that share a scale
 BLOCK_ROWS = {"row": 1, "tile": FP8_BLOCK}
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+LINEAR_TILES = {"auto": -1, "256x256": 0, "128x128": 1, "64x64": 2}
+LINEAR_FORMS = {"linear_rc": 0, "linear_rr": 1, "gated": 2, "gated_backward": 3, "weight_gradient": 4}
 
 # C functions exported by the library (the names include/pipegemm.h declares)
 EXPORTS = ("gemm_create", "gemm_run", "gemm_destroy", "gemm_set_tile", "gemm_query",
            "gemm_run_splitk", "gemm_query_splitk", "gemm_status_string", "gemm_last_hip_error",
            "gemm_run_splitk_noalloc", "gemm_occupancy", "gemm_run_streamk", "gemm_query_streamk",
            "gemm_run_fp8", "gemm_query_fp8", "gemm_quantize_fp8", "gemm_rms_fp8", "gemm_rms_backward",
-           "gemm_rms_backward_workspace")
+           "gemm_rms_backward_workspace", "gemm_linear", "gemm_gated", "gemm_gated_backward", "gemm_weight_gradient",
+           "gemm_query_linear")
 
 
 class GemmError(RuntimeError):
@@ -75,6 +80,14 @@ class Fp8Info(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in (
         "tile", "block_m", "block_n", "waves_k", "threads", "staged", "widened", "reserved")] + [
         ("grid", ctypes.c_int64), ("k_blocks", ctypes.c_int64), ("c_tiles", ctypes.c_int64)]
+
+    def as_dict(self):
+        return {n: getattr(self, n) for n, _ in self._fields_}
+
+
+class LinearInfo(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("tile", "block_m", "block_n", "threads", "rows16", "reserved")] + [
+        ("grid", ctypes.c_int64), ("k_tiles", ctypes.c_int64)]
 
     def as_dict(self):
         return {n: getattr(self, n) for n, _ in self._fields_}
@@ -133,6 +146,16 @@ def _lib():
         lib.gemm_rms_backward.restype = ci
         lib.gemm_rms_backward_workspace.argtypes = [i64, i64]
         lib.gemm_rms_backward_workspace.restype = i64
+        lib.gemm_linear.argtypes = [vp, i64, i64, i64] + [ci] * 5 + [vp, i64] * 4 + [vp] + [vp, i64] * 3 + [vp]
+        lib.gemm_linear.restype = ci
+        lib.gemm_gated.argtypes = [vp, i64, i64, i64] + [ci] * 4 + [vp, i64] * 3 + [vp, vp] + [vp, i64] * 3 + [vp]
+        lib.gemm_gated.restype = ci
+        lib.gemm_gated_backward.argtypes = [vp, i64, i64, i64] + [ci] * 3 + [vp, i64] * 7 + [vp]
+        lib.gemm_gated_backward.restype = ci
+        lib.gemm_weight_gradient.argtypes = [vp, i64, i64, i64] + [ci] * 3 + [vp, i64] * 3 + [vp, vp]
+        lib.gemm_weight_gradient.restype = ci
+        lib.gemm_query_linear.argtypes = [ci, i64, i64, i64] + [ci] * 3 + [ctypes.POINTER(LinearInfo)]
+        lib.gemm_query_linear.restype = ci
         lib.gemm_status_string.argtypes = [ci]
         lib.gemm_status_string.restype = ctypes.c_char_p
         lib.gemm_last_hip_error.argtypes = []
@@ -510,6 +533,146 @@ def rms_backward(dy, h, weight, rstd, *, dh=None, dx_out=None, stream=None):
         with _on_stream(stream, dy):
             return rms_backward(dy, h, weight, rstd, dh=dh, dx_out=dx_out)
     return (_OPS or _ops()).rms_backward(dy, h, weight, rstd, dh, dx_out)
+
+
+# ---- a feed-forward block in 16 bits ---------------------------------------
+
+def gemm_linear(h, M, N, K, dtype, layout, activation, bias_dtype, tile, A, lda, B, ldb, A2, lda2, B2, ldb2, bias, R, ldr,
+                Z, ldz, C, ldc, stream=None, check=True):
+    """Enqueue C = act(A B + A2 B2 + bias) + R; returns the status (raises on
+    error when check)."""
+    rc = _lib().gemm_linear(h, M, N, K, _enum(dtype, DTYPES), _enum(layout, LAYOUTS), _enum(activation, ACTIVATIONS),
+                            _enum(bias_dtype, DTYPES), _enum(tile, LINEAR_TILES), _ptr(A), lda, _ptr(B), ldb, _ptr(A2), lda2,
+                            _ptr(B2), ldb2, _ptr(bias), _ptr(R), ldr, _ptr(Z), ldz, _ptr(C), ldc, _stream(stream))
+    if check and rc != GEMM_OK:
+        raise GemmError(rc, "gemm_linear")
+    return rc
+
+
+def gemm_gated(h, M, N, K, dtype, activation, bias_dtype, tile, X, ldx, WG, ldwg, WU, ldwu, BG, BU, G, ldg, U, ldu, H, ldh,
+               stream=None, check=True):
+    """Enqueue H = act(X Wg + bg) * (X Wu + bu)."""
+    rc = _lib().gemm_gated(h, M, N, K, _enum(dtype, DTYPES), _enum(activation, ACTIVATIONS), _enum(bias_dtype, DTYPES),
+                           _enum(tile, LINEAR_TILES), _ptr(X), ldx, _ptr(WG), ldwg, _ptr(WU), ldwu, _ptr(BG), _ptr(BU),
+                           _ptr(G), ldg, _ptr(U), ldu, _ptr(H), ldh, _stream(stream))
+    if check and rc != GEMM_OK:
+        raise GemmError(rc, "gemm_gated")
+    return rc
+
+
+def gemm_gated_backward(h, M, N, K, dtype, activation, tile, DY, lddy, W, ldw, G, ldg, U, ldu, DG, lddg, DU, lddu, H, ldh,
+                        stream=None, check=True):
+    """Enqueue the gradients of a gated layer's (or an activation's) arguments."""
+    rc = _lib().gemm_gated_backward(h, M, N, K, _enum(dtype, DTYPES), _enum(activation, ACTIVATIONS),
+                                    _enum(tile, LINEAR_TILES), _ptr(DY), lddy, _ptr(W), ldw, _ptr(G), ldg, _ptr(U), ldu,
+                                    _ptr(DG), lddg, _ptr(DU), lddu, _ptr(H), ldh, _stream(stream))
+    if check and rc != GEMM_OK:
+        raise GemmError(rc, "gemm_gated_backward")
+    return rc
+
+
+def gemm_weight_gradient(h, M, N, K, dtype, accumulate, tile, DC, lddc, A, lda, DW, lddw, DB, stream=None, check=True):
+    """Enqueue DW = DC^T A, and DB, the sums of DC's columns."""
+    rc = _lib().gemm_weight_gradient(h, M, N, K, _enum(dtype, DTYPES), int(accumulate), _enum(tile, LINEAR_TILES), _ptr(DC),
+                                     lddc, _ptr(A), lda, _ptr(DW), lddw, _ptr(DB), _stream(stream))
+    if check and rc != GEMM_OK:
+        raise GemmError(rc, "gemm_weight_gradient")
+    return rc
+
+
+def gemm_query_linear(form, M, N, K, dtype="bf16", rows16=True, tile="auto", check=True):
+    """The kernel a call of these sizes would use (no HIP call).  Returns
+    (status, dict)."""
+    info = LinearInfo()
+    rc = _lib().gemm_query_linear(_enum(form, LINEAR_FORMS), M, N, K, _enum(dtype, DTYPES), int(rows16),
+                                  _enum(tile, LINEAR_TILES), ctypes.byref(info))
+    if check and rc != GEMM_OK:
+        raise GemmError(rc, "gemm_query_linear")
+    return rc, info.as_dict()
+
+
+def linear(a, b, *, layout="RC", bias=None, activation="none", residual=None, pair=None, keep=False, out=None, tile="auto",
+           stream=None):
+    """act(A B + A2 B2 + bias) + residual through gemm_linear: c, or (c, z) with
+    keep=True.
+
+    a: M x K, bfloat16 or float16; b: B's N x K transpose for layout "RC" (a
+    layer's weight as it lies), K x N for "RR" (the same weight in the gradient of
+    the layer's input).  pair: (a2, b2), shaped as a and b, whose product is
+    added before the rounding.  bias: N values of float32 or a's type.
+    activation: "none", "relu", "gelu", "gelu_tanh" or "silu".  residual: M x N,
+    added behind the activation.  z: the activation's argument in a's type,
+    what gated_backward takes.  c is written into out where it is given, which
+    may be residual.  Sums are float32, each result is rounded once.
+
+    The call is one kernel, enqueued on `stream` (a torch stream or its raw
+    handle; the current stream of a's device by default).  Argument errors raise
+    ValueError, or GemmError with the C status, before anything is enqueued.
+    The first call on a device sets it up, which a graph capture cannot hold
+    (RuntimeError).  Rows that start on 16 bytes are the fast case: a
+    matrix of an odd width is better held in padded rows."""
+    if stream is not None:
+        with _on_stream(stream, a):
+            return linear(a, b, layout=layout, bias=bias, activation=activation, residual=residual, pair=pair, keep=keep,
+                          out=out, tile=tile)
+    ops = _OPS or _ops()
+    a2, b2 = _pair(pair)
+    return ops.linear(a, b, _named(layout, LAYOUTS, "layout"), bias, _named(activation, ACTIVATIONS, "activation"), residual,
+                      a2, b2, keep, out, _named(tile, LINEAR_TILES, "tile"))
+
+
+def _pair(pair):
+    if pair is None:
+        return None, None
+    if not isinstance(pair, (tuple, list)) or len(pair) != 2 or pair[0] is None or pair[1] is None:
+        raise ValueError("pair must be two matrices")
+    return pair
+
+
+def gated(x, gate, up, *, gate_bias=None, up_bias=None, activation="silu", keep=False, out=None, tile="auto", stream=None):
+    """act(X Wg^T + bg) * (X Wu^T + bu) through gemm_gated: h, or (h, g, u) with
+    keep=True, g and u being the two factors' arguments.
+
+    x: M x K, bfloat16 or float16; gate, up: the weights, N x K of x's type;
+    gate_bias, up_bias: N values of float32 or x's type, both of one.  h is
+    formed before g and u are rounded, and written into out where it is given.
+    Activations, streams and errors as linear."""
+    if stream is not None:
+        with _on_stream(stream, x):
+            return gated(x, gate, up, gate_bias=gate_bias, up_bias=up_bias, activation=activation, keep=keep, out=out,
+                         tile=tile)
+    return (_OPS or _ops()).gated(x, gate, up, gate_bias, up_bias, _named(activation, ACTIVATIONS, "activation"), keep, out,
+                                  _named(tile, LINEAR_TILES, "tile"))
+
+
+def gated_backward(dy, w, g, u=None, *, activation="silu", keep=False, tile="auto", stream=None):
+    """The gradients of what a gated layer, or an activation, was taken of,
+    through gemm_gated_backward: with dh = dy w,
+        dg = dh u act'(g), du = dh act(g): (dg, du), or (dg, du, h) with
+        keep=True, h = act(g) u again (so that it need not be kept);
+        without u: dg = dh act'(g): dg, or (dg, h), h = act(g).
+
+    dy: M x K, the gradient of the next layer's output; w: that layer's weight
+    as it lies, K x N; g, u: what gated(keep=True) returned, or linear's z; all
+    of one type.  dh is not rounded.  Streams and errors as linear."""
+    if stream is not None:
+        with _on_stream(stream, dy):
+            return gated_backward(dy, w, g, u, activation=activation, keep=keep, tile=tile)
+    return (_OPS or _ops()).gated_backward(dy, w, g, u, _named(activation, ACTIVATIONS, "activation"), keep,
+                                           _named(tile, LINEAR_TILES, "tile"))
+
+
+def weight_gradient(dc, a, *, out=None, bias=False, bias_out=None, accumulate=False, tile="auto", stream=None):
+    """A layer's weight's gradient dC^T A through gemm_weight_gradient: dw (N x K,
+    float32), or (dw, db) with bias=True, db being the sums of dc's columns.
+
+    dc: M x N, the gradient of the layer's output (before its activation); a:
+    M x K, its input; bfloat16 or float16.  out, bias_out: where dw and db are
+    written, or with accumulate=True added.  Streams and errors as linear."""
+    if stream is not None:
+        with _on_stream(stream, dc):
+            return weight_gradient(dc, a, out=out, bias=bias, bias_out=bias_out, accumulate=accumulate, tile=tile)
+    return (_OPS or _ops()).weight_gradient(dc, a, out, bias, bias_out, accumulate, _named(tile, LINEAR_TILES, "tile"))
 
 
 class Gemm:

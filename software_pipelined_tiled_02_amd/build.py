@@ -5,7 +5,7 @@ the objects are linked into software_pipelined_tiled_02_amd/libpipegemm.so.
 Each kernel's register, LDS and occupancy figures, as the compiler reports
 them (its kernel-resource-usage remarks), are written to
 kernel_resources.json beside the library.  csrc/torch_ops.cpp (host code: the
-8-bit operators on torch tensors) becomes the module _torch_ops, linked to
+8-bit and the feed-forward operators on torch tensors) becomes the module _torch_ops, linked to
 the library.  Two standalone measurement
 programs are built beside it: `ceiling_probe`
 (csrc/ceiling_probe.hip: MFMA and HBM rates of the chip, no GEMM code) and
@@ -26,7 +26,8 @@ LIB = os.path.join(HERE, "libpipegemm.so")
 RESOURCES = os.path.join(HERE, "kernel_resources.json")
 PROBES = ["ceiling_probe", "lds_layout_probe"]
 SOURCES = ["kernels_i8.hip", "kernels_f16.hip", "kernels_bf16.hip", "kernels_f32.hip", "abi.hip",
-           "fp8_abi.hip", "fp8_stream.hip", "fp8_staged.hip", "fp8_waves.hip", "fp8_quantize.hip", "fp8_rms.hip"]
+           "fp8_abi.hip", "fp8_stream.hip", "fp8_staged.hip", "fp8_waves.hip", "fp8_quantize.hip", "fp8_rms.hip",
+           "linear_abi.hip", "linear_rc.hip", "linear_rr.hip", "linear_gated.hip", "linear_backward.hip", "linear_weight.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 CXX = os.environ.get("CXX", "g++")

@@ -1,0 +1,10 @@
+// linear_rc.hip -- layers: both factors with K along their rows.
+#include "linear_tile.h"
+
+namespace pg {
+
+const void* linear_rc_kernel(int xt, int tile, bool rows16) {
+    return linear_by_type<END_LINEAR, true, true, false>(xt, tile, rows16);
+}
+
+}  // namespace pg

@@ -1,4 +1,4 @@
-// torch_ops.cpp -- the 8-bit operators on torch tensors: argument checks,
+// torch_ops.cpp -- the 8-bit and the feed-forward operators on torch tensors: argument checks,
 // output allocation and the call of the C ABI, as a CPython module
 // (_torch_ops) that `binding` wraps.
 //
@@ -353,6 +353,163 @@ PyObject* rms_backward_(PyObject* const* arg, Py_ssize_t n) {
     return tuple_of({dxt, dw});
 }
 
+// ---- a feed-forward block in 16 bits ------------------------------------------
+
+// A matrix of bfloat16 or float16 (of one type, where given).
+Matrix halves(const at::Tensor& t, const char* what, int device = -1, int type = -1, int64_t rows = -1, int64_t cols = -1) {
+    const Matrix m = matrix(t, what, kFloats, device, type, rows, cols);
+    if (m.type == GEMM_F32) throw BadArgument{std::string(what) + " must be bfloat16 or float16"};
+    return m;
+}
+Matrix halves_or_none(PyObject* o, const char* what, const Matrix& like, int64_t rows, int64_t cols) {
+    return none(o) ? Matrix() : halves(tensor(o, what), what, like.device, like.type, rows, cols);
+}
+const void* bias_of(PyObject* o, const char* what, int64_t n, const Matrix& like, int* type) {
+    if (none(o)) return nullptr;
+    const at::Tensor& t = tensor(o, what);
+    *type = vector(t, what, n, like.device, like.type);
+    return t.data_ptr();
+}
+// A new M x N matrix, its rows one after another.
+at::Tensor made_like(const at::Tensor& t, int64_t rows, int64_t cols, Matrix* m) {
+    const at::Tensor made = empty({rows, cols}, {cols, 1}, t.scalar_type(), t.get_device());
+    m->p = (char*)made.data_ptr();
+    m->ld = cols;
+    return made;
+}
+void same_k(const Matrix& a, int64_t k, const char* what) {
+    if (a.cols != k)
+        throw BadArgument{"inner dimensions differ: " + std::to_string(a.cols) + ", and " + std::to_string(k) + " of " + what};
+}
+
+// linear(a, b, layout, bias, activation, residual, a2, b2, keep, out, tile)
+PyObject* linear_(PyObject* const* arg, Py_ssize_t n) {
+    arguments(n, 11);
+    const at::Tensor& at = tensor(arg[0], "a");
+    const Matrix a = halves(at, "a");
+    const Matrix b = halves(tensor(arg[1], "b"), "b", a.device, a.type);
+    const int64_t layout = integer(arg[2]), act = integer(arg[4]), tile = integer(arg[10]);
+    const bool rr = layout == GEMM_LAYOUT_RR, keep = truth(arg[8]);
+    const int64_t M = a.rows, K = a.cols, N = rr ? b.cols : b.rows;
+    same_k(a, rr ? b.rows : b.cols, "b");
+    int bias_type = GEMM_F32;
+    const void* const bias = bias_of(arg[3], "bias", N, a, &bias_type);
+    const Matrix r = halves_or_none(arg[5], "residual", a, M, N);
+    const Matrix a2 = halves_or_none(arg[6], "pair's a", a, M, K), b2 = halves_or_none(arg[7], "pair's b", a, b.rows, b.cols);
+    // (an empty matrix has no address, which would read as none given)
+    const bool second = a2.p != nullptr && b2.p != nullptr;
+    Matrix c = halves_or_none(arg[9], "out", a, M, N), z;
+    const gemm_handle_t h = handle_of(a.device);
+    at::Tensor ct, zt;
+    if (none(arg[9])) ct = made_like(at, M, N, &c);
+    else ct = THPVariable_Unpack(arg[9]);
+    if (keep) zt = made_like(at, M, N, &z);
+    void* const stream = raw_stream(a.device);
+    const int rc = enqueue([&] {
+        return gemm_linear(h, M, N, K, a.type, (int)layout, (int)act, bias_type, (int)tile, a.p, a.ld, b.p, b.ld, second ? a2.p : nullptr,
+                           a2.ld, second ? b2.p : nullptr, b2.ld, bias, r.p, r.ld, z.p, z.ld, c.p, c.ld, stream);
+    });
+    if (rc != GEMM_OK) return gemm_error(rc, "gemm_linear");
+    return keep ? tuple_of({ct, zt}) : THPVariable_Wrap(std::move(ct));
+}
+
+// gated(x, gate, up, gate_bias, up_bias, activation, keep, out, tile)
+PyObject* gated_(PyObject* const* arg, Py_ssize_t n) {
+    arguments(n, 9);
+    const at::Tensor& xt = tensor(arg[0], "x");
+    const Matrix x = halves(xt, "x");
+    const Matrix wg = halves(tensor(arg[1], "gate"), "gate", x.device, x.type);
+    same_k(x, wg.cols, "gate");
+    const int64_t M = x.rows, K = x.cols, N = wg.rows;
+    const Matrix wu = halves(tensor(arg[2], "up"), "up", x.device, x.type, N, K);
+    int type = GEMM_F32, type_u = GEMM_F32;
+    const void* const bg = bias_of(arg[3], "gate_bias", N, x, &type);
+    const void* const bu = bias_of(arg[4], "up_bias", N, x, &type_u);
+    if (bg != nullptr && bu != nullptr && type != type_u) throw BadArgument{"the biases must be of one type"};
+    if (bg == nullptr) type = type_u;
+    const int64_t act = integer(arg[5]), tile = integer(arg[8]);
+    const bool keep = truth(arg[6]);
+    Matrix ho = halves_or_none(arg[7], "out", x, M, N), g, u;
+    const gemm_handle_t h = handle_of(x.device);
+    at::Tensor ht, gt, ut;
+    if (none(arg[7])) ht = made_like(xt, M, N, &ho);
+    else ht = THPVariable_Unpack(arg[7]);
+    if (keep) {
+        gt = made_like(xt, M, N, &g);
+        ut = made_like(xt, M, N, &u);
+    }
+    void* const stream = raw_stream(x.device);
+    const int rc = enqueue([&] {
+        return gemm_gated(h, M, N, K, x.type, (int)act, type, (int)tile, x.p, x.ld, wg.p, wg.ld, wu.p, wu.ld, bg, bu, g.p, g.ld,
+                          u.p, u.ld, ho.p, ho.ld, stream);
+    });
+    if (rc != GEMM_OK) return gemm_error(rc, "gemm_gated");
+    return keep ? tuple_of({ht, gt, ut}) : THPVariable_Wrap(std::move(ht));
+}
+
+// gated_backward(dy, w, g, u, activation, keep, tile)
+PyObject* gated_backward_(PyObject* const* arg, Py_ssize_t n) {
+    arguments(n, 7);
+    const at::Tensor& dyt = tensor(arg[0], "dy");
+    const Matrix dy = halves(dyt, "dy");
+    const Matrix w = halves(tensor(arg[1], "w"), "w", dy.device, dy.type);
+    same_k(dy, w.rows, "w");
+    const int64_t M = dy.rows, K = dy.cols, N = w.cols, act = integer(arg[4]), tile = integer(arg[6]);
+    const Matrix g = halves(tensor(arg[2], "g"), "g", dy.device, dy.type, M, N), u = halves_or_none(arg[3], "u", dy, M, N);
+    const bool gate = !none(arg[3]), keep = truth(arg[5]);
+    const gemm_handle_t h = handle_of(dy.device);
+    Matrix dg, du, hm;
+    at::Tensor dut, ht;
+    at::Tensor dgt = made_like(dyt, M, N, &dg);
+    if (gate) dut = made_like(dyt, M, N, &du);
+    if (keep) ht = made_like(dyt, M, N, &hm);
+    void* const stream = raw_stream(dy.device);
+    const int rc = enqueue([&] {
+        return gemm_gated_backward(h, M, N, K, dy.type, (int)act, (int)tile, dy.p, dy.ld, w.p, w.ld, g.p, g.ld, u.p, u.ld, dg.p,
+                                   dg.ld, du.p, du.ld, hm.p, hm.ld, stream);
+    });
+    if (rc != GEMM_OK) return gemm_error(rc, "gemm_gated_backward");
+    if (gate) return keep ? tuple_of({dgt, dut, ht}) : tuple_of({dgt, dut});
+    return keep ? tuple_of({dgt, ht}) : THPVariable_Wrap(std::move(dgt));
+}
+
+// weight_gradient(dc, a, out, bias, bias_out, accumulate, tile)
+PyObject* weight_gradient_(PyObject* const* arg, Py_ssize_t n) {
+    arguments(n, 7);
+    const Matrix dc = halves(tensor(arg[0], "dc"), "dc");
+    const Matrix a = halves(tensor(arg[1], "a"), "a", dc.device, dc.type);
+    if (a.rows != dc.rows)
+        throw BadArgument{"dc and a must have as many rows (got " + std::to_string(dc.rows) + " and " + std::to_string(a.rows) + ")"};
+    const int64_t M = dc.rows, N = dc.cols, K = a.cols, tile = integer(arg[6]);
+    const bool bias = truth(arg[3]) || !none(arg[4]), accumulate = truth(arg[5]);
+    if (accumulate && (none(arg[2]) || (bias && none(arg[4])))) throw BadArgument{"accumulate needs out (and bias_out for the bias)"};
+    if (bias && K == 0 && N > 0) throw BadArgument{"the bias's gradient needs an input with columns"};
+    Matrix dw;
+    at::Tensor dwt, dbt;
+    if (!none(arg[2])) {
+        dwt = tensor(arg[2], "out");
+        dw = matrix(dwt, "out", kFloats, dc.device, GEMM_F32, N, K);
+    }
+    if (!none(arg[4])) {
+        dbt = tensor(arg[4], "bias_out");
+        if (vector(dbt, "bias_out", N, dc.device, -1) != GEMM_F32) throw BadArgument{"bias_out must be float32"};
+    }
+    const gemm_handle_t h = handle_of(dc.device);
+    if (none(arg[2])) {
+        dwt = empty({N, K}, {K, 1}, at::kFloat, dc.device);
+        dw.p = (char*)dwt.data_ptr();
+        dw.ld = K;
+    }
+    if (bias && none(arg[4])) dbt = empty({N}, {1}, at::kFloat, dc.device);
+    void* const stream = raw_stream(dc.device);
+    const int rc = enqueue([&] {
+        return gemm_weight_gradient(h, M, N, K, dc.type, accumulate, (int)tile, dc.p, dc.ld, a.p, a.ld, (float*)dw.p, dw.ld,
+                                    bias ? (float*)dbt.data_ptr() : nullptr, stream);
+    });
+    if (rc != GEMM_OK) return gemm_error(rc, "gemm_weight_gradient");
+    return bias ? tuple_of({dwt, dbt}) : THPVariable_Wrap(std::move(dwt));
+}
+
 // C++ errors as Python's.
 template <PyObject* (*F)(PyObject* const*, Py_ssize_t)>
 PyObject* guarded(PyObject*, PyObject* const* arg, Py_ssize_t n) {
@@ -371,6 +528,10 @@ PyMethodDef g_methods[] = {
     {"quantize_fp8", (PyCFunction)(void (*)())&guarded<quantize_fp8_>, METH_FASTCALL, nullptr},
     {"rms_fp8", (PyCFunction)(void (*)())&guarded<rms_fp8_>, METH_FASTCALL, nullptr},
     {"rms_backward", (PyCFunction)(void (*)())&guarded<rms_backward_>, METH_FASTCALL, nullptr},
+    {"linear", (PyCFunction)(void (*)())&guarded<linear_>, METH_FASTCALL, nullptr},
+    {"gated", (PyCFunction)(void (*)())&guarded<gated_>, METH_FASTCALL, nullptr},
+    {"gated_backward", (PyCFunction)(void (*)())&guarded<gated_backward_>, METH_FASTCALL, nullptr},
+    {"weight_gradient", (PyCFunction)(void (*)())&guarded<weight_gradient_>, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_torch_ops", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};

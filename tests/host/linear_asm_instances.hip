@@ -1,0 +1,13 @@
+// Instances with transposing LDS reads, for tests/test_linear_asm_waits.py.
+#include "linear_tile.h"
+
+namespace pg {
+
+const void* instances(int t, bool r16, bool rr, bool backward, bool sums) {
+    if (rr) return linear_by_tile<XT_BF16, END_LINEAR, true, false, false>(t, r16);
+    if (backward) return linear_by_tile<XT_F16, END_GATED_BACKWARD, true, false, false>(t, r16);
+    if (sums) return linear_by_tile<XT_BF16, END_WEIGHT, false, false, true>(t, r16);
+    return linear_by_tile<XT_F16, END_WEIGHT, false, false, false>(t, r16);
+}
+
+}  // namespace pg
