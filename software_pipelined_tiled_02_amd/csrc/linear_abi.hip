@@ -35,14 +35,15 @@ struct Operand {
 // Rows that start on 16 bytes are staged straight into LDS.
 bool rows16(const Operand& o) { return aligned(o.p, 16) && o.step() % 8 == 0; }
 
-const void* kernel(int form, int dtype, int tile, bool r16, bool sums) {
+// extra: a second product (linear), sums of DC's columns (weight gradients).
+const void* kernel(int form, int dtype, int tile, bool r16, bool extra) {
     const int xt = dtype == GEMM_BF16 ? pg::XT_BF16 : pg::XT_F16;
     switch (form) {
-    case GEMM_FORM_LINEAR_RC: return pg::linear_rc_kernel(xt, tile, r16);
-    case GEMM_FORM_LINEAR_RR: return pg::linear_rr_kernel(xt, tile, r16);
+    case GEMM_FORM_LINEAR_RC: return pg::linear_rc_kernel(xt, tile, r16, extra);
+    case GEMM_FORM_LINEAR_RR: return pg::linear_rr_kernel(xt, tile, r16, extra);
     case GEMM_FORM_GATED: return pg::gated_kernel(xt, tile, r16);
     case GEMM_FORM_GATED_BACKWARD: return pg::gated_backward_kernel(xt, tile, r16);
-    default: return pg::weight_gradient_kernel(xt, tile, r16, sums);
+    default: return pg::weight_gradient_kernel(xt, tile, r16, extra);
     }
 }
 
@@ -54,7 +55,7 @@ struct Plan {
 
 // The kernel for M x N sums over K (weight gradients: M and N are the weight's
 // rows and columns, K the tokens).  No HIP call.
-int plan_sums(int form, int64_t M, int64_t N, int64_t K, int dtype, bool r16, bool sums, int tile, int num_cus, Plan* plan) {
+int plan_sums(int form, int64_t M, int64_t N, int64_t K, int dtype, bool r16, bool extra, int tile, int num_cus, Plan* plan) {
     const bool gated = form == GEMM_FORM_GATED;
     auto tiles = [&](int t) {
         const pg::LinearShape sh = pg::linear_shape(t);
@@ -64,12 +65,12 @@ int plan_sums(int form, int64_t M, int64_t N, int64_t K, int dtype, bool r16, bo
     if (tc == GEMM_LINEAR_TILE_AUTO) {
         tc = pg::LINEAR_TILE_64;
         for (int t = 0; t < pg::LINEAR_TILE_COUNT; ++t)
-            if (kernel(form, dtype, t, r16, sums) != nullptr && tiles(t) >= num_cus) {
+            if (kernel(form, dtype, t, r16, extra) != nullptr && tiles(t) >= num_cus) {
                 tc = t;
                 break;
             }
     }
-    plan->fn = kernel(form, dtype, tc, r16, sums);
+    plan->fn = kernel(form, dtype, tc, r16, extra);
     if (plan->fn == nullptr) return GEMM_ERR_ALIGNMENT;
     const pg::LinearShape sh = pg::linear_shape(tc);
     const bool any = M > 0 && N > 0;
@@ -173,7 +174,7 @@ int gemm_linear(gemm_handle_t h, int64_t M, int64_t N, int64_t K, int dtype, int
     if (rc != GEMM_OK) return rc;
     if (bias != nullptr && !aligned(bias, bias_dtype == GEMM_F32 ? 4 : 2)) return GEMM_ERR_ALIGNMENT;
     Plan plan;
-    rc = plan_sums(rr ? GEMM_FORM_LINEAR_RR : GEMM_FORM_LINEAR_RC, M, N, K, dtype, r16, false, tile, h->num_cus, &plan);
+    rc = plan_sums(rr ? GEMM_FORM_LINEAR_RR : GEMM_FORM_LINEAR_RC, M, N, K, dtype, r16, products == 2, tile, h->num_cus, &plan);
     if (rc != GEMM_OK) return rc;
     pg::LinearArgs a;
     memset(&a, 0, sizeof a);
@@ -194,7 +195,6 @@ int gemm_linear(gemm_handle_t h, int64_t M, int64_t N, int64_t K, int dtype, int
     a.M = (int32_t)M;
     a.N = (int32_t)N;
     a.K = (int32_t)K;
-    a.products = products;
     a.act = activation;
     return launch(h, plan, a, stream);
 }
@@ -244,7 +244,6 @@ int gemm_gated(gemm_handle_t h, int64_t M, int64_t N, int64_t K, int dtype, int 
     a.M = (int32_t)M;
     a.N = (int32_t)N;
     a.K = (int32_t)K;
-    a.products = 1;
     a.act = activation;
     return launch(h, plan, a, stream);
 }
@@ -292,7 +291,6 @@ int gemm_gated_backward(gemm_handle_t h, int64_t M, int64_t N, int64_t K, int dt
     a.M = (int32_t)M;
     a.N = (int32_t)N;
     a.K = (int32_t)K;
-    a.products = 1;
     a.act = activation;
     return launch(h, plan, a, stream);
 }
@@ -331,7 +329,6 @@ int gemm_weight_gradient(gemm_handle_t h, int64_t M, int64_t N, int64_t K, int d
     a.M = (int32_t)N;
     a.N = (int32_t)K;
     a.K = (int32_t)M;
-    a.products = 1;
     a.accumulate = accumulate;
     return launch(h, plan, a, stream);
 }

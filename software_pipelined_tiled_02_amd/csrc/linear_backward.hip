@@ -4,7 +4,7 @@
 namespace pg {
 
 const void* gated_backward_kernel(int xt, int tile, bool rows16) {
-    return linear_by_type<END_GATED_BACKWARD, true, false, false>(xt, tile, rows16);
+    return linear_by_type<END_GATED_BACKWARD, true, false, 0>(xt, tile, rows16);
 }
 
 }  // namespace pg

@@ -33,9 +33,9 @@ struct LinearArgs {
     float* sums;             // weight_gradient: sums of dC's columns, or NULL
     int64_t lda[2], ldb[2], ldi[2], ldo[3];
     int32_t M, N, K;         // sums are M x N
-    int32_t products;        // added into one sum: 1 or 2
     int32_t tiles_m, tiles_n;
     int32_t act, bias_f32, accumulate;
+    int32_t stream;          // the outputs' rows are whole lines: past the caches
 };
 
 // Tile classes: the workgroup's part of the sums (gated: half of the columns are
@@ -43,13 +43,13 @@ struct LinearArgs {
 enum LinearTile : int { LINEAR_TILE_256 = 0, LINEAR_TILE_128 = 1, LINEAR_TILE_64 = 2, LINEAR_TILE_COUNT = 3 };
 struct LinearShape { int bm, bn, waves; };
 constexpr LinearShape linear_shape(int t) {
-    return t == LINEAR_TILE_256 ? LinearShape{256, 256, 8} : t == LINEAR_TILE_128 ? LinearShape{128, 128, 8} : LinearShape{64, 64, 4};
+    return t == LINEAR_TILE_256 ? LinearShape{256, 256, 4} : t == LINEAR_TILE_128 ? LinearShape{128, 128, 8} : LinearShape{64, 64, 4};
 }
 
 // The kernel for a call: XT_F16 or XT_BF16, a tile class, and whether all
 // rows of the factors start on 16 bytes (NULL: the class needs that).
-const void* linear_rc_kernel(int xt, int tile, bool rows16);
-const void* linear_rr_kernel(int xt, int tile, bool rows16);
+const void* linear_rc_kernel(int xt, int tile, bool rows16, bool pair);
+const void* linear_rr_kernel(int xt, int tile, bool rows16, bool pair);
 const void* gated_kernel(int xt, int tile, bool rows16);
 const void* gated_backward_kernel(int xt, int tile, bool rows16);
 const void* weight_gradient_kernel(int xt, int tile, bool rows16, bool sums);
@@ -85,41 +85,43 @@ __device__ __forceinline__ float logistic(float z, Logistic l) {      // |z| <= 
     return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * fmaf(l.c3 * z, z, l.c1)));
 }
 
-// Eight values through the activation.  The branches are the same for a whole
+// Values through the activation.  The branches are the same for a whole
 // launch.  A NaN stays one.
-__device__ __forceinline__ void activate(int act, float (&v)[8]) {
+template <int N>
+__device__ __forceinline__ void activate(int act, float (&v)[N]) {
     if (act == ACT_NONE) return;
     if (act == ACT_RELU) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = v[e] < 0.0f ? 0.0f : v[e];
+        for (int e = 0; e < N; ++e) v[e] = v[e] < 0.0f ? 0.0f : v[e];
     } else if (act == ACT_GELU) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < N; ++e) {
             const float q = normal_tail(v[e], __builtin_amdgcn_exp2f(-0.721347520f * v[e] * v[e]));
             v[e] *= v[e] > 0.0f ? 1.0f - q : q;
         }
     } else {
         const Logistic l = logistic_of(act);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] *= logistic(within128(v[e]), l);
+        for (int e = 0; e < N; ++e) v[e] *= logistic(within128(v[e]), l);
     }
 }
 
-// The activation a and its derivative d at eight values.  The derivative past |z|
+// The activation a and its derivative d at N values.  The derivative past |z|
 // = 128 is taken there: 0 or 1 in fp32.  A NaN stays one in both.
-__device__ __forceinline__ void activate_slope(int act, const float (&z)[8], float (&a)[8], float (&d)[8]) {
+template <int N>
+__device__ __forceinline__ void activate_slope(int act, const float (&z)[N], float (&a)[N], float (&d)[N]) {
     if (act == ACT_NONE) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) { a[e] = z[e]; d[e] = 1.0f; }
+        for (int e = 0; e < N; ++e) { a[e] = z[e]; d[e] = 1.0f; }
     } else if (act == ACT_RELU) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < N; ++e) {
             a[e] = z[e] < 0.0f ? 0.0f : z[e];
             d[e] = z[e] > 0.0f ? 1.0f : z[e] <= 0.0f ? 0.0f : z[e];
         }
     } else if (act == ACT_GELU) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < N; ++e) {
             const float c = within128(z[e]);
             const float x = __builtin_amdgcn_exp2f(-0.721347520f * c * c);
             const float q = normal_tail(c, x), p = c > 0.0f ? 1.0f - q : q;
@@ -130,7 +132,7 @@ __device__ __forceinline__ void activate_slope(int act, const float (&z)[8], flo
         const Logistic l = logistic_of(act);
         const float k1 = -0.693147181f * l.c1, k3 = -2.07944154f * l.c3;        // q' = k1 + k3 z^2, back from base 2
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < N; ++e) {
             const float c = within128(z[e]);
             const float s = logistic(c, l);
             a[e] = z[e] * s;
@@ -139,87 +141,176 @@ __device__ __forceinline__ void activate_slope(int act, const float (&z)[8], flo
     }
 }
 
+// Eight neighbouring values of a row, `left` of them before its end (WHOLE: eight
+// or more; else the access is one that fetch8 and store8 describe).
+template <int XT, bool WHOLE>
+__device__ __forceinline__ Raw8<XT> get8(const void* base, int64_t at, int64_t n, int left) {
+    if constexpr (!WHOLE) {
+        return fetch8<XT>(base, at, n, left);
+    } else if constexpr (XT == XT_F32) {
+        const float* p = (const float*)base + at;
+        struct Two { i32x4q a, b; } two = {*(const i32x4u*)p, *(const i32x4u*)(p + 4)};
+        return __builtin_bit_cast(Raw8<XT>, two);
+    } else {
+        return __builtin_bit_cast(Raw8<XT>, (i32x4q)*(const i32x4u*)((const uint16_t*)base + at));
+    }
+}
+template <int XT, bool WHOLE>
+__device__ __forceinline__ void read8(Raw8<XT> r, int64_t n, int left, float* f) {
+    if constexpr (!WHOLE) settle8<XT>(r, n, left);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = (float)r.v[e];
+}
+// STREAM: past the caches.
+template <int XT, bool WHOLE>
+__device__ __forceinline__ void put8(void* base, int64_t at, int left, const float* f, bool stream) {
+    typedef typename XTypeOf<XT>::type T;
+    if constexpr (!WHOLE) {
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = f[e];
+        store8<XT>(base, at, left, v);
+    } else {
+        Raw8<XT> r;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r.v[e] = (T)f[e];
+        T* p = (T*)base + at;
+        if constexpr (XT == XT_F32) {
+            struct Two { i32x4q a, b; };
+            const Two two = __builtin_bit_cast(Two, r);
+            if (stream) {
+                __builtin_nontemporal_store(two.a, (i32x4u*)p);
+                __builtin_nontemporal_store(two.b, (i32x4u*)(p + 4));
+            } else {
+                asm volatile("" ::: "memory");       // (or the two become one form)
+                *(i32x4u*)p = two.a;
+                *(i32x4u*)(p + 4) = two.b;
+                asm volatile("" ::: "memory");
+            }
+        } else if (stream) {
+            __builtin_nontemporal_store(__builtin_bit_cast(i32x4q, r), (i32x4u*)p);
+        } else {
+            asm volatile("" ::: "memory");
+            *(i32x4u*)p = __builtin_bit_cast(i32x4q, r);
+            asm volatile("" ::: "memory");
+        }
+    }
+}
+
 // What an ending reads beside the sums, for eight neighbouring outputs.
 template <int XT, int END>
-struct Beside { Raw8<XT> a, b; };
+struct Beside { Raw8<XT> a, b; Raw8<XT_F32> c; };
 
-template <int XT, int END>
+template <int XT, int END, bool WHOLE>
 __device__ __forceinline__ Beside<XT, END> fetch_beside(const LinearArgs& p, int64_t m, int64_t n) {
     Beside<XT, END> r;
     const int left = p.N - (int)n;
     if constexpr (END == END_LINEAR || END == END_GATED_BACKWARD)
-        if (p.in[0] != nullptr) r.a = fetch8<XT>(p.in[0], m * p.ldi[0] + n, n, left);
+        if (p.in[0] != nullptr) r.a = get8<XT, WHOLE>(p.in[0], m * p.ldi[0] + n, n, left);
     if constexpr (END == END_GATED_BACKWARD)
-        if (p.in[1] != nullptr) r.b = fetch8<XT>(p.in[1], m * p.ldi[1] + n, n, left);
+        if (p.in[1] != nullptr) r.b = get8<XT, WHOLE>(p.in[1], m * p.ldi[1] + n, n, left);
+    if constexpr (END == END_WEIGHT)
+        if (p.accumulate) r.c = get8<XT_F32, WHOLE>(p.out[0], m * p.ldo[0] + n, n, left);
     return r;
 }
 
-// v += bias.
-template <int XT>
-__device__ __forceinline__ void add_bias(const LinearArgs& p, int which, int64_t n, float (&v)[8]) {
-    if (p.bias[which] == nullptr) return;
-    float b[8];
-    const int left = p.N - (int)n;
-    if (p.bias_f32) load8<XT_F32>(p.bias[which], n, n, left, b);
-    else load8<XT>(p.bias[which], n, n, left, b);
+// The biases of eight neighbouring columns.
+template <int END>
+struct Biases { float v[8], u[8]; };
+
+template <int XT, int END>
+__device__ __forceinline__ Biases<END> fetch_biases(const LinearArgs& p, int64_t n) {
+    Biases<END> b;
+    const auto fetch = [&](const void* from, float (&f)[8]) {
+        const int left = p.N - (int)n;
+        if (from == nullptr) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] += b[e];
+            for (int e = 0; e < 8; ++e) f[e] = 0.0f;
+        } else if (p.bias_f32) {
+            load8<XT_F32>(from, n, n, left, f);
+        } else {
+            load8<XT>(from, n, n, left, f);
+        }
+    };
+    if constexpr (END == END_LINEAR || END == END_GATED) fetch(p.bias[0], b.v);
+    if constexpr (END == END_GATED) fetch(p.bias[1], b.u);
+    return b;
 }
 
-// The ending for outputs (m, n .. n + 7), m < M, n < N: v holds their sums,
-// u (gated) the second product's.
-template <int XT, int END>
-__device__ __forceinline__ void finish8(const LinearArgs& p, int64_t m, int64_t n, Beside<XT, END>& beside, float (&v)[8],
-                                        float (&u)[8]) {
+// The ending for outputs (m + q step, n .. n + 7), q < Q, rows m .. < M and n < N:
+// v holds their sums, u (gated) the second product's.
+template <int XT, int END, bool WHOLE, int Q>
+__device__ __forceinline__ void finish(const LinearArgs& p, int64_t m, int64_t step, int64_t n, Beside<XT, END> (&beside)[Q],
+                                       const Biases<END>& bias, float (&v)[8 * Q], float (&u)[8 * Q]) {
     const int left = p.N - (int)n;
+    const bool stream = p.stream;
+    const auto put = [&](int which, const float (&f)[8 * Q]) {
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+            put8<XT, WHOLE>(p.out[which], (m + q * step) * p.ldo[which] + n, left, f + 8 * q, stream);
+    };
     if constexpr (END == END_LINEAR) {
-        add_bias<XT>(p, 0, n, v);
-        if (p.out[1] != nullptr) store8<XT>(p.out[1], m * p.ldo[1] + n, left, v);
+#pragma unroll
+        for (int e = 0; e < 8 * Q; ++e) v[e] += bias.v[e % 8];
+        if (p.out[1] != nullptr) put(1, v);
         activate(p.act, v);
         if (p.in[0] != nullptr) {
-            float r[8];
-            settle8<XT>(beside.a, n, left);
-            to_f32<XT>(beside.a, r);
+            float r[8 * Q];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] += r[e];
+            for (int q = 0; q < Q; ++q) read8<XT, WHOLE>(beside[q].a, n, left, r + 8 * q);
+#pragma unroll
+            for (int e = 0; e < 8 * Q; ++e) v[e] += r[e];
         }
-        store8<XT>(p.out[0], m * p.ldo[0] + n, left, v);
+        put(0, v);
     } else if constexpr (END == END_GATED) {
-        add_bias<XT>(p, 0, n, v);
-        add_bias<XT>(p, 1, n, u);
+#pragma unroll
+        for (int e = 0; e < 8 * Q; ++e) {
+            v[e] += bias.v[e % 8];
+            u[e] += bias.u[e % 8];
+        }
         if (p.out[1] != nullptr) {
-            store8<XT>(p.out[1], m * p.ldo[1] + n, left, v);
-            store8<XT>(p.out[2], m * p.ldo[2] + n, left, u);
+            put(1, v);
+            put(2, u);
         }
         activate(p.act, v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] *= u[e];
-        store8<XT>(p.out[0], m * p.ldo[0] + n, left, v);
+        for (int e = 0; e < 8 * Q; ++e) v[e] *= u[e];
+        put(0, v);
     } else if constexpr (END == END_GATED_BACKWARD) {
-        float g[8], a[8], d[8];
-        settle8<XT>(beside.a, n, left);
-        to_f32<XT>(beside.a, g);
-        activate_slope(p.act, g, a, d);
-        if (p.in[1] != nullptr) {
-            float w[8], x[8];
-            settle8<XT>(beside.b, n, left);
-            to_f32<XT>(beside.b, w);
+        float a[8 * Q], d[8 * Q];
+        {
+            float g[8 * Q];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) { x[e] = v[e] * a[e]; d[e] *= w[e]; a[e] *= w[e]; }
-            store8<XT>(p.out[1], m * p.ldo[1] + n, left, x);
+            for (int q = 0; q < Q; ++q) read8<XT, WHOLE>(beside[q].a, n, left, g + 8 * q);
+            activate_slope(p.act, g, a, d);
         }
-        if (p.out[2] != nullptr) store8<XT>(p.out[2], m * p.ldo[2] + n, left, a);
+        if (p.in[1] != nullptr) {
+            float w[8 * Q], x[8 * Q];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] *= d[e];
-        store8<XT>(p.out[0], m * p.ldo[0] + n, left, v);
+            for (int q = 0; q < Q; ++q) read8<XT, WHOLE>(beside[q].b, n, left, w + 8 * q);
+#pragma unroll
+            for (int e = 0; e < 8 * Q; ++e) {
+                x[e] = v[e] * a[e];
+                d[e] *= w[e];
+                a[e] *= w[e];
+            }
+            put(1, x);
+        }
+        if (p.out[2] != nullptr) put(2, a);
+#pragma unroll
+        for (int e = 0; e < 8 * Q; ++e) v[e] *= d[e];
+        put(0, v);
     } else {
         if (p.accumulate) {
-            float c[8];
-            load8<XT_F32>(p.out[0], m * p.ldo[0] + n, n, left, c);
+            float c[8 * Q];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] += c[e];
+            for (int q = 0; q < Q; ++q) read8<XT_F32, WHOLE>(beside[q].c, n, left, c + 8 * q);
+#pragma unroll
+            for (int e = 0; e < 8 * Q; ++e) v[e] += c[e];
         }
-        store8<XT_F32>(p.out[0], m * p.ldo[0] + n, left, v);
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+            put8<XT_F32, WHOLE>(p.out[0], (m + q * step) * p.ldo[0] + n, left, v + 8 * q, stream);
     }
 }
 

@@ -3,6 +3,6 @@
 
 namespace pg {
 
-const void* gated_kernel(int xt, int tile, bool rows16) { return linear_by_type<END_GATED, true, true, false>(xt, tile, rows16); }
+const void* gated_kernel(int xt, int tile, bool rows16) { return linear_by_type<END_GATED, true, true, 0>(xt, tile, rows16); }
 
 }  // namespace pg

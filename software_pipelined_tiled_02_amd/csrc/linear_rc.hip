@@ -3,8 +3,8 @@
 
 namespace pg {
 
-const void* linear_rc_kernel(int xt, int tile, bool rows16) {
-    return linear_by_type<END_LINEAR, true, true, false>(xt, tile, rows16);
+const void* linear_rc_kernel(int xt, int tile, bool rows16, bool pair) {
+    return pair ? linear_by_type<END_LINEAR, true, true, 1>(xt, tile, rows16) : linear_by_type<END_LINEAR, true, true, 0>(xt, tile, rows16);
 }
 
 }  // namespace pg

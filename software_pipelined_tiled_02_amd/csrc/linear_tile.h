@@ -9,11 +9,12 @@
 // one 16-byte read per lane; K outside, as 64 rows of the tile's width, and
 // the same fragment is two of gfx950's transposing reads.
 //
-// The K loop is a ring of SLOTS K-tiles.  A K-tile is multiplied row of pieces
-// by row of pieces (16 x 16 each).  Once the last row's fragments are in
-// registers the wave waits for the next K-tile and crosses the one barrier;
-// under the last row's matrix instructions it reads the next K-tile's first
-// fragments, and starts the loads that take the place of the one it has read.
+// The K loop goes through rings of SA K-tiles of A and SB of B.  A K-tile is
+// multiplied row of pieces by row of pieces (16 x 16 each).  Once the last row's
+// fragments are in registers the wave waits for the next K-tile and crosses the
+// one barrier; under the last row's matrix instructions it reads the next
+// K-tile's first fragments, and starts the loads that take the places of the one
+// it has read: of B SB K-tiles on, then of A SA K-tiles on.
 #ifndef PIPEGEMM_LINEAR_TILE_H
 #define PIPEGEMM_LINEAR_TILE_H
 
@@ -32,6 +33,16 @@ __device__ __forceinline__ f32x4 multiply16(i32x4 x, i32x4 y, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, y), c, 0, 0, 0);
     else
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8l, x), __builtin_bit_cast(f16x8l, y), c, 0, 0, 0);
+}
+
+// The same written in place: the sum's registers are the destination's, and lie
+// in the second half of the register file.  (Left to itself the compiler moves
+// a wave's 64 sums of four between registers at every K-tile.)  It does not see
+// these as matrix instructions, so the loop pads their hazards itself.
+template <int XT>
+__device__ __forceinline__ void multiply16_in_place(i32x4 x, i32x4 y, i32x4& c) {
+    if constexpr (XT == XT_BF16) asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(x), "v"(y));
+    else asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(c) : "v"(x), "v"(y));
 }
 
 // At most N of this wave's LDS accesses are still in flight.
@@ -56,113 +67,152 @@ __device__ __forceinline__ void place_linear(const LinearArgs& a, int tile, int&
 // One factor's part of a tile: ROWS rows (of A, or of B's transpose), staged by
 // T threads.  INSIDE: K along the rows.  SPLIT: rows 0-15 of each 32 belong to
 // the first of two matrices, rows 16-31 to the second (gated).
-template <bool INSIDE, int ROWS, int T, bool SPLIT>
+template <bool INSIDE, int ROWS, int T, bool SPLIT, int P>
 struct Factor {
     static constexpr int L = ROWS * 8 / T;               // chunks of 16 bytes per lane and K-tile
     static constexpr int BYTES = ROWS * 128;
     static constexpr int CR = ROWS / 8;                  // K outside: chunks of a row
     static_assert(ROWS * 8 % T == 0 && L >= 1, "whole chunks per lane");
-    static_assert(INSIDE ? T % 128 == 0 : T % (16 * CR) == 0, "a lane's chunks have one place in the swizzle's period");
+    // A lane's chunks have one place in the swizzle's period, or (256 wide, K
+    // outside, 256 threads: 8 rows of K apart) two in turn, 2 chunks apart.
+    static constexpr bool TURNS = !INSIDE && T % (16 * CR) != 0;
+    static_assert(INSIDE ? T % 128 == 0 : T % (8 * CR) == 0, "places in the swizzle's period");
 
-    const uint8_t* base;             // this wave's matrix, at the tile's first row (column), k = 0
-    int64_t ld;                      // bytes from row to row
-    uint32_t off[L];                 // a lane's chunks
+    const uint8_t* base[P];          // this wave's matrix of each product, at the tile's first row (column), k = 0
+    int64_t ld[P];                   // bytes from row to row
+    uint32_t off[P][L];              // a lane's chunks
     int at;                          // K inside: the chunks' first k in a K-tile; K outside: their first column in the tile
-    int left;                        // K outside: columns of the matrix from the tile's first on
+    int left;                        // rows (K outside: columns) of the matrix from the tile's first on
 
-    // rows: of the matrix from the tile's first on; elements and ld in elements of 2 bytes.
-    __device__ __forceinline__ void locate(const void* p, int64_t first, int64_t ld_, int rows, int wave) {
+    // The K-tile whose loads are next.  The order in which they are multiplied:
+    // each product's last one, where it is not whole, then all whole ones, from
+    // number `first` on and round to it again.  Behind the last, a K-tile moves
+    // nothing (all is out of range), so that the number of loads in flight is
+    // always the same.
+    const uint8_t* from;             // its first row or column
+    int size;                        // bytes from there on that may be read
+    int rem;                         // values of K from there on
+    int kb;                          // its number among the whole ones, of all products
+    int more;                        // K-tiles from this one on
+    bool second;                     // of the second product
+
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t resource() const {
+        return __builtin_amdgcn_make_buffer_rsrc((void*)from, 0, size, kBufferWord3);
+    }
+    __device__ __forceinline__ uint32_t offset(int j) const { return P == 2 && second ? off[P - 1][j] : off[0][j]; }
+    // The same, out of range where the chunk lies past K (K outside: the size sees to that).
+    __device__ __forceinline__ uint32_t offset_in(int j) const { return offset(j) | (INSIDE && at >= rem ? kOutside : 0u); }
+
+    // Load j of the K-tile, straight into LDS.  `part`: it may not be a whole one.
+    __device__ __forceinline__ void load(int j, uint8_t PG_LDS* to, int wave, bool part = false) const {
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(resource(), (void PG_LDS*)(to + (j * T + 64 * wave) * kChunk), 16,
+                                                 part ? offset_in(j) : offset(j), 0, 0, 0);
+    }
+    __device__ __forceinline__ void load_all(uint8_t PG_LDS* to, int wave) const {
+#pragma unroll
+        for (int j = 0; j < L; ++j) load(j, to, wave, true);
+    }
+
+    // K-tile number i of the order.
+    __device__ __forceinline__ void start(int i, int K, int first) {
+        const int whole = K / kDeep, part = K % kDeep, parts = part != 0 ? P : 0;
+        more = parts + P * whole - i;
+        int q = 0, k = whole;
+        rem = part;
+        kb = first;
+        if (i >= parts) {
+            kb = i - parts + first;
+            kb = kb >= P * whole ? kb - P * whole : kb;
+            q = P == 2 && kb >= whole ? 1 : 0;
+            k = q ? kb - whole : kb;
+            rem = kDeep;
+        } else {
+            q = i;
+        }
+        second = q == 1;
+        const int64_t row = second ? ld[P - 1] : ld[0];
+        from = (second ? base[P - 1] : base[0]) + (int64_t)k * (INSIDE ? 128 : kDeep * row);
+        rem = more > 0 ? rem : 0;
+        size = more <= 0 ? 0 : INSIDE ? 0x7fffffff : (int)(rem * row);
+    }
+    // On to the next one, both whole (or behind the last).  Without a branch: one
+    // in the K loop costs some 50 cycles where it is taken (256 x 256 tiles: 2706
+    // cycles a K-tile with three of them, 2460 without).
+    __device__ __forceinline__ void next(int K) {
+        const int whole = K / kDeep;
+        const int64_t row = P == 2 && second ? ld[P - 1] : ld[0];
+        const uint8_t* to = from + (INSIDE ? 128 : kDeep * row);
+        ++kb;
+        --more;
+        if constexpr (P == 2) {
+            second = kb == whole ? true : second;
+            to = kb == whole ? base[P - 1] : to;
+        }
+        const bool round = kb == P * whole;
+        to = round ? base[0] : to;
+        second = round ? false : second;
+        kb = round ? 0 : kb;
+        from = to;
+        size = more > 0 ? (INSIDE ? 0x7fffffff : (int)(kDeep * (P == 2 && second ? ld[P - 1] : ld[0]))) : 0;
+    }
+
+    // Product q's matrix p; elements of 2 bytes, ld_ in elements.
+    __device__ __forceinline__ void locate(int q, const void* p, int64_t first, int64_t ld_, int rows) {
         const int tid = threadIdx.x;
-        ld = ld_ * 2;
+        ld[q] = ld_ * 2;
         left = rows;
         if constexpr (INSIDE) {
-            base = (const uint8_t*)p + first * ld;
+            base[q] = (const uint8_t*)p + first * ld[q];
             const int c = (tid % 8) ^ swz(8, tid / 8);
             at = c * 8;
 #pragma unroll
             for (int j = 0; j < L; ++j) {
                 const int row = (j * T + tid) / 8, r = SPLIT ? (row / 32) * 16 + row % 16 : row;
                 // rows past the matrix read one of it: they only feed sums that are not stored
-                off[j] = (uint32_t)(r < rows ? r : 0) * (uint32_t)ld + c * 16;
+                off[q][j] = (uint32_t)(r < rows ? r : 0) * (uint32_t)ld[q] + c * 16;
             }
         } else {
-            static_assert(INSIDE || !SPLIT, "");
-            base = (const uint8_t*)p + first * 2;
+            base[q] = (const uint8_t*)p + first * 2;
             const int k = tid / CR, c = (tid % CR) ^ swz_rr(DT_F16, ROWS * 2, k);
             at = c * 8;
 #pragma unroll
-            for (int j = 0; j < L; ++j) off[j] = (uint32_t)(j * T / CR + k) * (uint32_t)ld + (c * 8 < rows ? c * 16 : 0);
+            for (int j = 0; j < L; ++j) {
+                const int cj = TURNS && (j & 1) ? c ^ 2 : c;
+                off[q][j] = (uint32_t)(j * T / CR + k) * (uint32_t)ld[q] + (cj * 8 < rows ? cj * 16 : 0);
+            }
         }
     }
 };
 
-template <int XT, int END, bool AIN, bool BIN, bool DIRECT, int BM, int BN, int WM, int WN, int SLOTS, bool SUMS>
+template <int XT, int END, bool AIN, bool BIN, bool DIRECT, int BM, int BN, int WM, int WN, int SA, int SB, int EXTRA>
 struct Tile {
     static constexpr bool SPLIT = END == END_GATED;
+    static constexpr bool SUMS = END == END_WEIGHT && EXTRA != 0;        // of A's rows too
+    static constexpr int P = END == END_LINEAR && EXTRA != 0 ? 2 : 1;    // products
     static constexpr int T = WM * WN * 64;
     static constexpr int WTM = BM / WM, WTN = BN / WN, FM = WTM / 16, FN = WTN / 16;
-    typedef Factor<AIN, BM, T, false> FA;
-    typedef Factor<BIN, BN, T, SPLIT> FB;
+    typedef Factor<AIN, BM, T, false, P> FA;
+    typedef Factor<BIN, BN, T, SPLIT, P> FB;
     static constexpr int LA = FA::L, LB = FB::L, LPT = LA + LB;
-    static constexpr int SLOT = FA::BYTES + FB::BYTES;
-    static constexpr int STRIP_ROW = WTN * 4 + 16, STRIP = 16 * STRIP_ROW;     // fp32, rows padded to other banks
-    static constexpr int LDS = max3(SLOTS * SLOT, WM * WN * STRIP, 0);
+    static constexpr int RING_A = SA * FA::BYTES, RING = RING_A + SB * FB::BYTES;
+    // Loads that may be in flight when K-tile t + 1 has to be there: those of B's
+    // K-tiles t + 2 .. t + SB - 1 and of A's t + 2 .. t + SA - 1.
+    static constexpr int FLYING = (SB - 2) * LB + (SA - 2) * LA;
+    // The ending's parts of LDS: PIECES rows of pieces of each wave at a time, in
+    // fp32, rows padded to other banks.
+    static constexpr int STRIP_ROW = WTN * 4 + 16, PIECES = FM == 8 ? 4 : FM;
+    static constexpr int LDS = max3(RING, WM * WN * PIECES * 16 * STRIP_ROW, 0);
+    static constexpr bool QUADS = FM == 8 && FN == 8;    // one wave per SIMD
     static constexpr int OUTS = SPLIT ? WTN / 2 : WTN;   // a wave's outputs per row
     static_assert(LDS <= kLdsBudget && FM % 2 == 0 && (!SPLIT || FN % 2 == 0), "tile");
-    static_assert(DIRECT || SLOTS == 2, "register-staged K-tiles: two slots");
+    static_assert(!DIRECT ? SA == 2 && SB == 2 : QUADS ? SA == 3 && SB == 2 : SA == SB, "register-staged K-tiles: two slots");
 
     struct State {
         FA a;
         FB b;
         int m0, n0, wave, K, KB, nt;         // nt: K-tiles of all products
-        int product;                         // the one that the factors' places are of
+        int rot;                             // the K-tile that is multiplied first
     };
-
-    __device__ static __forceinline__ void locate(const LinearArgs& p, State& s, int q) {
-        s.product = q;
-        s.a.locate(p.A[q], s.m0, p.lda[q], p.M - s.m0, s.wave);
-        // gated: a load's 8 rows, and all of a wave's loads, belong to one matrix
-        const int w = SPLIT ? (s.wave >> 1) & 1 : q;
-        s.b.locate(p.B[w], s.n0, p.ldb[w], p.N - s.n0, s.wave);
-    }
-
-    // Where K-tile t's loads come from: one past the last moves nothing (all its
-    // offsets are out of range), so that the number in flight is always the same.
-    struct Issue {
-        __amdgpu_buffer_rsrc_t ra, rb;
-        uint32_t outa, outb;                 // K inside: the out-of-range bit for chunks past K
-        int rem;                             // values of K from the K-tile's first on
-        uint8_t PG_LDS* to;
-    };
-    template <class F, bool INSIDE>
-    __device__ static __forceinline__ __amdgpu_buffer_rsrc_t resource(const F& f, int kb, int rem) {
-        int64_t size = rem > 0 ? 0x7fffffff : 0;
-        if constexpr (!INSIDE) size = rem > 0 ? min((int64_t)rem * f.ld, (int64_t)0x7fffffff) : 0;
-        return __builtin_amdgcn_make_buffer_rsrc((void*)(f.base + (int64_t)kb * (INSIDE ? 128 : kDeep * f.ld)), 0, (int)size,
-                                                 kBufferWord3);
-    }
-    __device__ static __forceinline__ Issue start(const LinearArgs& p, State& s, uint8_t PG_LDS* smem, int t, int slot) {
-        if (END == END_LINEAR && t == s.KB && s.product == 0 && p.products == 2) locate(p, s, 1);
-        const int kb = END == END_LINEAR && t >= s.KB && p.products == 2 ? t - s.KB : t;
-        Issue x;
-        x.rem = t < s.nt ? s.K - kb * kDeep : 0;
-        x.ra = resource<FA, AIN>(s.a, kb, x.rem);
-        x.rb = resource<FB, BIN>(s.b, kb, x.rem);
-        x.outa = AIN && s.a.at >= x.rem ? kOutside : 0u;
-        x.outb = BIN && s.b.at >= x.rem ? kOutside : 0u;
-        x.to = smem + slot * SLOT;
-        return x;
-    }
-    // Load q of a K-tile's LPT, straight into LDS.
-    __device__ static __forceinline__ void load(const State& s, const Issue& x, int q) {
-        if (q < LA)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(x.ra, (void PG_LDS*)(x.to + (q * T + 64 * s.wave) * kChunk), 16,
-                                                     s.a.off[q] | x.outa, 0, 0, 0);
-        else
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                x.rb, (void PG_LDS*)(x.to + FA::BYTES + ((q - LA) * T + 64 * s.wave) * kChunk), 16,
-                s.b.off[q - LA] | x.outb, 0, 0, 0);
-    }
 
     // K inside and not a multiple of 8: the values at and past K of the chunk
     // that holds K - 1 become zero (what lies there may be a NaN).
@@ -177,12 +227,17 @@ struct Tile {
             *p = v;
         }
     }
-    __device__ static __forceinline__ bool cut(const State& s, int t) {      // K-tile t has such a chunk
-        return (AIN || BIN) && s.K % 8 != 0 && (t == s.KB - 1 || t == s.nt - 1);
-    }
-    __device__ static __forceinline__ void clear_tail(const State& s, uint8_t PG_LDS* slot) {
-        if constexpr (AIN) clear_rows<BM>(slot, s.K % kDeep);
-        if constexpr (BIN) clear_rows<BN>(slot + FA::BYTES, s.K % kDeep);
+    // ... in the K-tiles in places 0 .. P - 1, once they have landed.
+    template <class PA, class PB>
+    __device__ static __forceinline__ void clear_tails(const State& s, PA tile_a, PB tile_b) {
+        if (!(AIN || BIN) || s.K % 8 == 0) return;
+        wait_loads<0>();
+        barrier();
+#pragma unroll
+        for (int t = 0; t < P; ++t) {
+            if constexpr (AIN) clear_rows<BM>(tile_a(t), s.K % kDeep);
+            if constexpr (BIN) clear_rows<BN>(tile_b(t), s.K % kDeep);
+        }
         barrier();
     }
 
@@ -203,24 +258,21 @@ struct Tile {
         return v;
     }
     template <class F, bool INSIDE>
-    __device__ static __forceinline__ void gather(const F& f, __amdgpu_buffer_rsrc_t r, uint32_t out, int rem, i32x4* v) {
-        const bool ragged = INSIDE ? rem > 0 && rem < kDeep : f.left < F::CR * 8;
+    __device__ static __forceinline__ void gather(const F& f, i32x4* v) {
+        static_assert(!F::TURNS, "one place");
+        const __amdgpu_buffer_rsrc_t r = f.resource();
+        const bool ragged = INSIDE ? f.rem > 0 && f.rem < kDeep : f.left < F::CR * 8;
 #pragma unroll
         for (int j = 0; j < F::L; ++j) {
             // (K outside: a chunk's place past the matrix was moved to its first one, whole or not)
-            if (ragged) v[j] = load_some(r, f.off[j], INSIDE ? rem - f.at : min(f.at < f.left ? f.left - f.at : f.left, 8));
-            else v[j] = __builtin_amdgcn_raw_buffer_load_b128(r, f.off[j] | out, 0, 0);
+            if (ragged) v[j] = load_some(r, f.offset(j), INSIDE ? f.rem - f.at : min(f.at < f.left ? f.left - f.at : f.left, 8));
+            else v[j] = __builtin_amdgcn_raw_buffer_load_b128(r, f.offset_in(j), 0, 0);
         }
     }
-    __device__ static __forceinline__ void gather(const State& s, const Issue& x, i32x4 (&v)[LPT]) {
-        gather<FA, AIN>(s.a, x.ra, x.outa, x.rem, v);
-        gather<FB, BIN>(s.b, x.rb, x.outb, x.rem, v + LA);
-    }
-    __device__ static __forceinline__ void put(const Issue& x, const i32x4 (&v)[LPT]) {
+    template <class F>
+    __device__ static __forceinline__ void put(uint8_t PG_LDS* to, const i32x4* v) {
 #pragma unroll
-        for (int j = 0; j < LA; ++j) *(i32x4 PG_LDS*)(x.to + (j * T + threadIdx.x) * kChunk) = v[j];
-#pragma unroll
-        for (int j = 0; j < LB; ++j) *(i32x4 PG_LDS*)(x.to + FA::BYTES + (j * T + threadIdx.x) * kChunk) = v[LA + j];
+        for (int j = 0; j < F::L; ++j) *(i32x4 PG_LDS*)(to + (j * T + threadIdx.x) * kChunk) = v[j];
     }
 
     // ---- fragments -------------------------------------------------------------------
@@ -276,18 +328,61 @@ struct Tile {
         s.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         s.K = p.K;
         s.KB = (p.K + kDeep - 1) / kDeep;
-        s.nt = END == END_LINEAR ? s.KB * p.products : s.KB;
+        s.nt = s.KB * P;
         int tm, tn;
         place_linear(p, blockIdx.x, tm, tn);
         s.m0 = tm * BM;
         s.n0 = tn * (SPLIT ? BN / 2 : BN);
-        locate(p, s, 0);
+        // With more tiles than one round, XCD x starts at K-tile 9 x.
+        s.rot = gridDim.x > 256 && s.K >= kDeep ? (int)((blockIdx.x & 7) * 9u % (unsigned)(P * (s.K / kDeep))) : 0;
+#pragma unroll
+        for (int q = 0; q < P; ++q) {
+            s.a.locate(q, p.A[q], s.m0, p.lda[q], p.M - s.m0);
+            // gated: a load's 8 rows, and all of a wave's loads, belong to one matrix
+            const int w = SPLIT ? (s.wave >> 1) & 1 : q;
+            s.b.locate(q, p.B[w], s.n0, p.ldb[w], p.N - s.n0);
+        }
         const int wm = s.wave / WN, wn = s.wave % WN;
         RA ra;
         RB rb;
         ra.locate(wm * WTM);
         rb.locate(wn * WTN);
 
+        if constexpr (QUADS) {
+            // (apart to the end: where the two ways met, the sums would be moved before they are there)
+            if (SUMS && tn == 0) run_quads<SUMS>(p, s, smem, ra, rb, wm, wn);
+            else run_quads<false>(p, s, smem, ra, rb, wm, wn);
+        } else {
+            run_rows(p, s, smem, ra, rb, wm, wn, tn == 0);
+        }
+    }
+
+    // Sums of A's rows: products with a fragment of ones, whose every column is
+    // the row's sum.
+    __device__ static __forceinline__ i32x4 ones() {
+        constexpr int two = XT == XT_BF16 ? 0x3f803f80 : 0x3c003c00;
+        return i32x4{two, two, two, two};
+    }
+    // The same in vector instructions (beside matrix instructions in inline assembly,
+    // others in branches made the compiler move their sums): pair e of a
+    // chunk's eight values, added.
+    __device__ static __forceinline__ float add_pair(i32x4 chunk, int e, float sum) {
+        const uint32_t w = (uint32_t)(e == 0 ? chunk[0] : e == 1 ? chunk[1] : e == 2 ? chunk[2] : chunk[3]);
+        if constexpr (XT == XT_BF16) {
+            return sum + __uint_as_float(w << 16) + __uint_as_float(w & 0xffff0000u);
+        } else {
+            typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+            const f16x2 h = __builtin_bit_cast(f16x2, w);
+            return sum + (float)h[0] + (float)h[1];
+        }
+    }
+    __device__ static __forceinline__ void store_sums(const LinearArgs& p, int first, float v) {
+        const int m = first + (threadIdx.x & 15);
+        if ((threadIdx.x & 63) < 16 && m < p.M) p.sums[m] = p.accumulate ? p.sums[m] + v : v;
+    }
+
+    __device__ static __forceinline__ void run_rows(const LinearArgs& p, State& s, uint8_t PG_LDS* smem, const RA& ra, const RB& rb,
+                                                    int wm, int wn, bool first_columns) {
         f32x4 acc[FM][FN], sums[SUMS ? FM : 1];
 #pragma unroll
         for (int i = 0; i < FM; ++i)
@@ -295,33 +390,39 @@ struct Tile {
             for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < (SUMS ? FM : 1); ++i) sums[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        const bool adds = SUMS && tn == 0;
-        const int one = XT == XT_BF16 ? 0x3f803f80 : 0x3c003c00;
-        const i32x4 ones = {one, one, one, one};
-
+        const bool adds = SUMS && first_columns;
+        auto tile_a = [&](int slot) { return smem + slot * FA::BYTES; };
+        auto tile_b = [&](int slot) { return smem + RING_A + slot * FB::BYTES; };
         i32x4 staged[DIRECT ? 1 : LPT];
-        Issue x;
+        auto stage = [&](int t) {
+            s.a.start(t, s.K, s.rot);
+            s.b.start(t, s.K, s.rot);
+            gather<FA, AIN>(s.a, staged);
+            gather<FB, BIN>(s.b, staged + (DIRECT ? 0 : LA));
+        };
         if constexpr (DIRECT) {
 #pragma unroll
-            for (int t = 0; t < SLOTS; ++t) {
-                x = start(p, s, smem, t, t);
-#pragma unroll
-                for (int q = 0; q < LPT; ++q) load(s, x, q);
+            for (int t = 0; t < SB; ++t) {
+                s.a.start(t, s.K, s.rot);
+                s.b.start(t, s.K, s.rot);
+                s.b.load_all(tile_b(t), s.wave);
+                s.a.load_all(tile_a(t), s.wave);
             }
-            wait_loads<(SLOTS - 1) * LPT>();
+            wait_loads<FLYING + LA + LB>();
         } else {
-            x = start(p, s, smem, 0, 0);
-            gather(s, x, staged);
-            put(x, staged);
-            x = start(p, s, smem, 1, 1);
-            gather(s, x, staged);
+            stage(0);
+            put<FA>(tile_a(0), staged);
+            put<FB>(tile_b(0), staged + (DIRECT ? 0 : LA));
+            stage(1);
         }
         barrier();
-        if (DIRECT && cut(s, 0)) clear_tail(s, smem);
+        if constexpr (DIRECT) {
+            clear_tails(s, tile_a, tile_b);
+            s.a.start(SB, s.K, s.rot);
+            s.b.start(SB, s.K, s.rot);
+        }
 
         i32x4 fa[2][2], fb[FN][2];
-        auto tile_a = [&](int slot) { return smem + slot * SLOT; };
-        auto tile_b = [&](int slot) { return smem + slot * SLOT + FA::BYTES; };
 #pragma unroll
         for (int h = 0; h < 2; ++h) fa[0][h] = ra.read(tile_a(0), 0, h);
 #pragma unroll
@@ -330,25 +431,22 @@ struct Tile {
             for (int j = 0; j < FN; ++j) fb[j][h] = rb.read(tile_b(0), j, h);
 
         constexpr bool WAITS = !AIN || !BIN;     // the transposing reads' own waits
-        int slot = 0;
+        int slot_a = 0, slot_b = 0;
         for (int t = 0; t < s.nt; ++t) {
-            const int next = slot + 1 == SLOTS ? 0 : slot + 1;
+            const int next_a = slot_a + 1 == SA ? 0 : slot_a + 1, next_b = slot_b + 1 == SB ? 0 : slot_b + 1;
 #pragma unroll
             for (int i = 0; i < FM; ++i) {
                 if (i + 1 == FM) {
                     // every fragment of K-tile t is read: on to the next one
                     if constexpr (DIRECT) {
-                        wait_loads<(SLOTS - 2) * LPT>();     // K-tile t + 1 has landed (this wave's part)
-                        barrier();                           // ... everyone's, and slot t is free
-                        if (cut(s, t + 1)) clear_tail(s, smem + next * SLOT);
-                        x = start(p, s, smem, t + SLOTS, slot);
+                        wait_loads<FLYING>();                // K-tile t + 1 has landed (this wave's part)
+                        barrier();                           // ... everyone's, and K-tile t's places are free
                     } else {
-                        // (slot `next` was read before the last barrier)
-                        x.to = smem + next * SLOT;
-                        put(x, staged);
+                        // (those of K-tile t + 1 were read before the last barrier)
+                        put<FA>(tile_a(next_a), staged);
+                        put<FB>(tile_b(next_b), staged + (DIRECT ? 0 : LA));
                         barrier();
-                        x = start(p, s, smem, t + 2, slot);
-                        gather(s, x, staged);
+                        stage(t + 2);
                     }
                     __builtin_amdgcn_sched_barrier(0);
                 }
@@ -356,7 +454,7 @@ struct Tile {
                 for (int h = 0; h < 2; ++h) {
                     if constexpr (WAITS) {
                         // the row's fragments have landed; a K-tile's first row: all but B's second halves, then those
-                        if (i == 0 && h == 0) wait_reads<FN * (BIN ? 1 : 2)>();
+                        if (i == 0 && h == 0) wait_reads<(FN * (BIN ? 1 : 2) < 15 ? FN * (BIN ? 1 : 2) : 15)>();
                         else if (h == 0 || i == 0) wait_reads<0>();
                         __builtin_amdgcn_sched_barrier(0);
                     }
@@ -365,30 +463,38 @@ struct Tile {
                         const int u = h * FN + j;
                         acc[i][j] = multiply16<XT>(fb[j][h], fa[i & 1][h], acc[i][j]);
                         if constexpr (SUMS) {
-                            if (adds && j == 0 && i % WN == wn) sums[i] = multiply16<XT>(ones, fa[i & 1][h], sums[i]);
+                            if (adds && j == 0 && i % WN == wn) sums[i] = multiply16<XT>(ones(), fa[i & 1][h], sums[i]);
                         }
                         if (i + 1 < FM) {
                             // the next row's fragments (a K-tile's second row: behind the wait for B's second halves)
                             if (u == (i == 0 ? FN : 0)) {
-                                fa[(i + 1) & 1][0] = ra.read(tile_a(slot), i + 1, 0);
-                                fa[(i + 1) & 1][1] = ra.read(tile_a(slot), i + 1, 1);
+                                fa[(i + 1) & 1][0] = ra.read(tile_a(slot_a), i + 1, 0);
+                                fa[(i + 1) & 1][1] = ra.read(tile_a(slot_a), i + 1, 1);
                             }
                         } else {
                             if (u == 0) {
-                                fa[0][0] = ra.read(tile_a(next), 0, 0);
-                                fa[0][1] = ra.read(tile_a(next), 0, 1);
+                                fa[0][0] = ra.read(tile_a(next_a), 0, 0);
+                                fa[0][1] = ra.read(tile_a(next_a), 0, 1);
                             }
-                            fb[j][h] = rb.read(tile_b(next), j, h);
+                            fb[j][h] = rb.read(tile_b(next_b), j, h);
                             if constexpr (DIRECT) {
 #pragma unroll
-                                for (int q = u * LPT / (2 * FN); q < (u + 1) * LPT / (2 * FN); ++q) load(s, x, q);
+                                for (int q = u * LPT / (2 * FN); q < (u + 1) * LPT / (2 * FN); ++q) {
+                                    if (q < LB) s.b.load(q, tile_b(slot_b), s.wave);
+                                    else s.a.load(q - LB, tile_a(slot_a), s.wave);
+                                }
                             }
                         }
                         __builtin_amdgcn_sched_barrier(0);
                     }
                 }
             }
-            slot = next;
+            if constexpr (DIRECT) {
+                s.a.next(s.K);
+                s.b.next(s.K);
+            }
+            slot_a = next_a;
+            slot_b = next_b;
         }
         wait_loads<0>();                     // no write into LDS outlives the K loop, and no read is in flight
         barrier();
@@ -402,82 +508,255 @@ struct Tile {
         if constexpr (SUMS) {
             if (adds)
 #pragma unroll
-                for (int i = 0; i < FM; ++i) {
-                    // every column of the piece is the row's sum
-                    const int m = s.m0 + wm * WTM + 16 * i + (threadIdx.x & 15);
-                    if (i % WN == wn && (threadIdx.x & 63) < 16 && m < p.M)
-                        p.sums[m] = p.accumulate ? p.sums[m] + sums[i][0] : sums[i][0];
-                }
+                for (int i = 0; i < FM; ++i)
+                    if (i % WN == wn) store_sums(p, s.m0 + wm * WTM + 16 * i, sums[i][0]);
         }
         store(p, s, smem, wm, wn, acc);
     }
 
-    // A wave's sums: 16 rows at a time go through its own strip of LDS and
-    // come back as eight neighbouring columns per lane, whole rows of the
-    // wave's block at a time, for the ending.
+    // ---- 128 x 128 sums per wave, one wave per SIMD -----------------------------------
+    //
+    // The sums fill half of the register file, and both factors' fragments of a
+    // step (32 deep) leave no room for a second set.  So there is one, refilled in
+    // the order in which it is used: a step runs four quadrants of 16 pieces, (A
+    // 0-3, B 0-3), (A 0-3, B 4-7), (A 4-7, B 0-3), (A 4-7, B 4-7).  It reads its
+    // own B 4-7 and A 4-7 under the first, the next step's A 0-3 under the third
+    // and its B 0-3 under the fourth.  The second step of a K-tile waits for the
+    // next K-tile and crosses the barrier behind the first quadrant, when all of
+    // its own reads are done.
+    struct Frags { i32x4 a[8], b[8]; };
+
+    // The fragments that a K-tile starts with have landed, and their registers
+    // are not free before that.
+    __device__ static __forceinline__ void settle(const Frags& f) {
+        if constexpr (!AIN || !BIN) {
+            wait_reads<0>();
+#pragma unroll
+            for (int j = 0; j < 4; ++j) asm volatile("" ::"v"(f.a[j]), "v"(f.b[j]) : "memory");
+        }
+    }
+
+    // The loads of `factor`'s next K-tile go out in units [U0, 64) of the step.
+    template <int H, bool BAR, bool ADDS, class F>
+    __device__ static __forceinline__ void step(State& s, uint8_t PG_LDS* smem, const RA& ra, const RB& rb,
+                                                Frags& f, i32x4 (&acc)[8][8], const uint8_t PG_LDS* a, const uint8_t PG_LDS* b,
+                                                const uint8_t PG_LDS* na, const uint8_t PG_LDS* nb, F& factor,
+                                                uint8_t PG_LDS* to, float (&sums)[ADDS ? 8 : 1]) {
+        constexpr int U0 = BAR ? 16 : 0, NL = F::L;
+        constexpr int PA = AIN ? 1 : 2, PB = BIN ? 1 : 2;    // LDS reads of a fragment
+#pragma unroll
+        for (int u = 0; u < 64; ++u) {
+            const int q = u / 16, i = u % 16;
+            if constexpr (!AIN || !BIN) {
+                if (u == 0) wait_reads<0>();
+                if (!BAR && u == 16) wait_reads<4 * PA < 15 ? 4 * PA : 15>();
+                if (!BAR && u == 32) wait_reads<0>();
+            }
+            const int m = (q >> 1) * 4 + i / 4, n = (q & 1) * 4 + i % 4;
+            multiply16_in_place<XT>(f.b[n], f.a[m], acc[m][n]);
+            if constexpr (ADDS)
+                if (q & 1) sums[m] = add_pair(f.a[m], i % 4, sums[m]);
+            if (q == 0 && (i & 1) == 0) {
+                const int r = i / 2;
+                if (r < 4) f.b[4 + r] = rb.read(b, 4 + r, H);
+                else f.a[r] = ra.read(a, r, H);
+            }
+            if (q == 2 && (i & 3) == 0) f.a[i / 4] = ra.read(na, i / 4, 1 - H);
+            if (q == 3 && i < 4) f.b[i] = rb.read(nb, i, 1 - H);
+            if (u >= U0) {
+                const int j = (u - U0) * NL / (64 - U0);     // at most one load a unit
+                if ((u - U0 + 1) * NL / (64 - U0) > j) factor.load(j, to, s.wave);
+                if (u == 63) factor.next(s.K);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            if (BAR && u == 15) {
+                wait_loads<FLYING>();
+                barrier();
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+    }
+
+    template <bool ADDS>
+    __device__ static __forceinline__ void multiply_quads(State& s, uint8_t PG_LDS* smem, const RA& ra, const RB& rb, Frags& f,
+                                                          i32x4 (&acc)[8][8], float (&sums)[ADDS ? 8 : 1]) {
+        auto tile_a = [&](int slot) { return smem + slot * FA::BYTES; };
+        auto tile_b = [&](int slot) { return smem + RING_A + slot * FB::BYTES; };
+        int slot_a = 0, slot_b = 0;
+        for (int t = 0; t < s.nt; ++t) {
+            const int next_a = slot_a == 2 ? 0 : slot_a + 1, next_b = slot_b ^ 1, prev_a = slot_a == 0 ? 2 : slot_a - 1;
+            asm volatile("s_nop 4" ::: "memory");
+            step<0, false, ADDS>(s, smem, ra, rb, f, acc, tile_a(slot_a), tile_b(slot_b), tile_a(slot_a), tile_b(slot_b), s.a,
+                           tile_a(prev_a), sums);
+            step<1, true, ADDS>(s, smem, ra, rb, f, acc, tile_a(slot_a), tile_b(slot_b), tile_a(next_a), tile_b(next_b), s.b,
+                          tile_b(slot_b), sums);
+            slot_a = next_a;
+            slot_b = next_b;
+        }
+        settle(f);
+    }
+
+    template <bool ADDS>
+    __device__ static __forceinline__ void run_quads(const LinearArgs& p, State& s, uint8_t PG_LDS* smem, const RA& ra, const RB& rb,
+                                                     int wm, int wn) {
+        i32x4 acc[8][8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+        auto tile_a = [&](int slot) { return smem + slot * FA::BYTES; };
+        auto tile_b = [&](int slot) { return smem + RING_A + slot * FB::BYTES; };
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            s.a.start(t, s.K, s.rot);
+            s.b.start(t, s.K, s.rot);
+            s.a.load_all(tile_a(t), s.wave);
+            s.b.load_all(tile_b(t), s.wave);
+        }
+        wait_loads<LA + LB>();
+        barrier();
+        clear_tails(s, tile_a, tile_b);
+        s.a.start(2, s.K, s.rot);
+        s.b.start(2, s.K, s.rot);
+        Frags f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f.a[i] = ra.read(tile_a(0), i, 0);
+            f.b[i] = rb.read(tile_b(0), i, 0);
+        }
+        settle(f);
+        float sums[ADDS ? 8 : 1];
+#pragma unroll
+        for (int i = 0; i < (ADDS ? 8 : 1); ++i) sums[i] = 0.0f;
+        multiply_quads<ADDS>(s, smem, ra, rb, f, acc, sums);
+        asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory");
+        wait_loads<0>();
+        barrier();
+        if constexpr (ADDS) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                // lane (r, g) has added chunk g of each step's row r
+                float v = sums[i] + __shfl_xor(sums[i], 16);
+                v += __shfl_xor(v, 32);
+                if (wn == 0) store_sums(p, s.m0 + wm * WTM + 16 * i, v);
+            }
+        }
+        f32x4 c[8][8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) c[i][j] = __builtin_bit_cast(f32x4, acc[i][j]);
+        store(p, s, smem, wm, wn, c);
+    }
+
+    // A wave's sums go through its own part of LDS, as many rows at a time as fit,
+    // and come back as eight neighbouring columns per lane, whole rows of
+    // the wave's block at a time, for the ending.  A block that lies inside the
+    // matrix takes several passes at a time, without tests, their loads and the next
+    // ones' in flight together; any other goes row by row.  Neither loop is
+    // unrolled further: code that is run once is waited for (256 x 256 tiles at 4096^3,
+    // all of it unrolled: 61000 cycles of a tile's 240000).
     __device__ static __forceinline__ void store(const LinearArgs& p, const State& s, uint8_t PG_LDS* smem, int wm, int wn,
                                                  const f32x4 (&acc)[FM][FN]) {
         const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
-        constexpr int LANES = OUTS / 8, PASS = 64 / LANES, Q = 16 / PASS > 0 ? 16 / PASS : 1;
-        uint8_t PG_LDS* strip = smem + s.wave * STRIP;
+        constexpr int LANES = OUTS / 8, ROWS = 64 / LANES;           // lanes of a row, rows of a pass
+        constexpr int PASSES = PIECES * 16 / ROWS > 0 ? PIECES * 16 / ROWS : 1;
+        // (gated_backward's values of four passes would not fit the registers)
+        constexpr int MOST = END == END_GATED_BACKWARD ? 2 : 4, Q = PASSES < MOST ? PASSES : MOST, GROUPS = PASSES / Q;
+        static_assert(FM % PIECES == 0 && PASSES % Q == 0, "whole parts");
+        uint8_t PG_LDS* part = smem + s.wave * (PIECES * 16 * STRIP_ROW);
         const int row = lane / LANES, c = lane % LANES * 8;
-        const int64_t n = s.n0 + wn * OUTS + c;
+        const int mw = s.m0 + wm * WTM, nw = s.n0 + wn * OUTS;
+        const int64_t n = nw + c;
+        const bool whole = mw + WTM <= p.M && nw + OUTS <= p.N && ROWS <= PIECES * 16;
+        const bool in = n < p.N && row < PIECES * 16;
+        Biases<END> bias;
+        if (in) bias = fetch_biases<XT, END>(p, n);
+        const auto values = [&](int at, float* v, float* u) {
+            const uint8_t PG_LDS* from = part + at * STRIP_ROW + (SPLIT ? c / 16 * 32 + c % 16 : c) * 4;
+            const f32x4 v0 = *(const f32x4 PG_LDS*)from, v1 = *(const f32x4 PG_LDS*)(from + 16);
 #pragma unroll
-        for (int i = 0; i < FM; ++i) {
-            const int64_t m = s.m0 + wm * WTM + 16 * i + row;
-            Beside<XT, END> beside[Q];
+            for (int e = 0; e < 4; ++e) { v[e] = v0[e]; v[4 + e] = v1[e]; }
+            if constexpr (SPLIT) {
+                const f32x4 u0 = *(const f32x4 PG_LDS*)(from + 64), u1 = *(const f32x4 PG_LDS*)(from + 80);
 #pragma unroll
-            for (int q = 0; q < Q; ++q)
-                if (row < 16 && m + q * PASS < p.M && n < p.N) beside[q] = fetch_beside<XT, END>(p, m + q * PASS, n);
+                for (int e = 0; e < 4; ++e) { u[e] = u0[e]; u[4 + e] = u1[e]; }
+            }
+        };
+#pragma unroll 1
+        for (int i0 = 0; i0 < FM; i0 += PIECES) {
+            const int64_t m0 = mw + 16 * i0 + row;
+            Beside<XT, END> beside[Q], next[Q];
+            if (whole) {
 #pragma unroll
-            for (int j = 0; j < FN; ++j) *(f32x4 PG_LDS*)(strip + r * STRIP_ROW + (16 * j + 4 * g) * 4) = acc[i][j];
+                for (int q = 0; q < Q; ++q) next[q] = fetch_beside<XT, END, true>(p, m0 + q * ROWS, n);
+            }
 #pragma unroll
-            for (int q = 0; q < Q; ++q) {
-                if (row >= 16) break;
-                const uint8_t PG_LDS* at = strip + (row + q * PASS) * STRIP_ROW + (SPLIT ? c / 16 * 32 + c % 16 : c) * 4;
-                float v[8], u[8];
-                const f32x4 v0 = *(const f32x4 PG_LDS*)at, v1 = *(const f32x4 PG_LDS*)(at + 16);
-                f32x4 u0 = v0, u1 = v1;
-                if constexpr (SPLIT) {
-                    u0 = *(const f32x4 PG_LDS*)(at + 64);
-                    u1 = *(const f32x4 PG_LDS*)(at + 80);
+            for (int k = 0; k < FM; k += PIECES)
+                if (k == i0)
+#pragma unroll
+                    for (int i = 0; i < PIECES; ++i)
+#pragma unroll
+                        for (int j = 0; j < FN; ++j)
+                            *(f32x4 PG_LDS*)(part + (16 * i + r) * STRIP_ROW + (16 * j + 4 * g) * 4) = acc[k + i][j];
+            if (whole) {
+#pragma unroll 1
+                for (int k = 0; k < GROUPS; ++k) {
+#pragma unroll
+                    for (int q = 0; q < Q; ++q) beside[q] = next[q];
+                    float v[8 * Q], u[8 * Q];
+#pragma unroll
+                    for (int q = 0; q < Q; ++q) values(row + (k * Q + q) * ROWS, v + 8 * q, u + 8 * q);
+                    if (k + 1 < GROUPS) {
+#pragma unroll
+                        for (int q = 0; q < Q; ++q) next[q] = fetch_beside<XT, END, true>(p, m0 + ((k + 1) * Q + q) * ROWS, n);
+                    }
+                    finish<XT, END, true, Q>(p, m0 + k * Q * ROWS, ROWS, n, beside, bias, v, u);
                 }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) { v[e] = v0[e]; v[4 + e] = v1[e]; u[e] = u0[e]; u[4 + e] = u1[e]; }
-                if (m + q * PASS < p.M && n < p.N) finish8<XT, END>(p, m + q * PASS, n, beside[q], v, u);
+            } else {
+#pragma unroll 1
+                for (int q = 0; q < PASSES; ++q) {
+                    const int64_t m = m0 + q * ROWS;
+                    if (!in || m >= p.M) continue;
+                    Beside<XT, END> one[1] = {fetch_beside<XT, END, false>(p, m, n)};
+                    float v[8], u[8];
+                    values(row + q * ROWS, v, u);
+                    finish<XT, END, false, 1>(p, m, 0, n, one, bias, v, u);
+                }
             }
         }
     }
 };
 
-template <int XT, int END, bool AIN, bool BIN, bool DIRECT, int BM, int BN, int WM, int WN, int SLOTS, bool SUMS>
-__global__ void __launch_bounds__(512) linear_tile(LinearArgs p) {
-    typedef Tile<XT, END, AIN, BIN, DIRECT, BM, BN, WM, WN, SLOTS, SUMS> S;
+template <int XT, int END, bool AIN, bool BIN, bool DIRECT, int BM, int BN, int WM, int WN, int SA, int SB, int EXTRA>
+__global__ void __launch_bounds__(WM * WN == 4 && BM == 256 ? 256 : 512) linear_tile(LinearArgs p) {
+    typedef Tile<XT, END, AIN, BIN, DIRECT, BM, BN, WM, WN, SA, SB, EXTRA> S;
     __shared__ __attribute__((aligned(16))) uint8_t smem[S::LDS];
     S::run(p, (uint8_t PG_LDS*)smem);
 }
 
-// The classes of one ending: waves in rows x columns, so that a wave's rows of
-// outputs are as long as they can be.
-template <int XT, int END, bool AIN, bool BIN, bool SUMS>
+// The classes of one ending.  128 and 64 wide: waves in rows x columns, so that a
+// wave's rows of outputs are as long as they can be.  EXTRA: a second product
+// (linear), sums of A's rows (weight gradients).
+template <int XT, int END, bool AIN, bool BIN, int EXTRA>
 const void* linear_by_tile(int tile, bool rows16) {
     constexpr bool G = END == END_GATED;
     switch (tile) {
     case LINEAR_TILE_256:
-        return rows16 ? (const void*)&linear_tile<XT, END, AIN, BIN, true, 256, 256, G ? 4 : 2, G ? 2 : 4, 2, SUMS> : nullptr;
+        return rows16 ? (const void*)&linear_tile<XT, END, AIN, BIN, true, 256, 256, 2, 2, 3, 2, EXTRA> : nullptr;
     case LINEAR_TILE_128:
-        return rows16 ? (const void*)&linear_tile<XT, END, AIN, BIN, true, 128, 128, G ? 4 : 2, G ? 2 : 4, 4, SUMS>
-                      : (const void*)&linear_tile<XT, END, AIN, BIN, false, 128, 128, G ? 4 : 2, G ? 2 : 4, 2, SUMS>;
+        return rows16 ? (const void*)&linear_tile<XT, END, AIN, BIN, true, 128, 128, G ? 4 : 2, G ? 2 : 4, 4, 4, EXTRA>
+                      : (const void*)&linear_tile<XT, END, AIN, BIN, false, 128, 128, G ? 4 : 2, G ? 2 : 4, 2, 2, EXTRA>;
     case LINEAR_TILE_64:
-        return rows16 ? (const void*)&linear_tile<XT, END, AIN, BIN, true, 64, 64, 2, 2, 4, SUMS>
-                      : (const void*)&linear_tile<XT, END, AIN, BIN, false, 64, 64, 2, 2, 2, SUMS>;
+        return rows16 ? (const void*)&linear_tile<XT, END, AIN, BIN, true, 64, 64, 2, 2, 4, 4, EXTRA>
+                      : (const void*)&linear_tile<XT, END, AIN, BIN, false, 64, 64, 2, 2, 2, 2, EXTRA>;
     default: return nullptr;
     }
 }
-template <int END, bool AIN, bool BIN, bool SUMS>
+template <int END, bool AIN, bool BIN, int EXTRA>
 const void* linear_by_type(int xt, int tile, bool rows16) {
-    return xt == XT_BF16 ? linear_by_tile<XT_BF16, END, AIN, BIN, SUMS>(tile, rows16)
-                         : linear_by_tile<XT_F16, END, AIN, BIN, SUMS>(tile, rows16);
+    return xt == XT_BF16 ? linear_by_tile<XT_BF16, END, AIN, BIN, EXTRA>(tile, rows16)
+                         : linear_by_tile<XT_F16, END, AIN, BIN, EXTRA>(tile, rows16);
 }
 
 }  // namespace pg

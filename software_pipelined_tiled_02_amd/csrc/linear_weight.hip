@@ -4,8 +4,8 @@
 namespace pg {
 
 const void* weight_gradient_kernel(int xt, int tile, bool rows16, bool sums) {
-    return sums ? linear_by_type<END_WEIGHT, false, false, true>(xt, tile, rows16)
-                : linear_by_type<END_WEIGHT, false, false, false>(xt, tile, rows16);
+    return sums ? linear_by_type<END_WEIGHT, false, false, 1>(xt, tile, rows16)
+                : linear_by_type<END_WEIGHT, false, false, 0>(xt, tile, rows16);
 }
 
 }  // namespace pg

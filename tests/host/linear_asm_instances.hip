@@ -3,11 +3,12 @@
 
 namespace pg {
 
-const void* instances(int t, bool r16, bool rr, bool backward, bool sums) {
-    if (rr) return linear_by_tile<XT_BF16, END_LINEAR, true, false, false>(t, r16);
-    if (backward) return linear_by_tile<XT_F16, END_GATED_BACKWARD, true, false, false>(t, r16);
-    if (sums) return linear_by_tile<XT_BF16, END_WEIGHT, false, false, true>(t, r16);
-    return linear_by_tile<XT_F16, END_WEIGHT, false, false, false>(t, r16);
+const void* instances(int t, bool r16, bool rr, bool backward, bool sums, bool pair) {
+    if (pair) return linear_by_tile<XT_F16, END_LINEAR, true, false, 1>(t, r16);
+    if (rr) return linear_by_tile<XT_BF16, END_LINEAR, true, false, 0>(t, r16);
+    if (backward) return linear_by_tile<XT_F16, END_GATED_BACKWARD, true, false, 0>(t, r16);
+    if (sums) return linear_by_tile<XT_BF16, END_WEIGHT, false, false, 1>(t, r16);
+    return linear_by_tile<XT_F16, END_WEIGHT, false, false, 0>(t, r16);
 }
 
 }  // namespace pg
