@@ -494,14 +494,20 @@ int64_t gemm_rms_backward_workspace(int64_t M, int64_t D);
  * stated.  Sizes of zero are accepted.  Errors: GEMM_ERR_INVALID_ARG (NULL, a
  * negative size, an unknown type, a leading dimension below the row's length),
  * GEMM_ERR_ALIGNMENT (a pointer not aligned to its elements; a tile class asked
- * for that needs rows on 16 bytes), GEMM_ERR_UNSUPPORTED (256 rows of a factor
+ * for that needs rows on 16 bytes), GEMM_ERR_UNSUPPORTED (a tile class that the
+ * operator does not have; 256 rows of a factor
  * with K along its rows, or 64 of one with K across them, that span 2^31 bytes;
  * 2^32 threads), GEMM_ERR_HIP. */
 enum { GEMM_ACT_NONE = 0, GEMM_ACT_RELU = 1, GEMM_ACT_GELU = 2, GEMM_ACT_GELU_TANH = 3, GEMM_ACT_SILU = 4 };
 
 /* Part of the sums that one workgroup computes (gated: half of its columns are
- * the second product's).  GEMM_LINEAR_TILE_AUTO: chosen by the call's sizes. */
-enum { GEMM_LINEAR_TILE_AUTO = -1, GEMM_LINEAR_TILE_256x256 = 0, GEMM_LINEAR_TILE_128x128 = 1, GEMM_LINEAR_TILE_64x64 = 2 };
+ * the second product's).  From 64x64_K4 on each wave takes parts of K of its
+ * own; these, 256x256 and 128x256 need rows on 16 bytes.  Weight gradients have
+ * those down to 32x32, gated layers those down to 16x32.  GEMM_LINEAR_TILE_AUTO: chosen by
+ * the call's sizes. */
+enum { GEMM_LINEAR_TILE_AUTO = -1, GEMM_LINEAR_TILE_256x256 = 0, GEMM_LINEAR_TILE_128x256 = 1, GEMM_LINEAR_TILE_128x128 = 2,
+       GEMM_LINEAR_TILE_64x64 = 3, GEMM_LINEAR_TILE_64x64_K4 = 4, GEMM_LINEAR_TILE_64x32 = 5, GEMM_LINEAR_TILE_32x32 = 6,
+       GEMM_LINEAR_TILE_16x32 = 7, GEMM_LINEAR_TILE_16x16 = 8 };
 
 enum { GEMM_FORM_LINEAR_RC = 0, GEMM_FORM_LINEAR_RR = 1, GEMM_FORM_GATED = 2, GEMM_FORM_GATED_BACKWARD = 3,
        GEMM_FORM_WEIGHT_GRADIENT = 4 };

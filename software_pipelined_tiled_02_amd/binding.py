@@ -35,7 +35,8 @@ FP8_TILES = {"auto": -1, "256x256": 0, "256x128": 1, "128x128": 2, "64x64": 3, "
 FP8_BLOCK = 128   # values of a row that share a scale
 BLOCK_ROWS = {"row": 1, "tile": FP8_BLOCK}
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
-LINEAR_TILES = {"auto": -1, "256x256": 0, "128x128": 1, "64x64": 2}
+LINEAR_TILES = {"auto": -1, "256x256": 0, "128x256": 1, "128x128": 2, "64x64": 3, "64x64k4": 4, "64x32": 5, "32x32": 6,
+                "16x32": 7, "16x16": 8}
 LINEAR_FORMS = {"linear_rc": 0, "linear_rr": 1, "gated": 2, "gated_backward": 3, "weight_gradient": 4}
 
 # C functions exported by the library (the names include/pipegemm.h declares)

@@ -64,14 +64,14 @@ int plan_sums(int form, int64_t M, int64_t N, int64_t K, int dtype, bool r16, bo
     int tc = tile;
     if (tc == GEMM_LINEAR_TILE_AUTO) {
         tc = pg::LINEAR_TILE_64;
-        for (int t = 0; t < pg::LINEAR_TILE_COUNT; ++t)
+        for (int t = 0; t <= pg::LINEAR_TILE_64; ++t)
             if (kernel(form, dtype, t, r16, extra) != nullptr && tiles(t) >= num_cus) {
                 tc = t;
                 break;
             }
     }
     plan->fn = kernel(form, dtype, tc, r16, extra);
-    if (plan->fn == nullptr) return GEMM_ERR_ALIGNMENT;
+    if (plan->fn == nullptr) return kernel(form, dtype, tc, true, extra) == nullptr ? GEMM_ERR_UNSUPPORTED : GEMM_ERR_ALIGNMENT;
     const pg::LinearShape sh = pg::linear_shape(tc);
     const bool any = M > 0 && N > 0;
     plan->tiles_m = any ? ceil_div(M, sh.bm) : 0;

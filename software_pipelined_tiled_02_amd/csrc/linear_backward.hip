@@ -1,10 +1,20 @@
 // linear_backward.hip -- the gradients of an activation's or a gate's arguments.
-#include "linear_tile.h"
+#include "linear_few.h"
 
 namespace pg {
 
+namespace {
+
+template <int END, bool AIN, bool BIN, int EXTRA>
+const void* kernel(int xt, int tile, bool rows16) {
+    if (linear_few_tile(tile)) return rows16 ? few_by_type<END, AIN, BIN, EXTRA>(xt, tile) : nullptr;
+    return linear_by_type<END, AIN, BIN, EXTRA>(xt, tile, rows16);
+}
+
+}  // namespace
+
 const void* gated_backward_kernel(int xt, int tile, bool rows16) {
-    return linear_by_type<END_GATED_BACKWARD, true, false, 0>(xt, tile, rows16);
+    return kernel<END_GATED_BACKWARD, true, false, 0>(xt, tile, rows16);
 }
 
 }  // namespace pg

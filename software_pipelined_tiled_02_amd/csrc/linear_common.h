@@ -39,15 +39,28 @@ struct LinearArgs {
 };
 
 // Tile classes: the workgroup's part of the sums (gated: half of the columns are
-// the second product's), and its waves.
-enum LinearTile : int { LINEAR_TILE_256 = 0, LINEAR_TILE_128 = 1, LINEAR_TILE_64 = 2, LINEAR_TILE_COUNT = 3 };
+// the second product's), and its waves.  From 64K4 on each wave takes K-tiles of
+// its own.
+enum LinearTile : int { LINEAR_TILE_256 = 0, LINEAR_TILE_128x256 = 1, LINEAR_TILE_128 = 2, LINEAR_TILE_64 = 3,
+                        LINEAR_TILE_64K4 = 4, LINEAR_TILE_64x32 = 5, LINEAR_TILE_32 = 6, LINEAR_TILE_16x32 = 7,
+                        LINEAR_TILE_16 = 8, LINEAR_TILE_COUNT = 9 };
 struct LinearShape { int bm, bn, waves; };
 constexpr LinearShape linear_shape(int t) {
-    return t == LINEAR_TILE_256 ? LinearShape{256, 256, 4} : t == LINEAR_TILE_128 ? LinearShape{128, 128, 8} : LinearShape{64, 64, 4};
+    return t == LINEAR_TILE_256 ? LinearShape{256, 256, 4}
+         : t == LINEAR_TILE_128x256 ? LinearShape{128, 256, 4}
+         : t == LINEAR_TILE_128 ? LinearShape{128, 128, 4}
+         : t == LINEAR_TILE_64 ? LinearShape{64, 64, 4}
+         : t == LINEAR_TILE_64K4 ? LinearShape{64, 64, 4}
+         : t == LINEAR_TILE_64x32 ? LinearShape{64, 32, 4}
+         : t == LINEAR_TILE_32 ? LinearShape{32, 32, 8}
+         : t == LINEAR_TILE_16x32 ? LinearShape{16, 32, 8}
+                                  : LinearShape{16, 16, 8};
 }
+constexpr bool linear_few_tile(int t) { return t >= LINEAR_TILE_64K4; }
 
-// The kernel for a call: XT_F16 or XT_BF16, a tile class, and whether all
-// rows of the factors start on 16 bytes (NULL: the class needs that).
+// The kernel for a call: XT_F16 or XT_BF16, a tile class, whether all rows of
+// the factors start on 16 bytes (NULL: the class needs that), and a second
+// product (linear) or sums of A's rows (weight gradients).
 const void* linear_rc_kernel(int xt, int tile, bool rows16, bool pair);
 const void* linear_rr_kernel(int xt, int tile, bool rows16, bool pair);
 const void* gated_kernel(int xt, int tile, bool rows16);

@@ -1,8 +1,18 @@
 // linear_gated.hip -- gated layers: two products of one input.
-#include "linear_tile.h"
+#include "linear_few.h"
 
 namespace pg {
 
-const void* gated_kernel(int xt, int tile, bool rows16) { return linear_by_type<END_GATED, true, true, 0>(xt, tile, rows16); }
+namespace {
+
+template <int END, bool AIN, bool BIN, int EXTRA>
+const void* kernel(int xt, int tile, bool rows16) {
+    if (linear_few_tile(tile)) return rows16 ? few_by_type<END, AIN, BIN, EXTRA>(xt, tile) : nullptr;
+    return linear_by_type<END, AIN, BIN, EXTRA>(xt, tile, rows16);
+}
+
+}  // namespace
+
+const void* gated_kernel(int xt, int tile, bool rows16) { return kernel<END_GATED, true, true, 0>(xt, tile, rows16); }
 
 }  // namespace pg

@@ -9,12 +9,9 @@
 // one 16-byte read per lane; K outside, as 64 rows of the tile's width, and
 // the same fragment is two of gfx950's transposing reads.
 //
-// The K loop goes through rings of SA K-tiles of A and SB of B.  A K-tile is
-// multiplied row of pieces by row of pieces (16 x 16 each).  Once the last row's
-// fragments are in registers the wave waits for the next K-tile and crosses the
-// one barrier; under the last row's matrix instructions it reads the next
-// K-tile's first fragments, and starts the loads that take the places of the one
-// it has read: of B SB K-tiles on, then of A SA K-tiles on.
+// The K loop goes through rings of SA K-tiles of A and SB of B, with one barrier a
+// K-tile, in which each wave reads its fragments behind matrix instructions of the
+// fragments before.
 #ifndef PIPEGEMM_LINEAR_TILE_H
 #define PIPEGEMM_LINEAR_TILE_H
 
@@ -64,25 +61,44 @@ __device__ __forceinline__ void place_linear(const LinearArgs& a, int tile, int&
     tn = in / rows;
 }
 
+// Swizzle of a K-tile whose factor has K outside: row k (of `row_bytes`) has its
+// 16-byte chunk c in place c ^ out_swz.  A clock of the transposing read takes 32
+// bytes of rows 0-3 and of rows 8-11 (of each 16); rows of 256 bytes or more all
+// start in one bank, of which these 8 pieces have to fill all 64 (tile_layout.h has
+// the probe's figures): bits 0, 1 and 3 of k move a piece.  Shorter rows start
+// 128 or 64 bytes apart, and need fewer of them.
+constexpr int out_swz(int row_bytes, int k) {
+    return row_bytes >= 256 ? swz_rr(DT_F16, row_bytes, k)
+         : row_bytes == 128 ? ((k >> 1) & 1) * 4 ^ ((k >> 3) & 1) * 2
+         : row_bytes == 64  ? ((k >> 3) & 1) * 2
+                            : 0;
+}
+
 // One factor's part of a tile: ROWS rows (of A, or of B's transpose), staged by
-// T threads.  INSIDE: K along the rows.  SPLIT: rows 0-15 of each 32 belong to
-// the first of two matrices, rows 16-31 to the second (gated).
+// T threads (64: a wave by itself).  INSIDE: K along the rows.  SPLIT: rows 0-15
+// of each 32 belong to the first of two matrices, rows 16-31 to the second
+// (gated): a load's 8 rows belong to one, and so do all of a wave's where several
+// waves share the loads.
 template <bool INSIDE, int ROWS, int T, bool SPLIT, int P>
 struct Factor {
     static constexpr int L = ROWS * 8 / T;               // chunks of 16 bytes per lane and K-tile
     static constexpr int BYTES = ROWS * 128;
     static constexpr int CR = ROWS / 8;                  // K outside: chunks of a row
     static_assert(ROWS * 8 % T == 0 && L >= 1, "whole chunks per lane");
-    // A lane's chunks have one place in the swizzle's period, or (256 wide, K
-    // outside, 256 threads: 8 rows of K apart) two in turn, 2 chunks apart.
-    static constexpr bool TURNS = !INSIDE && T % (16 * CR) != 0;
-    static_assert(INSIDE ? T % 128 == 0 : T % (8 * CR) == 0, "places in the swizzle's period");
+    // A lane's chunks have one place in the swizzle's period of 16 rows, or (loads 8
+    // rows apart) two in turn, 2 chunks apart.
+    static constexpr bool TURNS = INSIDE ? T % 128 != 0 : T % (16 * CR) != 0;
+    static_assert(INSIDE ? T % 64 == 0 : T % (8 * CR) == 0, "places in the swizzle's period");
+    static_assert((swz(8, 0) ^ swz(8, 8)) == 2 && (swz(8, 7) ^ swz(8, 15)) == 2, "the swizzle's row bit 3");
+    static constexpr bool BOTH = SPLIT && T == 64;       // loads of the two matrices in turn
 
     const uint8_t* base[P];          // this wave's matrix of each product, at the tile's first row (column), k = 0
     int64_t ld[P];                   // bytes from row to row
     uint32_t off[P][L];              // a lane's chunks
     int at;                          // K inside: the chunks' first k in a K-tile; K outside: their first column in the tile
     int left;                        // rows (K outside: columns) of the matrix from the tile's first on
+    const uint8_t* base_u;           // BOTH: of the second matrix
+    const uint8_t* from_u;
 
     // The K-tile whose loads are next.  The order in which they are multiplied:
     // each product's last one, where it is not whole, then all whole ones, from
@@ -101,11 +117,15 @@ struct Factor {
     }
     __device__ __forceinline__ uint32_t offset(int j) const { return P == 2 && second ? off[P - 1][j] : off[0][j]; }
     // The same, out of range where the chunk lies past K (K outside: the size sees to that).
-    __device__ __forceinline__ uint32_t offset_in(int j) const { return offset(j) | (INSIDE && at >= rem ? kOutside : 0u); }
+    __device__ __forceinline__ uint32_t offset_in(int j) const {
+        return offset(j) | (INSIDE && (TURNS && (j & 1) ? at ^ 16 : at) >= rem ? kOutside : 0u);
+    }
 
     // Load j of the K-tile, straight into LDS.  `part`: it may not be a whole one.
     __device__ __forceinline__ void load(int j, uint8_t PG_LDS* to, int wave, bool part = false) const {
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(resource(), (void PG_LDS*)(to + (j * T + 64 * wave) * kChunk), 16,
+        const __amdgpu_buffer_rsrc_t r =
+            __builtin_amdgcn_make_buffer_rsrc((void*)(BOTH && ((j >> 1) & 1) ? from_u : from), 0, size, kBufferWord3);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (void PG_LDS*)(to + (j * T + 64 * wave) * kChunk), 16,
                                                  part ? offset_in(j) : offset(j), 0, 0, 0);
     }
     __device__ __forceinline__ void load_all(uint8_t PG_LDS* to, int wave) const {
@@ -134,6 +154,7 @@ struct Factor {
         from = (second ? base[P - 1] : base[0]) + (int64_t)k * (INSIDE ? 128 : kDeep * row);
         rem = more > 0 ? rem : 0;
         size = more <= 0 ? 0 : INSIDE ? 0x7fffffff : (int)(rem * row);
+        if constexpr (BOTH) from_u = base_u + (int64_t)k * 128;
     }
     // On to the next one, both whole (or behind the last).  Without a branch: one
     // in the K loop costs some 50 cycles where it is taken (256 x 256 tiles: 2706
@@ -156,24 +177,27 @@ struct Factor {
         size = more > 0 ? (INSIDE ? 0x7fffffff : (int)(kDeep * (P == 2 && second ? ld[P - 1] : ld[0]))) : 0;
     }
 
-    // Product q's matrix p; elements of 2 bytes, ld_ in elements.
-    __device__ __forceinline__ void locate(int q, const void* p, int64_t first, int64_t ld_, int rows) {
-        const int tid = threadIdx.x;
+    // Product q's matrix p; elements of 2 bytes, ld_ in elements.  tid: of T.
+    // BOTH: p_u, ld_u are the second matrix's.
+    __device__ __forceinline__ void locate(int tid, int q, const void* p, int64_t first, int64_t ld_, int rows,
+                                           const void* p_u = nullptr, int64_t ld_u = 0) {
         ld[q] = ld_ * 2;
         left = rows;
         if constexpr (INSIDE) {
             base[q] = (const uint8_t*)p + first * ld[q];
+            if constexpr (BOTH) base_u = (const uint8_t*)p_u + first * ld_u * 2;
             const int c = (tid % 8) ^ swz(8, tid / 8);
             at = c * 8;
 #pragma unroll
             for (int j = 0; j < L; ++j) {
                 const int row = (j * T + tid) / 8, r = SPLIT ? (row / 32) * 16 + row % 16 : row;
+                const int64_t step = BOTH && ((j >> 1) & 1) ? ld_u * 2 : ld[q];
                 // rows past the matrix read one of it: they only feed sums that are not stored
-                off[q][j] = (uint32_t)(r < rows ? r : 0) * (uint32_t)ld[q] + c * 16;
+                off[q][j] = (uint32_t)(r < rows ? r : 0) * (uint32_t)step + (TURNS && (j & 1) ? c ^ 2 : c) * 16;
             }
         } else {
             base[q] = (const uint8_t*)p + first * 2;
-            const int k = tid / CR, c = (tid % CR) ^ swz_rr(DT_F16, ROWS * 2, k);
+            const int k = tid / CR, c = (tid % CR) ^ out_swz(ROWS * 2, k);
             at = c * 8;
 #pragma unroll
             for (int j = 0; j < L; ++j) {
@@ -183,6 +207,79 @@ struct Factor {
         }
     }
 };
+
+// Lane (r = lane % 16, g = lane / 16) of a fragment holds row r and values
+// 8 g .. + 7 of its 32 deep.  K inside: `lane[h]` is that chunk's offset in
+// 16 rows, at depth 32 h.  K outside: `lane[i]` is the offset of what the
+// lane hands to the first transposing read of fragment i: 4 columns of row
+// 8 g + (lane % 16) / 4; the second read is 4 rows on.
+template <bool INSIDE, int ROWS, int F>
+struct Reader {
+    static constexpr int N = INSIDE ? 2 : F;
+    uint32_t lane[N];
+    __device__ __forceinline__ void locate(int first) {      // the wave's first row of the tile
+        const int l = threadIdx.x & 63, r = l & 15, g = l >> 4;
+        if constexpr (INSIDE) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) lane[h] = (uint32_t)((first + r) * 8 + ((4 * h + g) ^ swz(8, r))) * kChunk;
+        } else {
+            const int k = rr_lane_k(DT_F16, true, l);
+#pragma unroll
+            for (int i = 0; i < F; ++i) {
+                const int n = first + 16 * i + rr_lane_n(DT_F16, true, l);
+                lane[i] = (uint32_t)(k * ROWS * 2 + ((n / 8) ^ out_swz(ROWS * 2, k)) * kChunk + n % 8 * 2);
+            }
+        }
+    }
+    __device__ __forceinline__ i32x4 read(const uint8_t PG_LDS* rows, int i, int h) const {
+        if constexpr (INSIDE) {
+            return *(const i32x4 PG_LDS*)(rows + lane[h] + i * 16 * 128);
+        } else {
+            // Inline assembly: behind loads into LDS the compiler drains every
+            // load before a transposing read, which it cannot tell apart from
+            // them.  It does not see these reads' latency either, so the loop
+            // waits for them itself.
+            const uint32_t p = (uint32_t)(uintptr_t)(rows + lane[i]);
+            i32x2 lo, hi;
+            if (h == 0)
+                asm volatile("ds_read_b64_tr_b16 %0, %2\n\tds_read_b64_tr_b16 %1, %2 offset:%3"
+                             : "=&v"(lo), "=&v"(hi) : "v"(p), "i"(4 * ROWS * 2) : "memory");
+            else
+                asm volatile("ds_read_b64_tr_b16 %0, %2 offset:%3\n\tds_read_b64_tr_b16 %1, %2 offset:%4"
+                             : "=&v"(lo), "=&v"(hi) : "v"(p), "i"(32 * ROWS * 2), "i"(36 * ROWS * 2) : "memory");
+            return i32x4{lo[0], lo[1], hi[0], hi[1]};
+        }
+    }
+};
+
+// K inside and not a multiple of 8: the values at and past K of the chunk
+// that holds K - 1 become zero (what lies there may be a NaN).
+template <int ROWS, int T>
+__device__ __forceinline__ void clear_rows(int tid, uint8_t PG_LDS* rows, int k) {
+    const int c = k / 8, keep = k % 8;
+    for (int row = tid; row < ROWS; row += T) {
+        i32x4 PG_LDS* p = (i32x4 PG_LDS*)(rows + (row * 8 + (c ^ swz(8, row))) * kChunk);
+        i32x4 v = *p;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) v[w] = keep >= 2 * w + 2 ? v[w] : keep == 2 * w + 1 ? v[w] & 0xffff : 0;
+        *p = v;
+    }
+}
+
+// Sums of A's rows in vector instructions: pair e of a chunk's eight values, added.
+// (Beside matrix instructions in inline assembly others, in branches, made the
+// compiler move their sums.)
+template <int XT>
+__device__ __forceinline__ float add_pair(i32x4 chunk, int e, float sum) {
+    const uint32_t w = (uint32_t)(e == 0 ? chunk[0] : e == 1 ? chunk[1] : e == 2 ? chunk[2] : chunk[3]);
+    if constexpr (XT == XT_BF16) {
+        return sum + __uint_as_float(w << 16) + __uint_as_float(w & 0xffff0000u);
+    } else {
+        typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+        const f16x2 h = __builtin_bit_cast(f16x2, w);
+        return sum + (float)h[0] + (float)h[1];
+    }
+}
 
 template <int XT, int END, bool AIN, bool BIN, bool DIRECT, int BM, int BN, int WM, int WN, int SA, int SB, int EXTRA>
 struct Tile {
@@ -214,20 +311,7 @@ struct Tile {
         int rot;                             // the K-tile that is multiplied first
     };
 
-    // K inside and not a multiple of 8: the values at and past K of the chunk
-    // that holds K - 1 become zero (what lies there may be a NaN).
-    template <int ROWS>
-    __device__ static __forceinline__ void clear_rows(uint8_t PG_LDS* rows, int k) {
-        const int c = k / 8, keep = k % 8;
-        for (int row = threadIdx.x; row < ROWS; row += T) {
-            i32x4 PG_LDS* p = (i32x4 PG_LDS*)(rows + (row * 8 + (c ^ swz(8, row))) * kChunk);
-            i32x4 v = *p;
-#pragma unroll
-            for (int w = 0; w < 4; ++w) v[w] = keep >= 2 * w + 2 ? v[w] : keep == 2 * w + 1 ? v[w] & 0xffff : 0;
-            *p = v;
-        }
-    }
-    // ... in the K-tiles in places 0 .. P - 1, once they have landed.
+    // What clear_rows clears, in the K-tiles in places 0 .. P - 1, once they have landed.
     template <class PA, class PB>
     __device__ static __forceinline__ void clear_tails(const State& s, PA tile_a, PB tile_b) {
         if (!(AIN || BIN) || s.K % 8 == 0) return;
@@ -235,8 +319,8 @@ struct Tile {
         barrier();
 #pragma unroll
         for (int t = 0; t < P; ++t) {
-            if constexpr (AIN) clear_rows<BM>(tile_a(t), s.K % kDeep);
-            if constexpr (BIN) clear_rows<BN>(tile_b(t), s.K % kDeep);
+            if constexpr (AIN) clear_rows<BM, T>(threadIdx.x, tile_a(t), s.K % kDeep);
+            if constexpr (BIN) clear_rows<BN, T>(threadIdx.x, tile_b(t), s.K % kDeep);
         }
         barrier();
     }
@@ -277,49 +361,6 @@ struct Tile {
 
     // ---- fragments -------------------------------------------------------------------
 
-    // Lane (r = lane % 16, g = lane / 16) of a fragment holds row r and values
-    // 8 g .. + 7 of its 32 deep.  K inside: `lane[h]` is that chunk's offset in
-    // 16 rows, at depth 32 h.  K outside: `lane[i]` is the offset of what the
-    // lane hands to the first transposing read of fragment i: 4 columns of row
-    // 8 g + (lane % 16) / 4; the second read is 4 rows on.
-    template <bool INSIDE, int ROWS, int F>
-    struct Reader {
-        static constexpr int N = INSIDE ? 2 : F;
-        uint32_t lane[N];
-        __device__ __forceinline__ void locate(int first) {      // the wave's first row of the tile
-            const int l = threadIdx.x & 63, r = l & 15, g = l >> 4;
-            if constexpr (INSIDE) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) lane[h] = (uint32_t)((first + r) * 8 + ((4 * h + g) ^ swz(8, r))) * kChunk;
-            } else {
-                const int k = rr_lane_k(DT_F16, true, l);
-#pragma unroll
-                for (int i = 0; i < F; ++i) {
-                    const int n = first + 16 * i + rr_lane_n(DT_F16, true, l);
-                    lane[i] = (uint32_t)(k * ROWS * 2 + ((n / 8) ^ swz_rr(DT_F16, ROWS * 2, k)) * kChunk + n % 8 * 2);
-                }
-            }
-        }
-        __device__ __forceinline__ i32x4 read(const uint8_t PG_LDS* rows, int i, int h) const {
-            if constexpr (INSIDE) {
-                return *(const i32x4 PG_LDS*)(rows + lane[h] + i * 16 * 128);
-            } else {
-                // Inline assembly: behind loads into LDS the compiler drains every
-                // load before a transposing read, which it cannot tell apart from
-                // them.  It does not see these reads' latency either, so the loop
-                // waits for them itself.
-                const uint32_t p = (uint32_t)(uintptr_t)(rows + lane[i]);
-                i32x2 lo, hi;
-                if (h == 0)
-                    asm volatile("ds_read_b64_tr_b16 %0, %2\n\tds_read_b64_tr_b16 %1, %2 offset:%3"
-                                 : "=&v"(lo), "=&v"(hi) : "v"(p), "i"(4 * ROWS * 2) : "memory");
-                else
-                    asm volatile("ds_read_b64_tr_b16 %0, %2 offset:%3\n\tds_read_b64_tr_b16 %1, %2 offset:%4"
-                                 : "=&v"(lo), "=&v"(hi) : "v"(p), "i"(32 * ROWS * 2), "i"(36 * ROWS * 2) : "memory");
-                return i32x4{lo[0], lo[1], hi[0], hi[1]};
-            }
-        }
-    };
     typedef Reader<AIN, BM, FM> RA;
     typedef Reader<BIN, BN, FN> RB;
 
@@ -337,10 +378,10 @@ struct Tile {
         s.rot = gridDim.x > 256 && s.K >= kDeep ? (int)((blockIdx.x & 7) * 9u % (unsigned)(P * (s.K / kDeep))) : 0;
 #pragma unroll
         for (int q = 0; q < P; ++q) {
-            s.a.locate(q, p.A[q], s.m0, p.lda[q], p.M - s.m0);
+            s.a.locate(threadIdx.x, q, p.A[q], s.m0, p.lda[q], p.M - s.m0);
             // gated: a load's 8 rows, and all of a wave's loads, belong to one matrix
             const int w = SPLIT ? (s.wave >> 1) & 1 : q;
-            s.b.locate(q, p.B[w], s.n0, p.ldb[w], p.N - s.n0);
+            s.b.locate(threadIdx.x, q, p.B[w], s.n0, p.ldb[w], p.N - s.n0);
         }
         const int wm = s.wave / WN, wn = s.wave % WN;
         RA ra;
@@ -353,7 +394,7 @@ struct Tile {
             if (SUMS && tn == 0) run_quads<SUMS>(p, s, smem, ra, rb, wm, wn);
             else run_quads<false>(p, s, smem, ra, rb, wm, wn);
         } else {
-            run_rows(p, s, smem, ra, rb, wm, wn, tn == 0);
+            run_steps(p, s, smem, ra, rb, wm, wn, tn == 0);
         }
     }
 
@@ -363,155 +404,172 @@ struct Tile {
         constexpr int two = XT == XT_BF16 ? 0x3f803f80 : 0x3c003c00;
         return i32x4{two, two, two, two};
     }
-    // The same in vector instructions (beside matrix instructions in inline assembly,
-    // others in branches made the compiler move their sums): pair e of a
-    // chunk's eight values, added.
-    __device__ static __forceinline__ float add_pair(i32x4 chunk, int e, float sum) {
-        const uint32_t w = (uint32_t)(e == 0 ? chunk[0] : e == 1 ? chunk[1] : e == 2 ? chunk[2] : chunk[3]);
-        if constexpr (XT == XT_BF16) {
-            return sum + __uint_as_float(w << 16) + __uint_as_float(w & 0xffff0000u);
-        } else {
-            typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
-            const f16x2 h = __builtin_bit_cast(f16x2, w);
-            return sum + (float)h[0] + (float)h[1];
-        }
-    }
     __device__ static __forceinline__ void store_sums(const LinearArgs& p, int first, float v) {
         const int m = first + (threadIdx.x & 15);
         if ((threadIdx.x & 63) < 16 && m < p.M) p.sums[m] = p.accumulate ? p.sums[m] + v : v;
     }
 
-    __device__ static __forceinline__ void run_rows(const LinearArgs& p, State& s, uint8_t PG_LDS* smem, const RA& ra, const RB& rb,
-                                                    int wm, int wn, bool first_columns) {
+    // ---- both steps' fragments in registers ----------------------------------------------
+    //
+    // A K-tile is two steps, 32 deep each.  While a step's pieces are multiplied, the
+    // other set of registers takes the next step's fragments, evenly, since LDS
+    // is nearly as busy as the matrix cores (a 128 x 256 tile by four waves: 96 KB of
+    // fragments and 48 KB of loads in 1024 cycles of products).  When the first
+    // step is done all of a K-tile's fragments are in registers: there the wave
+    // waits for the next K-tile and crosses the barrier.  The loads that take the
+    // place of the K-tile it has read are spread from there on too, over a K-tile's
+    // time.  The loop begins behind the barrier, where no LDS read is in flight:
+    // across its end the compiler would wait for all of them.
+    struct Steps {
         f32x4 acc[FM][FN], sums[SUMS ? FM : 1];
+        i32x4 fa[2][FM], fb[2][FN];
+        bool adds;                           // this wave adds up rows of A (every WN-th row of pieces)
+    };
+    static constexpr bool WAITS = !AIN || !BIN;              // the transposing reads' own waits
+    static constexpr int UNITS = FM * FN, READS = FM + FN;   // matrix instructions and fragments of a step
+
+    // Unit `u` of the two steps behind the hand-over: its load, if it has one.
+    __device__ static __forceinline__ void spread(const State& s, int u, uint8_t PG_LDS* a_to, uint8_t PG_LDS* b_to) {
+        if constexpr (DIRECT) {
+            const int q = u * LPT / (2 * UNITS);
+            if ((u + 1) * LPT / (2 * UNITS) > q) {
+                if (q < LB) s.b.load(q, b_to, s.wave);
+                else s.a.load(q - LB, a_to, s.wave);
+            }
+        }
+    }
+    // Fragment r of step H of the K-tile at `a`, `b`, in the order of their use.
+    template <int H>
+    __device__ static __forceinline__ void read_one(const RA& ra, const RB& rb, Steps& f, const uint8_t PG_LDS* a,
+                                                    const uint8_t PG_LDS* b, int r) {
+        if (r == 0) f.fa[H][0] = ra.read(a, 0, H);
+        else if (r <= FN) f.fb[H][r - 1] = rb.read(b, r - 1, H);
+        else f.fa[H][r - FN] = ra.read(a, r - FN, H);
+    }
+    // Step H, under which the next step's fragments are read from the K-tile at
+    // `a`, `b` (MORE).
+    template <int H, bool MORE>
+    __device__ static __forceinline__ void step_of_two(const State& s, const RA& ra, const RB& rb, Steps& f, const uint8_t PG_LDS* a,
+                                                       const uint8_t PG_LDS* b, uint8_t PG_LDS* a_to, uint8_t PG_LDS* b_to, int wn) {
+        if constexpr (WAITS) {
+            wait_reads<0>();
+            __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int u = 0; u < UNITS; ++u) {
+            const int i = u / FN, j = u % FN;
+            f.acc[i][j] = multiply16<XT>(f.fb[H][j], f.fa[H][i], f.acc[i][j]);
+            if constexpr (SUMS) {
+                if (f.adds && j == 0 && i % WN == wn) f.sums[i] = multiply16<XT>(ones(), f.fa[H][i], f.sums[i]);
+            }
+            if constexpr (MORE) {
+                // all of them in the first three quarters of the step
+                constexpr int SPAN = UNITS * 3 / 4 > 0 ? UNITS * 3 / 4 : 1;
+#pragma unroll
+                for (int r = 0; r < READS; ++r)
+                    if (r * SPAN / READS == u) read_one<1 - H>(ra, rb, f, a, b, r);
+                spread(s, (H == 1 ? 0 : UNITS) + u, a_to, b_to);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+
+    __device__ static __forceinline__ void run_steps(const LinearArgs& p, State& s, uint8_t PG_LDS* smem, const RA& ra, const RB& rb,
+                                                    int wm, int wn, bool first_columns) {
+        Steps f;
 #pragma unroll
         for (int i = 0; i < FM; ++i)
 #pragma unroll
-            for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int j = 0; j < FN; ++j) f.acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int i = 0; i < (SUMS ? FM : 1); ++i) sums[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        const bool adds = SUMS && first_columns;
+        for (int i = 0; i < (SUMS ? FM : 1); ++i) f.sums[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        f.adds = SUMS && first_columns;
         auto tile_a = [&](int slot) { return smem + slot * FA::BYTES; };
         auto tile_b = [&](int slot) { return smem + RING_A + slot * FB::BYTES; };
-        i32x4 staged[DIRECT ? 1 : LPT];
-        auto stage = [&](int t) {
-            s.a.start(t, s.K, s.rot);
-            s.b.start(t, s.K, s.rot);
-            gather<FA, AIN>(s.a, staged);
-            gather<FB, BIN>(s.b, staged + (DIRECT ? 0 : LA));
+        auto first_fragments = [&] {
+#pragma unroll
+            for (int r = 0; r < READS; ++r) read_one<0>(ra, rb, f, tile_a(0), tile_b(0), r);
         };
         if constexpr (DIRECT) {
+            // The first SB - 1 K-tiles, and of the next one what a second step takes.
+            static_assert(SA == SB && SB > P && LPT % 2 == 0, "");
 #pragma unroll
             for (int t = 0; t < SB; ++t) {
                 s.a.start(t, s.K, s.rot);
                 s.b.start(t, s.K, s.rot);
-                s.b.load_all(tile_b(t), s.wave);
-                s.a.load_all(tile_a(t), s.wave);
+                if (t + 1 < SB) {
+                    s.b.load_all(tile_b(t), s.wave);
+                    s.a.load_all(tile_a(t), s.wave);
+                } else {
+#pragma unroll
+                    for (int u = 0; u < UNITS; ++u) spread(s, u, tile_a(t), tile_b(t));
+                }
             }
-            wait_loads<FLYING + LA + LB>();
-        } else {
-            stage(0);
-            put<FA>(tile_a(0), staged);
-            put<FB>(tile_b(0), staged + (DIRECT ? 0 : LA));
-            stage(1);
-        }
-        barrier();
-        if constexpr (DIRECT) {
+            wait_loads<(SB - 2) * LPT + LPT / 2>();
+            barrier();
             clear_tails(s, tile_a, tile_b);
-            s.a.start(SB, s.K, s.rot);
-            s.b.start(SB, s.K, s.rot);
-        }
-
-        i32x4 fa[2][2], fb[FN][2];
+            if (s.nt > 0) {
+                first_fragments();
+                step_of_two<0, true>(s, ra, rb, f, tile_a(0), tile_b(0), tile_a(SB - 1), tile_b(SB - 1), wn);
+                int slot = 0;
+                for (int t = 0; t + 1 < s.nt; ++t) {
+                    const int next = slot + 1 == SB ? 0 : slot + 1;
+                    s.a.next(s.K);
+                    s.b.next(s.K);
+                    wait_loads<(SB - 2) * LPT>();            // K-tile t + 1 has landed (this wave's part)
+                    barrier();                               // ... everyone's, and K-tile t's place is free
+                    step_of_two<1, true>(s, ra, rb, f, tile_a(next), tile_b(next), tile_a(slot), tile_b(slot), wn);
+                    step_of_two<0, true>(s, ra, rb, f, tile_a(next), tile_b(next), tile_a(slot), tile_b(slot), wn);
+                    slot = next;
+                }
+                step_of_two<1, false>(s, ra, rb, f, nullptr, nullptr, nullptr, nullptr, wn);
+            }
+        } else {
+            // REGS K-tiles are on the way in registers; groups of so many are whole,
+            // the K-tiles behind the last being zeros.
+            constexpr int REGS = 3;
+            i32x4 staged[REGS][LPT];
+            auto stage = [&](int t, i32x4 (&v)[LPT]) {
+                s.a.start(t, s.K, s.rot);
+                s.b.start(t, s.K, s.rot);
+                gather<FA, AIN>(s.a, v);
+                gather<FB, BIN>(s.b, v + LA);
+            };
+            stage(0, staged[0]);
+            put<FA>(tile_a(0), staged[0]);
+            put<FB>(tile_b(0), staged[0] + LA);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) fa[0][h] = ra.read(tile_a(0), 0, h);
+            for (int r = 0; r < REGS; ++r) stage(1 + r, staged[r]);
+            barrier();
+            if (s.nt > 0) {
+                first_fragments();
+                step_of_two<0, true>(s, ra, rb, f, tile_a(0), tile_b(0), nullptr, nullptr, wn);
+                int next = 1;
+                for (int t = 0; t + 1 < s.nt; t += REGS) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int j = 0; j < FN; ++j) fb[j][h] = rb.read(tile_b(0), j, h);
-
-        constexpr bool WAITS = !AIN || !BIN;     // the transposing reads' own waits
-        int slot_a = 0, slot_b = 0;
-        for (int t = 0; t < s.nt; ++t) {
-            const int next_a = slot_a + 1 == SA ? 0 : slot_a + 1, next_b = slot_b + 1 == SB ? 0 : slot_b + 1;
-#pragma unroll
-            for (int i = 0; i < FM; ++i) {
-                if (i + 1 == FM) {
-                    // every fragment of K-tile t is read: on to the next one
-                    if constexpr (DIRECT) {
-                        wait_loads<FLYING>();                // K-tile t + 1 has landed (this wave's part)
-                        barrier();                           // ... everyone's, and K-tile t's places are free
-                    } else {
-                        // (those of K-tile t + 1 were read before the last barrier)
-                        put<FA>(tile_a(next_a), staged);
-                        put<FB>(tile_b(next_b), staged + (DIRECT ? 0 : LA));
+                    for (int r = 0; r < REGS; ++r) {
+                        // (what was in the place was read before the last barrier)
+                        put<FA>(tile_a(next), staged[r]);
+                        put<FB>(tile_b(next), staged[r] + LA);
                         barrier();
-                        stage(t + 2);
-                    }
-                    __builtin_amdgcn_sched_barrier(0);
-                }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if constexpr (WAITS) {
-                        // the row's fragments have landed; a K-tile's first row: all but B's second halves, then those
-                        if (i == 0 && h == 0) wait_reads<(FN * (BIN ? 1 : 2) < 15 ? FN * (BIN ? 1 : 2) : 15)>();
-                        else if (h == 0 || i == 0) wait_reads<0>();
-                        __builtin_amdgcn_sched_barrier(0);
-                    }
-#pragma unroll
-                    for (int j = 0; j < FN; ++j) {
-                        const int u = h * FN + j;
-                        acc[i][j] = multiply16<XT>(fb[j][h], fa[i & 1][h], acc[i][j]);
-                        if constexpr (SUMS) {
-                            if (adds && j == 0 && i % WN == wn) sums[i] = multiply16<XT>(ones(), fa[i & 1][h], sums[i]);
-                        }
-                        if (i + 1 < FM) {
-                            // the next row's fragments (a K-tile's second row: behind the wait for B's second halves)
-                            if (u == (i == 0 ? FN : 0)) {
-                                fa[(i + 1) & 1][0] = ra.read(tile_a(slot_a), i + 1, 0);
-                                fa[(i + 1) & 1][1] = ra.read(tile_a(slot_a), i + 1, 1);
-                            }
-                        } else {
-                            if (u == 0) {
-                                fa[0][0] = ra.read(tile_a(next_a), 0, 0);
-                                fa[0][1] = ra.read(tile_a(next_a), 0, 1);
-                            }
-                            fb[j][h] = rb.read(tile_b(next_b), j, h);
-                            if constexpr (DIRECT) {
-#pragma unroll
-                                for (int q = u * LPT / (2 * FN); q < (u + 1) * LPT / (2 * FN); ++q) {
-                                    if (q < LB) s.b.load(q, tile_b(slot_b), s.wave);
-                                    else s.a.load(q - LB, tile_a(slot_a), s.wave);
-                                }
-                            }
-                        }
-                        __builtin_amdgcn_sched_barrier(0);
+                        stage(t + r + 1 + REGS, staged[r]);
+                        step_of_two<1, true>(s, ra, rb, f, tile_a(next), tile_b(next), nullptr, nullptr, wn);
+                        step_of_two<0, true>(s, ra, rb, f, tile_a(next), tile_b(next), nullptr, nullptr, wn);
+                        next ^= 1;
                     }
                 }
+                step_of_two<1, false>(s, ra, rb, f, nullptr, nullptr, nullptr, nullptr, wn);
             }
-            if constexpr (DIRECT) {
-                s.a.next(s.K);
-                s.b.next(s.K);
-            }
-            slot_a = next_a;
-            slot_b = next_b;
         }
-        wait_loads<0>();                     // no write into LDS outlives the K loop, and no read is in flight
+        wait_loads<0>();                     // no write into LDS outlives the K loop
         barrier();
-        if constexpr (WAITS) {
-            // the last reads' registers are not free before that
-            asm volatile("" ::"v"(fa[0][0]), "v"(fa[0][1]));
-#pragma unroll
-            for (int j = 0; j < FN; ++j) asm volatile("" ::"v"(fb[j][0]), "v"(fb[j][1]));
-        }
-
         if constexpr (SUMS) {
-            if (adds)
+            if (f.adds)
 #pragma unroll
                 for (int i = 0; i < FM; ++i)
-                    if (i % WN == wn) store_sums(p, s.m0 + wm * WTM + 16 * i, sums[i][0]);
+                    if (i % WN == wn) store_sums(p, s.m0 + wm * WTM + 16 * i, f.sums[i][0]);
         }
-        store(p, s, smem, wm, wn, acc);
+        store(p, s, smem, wm, wn, f.acc);
     }
 
     // ---- 128 x 128 sums per wave, one wave per SIMD -----------------------------------
@@ -555,7 +613,7 @@ struct Tile {
             const int m = (q >> 1) * 4 + i / 4, n = (q & 1) * 4 + i % 4;
             multiply16_in_place<XT>(f.b[n], f.a[m], acc[m][n]);
             if constexpr (ADDS)
-                if (q & 1) sums[m] = add_pair(f.a[m], i % 4, sums[m]);
+                if (q & 1) sums[m] = add_pair<XT>(f.a[m], i % 4, sums[m]);
             if (q == 0 && (i & 1) == 0) {
                 const int r = i / 2;
                 if (r < 4) f.b[4 + r] = rb.read(b, 4 + r, H);
@@ -729,24 +787,24 @@ struct Tile {
 };
 
 template <int XT, int END, bool AIN, bool BIN, bool DIRECT, int BM, int BN, int WM, int WN, int SA, int SB, int EXTRA>
-__global__ void __launch_bounds__(WM * WN == 4 && BM == 256 ? 256 : 512) linear_tile(LinearArgs p) {
+__global__ void __launch_bounds__(WM * WN * 64) linear_tile(LinearArgs p) {
     typedef Tile<XT, END, AIN, BIN, DIRECT, BM, BN, WM, WN, SA, SB, EXTRA> S;
     __shared__ __attribute__((aligned(16))) uint8_t smem[S::LDS];
     S::run(p, (uint8_t PG_LDS*)smem);
 }
 
-// The classes of one ending.  128 and 64 wide: waves in rows x columns, so that a
-// wave's rows of outputs are as long as they can be.  EXTRA: a second product
-// (linear), sums of A's rows (weight gradients).
+// The classes of one ending.  EXTRA: a second product (linear), sums of A's rows
+// (weight gradients).
 template <int XT, int END, bool AIN, bool BIN, int EXTRA>
 const void* linear_by_tile(int tile, bool rows16) {
-    constexpr bool G = END == END_GATED;
     switch (tile) {
     case LINEAR_TILE_256:
         return rows16 ? (const void*)&linear_tile<XT, END, AIN, BIN, true, 256, 256, 2, 2, 3, 2, EXTRA> : nullptr;
+    case LINEAR_TILE_128x256:
+        return rows16 ? (const void*)&linear_tile<XT, END, AIN, BIN, true, 128, 256, 2, 2, 3, 3, EXTRA> : nullptr;
     case LINEAR_TILE_128:
-        return rows16 ? (const void*)&linear_tile<XT, END, AIN, BIN, true, 128, 128, G ? 4 : 2, G ? 2 : 4, 4, 4, EXTRA>
-                      : (const void*)&linear_tile<XT, END, AIN, BIN, false, 128, 128, G ? 4 : 2, G ? 2 : 4, 2, 2, EXTRA>;
+        return rows16 ? (const void*)&linear_tile<XT, END, AIN, BIN, true, 128, 128, 2, 2, 4, 4, EXTRA>
+                      : (const void*)&linear_tile<XT, END, AIN, BIN, false, 128, 128, 2, 2, 2, 2, EXTRA>;
     case LINEAR_TILE_64:
         return rows16 ? (const void*)&linear_tile<XT, END, AIN, BIN, true, 64, 64, 2, 2, 4, 4, EXTRA>
                       : (const void*)&linear_tile<XT, END, AIN, BIN, false, 64, 64, 2, 2, 2, 2, EXTRA>;

@@ -1,11 +1,20 @@
 // linear_weight.hip -- gradients of weights: K across the rows of both factors.
-#include "linear_tile.h"
+#include "linear_few.h"
 
 namespace pg {
 
+namespace {
+
+template <int END, bool AIN, bool BIN, int EXTRA>
+const void* kernel(int xt, int tile, bool rows16) {
+    if (linear_few_tile(tile)) return rows16 ? few_by_type<END, AIN, BIN, EXTRA>(xt, tile) : nullptr;
+    return linear_by_type<END, AIN, BIN, EXTRA>(xt, tile, rows16);
+}
+
+}  // namespace
+
 const void* weight_gradient_kernel(int xt, int tile, bool rows16, bool sums) {
-    return sums ? linear_by_type<END_WEIGHT, false, false, 1>(xt, tile, rows16)
-                : linear_by_type<END_WEIGHT, false, false, 0>(xt, tile, rows16);
+    return sums ? kernel<END_WEIGHT, false, false, 1>(xt, tile, rows16) : kernel<END_WEIGHT, false, false, 0>(xt, tile, rows16);
 }
 
 }  // namespace pg
