@@ -502,7 +502,7 @@ enum { GEMM_ACT_NONE = 0, GEMM_ACT_RELU = 1, GEMM_ACT_GELU = 2, GEMM_ACT_GELU_TA
 
 /* Part of the sums that one workgroup computes (gated: half of its columns are
  * the second product's).  From 64x64_K4 on each wave takes parts of K of its
- * own; these, 256x256 and 128x256 need rows on 16 bytes.  Weight gradients have
+ * own.  128x128 and 64x64 take any rows, the others rows on 4 bytes.  Weight gradients have
  * those down to 32x32, gated layers those down to 16x32.  GEMM_LINEAR_TILE_AUTO: chosen by
  * the call's sizes. */
 enum { GEMM_LINEAR_TILE_AUTO = -1, GEMM_LINEAR_TILE_256x256 = 0, GEMM_LINEAR_TILE_128x256 = 1, GEMM_LINEAR_TILE_128x128 = 2,
@@ -516,7 +516,8 @@ typedef struct {
     int32_t tile;              /* GEMM_LINEAR_TILE_* chosen */
     int32_t block_m, block_n;  /* outputs of one workgroup */
     int32_t threads;           /* per workgroup */
-    int32_t rows16;            /* 1: K-tiles go straight into LDS */
+    int32_t rows_on;           /* bytes that all the factors' rows start on: 16, 4 or 2; from 4 on
+                                * K-tiles go straight into LDS */
     int32_t reserved;
     int64_t grid;              /* workgroups */
     int64_t k_tiles;           /* ceil(K / 64), K the length of the sums */
@@ -556,10 +557,10 @@ int gemm_weight_gradient(gemm_handle_t h, int64_t M, int64_t N, int64_t K, int d
                          const void *DC, int64_t lddc, const void *A, int64_t lda, float *DW, int64_t lddw, float *DB,
                          void *stream);
 
-/* What a call of these sizes would launch on a 256-CU device (rows_on_16:
- * whether all its factors' rows start on 16 bytes); M, N and K as the call
+/* What a call of these sizes would launch on a 256-CU device (rows_on: 16,
+ * 4 or 2, the bytes that all its factors' rows start on); M, N and K as the call
  * takes them.  No HIP call. */
-int gemm_query_linear(int form, int64_t M, int64_t N, int64_t K, int dtype, int rows_on_16, int tile,
+int gemm_query_linear(int form, int64_t M, int64_t N, int64_t K, int dtype, int rows_on, int tile,
                       gemm_linear_info_t *info);
 
 /* Static text for a status code (never NULL). */

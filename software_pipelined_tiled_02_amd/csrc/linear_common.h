@@ -35,6 +35,7 @@ struct LinearArgs {
     int32_t M, N, K;         // sums are M x N
     int32_t tiles_m, tiles_n;
     int32_t act, bias_f32, accumulate;
+    int32_t apart;           // some of the factors' rows do not start on 16 bytes
     int32_t stream;          // the outputs' rows are whole lines: past the caches
 };
 
@@ -59,13 +60,13 @@ constexpr LinearShape linear_shape(int t) {
 constexpr bool linear_few_tile(int t) { return t >= LINEAR_TILE_64K4; }
 
 // The kernel for a call: XT_F16 or XT_BF16, a tile class, whether all rows of
-// the factors start on 16 bytes (NULL: the class needs that), and a second
+// the factors start on 4 bytes (NULL: the class needs that), and a second
 // product (linear) or sums of A's rows (weight gradients).
-const void* linear_rc_kernel(int xt, int tile, bool rows16, bool pair);
-const void* linear_rr_kernel(int xt, int tile, bool rows16, bool pair);
-const void* gated_kernel(int xt, int tile, bool rows16);
-const void* gated_backward_kernel(int xt, int tile, bool rows16);
-const void* weight_gradient_kernel(int xt, int tile, bool rows16, bool sums);
+const void* linear_rc_kernel(int xt, int tile, bool rows4, bool pair);
+const void* linear_rr_kernel(int xt, int tile, bool rows4, bool pair);
+const void* gated_kernel(int xt, int tile, bool rows4);
+const void* gated_backward_kernel(int xt, int tile, bool rows4);
+const void* weight_gradient_kernel(int xt, int tile, bool rows4, bool sums);
 
 #if defined(__HIPCC__)
 

@@ -35,10 +35,12 @@ struct Few {
         // tiles of one column strip are neighbours: they share B
         const unsigned w = by_xcd(blockIdx.x, gridDim.x);
         const int m0 = (int)(w % (unsigned)p.tiles_m) * BM, tn = (int)(w / (unsigned)p.tiles_m), n0 = tn * OUTS;
-        const int K = p.K, nt = P * ((K + kDeep - 1) / kDeep), parts = K % kDeep != 0 ? P : 0;
+        const bool apart = p.apart != 0;
+        const Depth deep = depth_of(p.K, apart);
+        const int nt = P * ((p.K + kDeep - 1) / kDeep), parts = deep.part != 0 ? P : 0;
         // XCD x starts at K-tile 9 x: with every row read at the same k, rows at equal
         // distances would gather the reads on a few channels.
-        const int first = K >= kDeep ? (int)((blockIdx.x & 7) * 9u % (unsigned)(P * (K / kDeep))) : 0;
+        const int first = deep.whole > 0 ? (int)((blockIdx.x & 7) * 9u % (unsigned)(P * deep.whole)) : 0;
         FA a;
         FB b;
 #pragma unroll
@@ -52,10 +54,15 @@ struct Few {
         rb.locate(0);
 #pragma unroll
         for (int i = 0; i < SLOTS; ++i) {
-            a.start(wave + i * W, K, first);
-            b.start(wave + i * W, K, first);
-            a.load_all(ring + i * SLOT, 0);
-            b.load_all(ring + i * SLOT + FA::BYTES, 0);
+            a.start(wave + i * W, deep, first);
+            b.start(wave + i * W, deep, first);
+            if (i == 0 && wave < parts && apart) {
+                a.carry(ring, lane);
+                b.carry(ring + FA::BYTES, lane);
+            } else {
+                a.load_all(ring + i * SLOT, 0);
+                b.load_all(ring + i * SLOT + FA::BYTES, 0);
+            }
         }
         f32x4 acc[FM][FN];
         float sums[SUMS ? FM : 1];
@@ -70,9 +77,9 @@ struct Few {
         for (int t = wave; t < nt; t += W) {
             uint8_t PG_LDS* slot = ring + at * SLOT;
             wait_loads<(SLOTS - 1) * LPT>();                     // K-tile t has landed
-            if ((AIN || BIN) && t < parts && K % 8 != 0) {
-                if constexpr (AIN) clear_rows<BM, 64>(lane, slot, K % kDeep);
-                if constexpr (BIN) clear_rows<BN, 64>(lane, slot + FA::BYTES, K % kDeep);
+            if ((AIN || BIN) && t < parts && !apart && deep.part % 8 != 0) {
+                if constexpr (AIN) clear_rows<BM, 64>(lane, slot, deep.part);
+                if constexpr (BIN) clear_rows<BN, 64>(lane, slot + FA::BYTES, deep.part);
             }
             i32x4 fa[FM][2], fb[FN][2];
 #pragma unroll
@@ -93,8 +100,8 @@ struct Few {
                     for (int j = 0; j < FN; ++j) asm volatile("" : "+v"(fb[j][h])::"memory");
                 }
             }
-            a.start(t + SLOTS * W, K, first);
-            b.start(t + SLOTS * W, K, first);
+            a.start(t + SLOTS * W, deep, first);
+            b.start(t + SLOTS * W, deep, first);
             a.load_all(slot, 0);
             b.load_all(slot + FA::BYTES, 0);
 #pragma unroll

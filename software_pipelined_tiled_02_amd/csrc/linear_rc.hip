@@ -6,15 +6,15 @@ namespace pg {
 namespace {
 
 template <int END, bool AIN, bool BIN, int EXTRA>
-const void* kernel(int xt, int tile, bool rows16) {
-    if (linear_few_tile(tile)) return rows16 ? few_by_type<END, AIN, BIN, EXTRA>(xt, tile) : nullptr;
-    return linear_by_type<END, AIN, BIN, EXTRA>(xt, tile, rows16);
+const void* kernel(int xt, int tile, bool rows4) {
+    if (linear_few_tile(tile)) return rows4 ? few_by_type<END, AIN, BIN, EXTRA>(xt, tile) : nullptr;
+    return linear_by_type<END, AIN, BIN, EXTRA>(xt, tile, rows4);
 }
 
 }  // namespace
 
-const void* linear_rc_kernel(int xt, int tile, bool rows16, bool pair) {
-    return pair ? kernel<END_LINEAR, true, true, 1>(xt, tile, rows16) : kernel<END_LINEAR, true, true, 0>(xt, tile, rows16);
+const void* linear_rc_kernel(int xt, int tile, bool rows4, bool pair) {
+    return pair ? kernel<END_LINEAR, true, true, 1>(xt, tile, rows4) : kernel<END_LINEAR, true, true, 0>(xt, tile, rows4);
 }
 
 }  // namespace pg

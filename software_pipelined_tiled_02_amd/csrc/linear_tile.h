@@ -74,6 +74,30 @@ constexpr int out_swz(int row_bytes, int k) {
                             : 0;
 }
 
+// K as whole K-tiles and the values of one more, which is multiplied first.  Rows
+// that do not start on 16 bytes (`apart`) have their last K-tile there, whole or
+// not: all the others are read without a look at where rows and the matrix end.
+struct Depth { int whole, part; };
+__device__ __forceinline__ Depth depth_of(int K, bool apart) {
+    const int whole = (apart && K > 0 ? K - 1 : K) / kDeep;
+    return Depth{whole, K - whole * kDeep};
+}
+
+// Eight values of which `n` are there; the others become zero and are not read.
+__device__ __forceinline__ i32x4 load_some(__amdgpu_buffer_rsrc_t r, uint32_t off, int n) {
+    const uint32_t vb = n > 0 && n < 8 ? 2u * n : 0u;
+    i32x4 v = __builtin_amdgcn_raw_buffer_load_b128(r, n >= 8 ? off : kOutside, 0, 0);
+    const i32x2 p8 = __builtin_amdgcn_raw_buffer_load_b64(r, (vb & 8) ? off : kOutside, 0, 0);
+    const int p4 = (int)__builtin_amdgcn_raw_buffer_load_b32(r, (vb & 4) ? off + (vb & 8) : kOutside, 0, 0);
+    const int p2 = (int)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, (vb & 2) ? off + (vb & 12) : kOutside, 0, 0);
+    const uint32_t d4 = (vb & 8) >> 2, d2 = (vb & 12) >> 2;
+    v[0] |= p8[0] | (d4 == 0 ? p4 : 0) | (d2 == 0 ? p2 : 0);
+    v[1] |= p8[1] | (d2 == 1 ? p2 : 0);
+    v[2] |= (d4 == 2 ? p4 : 0) | (d2 == 2 ? p2 : 0);
+    v[3] |= d2 == 3 ? p2 : 0;
+    return v;
+}
+
 // One factor's part of a tile: ROWS rows (of A, or of B's transpose), staged by
 // T threads (64: a wave by itself).  INSIDE: K along the rows.  SPLIT: rows 0-15
 // of each 32 belong to the first of two matrices, rows 16-31 to the second
@@ -101,19 +125,19 @@ struct Factor {
     const uint8_t* from_u;
 
     // The K-tile whose loads are next.  The order in which they are multiplied:
-    // each product's last one, where it is not whole, then all whole ones, from
+    // each product's last one, where it goes apart, then all others, from
     // number `first` on and round to it again.  Behind the last, a K-tile moves
     // nothing (all is out of range), so that the number of loads in flight is
     // always the same.
     const uint8_t* from;             // its first row or column
     int size;                        // bytes from there on that may be read
     int rem;                         // values of K from there on
-    int kb;                          // its number among the whole ones, of all products
+    int kb;                          // its number among those behind the ones apart, of all products
     int more;                        // K-tiles from this one on
     bool second;                     // of the second product
 
-    __device__ __forceinline__ __amdgpu_buffer_rsrc_t resource() const {
-        return __builtin_amdgcn_make_buffer_rsrc((void*)from, 0, size, kBufferWord3);
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(int j) const {
+        return __builtin_amdgcn_make_buffer_rsrc((void*)(BOTH && ((j >> 1) & 1) ? from_u : from), 0, size, kBufferWord3);
     }
     __device__ __forceinline__ uint32_t offset(int j) const { return P == 2 && second ? off[P - 1][j] : off[0][j]; }
     // The same, out of range where the chunk lies past K (K outside: the size sees to that).
@@ -123,9 +147,7 @@ struct Factor {
 
     // Load j of the K-tile, straight into LDS.  `part`: it may not be a whole one.
     __device__ __forceinline__ void load(int j, uint8_t PG_LDS* to, int wave, bool part = false) const {
-        const __amdgpu_buffer_rsrc_t r =
-            __builtin_amdgcn_make_buffer_rsrc((void*)(BOTH && ((j >> 1) & 1) ? from_u : from), 0, size, kBufferWord3);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (void PG_LDS*)(to + (j * T + 64 * wave) * kChunk), 16,
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(resource(j), (void PG_LDS*)(to + (j * T + 64 * wave) * kChunk), 16,
                                                  part ? offset_in(j) : offset(j), 0, 0, 0);
     }
     __device__ __forceinline__ void load_all(uint8_t PG_LDS* to, int wave) const {
@@ -133,18 +155,41 @@ struct Factor {
         for (int j = 0; j < L; ++j) load(j, to, wave, true);
     }
 
+    // The K-tile through registers: the chunks at the ends of rows are read only as far
+    // as these go.
+    __device__ __forceinline__ void gather(i32x4 (&v)[L]) const {
+        const bool ragged = INSIDE ? rem > 0 && rem < kDeep : left < CR * 8;
+#pragma unroll
+        for (int j = 0; j < L; ++j) {
+            const __amdgpu_buffer_rsrc_t r = resource(j);
+            const int c = TURNS && (j & 1) ? at ^ 16 : at;
+            // (K outside: a chunk's place past the matrix was moved to its first one, whole or not)
+            if (ragged) v[j] = load_some(r, offset(j), INSIDE ? rem - c : min(c < left ? left - c : left, 8));
+            else v[j] = __builtin_amdgcn_raw_buffer_load_b128(r, offset_in(j), 0, 0);
+        }
+    }
+    __device__ __forceinline__ void put(uint8_t PG_LDS* to, const i32x4 (&v)[L], int tid) const {
+#pragma unroll
+        for (int j = 0; j < L; ++j) *(i32x4 PG_LDS*)(to + (j * T + tid) * kChunk) = v[j];
+    }
+    __device__ __forceinline__ void carry(uint8_t PG_LDS* to, int tid) const {
+        i32x4 v[L];
+        gather(v);
+        put(to, v, tid);
+    }
+
     // K-tile number i of the order.
-    __device__ __forceinline__ void start(int i, int K, int first) {
-        const int whole = K / kDeep, part = K % kDeep, parts = part != 0 ? P : 0;
-        more = parts + P * whole - i;
-        int q = 0, k = whole;
-        rem = part;
+    __device__ __forceinline__ void start(int i, Depth d, int first) {
+        const int parts = d.part != 0 ? P : 0;
+        more = parts + P * d.whole - i;
+        int q = 0, k = d.whole;
+        rem = d.part;
         kb = first;
         if (i >= parts) {
             kb = i - parts + first;
-            kb = kb >= P * whole ? kb - P * whole : kb;
-            q = P == 2 && kb >= whole ? 1 : 0;
-            k = q ? kb - whole : kb;
+            kb = kb >= P * d.whole ? kb - P * d.whole : kb;
+            q = P == 2 && kb >= d.whole ? 1 : 0;
+            k = q ? kb - d.whole : kb;
             rem = kDeep;
         } else {
             q = i;
@@ -159,17 +204,16 @@ struct Factor {
     // On to the next one, both whole (or behind the last).  Without a branch: one
     // in the K loop costs some 50 cycles where it is taken (256 x 256 tiles: 2706
     // cycles a K-tile with three of them, 2460 without).
-    __device__ __forceinline__ void next(int K) {
-        const int whole = K / kDeep;
+    __device__ __forceinline__ void next(Depth d) {
         const int64_t row = P == 2 && second ? ld[P - 1] : ld[0];
         const uint8_t* to = from + (INSIDE ? 128 : kDeep * row);
         ++kb;
         --more;
         if constexpr (P == 2) {
-            second = kb == whole ? true : second;
-            to = kb == whole ? base[P - 1] : to;
+            second = kb == d.whole ? true : second;
+            to = kb == d.whole ? base[P - 1] : to;
         }
-        const bool round = kb == P * whole;
+        const bool round = kb == P * d.whole;
         to = round ? base[0] : to;
         second = round ? false : second;
         kb = round ? 0 : kb;
@@ -307,56 +351,35 @@ struct Tile {
     struct State {
         FA a;
         FB b;
-        int m0, n0, wave, K, KB, nt;         // nt: K-tiles of all products
+        int m0, n0, wave, nt;                // nt: K-tiles of all products
+        Depth deep;
+        bool apart;                          // rows that do not start on 16 bytes
         int rot;                             // the K-tile that is multiplied first
     };
 
     // What clear_rows clears, in the K-tiles in places 0 .. P - 1, once they have landed.
     template <class PA, class PB>
     __device__ static __forceinline__ void clear_tails(const State& s, PA tile_a, PB tile_b) {
-        if (!(AIN || BIN) || s.K % 8 == 0) return;
+        if (!(AIN || BIN) || s.apart || s.deep.part % 8 == 0) return;
         wait_loads<0>();
         barrier();
 #pragma unroll
         for (int t = 0; t < P; ++t) {
-            if constexpr (AIN) clear_rows<BM, T>(threadIdx.x, tile_a(t), s.K % kDeep);
-            if constexpr (BIN) clear_rows<BN, T>(threadIdx.x, tile_b(t), s.K % kDeep);
+            if constexpr (AIN) clear_rows<BM, T>(threadIdx.x, tile_a(t), s.deep.part);
+            if constexpr (BIN) clear_rows<BN, T>(threadIdx.x, tile_b(t), s.deep.part);
         }
         barrier();
     }
 
-    // ---- rows at any address: through registers ---------------------------------
-
-    // Eight values of which `n` are there; the others become zero and are not read.
-    __device__ static __forceinline__ i32x4 load_some(__amdgpu_buffer_rsrc_t r, uint32_t off, int n) {
-        const uint32_t vb = n > 0 && n < 8 ? 2u * n : 0u;
-        i32x4 v = __builtin_amdgcn_raw_buffer_load_b128(r, n >= 8 ? off : kOutside, 0, 0);
-        const i32x2 p8 = __builtin_amdgcn_raw_buffer_load_b64(r, (vb & 8) ? off : kOutside, 0, 0);
-        const int p4 = (int)__builtin_amdgcn_raw_buffer_load_b32(r, (vb & 4) ? off + (vb & 8) : kOutside, 0, 0);
-        const int p2 = (int)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, (vb & 2) ? off + (vb & 12) : kOutside, 0, 0);
-        const uint32_t d4 = (vb & 8) >> 2, d2 = (vb & 12) >> 2;
-        v[0] |= p8[0] | (d4 == 0 ? p4 : 0) | (d2 == 0 ? p2 : 0);
-        v[1] |= p8[1] | (d2 == 1 ? p2 : 0);
-        v[2] |= (d4 == 2 ? p4 : 0) | (d2 == 2 ? p2 : 0);
-        v[3] |= d2 == 3 ? p2 : 0;
-        return v;
-    }
-    template <class F, bool INSIDE>
-    __device__ static __forceinline__ void gather(const F& f, i32x4* v) {
-        static_assert(!F::TURNS, "one place");
-        const __amdgpu_buffer_rsrc_t r = f.resource();
-        const bool ragged = INSIDE ? f.rem > 0 && f.rem < kDeep : f.left < F::CR * 8;
-#pragma unroll
-        for (int j = 0; j < F::L; ++j) {
-            // (K outside: a chunk's place past the matrix was moved to its first one, whole or not)
-            if (ragged) v[j] = load_some(r, f.offset(j), INSIDE ? f.rem - f.at : min(f.at < f.left ? f.left - f.at : f.left, 8));
-            else v[j] = __builtin_amdgcn_raw_buffer_load_b128(r, f.offset_in(j), 0, 0);
+    // K-tile number t of the order, one of the first, into its places.
+    __device__ static __forceinline__ void begin(const State& s, int t, uint8_t PG_LDS* a, uint8_t PG_LDS* b) {
+        if (t < P && s.apart) {
+            s.a.carry(a, threadIdx.x);
+            s.b.carry(b, threadIdx.x);
+        } else {
+            s.b.load_all(b, s.wave);
+            s.a.load_all(a, s.wave);
         }
-    }
-    template <class F>
-    __device__ static __forceinline__ void put(uint8_t PG_LDS* to, const i32x4* v) {
-#pragma unroll
-        for (int j = 0; j < F::L; ++j) *(i32x4 PG_LDS*)(to + (j * T + threadIdx.x) * kChunk) = v[j];
     }
 
     // ---- fragments -------------------------------------------------------------------
@@ -367,15 +390,15 @@ struct Tile {
     __device__ static __forceinline__ void run(const LinearArgs& p, uint8_t PG_LDS* smem) {
         State s;
         s.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-        s.K = p.K;
-        s.KB = (p.K + kDeep - 1) / kDeep;
-        s.nt = s.KB * P;
+        s.apart = p.apart != 0;
+        s.deep = depth_of(p.K, s.apart);
+        s.nt = P * ((p.K + kDeep - 1) / kDeep);
         int tm, tn;
         place_linear(p, blockIdx.x, tm, tn);
         s.m0 = tm * BM;
         s.n0 = tn * (SPLIT ? BN / 2 : BN);
         // With more tiles than one round, XCD x starts at K-tile 9 x.
-        s.rot = gridDim.x > 256 && s.K >= kDeep ? (int)((blockIdx.x & 7) * 9u % (unsigned)(P * (s.K / kDeep))) : 0;
+        s.rot = gridDim.x > 256 && s.deep.whole > 0 ? (int)((blockIdx.x & 7) * 9u % (unsigned)(P * s.deep.whole)) : 0;
 #pragma unroll
         for (int q = 0; q < P; ++q) {
             s.a.locate(threadIdx.x, q, p.A[q], s.m0, p.lda[q], p.M - s.m0);
@@ -495,11 +518,10 @@ struct Tile {
             static_assert(SA == SB && SB > P && LPT % 2 == 0, "");
 #pragma unroll
             for (int t = 0; t < SB; ++t) {
-                s.a.start(t, s.K, s.rot);
-                s.b.start(t, s.K, s.rot);
+                s.a.start(t, s.deep, s.rot);
+                s.b.start(t, s.deep, s.rot);
                 if (t + 1 < SB) {
-                    s.b.load_all(tile_b(t), s.wave);
-                    s.a.load_all(tile_a(t), s.wave);
+                    begin(s, t, tile_a(t), tile_b(t));
                 } else {
 #pragma unroll
                     for (int u = 0; u < UNITS; ++u) spread(s, u, tile_a(t), tile_b(t));
@@ -514,8 +536,8 @@ struct Tile {
                 int slot = 0;
                 for (int t = 0; t + 1 < s.nt; ++t) {
                     const int next = slot + 1 == SB ? 0 : slot + 1;
-                    s.a.next(s.K);
-                    s.b.next(s.K);
+                    s.a.next(s.deep);
+                    s.b.next(s.deep);
                     wait_loads<(SB - 2) * LPT>();            // K-tile t + 1 has landed (this wave's part)
                     barrier();                               // ... everyone's, and K-tile t's place is free
                     step_of_two<1, true>(s, ra, rb, f, tile_a(next), tile_b(next), tile_a(slot), tile_b(slot), wn);
@@ -525,21 +547,21 @@ struct Tile {
                 step_of_two<1, false>(s, ra, rb, f, nullptr, nullptr, nullptr, nullptr, wn);
             }
         } else {
-            // REGS K-tiles are on the way in registers; groups of so many are whole,
+            // Rows on 2 bytes go through registers.  REGS K-tiles are on the way in registers; groups of so many are whole,
             // the K-tiles behind the last being zeros.
             constexpr int REGS = 3;
-            i32x4 staged[REGS][LPT];
-            auto stage = [&](int t, i32x4 (&v)[LPT]) {
-                s.a.start(t, s.K, s.rot);
-                s.b.start(t, s.K, s.rot);
-                gather<FA, AIN>(s.a, v);
-                gather<FB, BIN>(s.b, v + LA);
+            i32x4 staged_a[REGS][LA], staged_b[REGS][LB];
+            auto stage = [&](int t, int r) {
+                s.a.start(t, s.deep, s.rot);
+                s.b.start(t, s.deep, s.rot);
+                s.a.gather(staged_a[r]);
+                s.b.gather(staged_b[r]);
             };
-            stage(0, staged[0]);
-            put<FA>(tile_a(0), staged[0]);
-            put<FB>(tile_b(0), staged[0] + LA);
+            stage(0, 0);
+            s.a.put(tile_a(0), staged_a[0], threadIdx.x);
+            s.b.put(tile_b(0), staged_b[0], threadIdx.x);
 #pragma unroll
-            for (int r = 0; r < REGS; ++r) stage(1 + r, staged[r]);
+            for (int r = 0; r < REGS; ++r) stage(1 + r, r);
             barrier();
             if (s.nt > 0) {
                 first_fragments();
@@ -549,10 +571,10 @@ struct Tile {
 #pragma unroll
                     for (int r = 0; r < REGS; ++r) {
                         // (what was in the place was read before the last barrier)
-                        put<FA>(tile_a(next), staged[r]);
-                        put<FB>(tile_b(next), staged[r] + LA);
+                        s.a.put(tile_a(next), staged_a[r], threadIdx.x);
+                        s.b.put(tile_b(next), staged_b[r], threadIdx.x);
                         barrier();
-                        stage(t + r + 1 + REGS, staged[r]);
+                        stage(t + r + 1 + REGS, r);
                         step_of_two<1, true>(s, ra, rb, f, tile_a(next), tile_b(next), nullptr, nullptr, wn);
                         step_of_two<0, true>(s, ra, rb, f, tile_a(next), tile_b(next), nullptr, nullptr, wn);
                         next ^= 1;
@@ -624,7 +646,7 @@ struct Tile {
             if (u >= U0) {
                 const int j = (u - U0) * NL / (64 - U0);     // at most one load a unit
                 if ((u - U0 + 1) * NL / (64 - U0) > j) factor.load(j, to, s.wave);
-                if (u == 63) factor.next(s.K);
+                if (u == 63) factor.next(s.deep);
             }
             __builtin_amdgcn_sched_barrier(0);
             if (BAR && u == 15) {
@@ -666,16 +688,15 @@ struct Tile {
         auto tile_b = [&](int slot) { return smem + RING_A + slot * FB::BYTES; };
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            s.a.start(t, s.K, s.rot);
-            s.b.start(t, s.K, s.rot);
-            s.a.load_all(tile_a(t), s.wave);
-            s.b.load_all(tile_b(t), s.wave);
+            s.a.start(t, s.deep, s.rot);
+            s.b.start(t, s.deep, s.rot);
+            begin(s, t, tile_a(t), tile_b(t));
         }
         wait_loads<LA + LB>();
         barrier();
         clear_tails(s, tile_a, tile_b);
-        s.a.start(2, s.K, s.rot);
-        s.b.start(2, s.K, s.rot);
+        s.a.start(2, s.deep, s.rot);
+        s.b.start(2, s.deep, s.rot);
         Frags f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -796,25 +817,25 @@ __global__ void __launch_bounds__(WM * WN * 64) linear_tile(LinearArgs p) {
 // The classes of one ending.  EXTRA: a second product (linear), sums of A's rows
 // (weight gradients).
 template <int XT, int END, bool AIN, bool BIN, int EXTRA>
-const void* linear_by_tile(int tile, bool rows16) {
+const void* linear_by_tile(int tile, bool rows4) {
     switch (tile) {
     case LINEAR_TILE_256:
-        return rows16 ? (const void*)&linear_tile<XT, END, AIN, BIN, true, 256, 256, 2, 2, 3, 2, EXTRA> : nullptr;
+        return rows4 ? (const void*)&linear_tile<XT, END, AIN, BIN, true, 256, 256, 2, 2, 3, 2, EXTRA> : nullptr;
     case LINEAR_TILE_128x256:
-        return rows16 ? (const void*)&linear_tile<XT, END, AIN, BIN, true, 128, 256, 2, 2, 3, 3, EXTRA> : nullptr;
+        return rows4 ? (const void*)&linear_tile<XT, END, AIN, BIN, true, 128, 256, 2, 2, 3, 3, EXTRA> : nullptr;
     case LINEAR_TILE_128:
-        return rows16 ? (const void*)&linear_tile<XT, END, AIN, BIN, true, 128, 128, 2, 2, 4, 4, EXTRA>
+        return rows4 ? (const void*)&linear_tile<XT, END, AIN, BIN, true, 128, 128, 2, 2, 4, 4, EXTRA>
                       : (const void*)&linear_tile<XT, END, AIN, BIN, false, 128, 128, 2, 2, 2, 2, EXTRA>;
     case LINEAR_TILE_64:
-        return rows16 ? (const void*)&linear_tile<XT, END, AIN, BIN, true, 64, 64, 2, 2, 4, 4, EXTRA>
+        return rows4 ? (const void*)&linear_tile<XT, END, AIN, BIN, true, 64, 64, 2, 2, 3, 3, EXTRA>
                       : (const void*)&linear_tile<XT, END, AIN, BIN, false, 64, 64, 2, 2, 2, 2, EXTRA>;
     default: return nullptr;
     }
 }
 template <int END, bool AIN, bool BIN, int EXTRA>
-const void* linear_by_type(int xt, int tile, bool rows16) {
-    return xt == XT_BF16 ? linear_by_tile<XT_BF16, END, AIN, BIN, EXTRA>(tile, rows16)
-                         : linear_by_tile<XT_F16, END, AIN, BIN, EXTRA>(tile, rows16);
+const void* linear_by_type(int xt, int tile, bool rows4) {
+    return xt == XT_BF16 ? linear_by_tile<XT_BF16, END, AIN, BIN, EXTRA>(tile, rows4)
+                         : linear_by_tile<XT_F16, END, AIN, BIN, EXTRA>(tile, rows4);
 }
 
 }  // namespace pg

@@ -63,6 +63,55 @@ def test_linear_rows_at_any_address(M, N, K, lda, ldb, offset, tile, layout):
     check_linear(a, b, c, None, "bf16", layout, what=tile)
 
 
+def on4(t, distance, offset):
+    """t in rows on 4 bytes, and not all on 16."""
+    assert distance % 2 == 0 and offset % 2 == 0 and (distance % 8 or offset % 8)
+    return place(t, distance, offset)
+
+
+# K: not a multiple of 8 of several K-tiles, exactly one and two of them, less than one, less than 8
+@pytest.mark.parametrize("dtype", ("bf16", "f16"))
+@pytest.mark.parametrize("layout", ("RC", "RR"))
+@pytest.mark.parametrize("tile", TILES + ("auto",))
+@pytest.mark.parametrize("M,N,K,lda,ldb,offset", ((300, 262, 202, 202, 6, 0), (70, 100, 64, 66, 0, 2), (257, 130, 128, 128, 10, 4),
+                                                  (33, 65, 62, 62, 5, 6), (1, 9, 5, 6, 1, 0), (520, 37, 1004, 1004, 1, 2)))
+def test_linear_rows_on_4_bytes(M, N, K, lda, ldb, offset, tile, layout, dtype):
+    g = gen(20)
+    shape = (N, K) if layout == "RC" else (K, N)
+    a, b, a2, b2 = (rand(g, *s, dtype, z) for s, z in ((( M, K), 1.0), (shape, K ** -0.5)) * 2)
+    r, bias = rand(g, M, N, dtype), torch.randn(N, generator=g, device="cuda")
+    ldb = (shape[1] + ldb) // 2 * 2
+    at = on4(a, lda, offset + 2 * (lda % 8 == 0 and offset % 8 == 0)), place(b, ldb, 2)
+    c, z = binding.linear(*at, layout=layout, bias=bias, activation="gelu", residual=r, keep=True, tile=tile)
+    check_linear(a, b, c, z, dtype, layout, bias, "gelu", r, what=tile)
+    c = binding.linear(*at, layout=layout, pair=(rows16(a2), place(b2, ldb + 4, 4)), tile=tile)
+    check_linear(a, b, c, None, dtype, layout, pair=(a2, b2), what=tile)
+
+
+@pytest.mark.parametrize("tile", TILES + ("auto",))
+@pytest.mark.parametrize("M,N,K", ((300, 140, 202), (65, 33, 64), (1, 1, 2), (257, 18, 129), (40, 200, 1004)))
+def test_others_of_rows_on_4_bytes(M, N, K, tile):
+    g, dtype = gen(21), "bf16"
+    even = lambda n: (n + 1) // 2 * 2  # noqa: E731
+    x, wg, wu = rand(g, M, K, dtype), rand(g, N, K, dtype, K ** -0.5), rand(g, N, K, dtype, K ** -0.5)
+    if tile in TILES[:-1] + ("auto",):
+        got = binding.gated(on4(x, even(K) + 2, 2), rows16(wg), place(wu, even(K), 4), keep=True, tile=tile)
+        for v, (want, off), name in zip(got, R.gated(x.double(), wg.double(), wu.double(), dtype, "silu"), "hgu"):
+            assert_within(v, want, off, name)
+    w, gate, up = rand(g, K, N, dtype, K ** -0.5), rand(g, M, N, dtype, 2.0), rand(g, M, N, dtype)
+    for at in ((on4(x, even(K), 2), rows16(w)), (rows16(x), on4(w, even(N), 6)), (on4(x, even(K) + 4, 2), on4(w, even(N) + 6, 2))):
+        got = binding.gated_backward(*at, gate, up, keep=True, tile=tile)
+        for v, (want, off) in zip(got, R.gated_backward(x.double(), w.double(), gate.double(), up.double(), dtype, "silu")):
+            assert_within(v, want, off, tile)
+    if tile not in TILES[7:]:
+        dc = rand(g, M, N, dtype)
+        dw, off, db, db_off = R.weight_gradient(dc.double(), x.double())
+        for at in ((on4(dc, even(N), 2), rows16(x)), (rows16(dc), on4(x, even(K), 6)), (on4(dc, even(N) + 2, 4), on4(x, even(K) + 4, 2))):
+            got, sums = binding.weight_gradient(*at, bias=True, tile=tile)
+            assert_within(got, dw, off, "dw")
+            assert_within(sums, db, db_off, "db")
+
+
 @pytest.mark.parametrize("layout", ("RC", "RR"))
 @pytest.mark.parametrize("tile", TILES + ("auto",))
 @pytest.mark.parametrize("M,N,K,odd", ((300, 280, 136, False), (65, 72, 67, False), (129, 100, 203, True), (20, 33, 64, True), (40, 40, 7, True)))

@@ -70,20 +70,23 @@ def test_plan():
     for form in binding.LINEAR_FORMS:
         for M, N, K in ((1, 4096, 4096), (64, 8192, 8192), (500, 4104, 4100), (8192, 8192, 8200), (0, 16, 16), (16, 0, 16), (16, 16, 0),
                         (8192, 1000, 24), (7, 100000, 3)):
-            for r16 in (True, False):
-                rc, info = q(form, M, N, K, rows16=r16)
-                assert rc == OK and info["rows16"] == int(r16)
+            for on in (16, 4, 2):
+                rc, info = q(form, M, N, K, rows_on=on)
+                assert rc == OK and info["rows_on"] == on
                 rows, cols, depth = (N, K, M) if form == "weight_gradient" else (M, N, K)
                 want = -(-rows // info["block_m"]) * -(-cols // info["block_n"]) if rows and cols else 0
                 assert info["grid"] == want and info["k_tiles"] == -(-depth // 64), (form, M, N, K, info)
-                assert r16 or info["tile"] in (binding.LINEAR_TILES["128x128"], binding.LINEAR_TILES["64x64"])
+                assert on >= 4 or info["tile"] in (binding.LINEAR_TILES["128x128"], binding.LINEAR_TILES["64x64"])
     assert q("linear_rc", 8192, 8192, 8200)[1]["tile"] == binding.LINEAR_TILES["256x256"]
-    assert q("linear_rc", 512, 512, 512, tile="256x256", rows16=False)[0] == ALIGN
+    for tile in binding.LINEAR_TILES:
+        want = OK if tile in ("auto", "128x128", "64x64") else ALIGN
+        assert q("linear_rc", 512, 512, 512, tile=tile, rows_on=4)[0] == OK
+        assert q("linear_rc", 512, 512, 512, tile=tile, rows_on=2)[0] == want
 
 
 def test_query_refusals():
     assert q(5, 1, 1, 1)[0] == BAD and q(-1, 1, 1, 1)[0] == BAD
-    for bad in (dict(dtype="f32"), dict(dtype="i8"), dict(rows16=2), dict(tile=99), dict(tile=-2)):
+    for bad in (dict(dtype="f32"), dict(dtype="i8"), dict(rows_on=8), dict(rows_on=0), dict(tile=99), dict(tile=-2)):
         assert q("gated", 1, 1, 1, **bad)[0] == BAD, bad
     assert q("gated", -1, 1, 1)[0] == BAD and q("gated", 1, -1, 1)[0] == BAD and q("gated", 1, 1, -1)[0] == BAD
     assert q("linear_rc", 2 ** 31, 1, 1)[0] == UNSUP and q("linear_rc", 1, 2 ** 31, 1)[0] == UNSUP
