@@ -55,23 +55,23 @@ const void* kernel(int form, int dtype, int tile, int rows, bool extra) {
 
 // Microseconds that the classes take: for a K-tile when few workgroups are there,
 // and when every CU has all that fit (`resident`); for the start and the ending of
-// a workgroup.  Fitted to 4000 times of 600 calls of all forms (1 to 8192 rows, 64 to
-// 8192 columns and depth, operands in the caches where they fit).  The class of the
-// least time takes 1.7% longer than the best one on average; the largest class
-// that gives every CU a workgroup, which is the rule before it, takes 17% longer, and
-// three times as long at worst (350 x 512 x 8192: 17.5 us by 64 x 64 tiles, 8.0 by
-// 32 x 32; 1024 x 4096 x 4096: 74 us by 256 x 256, 32 by 128 x 128).
+// a workgroup.  Fitted to 5000 times of 630 calls of all forms (1 to 8192 rows, 64 to
+// 8192 columns and depth, factors from HBM).  The class of the least time takes
+// 1.7% longer than the best one on average; with the largest class that gives
+// every CU a workgroup it was 17% (factors in the caches), and three times as long
+// at worst.  64 x 8192 x 8192: 64x32 31.8 us, 32x32 41.4; 1024 x 4096 x 4096: 128x128
+// 38, 256x256 78; 1 x 4096 x 4096: 16x16 8.6, 64x64 25.8.
 struct Cost { double few, all, ends; int resident; };
-constexpr Cost kCost[pg::LINEAR_TILE_COUNT] = {{0.84, 1.37, 9.8, 1}, {0.49, 0.77, 5.7, 1}, {0.28, 0.43, 3.9, 1},
-                                               {0.13, 0.49, 2.1, 3}, {0.45, 0.97, 3.0, 1}, {0.29, 0.75, 2.3, 1},
-                                               {0.38, 0.95, 1.8, 1}, {0.25, 0.65, 1.9, 1}, {0.21, 0.57, 1.7, 1}};
+constexpr Cost kCost[pg::LINEAR_TILE_COUNT] = {{0.95, 1.80, 9.8, 1}, {0.60, 0.99, 5.8, 1}, {0.35, 0.63, 3.9, 1},
+                                               {0.20, 0.67, 2.1, 3}, {0.79, 1.16, 2.9, 1}, {0.60, 0.91, 2.3, 1},
+                                               {0.85, 1.20, 1.7, 1}, {0.63, 0.82, 1.9, 1}, {0.52, 0.63, 1.7, 1}};
 
 double linear_time(int tile, int form, int rows, int64_t tiles, int64_t k_tiles, int num_cus) {
     const Cost& c = kCost[tile];
     const bool waves = pg::linear_few_tile(tile);            // (each has K-tiles of its own)
-    // factors with K outside are read by the transposing reads; rows that start inside lines take more of them
-    double k = form == GEMM_FORM_LINEAR_RC || form == GEMM_FORM_GATED ? 1.0 : waves ? 1.07 : 1.27;
-    k *= rows == 16 ? 1.0 : rows == 4 ? (waves ? 1.46 : 1.34) : 3.4;
+    // factors with K outside are read by the transposing reads; rows that start inside lines touch more of these
+    double k = form == GEMM_FORM_LINEAR_RC || form == GEMM_FORM_GATED ? 1.0 : 1.08;
+    k *= rows == 16 ? 1.0 : rows == 4 ? 1.55 : 3.0;
     const double ends = c.ends * (form == GEMM_FORM_GATED_BACKWARD ? 1.6 : 1.0);
     const int64_t own = waves ? ceil_div(k_tiles, pg::linear_shape(tile).waves) : k_tiles;
     const int64_t slots = (int64_t)c.resident * num_cus, rounds = tiles / slots, rest = tiles % slots;

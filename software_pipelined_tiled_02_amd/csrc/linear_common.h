@@ -36,7 +36,6 @@ struct LinearArgs {
     int32_t tiles_m, tiles_n;
     int32_t act, bias_f32, accumulate;
     int32_t apart;           // some of the factors' rows do not start on 16 bytes
-    int32_t stream;          // the outputs' rows are whole lines: past the caches
 };
 
 // Tile classes: the workgroup's part of the sums (gated: half of the columns are
@@ -175,9 +174,8 @@ __device__ __forceinline__ void read8(Raw8<XT> r, int64_t n, int left, float* f)
 #pragma unroll
     for (int e = 0; e < 8; ++e) f[e] = (float)r.v[e];
 }
-// STREAM: past the caches.
 template <int XT, bool WHOLE>
-__device__ __forceinline__ void put8(void* base, int64_t at, int left, const float* f, bool stream) {
+__device__ __forceinline__ void put8(void* base, int64_t at, int left, const float* f) {
     typedef typename XTypeOf<XT>::type T;
     if constexpr (!WHOLE) {
         float v[8];
@@ -192,21 +190,10 @@ __device__ __forceinline__ void put8(void* base, int64_t at, int left, const flo
         if constexpr (XT == XT_F32) {
             struct Two { i32x4q a, b; };
             const Two two = __builtin_bit_cast(Two, r);
-            if (stream) {
-                __builtin_nontemporal_store(two.a, (i32x4u*)p);
-                __builtin_nontemporal_store(two.b, (i32x4u*)(p + 4));
-            } else {
-                asm volatile("" ::: "memory");       // (or the two become one form)
-                *(i32x4u*)p = two.a;
-                *(i32x4u*)(p + 4) = two.b;
-                asm volatile("" ::: "memory");
-            }
-        } else if (stream) {
-            __builtin_nontemporal_store(__builtin_bit_cast(i32x4q, r), (i32x4u*)p);
+            *(i32x4u*)p = two.a;
+            *(i32x4u*)(p + 4) = two.b;
         } else {
-            asm volatile("" ::: "memory");
             *(i32x4u*)p = __builtin_bit_cast(i32x4q, r);
-            asm volatile("" ::: "memory");
         }
     }
 }
@@ -257,11 +244,10 @@ template <int XT, int END, bool WHOLE, int Q>
 __device__ __forceinline__ void finish(const LinearArgs& p, int64_t m, int64_t step, int64_t n, Beside<XT, END> (&beside)[Q],
                                        const Biases<END>& bias, float (&v)[8 * Q], float (&u)[8 * Q]) {
     const int left = p.N - (int)n;
-    const bool stream = p.stream;
     const auto put = [&](int which, const float (&f)[8 * Q]) {
 #pragma unroll
         for (int q = 0; q < Q; ++q)
-            put8<XT, WHOLE>(p.out[which], (m + q * step) * p.ldo[which] + n, left, f + 8 * q, stream);
+            put8<XT, WHOLE>(p.out[which], (m + q * step) * p.ldo[which] + n, left, f + 8 * q);
     };
     if constexpr (END == END_LINEAR) {
 #pragma unroll
@@ -324,7 +310,7 @@ __device__ __forceinline__ void finish(const LinearArgs& p, int64_t m, int64_t s
         }
 #pragma unroll
         for (int q = 0; q < Q; ++q)
-            put8<XT_F32, WHOLE>(p.out[0], (m + q * step) * p.ldo[0] + n, left, v + 8 * q, stream);
+            put8<XT_F32, WHOLE>(p.out[0], (m + q * step) * p.ldo[0] + n, left, v + 8 * q);
     }
 }
 
