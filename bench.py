@@ -30,6 +30,9 @@ the ceiling of the same box.
 --workload fp8_linear is not one of the five: its step is one linear layer
 behind a norm, forward and backward, through the 8-bit operators, on bf16
 tokens; `value` is TFLOP/s of its three products, over all the step's time.
+--workload feed_forward is not either: one gated feed-forward block in bf16 with
+its residual, forward and backward, through the 16-bit operators; `value` is
+TFLOP/s of its nine products.
 
 Prints one JSON line.  `value` is TOP/s (int8) or TFLOP/s (fp) counting
 2*M*N*K operations (the convention of the pipelining study's benchmark
@@ -91,6 +94,8 @@ HEADLINE = "int8_4096"
 
 # The 8-bit linear layer: tokens, inputs and outputs.
 FP8_LINEAR = (8192, 4096, 4096)
+# The feed-forward block: tokens, inputs (and outputs), inner values.
+FEED_FORWARD = (8192, 4096, 8192)
 
 # MI355X published dense peaks (per GPU)
 PEAK = {"i8": 5033.2, "f16": 2516.6, "bf16": 2516.6, "f32": 157.3, "fp8": 5033.2}   # TOP/s, TFLOP/s
@@ -473,30 +478,76 @@ def measure_fp8_linear(args):
     import torch
 
     M, D, N = FP8_LINEAR
-    g = torch.Generator(device="cuda").manual_seed(0)
-
-    def normal(*shape):
-        return torch.randn(shape, generator=g, device="cuda")
-
+    normal = generator()
     sets = []
     for _ in range(2):                       # a set's tensors and the step's own exceed ROTATE_BYTES
         sets.append([normal(M, D).bfloat16(), normal(M, D).bfloat16(), (1 + 0.2 * normal(D)).bfloat16(),
                      normal(N, D) / D ** 0.5, normal(M, N).bfloat16(), normal(M, D).bfloat16(),
                      torch.zeros((N, D), device="cuda")])
+    return measure_step(args, fp8_linear_step, sets)
+
+
+def generator():
+    import torch
+
+    g = torch.Generator(device="cuda").manual_seed(0)
+    return lambda *shape: torch.randn(shape, generator=g, device="cuda")
+
+
+def feed_forward_step(x, gate, up, down, bias, dy, grads, mark=lambda name: None):
+    """y = x + (silu(x gate^T + bias) * (x up^T)) down^T, its gradient for x, and
+    added to `grads` those of gate, up, down and bias.  mark(name) is called
+    behind every operator."""
+    from software_pipelined_tiled_02_amd import binding
+
+    h, g, u = binding.gated(x, gate, up, gate_bias=bias, keep=True)
+    mark("gated")
+    y = binding.linear(h, down, residual=x)
+    mark("linear with residual")
+    dg, du, h = binding.gated_backward(dy, down, g, u, keep=True)
+    mark("gated backward")
+    binding.weight_gradient(dy, h, out=grads[2], accumulate=True)
+    mark("down's gradient (fp32, added)")
+    binding.weight_gradient(dg, x, out=grads[0], bias_out=grads[3], accumulate=True)
+    mark("gate's gradient and the bias's")
+    binding.weight_gradient(du, x, out=grads[1], accumulate=True)
+    mark("up's gradient")
+    dx = binding.linear(dg, gate, layout="RR", pair=(du, up), residual=dy)
+    mark("linear of two products for dx")
+    return y, dx
+
+
+def measure_feed_forward(args):
+    import torch
+
+    M, D, F = FEED_FORWARD
+    normal = generator()
+    sets = []
+    for _ in range(2):
+        sets.append([normal(M, D).bfloat16(), *((normal(*s) / s[1] ** 0.5).bfloat16() for s in ((F, D), (F, D), (D, F))),
+                     normal(F), normal(M, D).bfloat16(),
+                     [torch.zeros(s, device="cuda") for s in ((F, D), (F, D), (D, F), (F,))]])
+    return measure_step(args, feed_forward_step, sets)
+
+
+def measure_step(args, step, sets):
+    """Times `step` on the sets in turn: milliseconds, all rounds', and each operator's microseconds."""
+    import torch
+
     stream = torch.cuda.current_stream()
     deadline = time.monotonic() + 0.5        # settle the clocks
     while time.monotonic() < deadline:
-        fp8_linear_step(*sets[0])
+        step(*sets[0])
         torch.cuda.synchronize()
     rounds = []
     for _ in range(args.rounds):
         for i in range(args.warmup):
-            fp8_linear_step(*sets[i % 2])
+            step(*sets[i % 2])
         torch.cuda.synchronize()
         t0, t1 = (torch.cuda.Event(enable_timing=True) for _ in range(2))
         t0.record(stream)
         for i in range(args.steps):
-            fp8_linear_step(*sets[i % 2])
+            step(*sets[i % 2])
         t1.record(stream)
         torch.cuda.synchronize()
         rounds.append(t0.elapsed_time(t1) / args.steps)
@@ -512,7 +563,7 @@ def measure_fp8_linear(args):
             e.record(stream)
             marks.append((name, e))
 
-        fp8_linear_step(*sets[i % 2], mark=mark)
+        step(*sets[i % 2], mark=mark)
         torch.cuda.synchronize()
         for (_, a), (name, b) in zip(marks, marks[1:]):
             spent.setdefault(name, []).append(a.elapsed_time(b) * 1e3)
@@ -540,13 +591,32 @@ def fp8_linear(args):
         "rounds_ms": [round(t, 5) for t in rounds], "operators_us": spent}), flush=True)
 
 
+def feed_forward(args):
+    import torch
+
+    if not torch.cuda.is_available():
+        print("bench.py needs a GPU", file=sys.stderr)
+        sys.exit(1)
+    ms, rounds, spent = measure_feed_forward(args)
+    M, D, F = FEED_FORWARD
+    value = 9 * flops(M, F, D) / (ms * 1e-3) / 1e12
+    print(json.dumps({
+        "metric": "gated feed-forward block, forward and backward: TFLOP/s of its products over the whole step, 1 GPU",
+        "value": round(value, 2), "unit": "TFLOP/s", "n_gpus": 1, "steps": args.steps, "warmup": args.warmup,
+        "ms_per_step": round(ms, 5), "higher_is_better": True, "scaling": "weak", "vs_baseline": None,
+        "dtype": "bf16, weights' gradients in fp32", "data": "synthetic (seeded)",
+        "config": {"workload": "feed_forward", "tokens": M, "inputs": D, "inner": F},
+        "roofline": {"bound": "mfma", "peak_TFLOP/s": PEAK["bf16"], "frac_peak": round(value / PEAK["bf16"], 4)},
+        "rounds_ms": [round(t, 5) for t in rounds], "operators_us": spent}), flush=True)
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--gpus", type=int, default=1)
     ap.add_argument("--steps", type=int, default=20)
     ap.add_argument("--warmup", type=int, default=15)
     ap.add_argument("--rounds", type=int, default=3, help="rounds over all pairs; each pair reports its median")
-    ap.add_argument("--workload", default="all", choices=["all", "fp8_linear"] + sorted(WORKLOADS),
+    ap.add_argument("--workload", default="all", choices=["all", "fp8_linear", "feed_forward"] + sorted(WORKLOADS),
                     help="one workload, or all: the five benchmark workloads (headline int8 4096^3)")
     ap.add_argument("--pairs", default="all", help="comma list like 3:direct,2:reg, or all")
     ap.add_argument("--tile", default="auto", help="tile class: auto, 256x256, 256x256w8, 128x128, 32x64")
@@ -572,6 +642,8 @@ def main():
 
     if args.workload == "fp8_linear":
         return fp8_linear(args)
+    if args.workload == "feed_forward":
+        return feed_forward(args)
     names = FIVE if args.workload == "all" else [args.workload]
 
     # The ceiling probe runs first, as a child process, before this process
