@@ -483,9 +483,9 @@ int64_t gemm_rms_backward_workspace(int64_t M, int64_t D);
  * 2^-16 of its value of z as summed.  A NaN stays one.
  *
  * Leading dimensions are in elements; all rows may lie at any address that is
- * aligned to their elements.  Where every factor of a call has its base and
- * leading dimension on 16 bytes, K-tiles go straight into LDS; where one has
- * not, they pass through registers, which is slower.  No value of
+ * aligned to their elements.  Where all rows of a call's factors start on 4 bytes,
+ * K-tiles go straight into LDS (on 16 bytes, and with whole lines of 128, fastest);
+ * where one does not, they pass through registers, which is slower.  No value of
  * a factor outside its matrix counts, whatever it holds.
  *
  * Asynchronous: each enqueues one kernel on `stream`, on the handle's device,
@@ -494,10 +494,9 @@ int64_t gemm_rms_backward_workspace(int64_t M, int64_t D);
  * stated.  Sizes of zero are accepted.  Errors: GEMM_ERR_INVALID_ARG (NULL, a
  * negative size, an unknown type, a leading dimension below the row's length),
  * GEMM_ERR_ALIGNMENT (a pointer not aligned to its elements; a tile class asked
- * for that needs rows on 16 bytes), GEMM_ERR_UNSUPPORTED (a tile class that the
- * operator does not have; 256 rows of a factor
- * with K along its rows, or 64 of one with K across them, that span 2^31 bytes;
- * 2^32 threads), GEMM_ERR_HIP. */
+ * for that needs rows on 4 bytes), GEMM_ERR_UNSUPPORTED (a tile class that the
+ * operator does not have; 256 rows of a factor with K along its rows, or 64 of
+ * one with K across them, that span 2^31 bytes; 2^32 threads), GEMM_ERR_HIP. */
 enum { GEMM_ACT_NONE = 0, GEMM_ACT_RELU = 1, GEMM_ACT_GELU = 2, GEMM_ACT_GELU_TANH = 3, GEMM_ACT_SILU = 4 };
 
 /* Part of the sums that one workgroup computes (gated: half of its columns are
