@@ -94,11 +94,13 @@ int plan_sums(int form, int64_t M, int64_t N, int64_t K, int dtype, int rows, bo
         const pg::LinearShape sh = pg::linear_shape(t);
         return ceil_div(M, sh.bm) * ceil_div(N, gated ? sh.bn / 2 : sh.bn);
     };
+    // a launch has fewer than 2^32 threads
+    auto fits = [&](int t) { return tiles(t) < ((int64_t)1 << 32) / (64 * pg::linear_shape(t).waves); };
     int tc = tile;
     if (tc == GEMM_LINEAR_TILE_AUTO) {
         double best = 0.0;
         for (int t = 0; t < pg::LINEAR_TILE_COUNT; ++t) {
-            if (kernel(form, dtype, t, rows, extra) == nullptr) continue;
+            if (kernel(form, dtype, t, rows, extra) == nullptr || !fits(t)) continue;
             const double time = linear_time(t, form, rows, tiles(t), ceil_div(K, 64), num_cus);
             if (tc == GEMM_LINEAR_TILE_AUTO || time < best) {
                 tc = t;
@@ -106,6 +108,7 @@ int plan_sums(int form, int64_t M, int64_t N, int64_t K, int dtype, int rows, bo
             }
         }
     }
+    if (tc == GEMM_LINEAR_TILE_AUTO || !fits(tc)) return GEMM_ERR_UNSUPPORTED;
     plan->fn = kernel(form, dtype, tc, rows, extra);
     if (plan->fn == nullptr) return kernel(form, dtype, tc, 16, extra) == nullptr ? GEMM_ERR_UNSUPPORTED : GEMM_ERR_ALIGNMENT;
     const pg::LinearShape sh = pg::linear_shape(tc);
@@ -113,7 +116,6 @@ int plan_sums(int form, int64_t M, int64_t N, int64_t K, int dtype, int rows, bo
     plan->tiles_m = any ? ceil_div(M, sh.bm) : 0;
     plan->tiles_n = any ? ceil_div(N, gated ? sh.bn / 2 : sh.bn) : 0;
     const int64_t grid = plan->tiles_m * plan->tiles_n;
-    if (grid >= ((int64_t)1 << 32) / (64 * sh.waves) || grid > INT_MAX) return GEMM_ERR_UNSUPPORTED;
     gemm_linear_info_t& in = plan->info;
     memset(&in, 0, sizeof in);
     in.tile = tc;

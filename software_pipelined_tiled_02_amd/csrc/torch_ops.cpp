@@ -382,6 +382,34 @@ void same_k(const Matrix& a, int64_t k, const char* what) {
         throw BadArgument{"inner dimensions differ: " + std::to_string(a.cols) + ", and " + std::to_string(k) + " of " + what};
 }
 
+Matrix row_of(const void* p, int64_t cols, int type) {
+    Matrix m;
+    m.p = (char*)p;
+    m.rows = 1;
+    m.cols = m.ld = cols;
+    m.type = type;
+    return m;
+}
+// Whether two matrices have a byte in common.  Columns beside one another in rows of
+// one distance have none; of rows of two distances in each other's range that is
+// not worked out.
+bool touch(const Matrix& x, const Matrix& y) {
+    if (x.p == nullptr || y.p == nullptr || x.rows == 0 || y.rows == 0 || x.cols == 0 || y.cols == 0) return false;
+    const int64_t xs = x.type == GEMM_F32 ? 4 : 2, ys = y.type == GEMM_F32 ? 4 : 2;
+    const char* const x_end = x.p + ((x.rows - 1) * x.ld + x.cols) * xs;
+    const char* const y_end = y.p + ((y.rows - 1) * y.ld + y.cols) * ys;
+    if (x_end <= y.p || y_end <= x.p) return false;
+    const int64_t row = x.ld * xs;
+    if (x.rows == 1 || y.rows == 1 || y.ld * ys != row) return true;
+    const int64_t d = ((y.p - x.p) % row + row) % row;
+    return d < x.cols * xs || d + y.cols * ys > row;
+}
+// What is written lies apart from everything else.
+void apart(const Matrix& written, const char* what, std::initializer_list<Matrix> others) {
+    for (const Matrix& o : others)
+        if (touch(written, o)) throw BadArgument{std::string(what) + " overlaps another operand"};
+}
+
 // linear(a, b, layout, bias, activation, residual, a2, b2, keep, out, tile)
 PyObject* linear_(PyObject* const* arg, Py_ssize_t n) {
     arguments(n, 11);
@@ -399,6 +427,8 @@ PyObject* linear_(PyObject* const* arg, Py_ssize_t n) {
     // (an empty matrix has no address, which would read as none given)
     const bool second = a2.p != nullptr && b2.p != nullptr;
     Matrix c = halves_or_none(arg[9], "out", a, M, N), z;
+    apart(c, "out", {a, b, a2, b2, row_of(bias, N, bias_type)});
+    if (r.p != c.p || (r.ld != c.ld && M > 1)) apart(c, "out", {r});
     const gemm_handle_t h = handle_of(a.device);
     at::Tensor ct, zt;
     if (none(arg[9])) ct = made_like(at, M, N, &c);
@@ -430,6 +460,7 @@ PyObject* gated_(PyObject* const* arg, Py_ssize_t n) {
     const int64_t act = integer(arg[5]), tile = integer(arg[8]);
     const bool keep = truth(arg[6]);
     Matrix ho = halves_or_none(arg[7], "out", x, M, N), g, u;
+    apart(ho, "out", {x, wg, wu, row_of(bg, N, type), row_of(bu, N, type)});
     const gemm_handle_t h = handle_of(x.device);
     at::Tensor ht, gt, ut;
     if (none(arg[7])) ht = made_like(xt, M, N, &ho);
@@ -493,7 +524,9 @@ PyObject* weight_gradient_(PyObject* const* arg, Py_ssize_t n) {
     if (!none(arg[4])) {
         dbt = tensor(arg[4], "bias_out");
         if (vector(dbt, "bias_out", N, dc.device, -1) != GEMM_F32) throw BadArgument{"bias_out must be float32"};
+        apart(row_of(dbt.data_ptr(), N, GEMM_F32), "bias_out", {dc, a, dw});
     }
+    apart(dw, "out", {dc, a});
     const gemm_handle_t h = handle_of(dc.device);
     if (none(arg[2])) {
         dwt = empty({N, K}, {K, 1}, at::kFloat, dc.device);

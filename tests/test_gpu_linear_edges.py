@@ -172,3 +172,28 @@ def test_refusals():
         W(r, x, tile="16x32")
     assert err.value.status == binding.GEMM_ERR_UNSUPPORTED
     assert bool((L(x, w) == 64).all())                         # and the next call is fine
+
+
+def test_results_over_what_is_read():
+    """Refused, but for a residual's own place; columns beside one another do not overlap."""
+    g = gen(36)
+    buf = rand(g, 96, 256)
+    a, w, r = buf[:64, :64], rand(g, 64, 64), rand(g, 64, 64)
+    L, G, W = binding.linear, binding.gated, binding.weight_gradient
+    other = rand(g, 64, 64)
+    floats = torch.zeros((64, 65), device="cuda")
+    for call in (lambda: L(a, w, out=a), lambda: L(a, w, out=w), lambda: L(a, w, out=buf[32:, :64]), lambda: L(a, w, out=buf[:64, 63:127]),
+                 lambda: L(a, w, out=buf[:64, 1:65]), lambda: L(other, w, pair=(a, r), out=buf[5:69, :64]),
+                 lambda: L(other, w, residual=a, out=buf[1:65, :64]), lambda: L(other, w, residual=a, out=buf.view(192, 128)[:64, :64]),
+                 lambda: L(other, w, bias=buf[70, 3:67], out=buf[20:84, :64]), lambda: G(a, w, r, out=a), lambda: G(other, w, r, out=r),
+                 lambda: G(other, w, r, up_bias=buf[0, :64], out=a),
+                 lambda: W(other.float()[:1].view(torch.bfloat16)[:, :64], a, out=floats[:, :64], bias_out=floats[3, :64]),
+                 lambda: W(floats.view(torch.bfloat16)[:, :64], a, out=floats[:, :64])):
+        with pytest.raises(ValueError):
+            call()
+    want = L(a, w, residual=r)
+    got = buf[:64, 64:128]
+    assert L(a, w, residual=r, out=got) is got and torch.equal(got, want)
+    got = buf[:64, 128:192].copy_(r)
+    assert torch.equal(L(a, w, residual=got, out=got), want)
+    assert torch.equal(G(a, w, r, out=buf[3:67, 192:]), G(a, w, r))

@@ -84,6 +84,16 @@ def test_plan():
         assert q("linear_rc", 512, 512, 512, tile=tile, rows_on=2)[0] == want
 
 
+def test_plan_of_a_great_many_tiles():
+    """The smallest classes would take more threads than a launch may have: others do it."""
+    big = 2 ** 31 - 1024
+    for form, M, N, K in (("linear_rc", 1, big, 64), ("linear_rr", big, 1, 64), ("gated", 3, big // 2, 64), ("weight_gradient", 2, big, 1)):
+        for on in (16, 4, 2):
+            rc, info = q(form, M, N, K, rows_on=on)
+            assert rc == OK and info["grid"] * info["threads"] < 2 ** 32, (form, info)
+    assert q("linear_rc", 1, big, 64, tile="16x16")[0] == UNSUP and q("linear_rc", big, big, 64)[0] == UNSUP
+
+
 def test_query_refusals():
     assert q(5, 1, 1, 1)[0] == BAD and q(-1, 1, 1, 1)[0] == BAD
     for bad in (dict(dtype="f32"), dict(dtype="i8"), dict(rows_on=8), dict(rows_on=0), dict(tile=99), dict(tile=-2)):
