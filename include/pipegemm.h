@@ -483,9 +483,8 @@ int64_t gemm_rms_backward_workspace(int64_t M, int64_t D);
  * 2^-16 of its value of z as summed.  A NaN stays one.
  *
  * Leading dimensions are in elements; all rows may lie at any address that is
- * aligned to their elements.  Where all rows of a call's factors start on 4 bytes,
- * K-tiles go straight into LDS (on 16 bytes, and with whole lines of 128, fastest);
- * where one does not, they pass through registers, which is slower.  No value of
+ * aligned to their elements; rows on 16 bytes, and with whole lines of 128, are
+ * fastest.  No value of
  * a factor outside its matrix counts, whatever it holds.
  *
  * Asynchronous: each enqueues one kernel on `stream`, on the handle's device,
@@ -493,15 +492,14 @@ int64_t gemm_rms_backward_workspace(int64_t M, int64_t D);
  * can capture them.  Outputs must not overlap inputs or one another, but where
  * stated.  Sizes of zero are accepted.  Errors: GEMM_ERR_INVALID_ARG (NULL, a
  * negative size, an unknown type, a leading dimension below the row's length),
- * GEMM_ERR_ALIGNMENT (a pointer not aligned to its elements; a tile class asked
- * for that needs rows on 4 bytes), GEMM_ERR_UNSUPPORTED (a tile class that the
+ * GEMM_ERR_ALIGNMENT (a pointer not aligned to its elements), GEMM_ERR_UNSUPPORTED (a tile class that the
  * operator does not have; 256 rows of a factor with K along its rows, or 64 of
  * one with K across them, that span 2^31 bytes; 2^32 threads), GEMM_ERR_HIP. */
 enum { GEMM_ACT_NONE = 0, GEMM_ACT_RELU = 1, GEMM_ACT_GELU = 2, GEMM_ACT_GELU_TANH = 3, GEMM_ACT_SILU = 4 };
 
 /* Part of the sums that one workgroup computes (gated: half of its columns are
  * the second product's).  From 64x64_K4 on each wave takes parts of K of its
- * own.  128x128 and 64x64 take any rows, the others rows on 4 bytes.  Weight gradients have
+ * own.  Weight gradients have
  * those down to 32x32, gated layers those down to 16x32.  GEMM_LINEAR_TILE_AUTO: chosen by
  * the call's sizes. */
 enum { GEMM_LINEAR_TILE_AUTO = -1, GEMM_LINEAR_TILE_256x256 = 0, GEMM_LINEAR_TILE_128x256 = 1, GEMM_LINEAR_TILE_128x128 = 2,
@@ -515,8 +513,7 @@ typedef struct {
     int32_t tile;              /* GEMM_LINEAR_TILE_* chosen */
     int32_t block_m, block_n;  /* outputs of one workgroup */
     int32_t threads;           /* per workgroup */
-    int32_t rows_on;           /* bytes that all the factors' rows start on: 16, 4 or 2; from 4 on
-                                * K-tiles go straight into LDS */
+    int32_t rows16;            /* 1: all the factors' rows start on 16 bytes */
     int32_t reserved;
     int64_t grid;              /* workgroups */
     int64_t k_tiles;           /* ceil(K / 64), K the length of the sums */
@@ -556,10 +553,10 @@ int gemm_weight_gradient(gemm_handle_t h, int64_t M, int64_t N, int64_t K, int d
                          const void *DC, int64_t lddc, const void *A, int64_t lda, float *DW, int64_t lddw, float *DB,
                          void *stream);
 
-/* What a call of these sizes would launch on a 256-CU device (rows_on: 16,
- * 4 or 2, the bytes that all its factors' rows start on); M, N and K as the call
+/* What a call of these sizes would launch on a 256-CU device (rows_on_16:
+ * whether all its factors' rows start on 16 bytes); M, N and K as the call
  * takes them.  No HIP call. */
-int gemm_query_linear(int form, int64_t M, int64_t N, int64_t K, int dtype, int rows_on, int tile,
+int gemm_query_linear(int form, int64_t M, int64_t N, int64_t K, int dtype, int rows_on_16, int tile,
                       gemm_linear_info_t *info);
 
 /* Static text for a status code (never NULL). */

@@ -87,7 +87,7 @@ class Fp8Info(ctypes.Structure):
 
 
 class LinearInfo(ctypes.Structure):
-    _fields_ = [(n, ctypes.c_int32) for n in ("tile", "block_m", "block_n", "threads", "rows_on", "reserved")] + [
+    _fields_ = [(n, ctypes.c_int32) for n in ("tile", "block_m", "block_n", "threads", "rows16", "reserved")] + [
         ("grid", ctypes.c_int64), ("k_tiles", ctypes.c_int64)]
 
     def as_dict(self):
@@ -581,11 +581,11 @@ def gemm_weight_gradient(h, M, N, K, dtype, accumulate, tile, DC, lddc, A, lda, 
     return rc
 
 
-def gemm_query_linear(form, M, N, K, dtype="bf16", rows_on=16, tile="auto", check=True):
+def gemm_query_linear(form, M, N, K, dtype="bf16", rows16=True, tile="auto", check=True):
     """The kernel a call of these sizes would use (no HIP call).  Returns
     (status, dict)."""
     info = LinearInfo()
-    rc = _lib().gemm_query_linear(_enum(form, LINEAR_FORMS), M, N, K, _enum(dtype, DTYPES), int(rows_on),
+    rc = _lib().gemm_query_linear(_enum(form, LINEAR_FORMS), M, N, K, _enum(dtype, DTYPES), int(rows16),
                                   _enum(tile, LINEAR_TILES), ctypes.byref(info))
     if check and rc != GEMM_OK:
         raise GemmError(rc, "gemm_query_linear")
@@ -610,9 +610,9 @@ def linear(a, b, *, layout="RC", bias=None, activation="none", residual=None, pa
     handle; the current stream of a's device by default).  Argument errors raise
     ValueError, or GemmError with the C status, before anything is enqueued.
     The first call on a device sets it up, which a graph capture cannot hold
-    (RuntimeError).  Rows that start on 16 bytes are the fast case, rows on 4
-    take a few percent to half longer, others up to three times: a matrix of an
-    odd width is better held in padded rows.  out must overlap nothing else that the
+    (RuntimeError).  Rows that start on 16 bytes are the fast case, others take a
+    few percent to half longer: a matrix of an odd width is better held in padded
+    rows.  out must overlap nothing else that the
     call reads or writes."""
     if stream is not None:
         with _on_stream(stream, a):

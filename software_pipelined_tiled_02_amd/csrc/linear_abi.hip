@@ -32,24 +32,18 @@ struct Operand {
     int64_t step() const { return rows > 1 ? ld : (cols + 7) / 8 * 8; }
 };
 
-// What all of a factor's rows start on: 16, 4 or 2 bytes.  From 4 on they are staged
-// straight into LDS, from 16 on their last K-tiles too.
-int rows_on(const Operand& o) {
-    for (int n : {16, 4})
-        if (aligned(o.p, n) && o.step() * 2 % n == 0) return n;
-    return 2;
-}
+// Whether all of a factor's rows start on 16 bytes: the others' last K-tiles go through registers.
+bool rows16(const Operand& o) { return aligned(o.p, 16) && o.step() % 8 == 0; }
 
 // extra: a second product (linear), sums of DC's columns (weight gradients).
-const void* kernel(int form, int dtype, int tile, int rows, bool extra) {
+const void* kernel(int form, int dtype, int tile, bool extra) {
     const int xt = dtype == GEMM_BF16 ? pg::XT_BF16 : pg::XT_F16;
-    const bool r4 = rows >= 4;
     switch (form) {
-    case GEMM_FORM_LINEAR_RC: return pg::linear_rc_kernel(xt, tile, r4, extra);
-    case GEMM_FORM_LINEAR_RR: return pg::linear_rr_kernel(xt, tile, r4, extra);
-    case GEMM_FORM_GATED: return pg::gated_kernel(xt, tile, r4);
-    case GEMM_FORM_GATED_BACKWARD: return pg::gated_backward_kernel(xt, tile, r4);
-    default: return pg::weight_gradient_kernel(xt, tile, r4, extra);
+    case GEMM_FORM_LINEAR_RC: return pg::linear_rc_kernel(xt, tile, extra);
+    case GEMM_FORM_LINEAR_RR: return pg::linear_rr_kernel(xt, tile, extra);
+    case GEMM_FORM_GATED: return pg::gated_kernel(xt, tile);
+    case GEMM_FORM_GATED_BACKWARD: return pg::gated_backward_kernel(xt, tile);
+    default: return pg::weight_gradient_kernel(xt, tile, extra);
     }
 }
 
@@ -66,12 +60,12 @@ constexpr Cost kCost[pg::LINEAR_TILE_COUNT] = {{0.95, 1.80, 9.8, 1}, {0.60, 0.99
                                                {0.20, 0.67, 2.1, 3}, {0.79, 1.16, 2.9, 1}, {0.60, 0.91, 2.3, 1},
                                                {0.85, 1.20, 1.7, 1}, {0.63, 0.82, 1.9, 1}, {0.52, 0.63, 1.7, 1}};
 
-double linear_time(int tile, int form, int rows, int64_t tiles, int64_t k_tiles, int num_cus) {
+double linear_time(int tile, int form, bool r16, int64_t tiles, int64_t k_tiles, int num_cus) {
     const Cost& c = kCost[tile];
     const bool waves = pg::linear_few_tile(tile);            // (each has K-tiles of its own)
     // factors with K outside are read by the transposing reads; rows that start inside lines touch more of these
     double k = form == GEMM_FORM_LINEAR_RC || form == GEMM_FORM_GATED ? 1.0 : 1.08;
-    k *= rows == 16 ? 1.0 : rows == 4 ? 1.55 : 3.0;
+    k *= r16 ? 1.0 : 1.55;
     const double ends = c.ends * (form == GEMM_FORM_GATED_BACKWARD ? 1.6 : 1.0);
     const int64_t own = waves ? ceil_div(k_tiles, pg::linear_shape(tile).waves) : k_tiles;
     const int64_t slots = (int64_t)c.resident * num_cus, rounds = tiles / slots, rest = tiles % slots;
@@ -88,7 +82,7 @@ struct Plan {
 
 // The kernel for M x N sums over K (weight gradients: M and N are the weight's
 // rows and columns, K the tokens).  No HIP call.
-int plan_sums(int form, int64_t M, int64_t N, int64_t K, int dtype, int rows, bool extra, int tile, int num_cus, Plan* plan) {
+int plan_sums(int form, int64_t M, int64_t N, int64_t K, int dtype, bool r16, bool extra, int tile, int num_cus, Plan* plan) {
     const bool gated = form == GEMM_FORM_GATED;
     auto tiles = [&](int t) {
         const pg::LinearShape sh = pg::linear_shape(t);
@@ -100,8 +94,8 @@ int plan_sums(int form, int64_t M, int64_t N, int64_t K, int dtype, int rows, bo
     if (tc == GEMM_LINEAR_TILE_AUTO) {
         double best = 0.0;
         for (int t = 0; t < pg::LINEAR_TILE_COUNT; ++t) {
-            if (kernel(form, dtype, t, rows, extra) == nullptr || !fits(t)) continue;
-            const double time = linear_time(t, form, rows, tiles(t), ceil_div(K, 64), num_cus);
+            if (kernel(form, dtype, t, extra) == nullptr || !fits(t)) continue;
+            const double time = linear_time(t, form, r16, tiles(t), ceil_div(K, 64), num_cus);
             if (tc == GEMM_LINEAR_TILE_AUTO || time < best) {
                 tc = t;
                 best = time;
@@ -109,8 +103,8 @@ int plan_sums(int form, int64_t M, int64_t N, int64_t K, int dtype, int rows, bo
         }
     }
     if (tc == GEMM_LINEAR_TILE_AUTO || !fits(tc)) return GEMM_ERR_UNSUPPORTED;
-    plan->fn = kernel(form, dtype, tc, rows, extra);
-    if (plan->fn == nullptr) return kernel(form, dtype, tc, 16, extra) == nullptr ? GEMM_ERR_UNSUPPORTED : GEMM_ERR_ALIGNMENT;
+    plan->fn = kernel(form, dtype, tc, extra);
+    if (plan->fn == nullptr) return GEMM_ERR_UNSUPPORTED;
     const pg::LinearShape sh = pg::linear_shape(tc);
     const bool any = M > 0 && N > 0;
     plan->tiles_m = any ? ceil_div(M, sh.bm) : 0;
@@ -122,7 +116,7 @@ int plan_sums(int form, int64_t M, int64_t N, int64_t K, int dtype, int rows, bo
     in.block_m = sh.bm;
     in.block_n = gated ? sh.bn / 2 : sh.bn;
     in.threads = 64 * sh.waves;
-    in.rows_on = rows;
+    in.rows16 = r16 ? 1 : 0;
     in.grid = grid;
     in.k_tiles = ceil_div(K, 64);
     return GEMM_OK;
@@ -162,7 +156,7 @@ int first_of(std::initializer_list<int> codes) {
 int launch(gemm_handle_t h, const Plan& plan, pg::LinearArgs& a, void* stream) {
     a.tiles_m = (int32_t)plan.tiles_m;
     a.tiles_n = (int32_t)plan.tiles_n;
-    a.apart = plan.info.rows_on < 16 ? 1 : 0;
+    a.apart = plan.info.rows16 ? 0 : 1;
     void* kargs[] = {&a};
     return pg::on_device(h, [&] {
         const hipError_t e = hipLaunchKernel(plan.fn, dim3((unsigned)plan.info.grid), dim3((unsigned)plan.info.threads), kargs, 0,
@@ -175,13 +169,13 @@ int launch(gemm_handle_t h, const Plan& plan, pg::LinearArgs& a, void* stream) {
 
 extern "C" {
 
-int gemm_query_linear(int form, int64_t M, int64_t N, int64_t K, int dtype, int rows_on, int tile, gemm_linear_info_t* info) {
-    if (info == nullptr || !is_form(form) || (rows_on != 16 && rows_on != 4 && rows_on != 2)) return GEMM_ERR_INVALID_ARG;
+int gemm_query_linear(int form, int64_t M, int64_t N, int64_t K, int dtype, int rows_on_16, int tile, gemm_linear_info_t* info) {
+    if (info == nullptr || !is_form(form) || (rows_on_16 != 0 && rows_on_16 != 1)) return GEMM_ERR_INVALID_ARG;
     const int rc = check_sizes(M, N, K, dtype, tile);
     if (rc != GEMM_OK) return rc;
     Plan plan;
     const bool weight = form == GEMM_FORM_WEIGHT_GRADIENT;
-    const int got = plan_sums(form, weight ? N : M, weight ? K : N, weight ? M : K, dtype, rows_on, false, tile, kDefaultCus,
+    const int got = plan_sums(form, weight ? N : M, weight ? K : N, weight ? M : K, dtype, rows_on_16 == 1, false, tile, kDefaultCus,
                               &plan);
     if (got == GEMM_OK) *info = plan.info;
     return got;
@@ -201,19 +195,19 @@ int gemm_linear(gemm_handle_t h, int64_t M, int64_t N, int64_t K, int dtype, int
     const int products = A2 != nullptr ? 2 : 1;
     const Operand o[4] = {{A, lda, M, K, true}, {B, ldb, rr ? K : N, rr ? N : K, !rr},
                           {A2, lda2, M, K, true}, {B2, ldb2, rr ? K : N, rr ? N : K, !rr}};
-    int rows = 16;
+    bool r16 = true;
     if (reads)
         for (int i = 0; i < 2 * products; ++i) {
             if ((rc = check_factor(o[i])) != GEMM_OK) return rc;
             if (!factor_fits(o[i])) return GEMM_ERR_UNSUPPORTED;
-            rows = std::min(rows, rows_on(o[i]));
+            r16 = r16 && rows16(o[i]);
         }
     if (!any) return GEMM_OK;
     rc = first_of({check_rows(R, ldr, N, 2, false), check_rows(Z, ldz, N, 2, false), check_rows(C, ldc, N, 2, true)});
     if (rc != GEMM_OK) return rc;
     if (bias != nullptr && !aligned(bias, bias_dtype == GEMM_F32 ? 4 : 2)) return GEMM_ERR_ALIGNMENT;
     Plan plan;
-    rc = plan_sums(rr ? GEMM_FORM_LINEAR_RR : GEMM_FORM_LINEAR_RC, M, N, K, dtype, rows, products == 2, tile, h->num_cus, &plan);
+    rc = plan_sums(rr ? GEMM_FORM_LINEAR_RR : GEMM_FORM_LINEAR_RC, M, N, K, dtype, r16, products == 2, tile, h->num_cus, &plan);
     if (rc != GEMM_OK) return rc;
     pg::LinearArgs a;
     memset(&a, 0, sizeof a);
@@ -248,12 +242,12 @@ int gemm_gated(gemm_handle_t h, int64_t M, int64_t N, int64_t K, int dtype, int 
     if ((G == nullptr) != (U == nullptr)) return GEMM_ERR_INVALID_ARG;
     const bool any = M > 0 && N > 0, reads = any && K > 0;
     const Operand o[3] = {{X, ldx, M, K, true}, {WG, ldwg, N, K, true}, {WU, ldwu, N, K, true}};
-    int rows = 16;
+    bool r16 = true;
     if (reads)
         for (int i = 0; i < 3; ++i) {
             if ((rc = check_factor(o[i])) != GEMM_OK) return rc;
             if (!factor_fits(o[i])) return GEMM_ERR_UNSUPPORTED;
-            rows = std::min(rows, rows_on(o[i]));
+            r16 = r16 && rows16(o[i]);
         }
     if (!any) return GEMM_OK;
     rc = first_of({check_rows(G, ldg, N, 2, false), check_rows(U, ldu, N, 2, false), check_rows(H, ldh, N, 2, true)});
@@ -261,7 +255,7 @@ int gemm_gated(gemm_handle_t h, int64_t M, int64_t N, int64_t K, int dtype, int 
     const int bias_size = bias_dtype == GEMM_F32 ? 4 : 2;
     if (!aligned(BG, bias_size) || !aligned(BU, bias_size)) return GEMM_ERR_ALIGNMENT;
     Plan plan;
-    rc = plan_sums(GEMM_FORM_GATED, M, N, K, dtype, rows, false, tile, h->num_cus, &plan);
+    rc = plan_sums(GEMM_FORM_GATED, M, N, K, dtype, r16, false, tile, h->num_cus, &plan);
     if (rc != GEMM_OK) return rc;
     pg::LinearArgs a;
     memset(&a, 0, sizeof a);
@@ -296,12 +290,12 @@ int gemm_gated_backward(gemm_handle_t h, int64_t M, int64_t N, int64_t K, int dt
     if (rc != GEMM_OK) return rc;
     const bool any = M > 0 && N > 0, reads = any && K > 0;
     const Operand o[2] = {{DY, lddy, M, K, true}, {W, ldw, K, N, false}};
-    int rows = 16;
+    bool r16 = true;
     if (reads)
         for (int i = 0; i < 2; ++i) {
             if ((rc = check_factor(o[i])) != GEMM_OK) return rc;
             if (!factor_fits(o[i])) return GEMM_ERR_UNSUPPORTED;
-            rows = std::min(rows, rows_on(o[i]));
+            r16 = r16 && rows16(o[i]);
         }
     if (!any) return GEMM_OK;
     if ((U == nullptr) != (DU == nullptr)) return GEMM_ERR_INVALID_ARG;
@@ -309,7 +303,7 @@ int gemm_gated_backward(gemm_handle_t h, int64_t M, int64_t N, int64_t K, int dt
                    check_rows(DU, lddu, N, 2, false), check_rows(H, ldh, N, 2, false)});
     if (rc != GEMM_OK) return rc;
     Plan plan;
-    rc = plan_sums(GEMM_FORM_GATED_BACKWARD, M, N, K, dtype, rows, false, tile, h->num_cus, &plan);
+    rc = plan_sums(GEMM_FORM_GATED_BACKWARD, M, N, K, dtype, r16, false, tile, h->num_cus, &plan);
     if (rc != GEMM_OK) return rc;
     pg::LinearArgs a;
     memset(&a, 0, sizeof a);
@@ -343,18 +337,18 @@ int gemm_weight_gradient(gemm_handle_t h, int64_t M, int64_t N, int64_t K, int d
     const bool any = N > 0 && K > 0, reads = any && M > 0;
     if (N > 0 && K == 0 && DB != nullptr) return GEMM_ERR_UNSUPPORTED;      // no tile would add them
     const Operand o[2] = {{DC, lddc, M, N, false}, {A, lda, M, K, false}};
-    int rows = 16;
+    bool r16 = true;
     if (reads)
         for (int i = 0; i < 2; ++i) {
             if ((rc = check_factor(o[i])) != GEMM_OK) return rc;
             if (!factor_fits(o[i])) return GEMM_ERR_UNSUPPORTED;
-            rows = std::min(rows, rows_on(o[i]));
+            r16 = r16 && rows16(o[i]);
         }
     if (!any) return GEMM_OK;
     rc = first_of({check_rows(DW, lddw, K, 4, true), aligned(DB, 4) ? GEMM_OK : GEMM_ERR_ALIGNMENT});
     if (rc != GEMM_OK) return rc;
     Plan plan;
-    rc = plan_sums(GEMM_FORM_WEIGHT_GRADIENT, N, K, M, dtype, rows, DB != nullptr, tile, h->num_cus, &plan);
+    rc = plan_sums(GEMM_FORM_WEIGHT_GRADIENT, N, K, M, dtype, r16, DB != nullptr, tile, h->num_cus, &plan);
     if (rc != GEMM_OK) return rc;
     pg::LinearArgs a;
     memset(&a, 0, sizeof a);

@@ -6,15 +6,14 @@ namespace pg {
 namespace {
 
 template <int END, bool AIN, bool BIN, int EXTRA>
-const void* kernel(int xt, int tile, bool rows4) {
-    if (linear_few_tile(tile)) return rows4 ? few_by_type<END, AIN, BIN, EXTRA>(xt, tile) : nullptr;
-    return linear_by_type<END, AIN, BIN, EXTRA>(xt, tile, rows4);
+const void* kernel(int xt, int tile) {
+    return linear_few_tile(tile) ? few_by_type<END, AIN, BIN, EXTRA>(xt, tile) : linear_by_type<END, AIN, BIN, EXTRA>(xt, tile);
 }
 
 }  // namespace
 
-const void* gated_backward_kernel(int xt, int tile, bool rows4) {
-    return kernel<END_GATED_BACKWARD, true, false, 0>(xt, tile, rows4);
+const void* gated_backward_kernel(int xt, int tile) {
+    return kernel<END_GATED_BACKWARD, true, false, 0>(xt, tile);
 }
 
 }  // namespace pg

@@ -58,14 +58,14 @@ constexpr LinearShape linear_shape(int t) {
 }
 constexpr bool linear_few_tile(int t) { return t >= LINEAR_TILE_64K4; }
 
-// The kernel for a call: XT_F16 or XT_BF16, a tile class, whether all rows of
-// the factors start on 4 bytes (NULL: the class needs that), and a second
-// product (linear) or sums of A's rows (weight gradients).
-const void* linear_rc_kernel(int xt, int tile, bool rows4, bool pair);
-const void* linear_rr_kernel(int xt, int tile, bool rows4, bool pair);
-const void* gated_kernel(int xt, int tile, bool rows4);
-const void* gated_backward_kernel(int xt, int tile, bool rows4);
-const void* weight_gradient_kernel(int xt, int tile, bool rows4, bool sums);
+// The kernel for a call: XT_F16 or XT_BF16, a tile class (NULL: the operator does not
+// have it), and whether there is a second product (linear) or sums of A's rows
+// (weight gradients).
+const void* linear_rc_kernel(int xt, int tile, bool pair);
+const void* linear_rr_kernel(int xt, int tile, bool pair);
+const void* gated_kernel(int xt, int tile);
+const void* gated_backward_kernel(int xt, int tile);
+const void* weight_gradient_kernel(int xt, int tile, bool sums);
 
 #if defined(__HIPCC__)
 

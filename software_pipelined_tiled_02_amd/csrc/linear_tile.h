@@ -85,10 +85,12 @@ constexpr int out_swz(int row_bytes, int k) {
 // K as whole K-tiles and the values of one more, which is multiplied first.  Rows
 // that do not start on 16 bytes (`apart`) have their last K-tile there, whole or
 // not: all the others are read without a look at where rows and the matrix end.
-struct Depth { int whole, part; };
+// With K outside, their last row's last value may share a dword with the next row's
+// first one, so that many bytes more (`over`) are in range.
+struct Depth { int whole, part, over; };
 __device__ __forceinline__ Depth depth_of(int K, bool apart) {
     const int whole = (apart && K > 0 ? K - 1 : K) / kDeep;
-    return Depth{whole, K - whole * kDeep};
+    return Depth{whole, K - whole * kDeep, apart ? 2 : 0};
 }
 
 // Eight values of which `n` are there; the others become zero and are not read.
@@ -165,25 +167,18 @@ struct Factor {
 
     // The K-tile through registers: the chunks at the ends of rows are read only as far
     // as these go.
-    __device__ __forceinline__ void gather(i32x4 (&v)[L]) const {
-        const bool ragged = INSIDE ? rem > 0 && rem < kDeep : left < CR * 8;
+    __device__ __forceinline__ void carry(uint8_t PG_LDS* to, int tid) const {
+        const bool ragged = INSIDE ? rem < kDeep : left < CR * 8;
+        i32x4 v[L];
 #pragma unroll
         for (int j = 0; j < L; ++j) {
-            const __amdgpu_buffer_rsrc_t r = resource(j);
             const int c = TURNS && (j & 1) ? at ^ 16 : at;
             // (K outside: a chunk's place past the matrix was moved to its first one, whole or not)
-            if (ragged) v[j] = load_some(r, offset(j), INSIDE ? rem - c : min(c < left ? left - c : left, 8));
-            else v[j] = __builtin_amdgcn_raw_buffer_load_b128(r, offset_in(j), 0, 0);
+            if (ragged) v[j] = load_some(resource(j), offset(j), INSIDE ? rem - c : min(c < left ? left - c : left, 8));
+            else v[j] = __builtin_amdgcn_raw_buffer_load_b128(resource(j), offset(j), 0, 0);
         }
-    }
-    __device__ __forceinline__ void put(uint8_t PG_LDS* to, const i32x4 (&v)[L], int tid) const {
 #pragma unroll
         for (int j = 0; j < L; ++j) *(i32x4 PG_LDS*)(to + (j * T + tid) * kChunk) = v[j];
-    }
-    __device__ __forceinline__ void carry(uint8_t PG_LDS* to, int tid) const {
-        i32x4 v[L];
-        gather(v);
-        put(to, v, tid);
     }
 
     // K-tile number i of the order.
@@ -206,7 +201,7 @@ struct Factor {
         const int64_t row = second ? ld[P - 1] : ld[0];
         from = (second ? base[P - 1] : base[0]) + (int64_t)k * (INSIDE ? 128 : kDeep * row);
         rem = more > 0 ? rem : 0;
-        size = more <= 0 ? 0 : INSIDE ? 0x7fffffff : (int)(rem * row);
+        size = more <= 0 ? 0 : INSIDE ? 0x7fffffff : (int)(rem * row) + (i >= parts ? d.over : 0);
         if constexpr (BOTH) from_u = base_u + (int64_t)k * 128;
     }
     // On to the next one, both whole (or behind the last).  Without a branch: one
@@ -226,7 +221,7 @@ struct Factor {
         second = round ? false : second;
         kb = round ? 0 : kb;
         from = to;
-        size = more > 0 ? (INSIDE ? 0x7fffffff : (int)(kDeep * (P == 2 && second ? ld[P - 1] : ld[0]))) : 0;
+        size = more > 0 ? (INSIDE ? 0x7fffffff : (int)(kDeep * (P == 2 && second ? ld[P - 1] : ld[0])) + d.over) : 0;
     }
 
     // Product q's matrix p; elements of 2 bytes, ld_ in elements.  tid: of T.
@@ -333,7 +328,7 @@ __device__ __forceinline__ float add_pair(i32x4 chunk, int e, float sum) {
     }
 }
 
-template <int XT, int END, bool AIN, bool BIN, bool DIRECT, int BM, int BN, int WM, int WN, int SA, int SB, int EXTRA>
+template <int XT, int END, bool AIN, bool BIN, int BM, int BN, int WM, int WN, int SA, int SB, int EXTRA>
 struct Tile {
     static constexpr bool SPLIT = END == END_GATED;
     static constexpr bool SUMS = END == END_WEIGHT && EXTRA != 0;        // of A's rows too
@@ -354,7 +349,7 @@ struct Tile {
     static constexpr bool QUADS = FM == 8 && FN == 8;    // one wave per SIMD
     static constexpr int OUTS = SPLIT ? WTN / 2 : WTN;   // a wave's outputs per row
     static_assert(LDS <= kLdsBudget && FM % 2 == 0 && (!SPLIT || FN % 2 == 0), "tile");
-    static_assert(!DIRECT ? SA == 2 && SB == 2 : QUADS ? SA == 3 && SB == 2 : SA == SB, "register-staged K-tiles: two slots");
+    static_assert(QUADS ? SA == 3 && SB == 2 : SA == SB, "slots");
 
     struct State {
         FA a;
@@ -463,12 +458,10 @@ struct Tile {
 
     // Unit `u` of the two steps behind the hand-over: its load, if it has one.
     __device__ static __forceinline__ void spread(const State& s, int u, uint8_t PG_LDS* a_to, uint8_t PG_LDS* b_to) {
-        if constexpr (DIRECT) {
-            const int q = u * LPT / (2 * UNITS);
-            if ((u + 1) * LPT / (2 * UNITS) > q) {
-                if (q < LB) s.b.load(q, b_to, s.wave);
-                else s.a.load(q - LB, a_to, s.wave);
-            }
+        const int q = u * LPT / (2 * UNITS);
+        if ((u + 1) * LPT / (2 * UNITS) > q) {
+            if (q < LB) s.b.load(q, b_to, s.wave);
+            else s.a.load(q - LB, a_to, s.wave);
         }
     }
     // Fragment r of step H of the K-tile at `a`, `b`, in the order of their use.
@@ -523,76 +516,37 @@ struct Tile {
 #pragma unroll
             for (int r = 0; r < READS; ++r) read_one<0>(ra, rb, f, tile_a(0), tile_b(0), r);
         };
-        if constexpr (DIRECT) {
-            // The first SB - 1 K-tiles, and of the next one what a second step takes.
-            static_assert(SA == SB && SB > P && LPT % 2 == 0, "");
+        // The first SB - 1 K-tiles, and of the next one what a second step takes.
+        static_assert(SA == SB && SB > P && LPT % 2 == 0, "");
 #pragma unroll
-            for (int t = 0; t < SB; ++t) {
-                s.a.start(t, s.deep, s.rot);
-                s.b.start(t, s.deep, s.rot);
-                if (t + 1 < SB) {
-                    begin(s, t, tile_a(t), tile_b(t));
-                } else {
+        for (int t = 0; t < SB; ++t) {
+            s.a.start(t, s.deep, s.rot);
+            s.b.start(t, s.deep, s.rot);
+            if (t + 1 < SB) {
+                begin(s, t, tile_a(t), tile_b(t));
+            } else {
 #pragma unroll
-                    for (int u = 0; u < UNITS; ++u) spread(s, u, tile_a(t), tile_b(t));
-                }
+                for (int u = 0; u < UNITS; ++u) spread(s, u, tile_a(t), tile_b(t));
             }
-            wait_loads<(SB - 2) * LPT + LPT / 2>();
-            barrier();
-            clear_tails(s, tile_a, tile_b);
-            if (s.nt > 0) {
-                first_fragments();
-                step_of_two<0, true>(s, ra, rb, f, tile_a(0), tile_b(0), tile_a(SB - 1), tile_b(SB - 1), wn);
-                int slot = 0;
-                for (int t = 0; t + 1 < s.nt; ++t) {
-                    const int next = slot + 1 == SB ? 0 : slot + 1;
-                    s.a.next(s.deep);
-                    s.b.next(s.deep);
-                    wait_loads<(SB - 2) * LPT>();            // K-tile t + 1 has landed (this wave's part)
-                    barrier();                               // ... everyone's, and K-tile t's place is free
-                    step_of_two<1, true>(s, ra, rb, f, tile_a(next), tile_b(next), tile_a(slot), tile_b(slot), wn);
-                    step_of_two<0, true>(s, ra, rb, f, tile_a(next), tile_b(next), tile_a(slot), tile_b(slot), wn);
-                    slot = next;
-                }
-                step_of_two<1, false>(s, ra, rb, f, nullptr, nullptr, nullptr, nullptr, wn);
+        }
+        wait_loads<(SB - 2) * LPT + LPT / 2>();
+        barrier();
+        clear_tails(s, tile_a, tile_b);
+        if (s.nt > 0) {
+            first_fragments();
+            step_of_two<0, true>(s, ra, rb, f, tile_a(0), tile_b(0), tile_a(SB - 1), tile_b(SB - 1), wn);
+            int slot = 0;
+            for (int t = 0; t + 1 < s.nt; ++t) {
+                const int next = slot + 1 == SB ? 0 : slot + 1;
+                s.a.next(s.deep);
+                s.b.next(s.deep);
+                wait_loads<(SB - 2) * LPT>();            // K-tile t + 1 has landed (this wave's part)
+                barrier();                               // ... everyone's, and K-tile t's place is free
+                step_of_two<1, true>(s, ra, rb, f, tile_a(next), tile_b(next), tile_a(slot), tile_b(slot), wn);
+                step_of_two<0, true>(s, ra, rb, f, tile_a(next), tile_b(next), tile_a(slot), tile_b(slot), wn);
+                slot = next;
             }
-        } else {
-            // Rows on 2 bytes go through registers (500 x 4104 x 4100: 50 us, 42
-            // straight into LDS; x 4104 in rows on 16 39).  REGS K-tiles are on the way in registers; groups of so many are whole,
-            // the K-tiles behind the last being zeros.
-            constexpr int REGS = 3;
-            i32x4 staged_a[REGS][LA], staged_b[REGS][LB];
-            auto stage = [&](int t, int r) {
-                s.a.start(t, s.deep, s.rot);
-                s.b.start(t, s.deep, s.rot);
-                s.a.gather(staged_a[r]);
-                s.b.gather(staged_b[r]);
-            };
-            stage(0, 0);
-            s.a.put(tile_a(0), staged_a[0], threadIdx.x);
-            s.b.put(tile_b(0), staged_b[0], threadIdx.x);
-#pragma unroll
-            for (int r = 0; r < REGS; ++r) stage(1 + r, r);
-            barrier();
-            if (s.nt > 0) {
-                first_fragments();
-                step_of_two<0, true>(s, ra, rb, f, tile_a(0), tile_b(0), nullptr, nullptr, wn);
-                int next = 1;
-                for (int t = 0; t + 1 < s.nt; t += REGS) {
-#pragma unroll
-                    for (int r = 0; r < REGS; ++r) {
-                        // (what was in the place was read before the last barrier)
-                        s.a.put(tile_a(next), staged_a[r], threadIdx.x);
-                        s.b.put(tile_b(next), staged_b[r], threadIdx.x);
-                        barrier();
-                        stage(t + r + 1 + REGS, r);
-                        step_of_two<1, true>(s, ra, rb, f, tile_a(next), tile_b(next), nullptr, nullptr, wn);
-                        step_of_two<0, true>(s, ra, rb, f, tile_a(next), tile_b(next), nullptr, nullptr, wn);
-                        next ^= 1;
-                    }
-                }
-                step_of_two<1, false>(s, ra, rb, f, nullptr, nullptr, nullptr, nullptr, wn);
-            }
+            step_of_two<1, false>(s, ra, rb, f, nullptr, nullptr, nullptr, nullptr, wn);
         }
         wait_loads<0>();                     // no write into LDS outlives the K loop
         barrier();
@@ -819,9 +773,9 @@ struct Tile {
     }
 };
 
-template <int XT, int END, bool AIN, bool BIN, bool DIRECT, int BM, int BN, int WM, int WN, int SA, int SB, int EXTRA>
+template <int XT, int END, bool AIN, bool BIN, int BM, int BN, int WM, int WN, int SA, int SB, int EXTRA>
 __global__ void __launch_bounds__(WM * WN * 64) linear_tile(LinearArgs p) {
-    typedef Tile<XT, END, AIN, BIN, DIRECT, BM, BN, WM, WN, SA, SB, EXTRA> S;
+    typedef Tile<XT, END, AIN, BIN, BM, BN, WM, WN, SA, SB, EXTRA> S;
     __shared__ __attribute__((aligned(16))) uint8_t smem[S::LDS];
     S::run(p, (uint8_t PG_LDS*)smem);
 }
@@ -829,25 +783,18 @@ __global__ void __launch_bounds__(WM * WN * 64) linear_tile(LinearArgs p) {
 // The classes of one ending.  EXTRA: a second product (linear), sums of A's rows
 // (weight gradients).
 template <int XT, int END, bool AIN, bool BIN, int EXTRA>
-const void* linear_by_tile(int tile, bool rows4) {
+const void* linear_by_tile(int tile) {
     switch (tile) {
-    case LINEAR_TILE_256:
-        return rows4 ? (const void*)&linear_tile<XT, END, AIN, BIN, true, 256, 256, 2, 2, 3, 2, EXTRA> : nullptr;
-    case LINEAR_TILE_128x256:
-        return rows4 ? (const void*)&linear_tile<XT, END, AIN, BIN, true, 128, 256, 2, 2, 3, 3, EXTRA> : nullptr;
-    case LINEAR_TILE_128:
-        return rows4 ? (const void*)&linear_tile<XT, END, AIN, BIN, true, 128, 128, 2, 2, 4, 4, EXTRA>
-                      : (const void*)&linear_tile<XT, END, AIN, BIN, false, 128, 128, 2, 2, 2, 2, EXTRA>;
-    case LINEAR_TILE_64:
-        return rows4 ? (const void*)&linear_tile<XT, END, AIN, BIN, true, 64, 64, 2, 2, 3, 3, EXTRA>
-                      : (const void*)&linear_tile<XT, END, AIN, BIN, false, 64, 64, 2, 2, 2, 2, EXTRA>;
+    case LINEAR_TILE_256: return (const void*)&linear_tile<XT, END, AIN, BIN, 256, 256, 2, 2, 3, 2, EXTRA>;
+    case LINEAR_TILE_128x256: return (const void*)&linear_tile<XT, END, AIN, BIN, 128, 256, 2, 2, 3, 3, EXTRA>;
+    case LINEAR_TILE_128: return (const void*)&linear_tile<XT, END, AIN, BIN, 128, 128, 2, 2, 4, 4, EXTRA>;
+    case LINEAR_TILE_64: return (const void*)&linear_tile<XT, END, AIN, BIN, 64, 64, 2, 2, 3, 3, EXTRA>;
     default: return nullptr;
     }
 }
 template <int END, bool AIN, bool BIN, int EXTRA>
-const void* linear_by_type(int xt, int tile, bool rows4) {
-    return xt == XT_BF16 ? linear_by_tile<XT_BF16, END, AIN, BIN, EXTRA>(tile, rows4)
-                         : linear_by_tile<XT_F16, END, AIN, BIN, EXTRA>(tile, rows4);
+const void* linear_by_type(int xt, int tile) {
+    return xt == XT_BF16 ? linear_by_tile<XT_BF16, END, AIN, BIN, EXTRA>(tile) : linear_by_tile<XT_F16, END, AIN, BIN, EXTRA>(tile);
 }
 
 }  // namespace pg

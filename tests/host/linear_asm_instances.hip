@@ -3,12 +3,12 @@
 
 namespace pg {
 
-const void* instances(int t, bool r16, bool rr, bool backward, bool sums, bool pair) {
-    if (pair) return linear_by_tile<XT_F16, END_LINEAR, true, false, 1>(t, r16);
-    if (rr) return linear_by_tile<XT_BF16, END_LINEAR, true, false, 0>(t, r16);
-    if (backward) return linear_by_tile<XT_F16, END_GATED_BACKWARD, true, false, 0>(t, r16);
-    if (sums) return linear_by_tile<XT_BF16, END_WEIGHT, false, false, 1>(t, r16);
-    return linear_by_tile<XT_F16, END_WEIGHT, false, false, 0>(t, r16);
+const void* instances(int t, bool rr, bool backward, bool sums, bool pair) {
+    if (pair) return linear_by_tile<XT_F16, END_LINEAR, true, false, 1>(t);
+    if (rr) return linear_by_tile<XT_BF16, END_LINEAR, true, false, 0>(t);
+    if (backward) return linear_by_tile<XT_F16, END_GATED_BACKWARD, true, false, 0>(t);
+    if (sums) return linear_by_tile<XT_BF16, END_WEIGHT, false, false, 1>(t);
+    return linear_by_tile<XT_F16, END_WEIGHT, false, false, 0>(t);
 }
 
 const void* few_instances(int t, bool rr, bool backward, bool sums, bool pair) {

@@ -11,7 +11,6 @@ from tests.linear_ref import FT, assert_within, place
 pytestmark = pytest.mark.gpu
 
 TILES = ("256x256", "128x256", "128x128", "64x64", "64x64k4", "64x32", "32x32", "16x32", "16x16")
-ANY_ROWS = ("128x128", "64x64", "auto")                # the classes that take rows at any address
 
 
 def rand(g, rows, cols, dtype, size=1.0):
@@ -52,7 +51,7 @@ def test_linear_every_class(M, N, K, tile, layout, dtype):
 
 
 @pytest.mark.parametrize("layout", ("RC", "RR"))
-@pytest.mark.parametrize("tile", ("128x128", "64x64"))
+@pytest.mark.parametrize("tile", TILES)
 @pytest.mark.parametrize("M,N,K,lda,ldb,offset", ((130, 260, 77, 77, None, 0), (70, 67, 130, 131, None, 1), (150, 300, 200, 203, None, 3),
                                                   (65, 7, 5, 5, None, 0), (3, 129, 64, 71, None, 5), (1, 9, 300, 300, None, 1)))
 def test_linear_rows_at_any_address(M, N, K, lda, ldb, offset, tile, layout):
@@ -112,12 +111,43 @@ def test_others_of_rows_on_4_bytes(M, N, K, tile):
             assert_within(sums, db, db_off, "db")
 
 
+def tight(t):
+    """t in rows without a gap, at an address on 2 bytes only; its buffer ends with it."""
+    return place(t, t.shape[1], 1)
+
+
+# rows of odd lengths one behind another, which share dwords; one value, and one more than whole K-tiles of them
+@pytest.mark.parametrize("dtype", ("bf16", "f16"))
+@pytest.mark.parametrize("tile", TILES + ("auto",))
+@pytest.mark.parametrize("M,N,K", ((65, 1, 129), (129, 33, 65), (1, 257, 193), (200, 65, 1), (130, 7, 257), (67, 131, 64), (257, 263, 321)))
+def test_odd_rows_without_a_gap(M, N, K, tile, dtype):
+    g = gen(22)
+    x, w, w2 = rand(g, M, K, dtype), rand(g, N, K, dtype, K ** -0.5), rand(g, N, K, dtype, K ** -0.5)
+    r, up = rand(g, M, N, dtype), rand(g, M, N, dtype)
+    rr, rr2 = w.t().contiguous(), w2.t().contiguous()
+    check_linear(x, w, binding.linear(tight(x), tight(w), residual=tight(r), tile=tile), None, dtype, residual=r, what="RC")
+    check_linear(x, rr, binding.linear(tight(x), tight(rr), layout="RR", tile=tile), None, dtype, "RR", what="RR")
+    check_linear(x, rr, binding.linear(tight(x), tight(rr), layout="RR", pair=(tight(x), tight(rr2)), tile=tile), None, dtype, "RR",
+                 pair=(x, rr2), what="pair")
+    if tile != "16x16":
+        for v, (want, off), name in zip(binding.gated(tight(x), tight(w), tight(w2), keep=True, tile=tile),
+                                        R.gated(x.double(), w.double(), w2.double(), dtype, "silu"), "hgu"):
+            assert_within(v, want, off, name)
+    for v, (want, off) in zip(binding.gated_backward(tight(x), tight(rr), tight(r), tight(up), keep=True, tile=tile),
+                              R.gated_backward(x.double(), rr.double(), r.double(), up.double(), dtype, "silu")):
+        assert_within(v, want, off, "backward")
+    if tile not in TILES[7:]:
+        # K tokens of an N x M weight
+        dw, off, db, db_off = R.weight_gradient(rr.double(), x.double().t())
+        got, sums = binding.weight_gradient(tight(rr), tight(x.t().contiguous()), bias=True, tile=tile)
+        assert_within(got, dw, off, "dw")
+        assert_within(sums, db, db_off, "db")
+
+
 @pytest.mark.parametrize("layout", ("RC", "RR"))
 @pytest.mark.parametrize("tile", TILES + ("auto",))
 @pytest.mark.parametrize("M,N,K,odd", ((300, 280, 136, False), (65, 72, 67, False), (129, 100, 203, True), (20, 33, 64, True), (40, 40, 7, True)))
 def test_linear_two_products(M, N, K, odd, tile, layout):
-    if odd and tile not in ANY_ROWS:
-        pytest.skip("a class of rows on 16 bytes")
     g, shape = gen(3), (N, K) if layout == "RC" else (K, N)
     ms = [rand(g, M, K, "bf16"), rand(g, *shape, "bf16", K ** -0.5), rand(g, M, K, "bf16"), rand(g, *shape, "bf16", K ** -0.5)]
     r = rand(g, M, N, "bf16")
@@ -229,8 +259,6 @@ def test_empty_sizes():
 @pytest.mark.parametrize("M,N,K,odd", ((300, 140, 200, False), (65, 33, 64, False), (1, 1, 1, False), (257, 17, 129, False),
                                        (130, 200, 77, True), (31, 64, 128, True), (1, 3, 9, True)))
 def test_gated(M, N, K, odd, tile, dtype):
-    if odd and tile not in ANY_ROWS:
-        pytest.skip("a class of rows on 16 bytes")
     g = gen(7)
     x, wg, wu = rand(g, M, K, dtype), rand(g, N, K, dtype, K ** -0.5), rand(g, N, K, dtype, K ** -0.5)
     bg, bu = (torch.randn(N, generator=g, device="cuda").to(FT[dtype]) for _ in range(2))
@@ -251,8 +279,6 @@ def test_gated(M, N, K, odd, tile, dtype):
 @pytest.mark.parametrize("M,N,K,odd", ((300, 264, 200, False), (65, 67, 64, False), (1, 1, 1, False), (130, 201, 77, True),
                                        (31, 6, 128, True), (2, 130, 3, True)))
 def test_gated_backward(M, N, K, odd, tile, gate, dtype):
-    if odd and tile not in ANY_ROWS:
-        pytest.skip("a class of rows on 16 bytes")
     rng = gen(8)
     dy, w = rand(rng, M, K, dtype, 0.1), rand(rng, K, N, dtype, K ** -0.5)
     g, u = rand(rng, M, N, dtype, 2.0), rand(rng, M, N, dtype) if gate else None
@@ -276,8 +302,6 @@ def test_gated_backward(M, N, K, odd, tile, gate, dtype):
 @pytest.mark.parametrize("M,N,K,odd", ((200, 300, 264, False), (64, 257, 130, False), (1, 70, 33, False), (129, 1, 1, False),
                                        (330, 129, 513, False), (77, 130, 201, True), (65, 9, 6, True), (1, 31, 67, True), (3, 2, 130, True)))
 def test_weight_gradient(M, N, K, odd, tile, dtype):
-    if odd and tile not in ANY_ROWS:
-        pytest.skip("a class of rows on 16 bytes")
     g = gen(9)
     dc, a = rand(g, M, N, dtype), rand(g, M, K, dtype)
     at = [place(dc, N + 1, 1), place(a, K + 3, 3)] if odd else [rows16(dc), rows16(a)]

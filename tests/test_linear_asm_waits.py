@@ -54,7 +54,7 @@ def kernels():
 
 
 def test_every_transposing_read_is_waited_for(kernels):
-    assert len(kernels) == 51, sorted(kernels)
+    assert len(kernels) == 41, sorted(kernels)
     for name, insts in kernels.items():
         assert any(k == "inst" and t.startswith("ds_read_b64_tr") for k, t in insts), name
         bad = check(insts)

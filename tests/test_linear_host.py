@@ -70,33 +70,28 @@ def test_plan():
     for form in binding.LINEAR_FORMS:
         for M, N, K in ((1, 4096, 4096), (64, 8192, 8192), (500, 4104, 4100), (8192, 8192, 8200), (0, 16, 16), (16, 0, 16), (16, 16, 0),
                         (8192, 1000, 24), (7, 100000, 3)):
-            for on in (16, 4, 2):
-                rc, info = q(form, M, N, K, rows_on=on)
-                assert rc == OK and info["rows_on"] == on
+            for r16 in (True, False):
+                rc, info = q(form, M, N, K, rows16=r16)
+                assert rc == OK and info["rows16"] == int(r16)
                 rows, cols, depth = (N, K, M) if form == "weight_gradient" else (M, N, K)
                 want = -(-rows // info["block_m"]) * -(-cols // info["block_n"]) if rows and cols else 0
                 assert info["grid"] == want and info["k_tiles"] == -(-depth // 64), (form, M, N, K, info)
-                assert on >= 4 or info["tile"] in (binding.LINEAR_TILES["128x128"], binding.LINEAR_TILES["64x64"])
     assert q("linear_rc", 8192, 8192, 8200)[1]["tile"] == binding.LINEAR_TILES["256x256"]
-    for tile in binding.LINEAR_TILES:
-        want = OK if tile in ("auto", "128x128", "64x64") else ALIGN
-        assert q("linear_rc", 512, 512, 512, tile=tile, rows_on=4)[0] == OK
-        assert q("linear_rc", 512, 512, 512, tile=tile, rows_on=2)[0] == want
 
 
 def test_plan_of_a_great_many_tiles():
     """The smallest classes would take more threads than a launch may have: others do it."""
     big = 2 ** 31 - 1024
     for form, M, N, K in (("linear_rc", 1, big, 64), ("linear_rr", big, 1, 64), ("gated", 3, big // 2, 64), ("weight_gradient", 2, big, 1)):
-        for on in (16, 4, 2):
-            rc, info = q(form, M, N, K, rows_on=on)
+        for r16 in (True, False):
+            rc, info = q(form, M, N, K, rows16=r16)
             assert rc == OK and info["grid"] * info["threads"] < 2 ** 32, (form, info)
     assert q("linear_rc", 1, big, 64, tile="16x16")[0] == UNSUP and q("linear_rc", big, big, 64)[0] == UNSUP
 
 
 def test_query_refusals():
     assert q(5, 1, 1, 1)[0] == BAD and q(-1, 1, 1, 1)[0] == BAD
-    for bad in (dict(dtype="f32"), dict(dtype="i8"), dict(rows_on=8), dict(rows_on=0), dict(tile=99), dict(tile=-2)):
+    for bad in (dict(dtype="f32"), dict(dtype="i8"), dict(rows16=2), dict(tile=99), dict(tile=-2)):
         assert q("gated", 1, 1, 1, **bad)[0] == BAD, bad
     assert q("gated", -1, 1, 1)[0] == BAD and q("gated", 1, -1, 1)[0] == BAD and q("gated", 1, 1, -1)[0] == BAD
     assert q("linear_rc", 2 ** 31, 1, 1)[0] == UNSUP and q("linear_rc", 1, 2 ** 31, 1)[0] == UNSUP
@@ -153,7 +148,6 @@ def test_refusals_of_every_operator():
         if fn is not linear:
             for p in ps:
                 assert fn(**{p: None}) == BAD, p
-        assert fn(tile="256x256", **{lds[0]: 65}) == ALIGN and fn(tile="256x256", **{ps[-1]: P + 2}) == ALIGN
     for fn, ps, lds, needed in OTHERS:
         size = 4 if fn is weight else 2
         for p in ps:
