@@ -95,7 +95,8 @@ int plan_sums(int form, int64_t M, int64_t N, int64_t K, int dtype, bool r16, bo
         double best = 0.0;
         for (int t = 0; t < pg::LINEAR_TILE_COUNT; ++t) {
             if (kernel(form, dtype, t, extra) == nullptr || !fits(t)) continue;
-            const double time = linear_time(t, form, r16, tiles(t), ceil_div(K, 64), num_cus);
+            const int64_t products = extra && form <= GEMM_FORM_LINEAR_RR ? 2 : 1;
+            const double time = linear_time(t, form, r16, tiles(t), products * ceil_div(K, 64), num_cus);
             if (tc == GEMM_LINEAR_TILE_AUTO || time < best) {
                 tc = t;
                 best = time;
