@@ -480,7 +480,8 @@ int64_t gemm_rms_backward_workspace(int64_t M, int64_t D);
  * Activations: relu(z) = max(z, 0), its derivative 0 at 0; gelu(z) = z F(z),
  * F the normal distribution's function; gelu_tanh(z) = z (1 + tanh(sqrt(2 /
  * pi) (z + 0.044715 z^3))) / 2; silu(z) = z / (1 + exp(-z)).  Each is within
- * 2^-16 of its value of z as summed.  A NaN stays one.
+ * 2^-16 of its value of z as summed, a derivative within 2^-16 of its two terms (act(z) = z s(z):
+ * s and z s'); what is under 2^-126 in size may be 0.  A NaN stays one.
  *
  * Leading dimensions are in elements; all rows may lie at any address that is
  * aligned to their elements; rows on 16 bytes, and with whole lines of 128, are

@@ -69,19 +69,25 @@ const void* weight_gradient_kernel(int xt, int tile, bool sums);
 
 #if defined(__HIPCC__)
 
+// Both tails are formed 2^8 times as large, and z's part of a result 2^-8 times: the
+// factor's value may lie below 2^-126, where exp2 and rcp give 0, and the
+// result's not (silu(-88) = -5.3e-37; factors themselves: -0).
+
 // The distribution function of the normal distribution at -|z|, from
-// e = exp(-z^2 / 2): e times half of exp(x^2) erfc(x), x = |z| / sqrt 2, which is
-// a polynomial in t = 1 / (1 + 0.54 x) to 4e-6 (fitted here, by least
+// e = 2^8 exp(-z^2 / 2): e times half of exp(x^2) erfc(x), x = |z| / sqrt 2,
+// which is a polynomial in t = 1 / (1 + 0.54 x) to 4e-6 (fitted here, by least
 // squares with weights moved to the largest relative errors).  5e-6 off for |z| <
 // 6 in fp32, a hundredth of fp16's half step; the far tail keeps its relative error.
+__device__ __forceinline__ float normal_exp(float z) { return __builtin_amdgcn_exp2f(fmaf(-0.721347520f * z, z, 8.0f)); }
 __device__ __forceinline__ float normal_tail(float z, float e) {
+    constexpr float s = 0x1p-8f;
     const float t = __builtin_amdgcn_rcpf(fmaf(0.381837662f, fabsf(z), 1.0f));
-    float p = fmaf(0.0480623953f, t, -0.155210704f);
-    p = fmaf(p, t, 0.105571732f);
-    p = fmaf(p, t, 0.063943103f);
-    p = fmaf(p, t, 0.133146182f);
-    p = fmaf(p, t, 0.152152315f);
-    p = fmaf(p, t, 0.152334273f);
+    float p = fmaf(0.0480623953f * s, t, -0.155210704f * s);
+    p = fmaf(p, t, 0.105571732f * s);
+    p = fmaf(p, t, 0.063943103f * s);
+    p = fmaf(p, t, 0.133146182f * s);
+    p = fmaf(p, t, 0.152152315f * s);
+    p = fmaf(p, t, 0.152334273f * s);
     return e * p * t;
 }
 
@@ -94,8 +100,8 @@ __device__ __forceinline__ Logistic logistic_of(int act) {
     return act == ACT_SILU ? Logistic{-1.44269504f, 0.0f} : Logistic{-2.30220818f, -0.102943240f};
 }
 __device__ __forceinline__ float within128(float z) { return __builtin_amdgcn_fmed3f(z, -128.0f, 128.0f); }   // (a NaN too)
-__device__ __forceinline__ float logistic(float z, Logistic l) {      // |z| <= 128
-    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * fmaf(l.c3 * z, z, l.c1)));
+__device__ __forceinline__ float logistic_256(float z, Logistic l) {  // 2^8 s, |z| <= 128
+    return __builtin_amdgcn_rcpf(0x1p-8f + __builtin_amdgcn_exp2f(fmaf(z, fmaf(l.c3 * z, z, l.c1), -8.0f)));
 }
 
 // Values through the activation.  The branches are the same for a whole
@@ -109,13 +115,13 @@ __device__ __forceinline__ void activate(int act, float (&v)[N]) {
     } else if (act == ACT_GELU) {
 #pragma unroll
         for (int e = 0; e < N; ++e) {
-            const float q = normal_tail(v[e], __builtin_amdgcn_exp2f(-0.721347520f * v[e] * v[e]));
+            const float q = normal_tail(v[e], normal_exp(v[e]));
             v[e] *= v[e] > 0.0f ? 1.0f - q : q;
         }
     } else {
         const Logistic l = logistic_of(act);
 #pragma unroll
-        for (int e = 0; e < N; ++e) v[e] *= logistic(within128(v[e]), l);
+        for (int e = 0; e < N; ++e) v[e] = 0x1p-8f * v[e] * logistic_256(within128(v[e]), l);
     }
 }
 
@@ -136,10 +142,10 @@ __device__ __forceinline__ void activate_slope(int act, const float (&z)[N], flo
 #pragma unroll
         for (int e = 0; e < N; ++e) {
             const float c = within128(z[e]);
-            const float x = __builtin_amdgcn_exp2f(-0.721347520f * c * c);
+            const float x = normal_exp(c);
             const float q = normal_tail(c, x), p = c > 0.0f ? 1.0f - q : q;
             a[e] = z[e] * p;
-            d[e] = z[e] == z[e] ? fmaf(0.398942280f * c, x, p) : z[e];
+            d[e] = z[e] == z[e] ? fmaf(0.398942280f * 0x1p-8f * c, x, p) : z[e];
         }
     } else {
         const Logistic l = logistic_of(act);
@@ -147,9 +153,9 @@ __device__ __forceinline__ void activate_slope(int act, const float (&z)[N], flo
 #pragma unroll
         for (int e = 0; e < N; ++e) {
             const float c = within128(z[e]);
-            const float s = logistic(c, l);
-            a[e] = z[e] * s;
-            d[e] = z[e] == z[e] ? fmaf(c * s * (1.0f - s), fmaf(k3 * c, c, k1), s) : z[e];
+            const float s256 = logistic_256(c, l), s = 0x1p-8f * s256;
+            a[e] = 0x1p-8f * z[e] * s256;
+            d[e] = z[e] == z[e] ? fmaf(0x1p-8f * c * s256 * (1.0f - s), fmaf(k3 * c, c, k1), s) : z[e];
         }
     }
 }
