@@ -508,7 +508,8 @@ enum { GEMM_LINEAR_TILE_AUTO = -1, GEMM_LINEAR_TILE_256x256 = 0, GEMM_LINEAR_TIL
        GEMM_LINEAR_TILE_16x32 = 7, GEMM_LINEAR_TILE_16x16 = 8 };
 
 enum { GEMM_FORM_LINEAR_RC = 0, GEMM_FORM_LINEAR_RR = 1, GEMM_FORM_GATED = 2, GEMM_FORM_GATED_BACKWARD = 3,
-       GEMM_FORM_WEIGHT_GRADIENT = 4 };
+       GEMM_FORM_WEIGHT_GRADIENT = 4,
+       GEMM_FORM_LINEAR_RC_PAIR = 16, GEMM_FORM_LINEAR_RR_PAIR = 17 };    /* with A2 and B2: for the query */
 
 typedef struct {
     int32_t tile;              /* GEMM_LINEAR_TILE_* chosen */
@@ -517,7 +518,7 @@ typedef struct {
     int32_t rows16;            /* 1: all the factors' rows start on 16 bytes */
     int32_t reserved;
     int64_t grid;              /* workgroups */
-    int64_t k_tiles;           /* ceil(K / 64), K the length of the sums */
+    int64_t k_tiles;           /* ceil(K / 64), K the length of a product's sums */
 } gemm_linear_info_t;
 
 /* C = act(A B + A2 B2 + bias) + R, and Z = the activation's argument.
@@ -556,7 +557,9 @@ int gemm_weight_gradient(gemm_handle_t h, int64_t M, int64_t N, int64_t K, int d
 
 /* What a call of these sizes would launch on a 256-CU device (rows_on_16:
  * whether all its factors' rows start on 16 bytes); M, N and K as the call
- * takes them.  No HIP call. */
+ * takes them.  A second product counts in the choice of the class, so such a
+ * call has a form of its own here; a bias, a bias's gradient and what else an
+ * operator reads or keeps do not.  No HIP call. */
 int gemm_query_linear(int form, int64_t M, int64_t N, int64_t K, int dtype, int rows_on_16, int tile,
                       gemm_linear_info_t *info);
 

@@ -37,7 +37,8 @@ BLOCK_ROWS = {"row": 1, "tile": FP8_BLOCK}
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 LINEAR_TILES = {"auto": -1, "256x256": 0, "128x256": 1, "128x128": 2, "64x64": 3, "64x64k4": 4, "64x32": 5, "32x32": 6,
                 "16x32": 7, "16x16": 8}
-LINEAR_FORMS = {"linear_rc": 0, "linear_rr": 1, "gated": 2, "gated_backward": 3, "weight_gradient": 4}
+LINEAR_FORMS = {"linear_rc": 0, "linear_rr": 1, "gated": 2, "gated_backward": 3, "weight_gradient": 4, "linear_rc_pair": 16,
+                "linear_rr_pair": 17}
 
 # C functions exported by the library (the names include/pipegemm.h declares)
 EXPORTS = ("gemm_create", "gemm_run", "gemm_destroy", "gemm_set_tile", "gemm_query",
@@ -582,8 +583,8 @@ def gemm_weight_gradient(h, M, N, K, dtype, accumulate, tile, DC, lddc, A, lda, 
 
 
 def gemm_query_linear(form, M, N, K, dtype="bf16", rows16=True, tile="auto", check=True):
-    """The kernel a call of these sizes would use (no HIP call).  Returns
-    (status, dict)."""
+    """The kernel a call of these sizes would use (no HIP call); forms "linear_rc_pair"
+    and "linear_rr_pair" are linear's with a second product.  Returns (status, dict)."""
     info = LinearInfo()
     rc = _lib().gemm_query_linear(_enum(form, LINEAR_FORMS), M, N, K, _enum(dtype, DTYPES), int(rows16),
                                   _enum(tile, LINEAR_TILES), ctypes.byref(info))

@@ -21,6 +21,7 @@ bool aligned(const void* p, int64_t n) { return (uintptr_t)p % (uintptr_t)n == 0
 bool is_half(int t) { return t == GEMM_F16 || t == GEMM_BF16; }
 bool is_act(int a) { return a >= GEMM_ACT_NONE && a <= GEMM_ACT_SILU; }
 bool is_form(int f) { return f >= GEMM_FORM_LINEAR_RC && f <= GEMM_FORM_WEIGHT_GRADIENT; }
+bool is_pair(int f) { return f == GEMM_FORM_LINEAR_RC_PAIR || f == GEMM_FORM_LINEAR_RR_PAIR; }
 
 // A factor of a product: `rows` rows of `cols` values, K along them (`inside`)
 // or across.
@@ -171,12 +172,14 @@ int launch(gemm_handle_t h, const Plan& plan, pg::LinearArgs& a, void* stream) {
 extern "C" {
 
 int gemm_query_linear(int form, int64_t M, int64_t N, int64_t K, int dtype, int rows_on_16, int tile, gemm_linear_info_t* info) {
+    const bool pair = is_pair(form);
+    if (pair) form -= GEMM_FORM_LINEAR_RC_PAIR - GEMM_FORM_LINEAR_RC;
     if (info == nullptr || !is_form(form) || (rows_on_16 != 0 && rows_on_16 != 1)) return GEMM_ERR_INVALID_ARG;
     const int rc = check_sizes(M, N, K, dtype, tile);
     if (rc != GEMM_OK) return rc;
     Plan plan;
     const bool weight = form == GEMM_FORM_WEIGHT_GRADIENT;
-    const int got = plan_sums(form, weight ? N : M, weight ? K : N, weight ? M : K, dtype, rows_on_16 == 1, false, tile, kDefaultCus,
+    const int got = plan_sums(form, weight ? N : M, weight ? K : N, weight ? M : K, dtype, rows_on_16 == 1, pair, tile, kDefaultCus,
                               &plan);
     if (got == GEMM_OK) *info = plan.info;
     return got;
