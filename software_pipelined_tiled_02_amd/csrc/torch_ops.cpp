@@ -22,6 +22,7 @@
 #include <mutex>
 #include <string>
 
+#include "linear_rows.h"
 #include "pipegemm.h"
 
 namespace {
@@ -390,19 +391,14 @@ Matrix row_of(const void* p, int64_t cols, int type) {
     m.type = type;
     return m;
 }
-// Whether two matrices have a byte in common.  Columns beside one another in rows of
-// one distance have none; of rows of two distances in each other's range that is
-// not worked out.
+// Whether two matrices have a byte in common.
 bool touch(const Matrix& x, const Matrix& y) {
-    if (x.p == nullptr || y.p == nullptr || x.rows == 0 || y.rows == 0 || x.cols == 0 || y.cols == 0) return false;
-    const int64_t xs = x.type == GEMM_F32 ? 4 : 2, ys = y.type == GEMM_F32 ? 4 : 2;
-    const char* const x_end = x.p + ((x.rows - 1) * x.ld + x.cols) * xs;
-    const char* const y_end = y.p + ((y.rows - 1) * y.ld + y.cols) * ys;
-    if (x_end <= y.p || y_end <= x.p) return false;
-    const int64_t row = x.ld * xs;
-    if (x.rows == 1 || y.rows == 1 || y.ld * ys != row) return true;
-    const int64_t d = ((y.p - x.p) % row + row) % row;
-    return d < x.cols * xs || d + y.cols * ys > row;
+    if (x.p == nullptr || y.p == nullptr) return false;
+    const auto bytes = [](const Matrix& m) {
+        const int64_t size = m.type == GEMM_F32 ? 4 : 2;
+        return pg::ByteRows{(int64_t)m.p, m.rows, m.cols * size, m.ld * size};
+    };
+    return pg::rows_meet(bytes(x), bytes(y));
 }
 // What is written lies apart from everything else.
 void apart(const Matrix& written, const char* what, std::initializer_list<Matrix> others) {
