@@ -406,6 +406,12 @@ void apart(const Matrix& written, const char* what, std::initializer_list<Matrix
         if (touch(written, o)) throw BadArgument{std::string(what) + " overlaps another operand"};
 }
 
+// A caller's tensor was written: autograd counts such writes, and refuses a backward
+// pass that needs what was there.  (Tensors of inference mode have no count.)
+void written(const at::Tensor& t) {
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 // linear(a, b, layout, bias, activation, residual, a2, b2, keep, out, tile)
 PyObject* linear_(PyObject* const* arg, Py_ssize_t n) {
     arguments(n, 11);
@@ -436,6 +442,7 @@ PyObject* linear_(PyObject* const* arg, Py_ssize_t n) {
                            a2.ld, second ? b2.p : nullptr, b2.ld, bias, r.p, r.ld, z.p, z.ld, c.p, c.ld, stream);
     });
     if (rc != GEMM_OK) return gemm_error(rc, "gemm_linear");
+    if (!none(arg[9])) written(ct);
     return keep ? tuple_of({ct, zt}) : THPVariable_Wrap(std::move(ct));
 }
 
@@ -471,6 +478,7 @@ PyObject* gated_(PyObject* const* arg, Py_ssize_t n) {
                           u.p, u.ld, ho.p, ho.ld, stream);
     });
     if (rc != GEMM_OK) return gemm_error(rc, "gemm_gated");
+    if (!none(arg[7])) written(ht);
     return keep ? tuple_of({ht, gt, ut}) : THPVariable_Wrap(std::move(ht));
 }
 
@@ -536,6 +544,8 @@ PyObject* weight_gradient_(PyObject* const* arg, Py_ssize_t n) {
                                     bias ? (float*)dbt.data_ptr() : nullptr, stream);
     });
     if (rc != GEMM_OK) return gemm_error(rc, "gemm_weight_gradient");
+    if (!none(arg[2])) written(dwt);
+    if (!none(arg[4])) written(dbt);
     return bias ? tuple_of({dwt, dbt}) : THPVariable_Wrap(std::move(dwt));
 }
 
