@@ -613,8 +613,12 @@ def linear(a, b, *, layout="RC", bias=None, activation="none", residual=None, pa
     The first call on a device sets it up, which a graph capture cannot hold
     (RuntimeError).  Rows that start on 16 bytes are the fast case, others take a
     few percent to half longer: a matrix of an odd width is better held in padded
-    rows.  out must overlap nothing else that the
-    call reads or writes."""
+    rows.  out must overlap nothing else that the call reads or writes.
+
+    Nothing is recorded for torch's autograd: results carry no gradient, also
+    where an argument requires one.  The backward pass is the caller's, of
+    gated_backward, linear with layout "RR" and weight_gradient, for instance in a
+    torch.autograd.Function."""
     if stream is not None:
         with _on_stream(stream, a):
             return linear(a, b, layout=layout, bias=bias, activation=activation, residual=residual, pair=pair, keep=keep,
@@ -640,7 +644,7 @@ def gated(x, gate, up, *, gate_bias=None, up_bias=None, activation="silu", keep=
     x: M x K, bfloat16 or float16; gate, up: the weights, N x K of x's type;
     gate_bias, up_bias: N values of float32 or x's type, both of one.  h is
     formed before g and u are rounded, and written into out where it is given.
-    Activations, streams and errors as linear."""
+    Activations, streams, errors and autograd as linear."""
     if stream is not None:
         with _on_stream(stream, x):
             return gated(x, gate, up, gate_bias=gate_bias, up_bias=up_bias, activation=activation, keep=keep, out=out,
@@ -658,7 +662,7 @@ def gated_backward(dy, w, g, u=None, *, activation="silu", keep=False, tile="aut
 
     dy: M x K, the gradient of the next layer's output; w: that layer's weight
     as it lies, K x N; g, u: what gated(keep=True) returned, or linear's z; all
-    of one type.  dh is not rounded.  Streams and errors as linear."""
+    of one type.  dh is not rounded.  Streams, errors and autograd as linear."""
     if stream is not None:
         with _on_stream(stream, dy):
             return gated_backward(dy, w, g, u, activation=activation, keep=keep, tile=tile)
@@ -672,7 +676,7 @@ def weight_gradient(dc, a, *, out=None, bias=False, bias_out=None, accumulate=Fa
 
     dc: M x N, the gradient of the layer's output (before its activation); a:
     M x K, its input; bfloat16 or float16.  out, bias_out: where dw and db are
-    written, or with accumulate=True added.  Streams and errors as linear."""
+    written, or with accumulate=True added.  Streams, errors and autograd as linear."""
     if stream is not None:
         with _on_stream(stream, dc):
             return weight_gradient(dc, a, out=out, bias=bias, bias_out=bias_out, accumulate=accumulate, tile=tile)
