@@ -51,11 +51,14 @@ const void* kernel(int form, int dtype, int tile, bool extra) {
 // Microseconds that the classes take: for a K-tile when few workgroups are there,
 // and when every CU has all that fit (`resident`); for the start and the ending of
 // a workgroup.  Fitted to 5000 times of 630 calls of all forms (1 to 8192 rows, 64 to
-// 8192 columns and depth, factors from HBM).  The class of the least time takes
-// 1.7% longer than the best one on average; with the largest class that gives
-// every CU a workgroup it was 17% (factors in the caches), and three times as long
-// at worst.  64 x 8192 x 8192: 64x32 31.8 us, 32x32 41.4; 1024 x 4096 x 4096: 128x128
-// 38, 256x256 78; 1 x 4096 x 4096: 16x16 8.6, 64x64 25.8.
+// 8192 columns and depth, factors from HBM).  Rows on 2 bytes were not fitted by
+// themselves since they go straight into LDS: they take the factor of rows on 4.  Over
+// 300 other calls of the kernels as they are the class of the least time takes 0.7%
+// (rows on 16 bytes), 3.1% (on 4) and 1.7% (on 2) longer than the best one on average,
+// 1.6 times at worst; with the largest class that gives every CU a workgroup it was
+// 17% (factors in the caches), and three times as long at worst.  64 x 8192 x 8192:
+// 64x32 31.8 us, 32x32 41.4; 1024 x 4096 x 4096: 128x128 38, 256x256 78; 1 x 4096 x
+// 4096: 16x16 8.6, 64x64 25.8.
 struct Cost { double few, all, ends; int resident; };
 constexpr Cost kCost[pg::LINEAR_TILE_COUNT] = {{0.95, 1.80, 9.8, 1}, {0.60, 0.99, 5.8, 1}, {0.35, 0.63, 3.9, 1},
                                                {0.20, 0.67, 2.1, 3}, {0.79, 1.16, 2.9, 1}, {0.60, 0.91, 2.3, 1},
