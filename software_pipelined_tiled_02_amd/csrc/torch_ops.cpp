@@ -200,6 +200,12 @@ void arguments(Py_ssize_t got, Py_ssize_t wanted) {
     TORCH_CHECK(got == wanted, "takes ", wanted, " arguments, got ", got);
 }
 
+// A caller's tensor was written: autograd counts such writes, and refuses a backward
+// pass that needs what was there.  (Tensors of inference mode have no count.)
+void written(const at::Tensor& t) {
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 // run_fp8(a, sa, b, sb, out, out_dtype, accumulate, tile)
 PyObject* run_fp8_(PyObject* const* arg, Py_ssize_t n) {
     arguments(n, 8);
@@ -246,6 +252,7 @@ PyObject* run_fp8_(PyObject* const* arg, Py_ssize_t n) {
     });
     if (rc != GEMM_OK) return gemm_error(rc, "gemm_run_fp8");
     if (none(arg[4])) return THPVariable_Wrap(std::move(made));
+    written(THPVariable_Unpack(arg[4]));
     Py_INCREF(arg[4]);
     return arg[4];
 }
@@ -313,6 +320,7 @@ PyObject* rms_fp8_(PyObject* const* arg, Py_ssize_t n) {
                             (float*)s.data_ptr(), 1, M, (float*)rstd.data_ptr(), stream);
     });
     if (rc != GEMM_OK) return gemm_error(rc, "gemm_rms_fp8");
+    if (!none(arg[7])) written(ht);
     return norm ? tuple_of({q, s, ht, rstd, y}) : tuple_of({q, s, ht, rstd});
 }
 
@@ -351,6 +359,7 @@ PyObject* rms_backward_(PyObject* const* arg, Py_ssize_t n) {
                                  bytes > 0 ? ws.data_ptr() : nullptr, bytes, stream);
     });
     if (rc != GEMM_OK) return gemm_error(rc, "gemm_rms_backward");
+    if (!none(arg[5])) written(dxt);
     return tuple_of({dxt, dw});
 }
 
@@ -404,12 +413,6 @@ bool touch(const Matrix& x, const Matrix& y) {
 void apart(const Matrix& written, const char* what, std::initializer_list<Matrix> others) {
     for (const Matrix& o : others)
         if (touch(written, o)) throw BadArgument{std::string(what) + " overlaps another operand"};
-}
-
-// A caller's tensor was written: autograd counts such writes, and refuses a backward
-// pass that needs what was there.  (Tensors of inference mode have no count.)
-void written(const at::Tensor& t) {
-    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
 }
 
 // linear(a, b, layout, bias, activation, residual, a2, b2, keep, out, tile)
